@@ -14,10 +14,11 @@ that attention hardly looks at are dropped.  The operators:
 ``run`` computes an operator in elementary torch operations, or, where ``own``
 is set, through the library's entry points on the same inputs.
 
-The 4-bit page: uint8 [num_pages][2][Hkv][P * D / 2 + P * D / 16]; a (page,
-K/V, KV head) block is P rows of D / 2 bytes (dim 2i in the low nibble of byte
-i, dim 2i + 1 in the high one; sign and e2m1 magnitude), then P rows of D / 16
-e4m3 scales, one per 16 dims.  A value is e2m1 * e4m3 * k_scale (v_scale).
+The 4-bit page: uint8 [num_pages][2][Hkv][P / 16][16 * D / 2 + 16 * D / 16]; a
+(page, K/V, KV head) block holds its tokens in sixteens, each 16 rows of D / 2
+bytes (dim 2i in the low nibble of byte i, dim 2i + 1 in the high one; sign and
+e2m1 magnitude), then 16 rows of D / 16 e4m3 scales, one per 16 dims.  A value
+is e2m1 * e4m3 * k_scale (v_scale).
 """
 import math
 import random
@@ -179,14 +180,12 @@ def _kv_rows(g, rows, Hkv, D, v_scale):
 
 def _pool4(g, num_pages, Hkv, P, D):
     """A 4-bit pool as bell-shaped rows leave it: codes by their share, and scales within a few octaves of 0.4."""
-    n = num_pages * 2 * Hkv
-    codes = (_normal(g, n, P * D // 2).abs_() * 3.0).clamp_(max=6.49).to(torch.uint8)      # two draws a byte: low
-    high = torch.randint(0, 16, (n, P * D // 2), device="cuda", generator=g, dtype=torch.uint8)
-    sign = (high & 8)
-    scale = torch.exp2(0.7 * _normal(g, n, P * D // GROUP) - 1.3).to(torch.float8_e4m3fn).view(torch.uint8)
-    low = codes | sign
-    both = low | ((high ^ (codes >> 1)) << 4)
-    return torch.cat([both, scale], dim=1).view(num_pages, 2, Hkv, -1)
+    n = num_pages * 2 * Hkv * (P // 16)
+    codes = (_normal(g, n, 8 * D).abs_() * 3.0).clamp_(max=6.49).to(torch.uint8)
+    high = torch.randint(0, 16, (n, 8 * D), device="cuda", generator=g, dtype=torch.uint8)
+    scale = torch.exp2(0.7 * _normal(g, n, D) - 1.3).to(torch.float8_e4m3fn).view(torch.uint8)
+    both = codes | (high & 8) | ((high ^ (codes >> 1)) << 4)
+    return torch.cat([both, scale], dim=1).view(num_pages, 2, Hkv, P // 16, 9 * D)
 
 
 def prepare(case, seed):
@@ -256,12 +255,17 @@ def _table(device):
     return torch.tensor(MAGNITUDES + tuple(-m for m in MAGNITUDES), device=device)
 
 
-def _unpack(blocks, P, D):
-    """[..., block bytes] -> fp32 [..., P, D], without the pool's scale."""
-    rows = blocks[..., :P * D // 2].unflatten(-1, (P, D // 2))
-    scales = blocks[..., P * D // 2:].contiguous().view(torch.float8_e4m3fn).float().unflatten(-1, (P, D // GROUP))
+def _views(pool, D):
+    """A pool's code bytes [..., P / 16, 16, D / 2] and scale bytes [..., P / 16, 16, D / 16]."""
+    return pool[..., :8 * D].unflatten(-1, (16, D // 2)), pool[..., 8 * D:].unflatten(-1, (16, D // GROUP))
+
+
+def _unpack(blocks, D):
+    """[..., P / 16, 9 * D] bytes -> fp32 [..., P, D], without the pool's scale."""
+    rows, scales = _views(blocks, D)
+    scales = scales.contiguous().view(torch.float8_e4m3fn).float()
     codes = torch.stack([rows & 15, rows >> 4], dim=-1).flatten(-2)
-    return _table(blocks.device)[codes.int()] * scales.repeat_interleave(GROUP, dim=-1)
+    return (_table(blocks.device)[codes.int()] * scales.repeat_interleave(GROUP, dim=-1)).flatten(-3, -2)
 
 
 def _pack(x, scale):
@@ -297,26 +301,25 @@ def _gather_kv(s, half):
     n = (s["max_kv"] + P - 1) // P
     pages = _token_pages(s, torch.arange(n, device="cuda")[None] * P)[0]
     x = s["pool"][pages, half]
-    x = _unpack(x, P, D) * (s["v_scale"] if half else s["k_scale"]) if x.dtype == torch.uint8 else x.float()
+    x = _unpack(x, D) * (s["v_scale"] if half else s["k_scale"]) if x.dtype == torch.uint8 else x.float()
     return x.permute(0, 2, 1, 3, 4).flatten(2, 3)[:, :, :s["max_kv"]]
 
 
-def _plain_expand(pool, page_ids, P, D, k_scale, v_scale):
+def _plain_expand(pool, page_ids, D, k_scale, v_scale):
     f = torch.tensor([k_scale, v_scale], device="cuda")[None, :, None, None, None]
-    return (_unpack(pool[page_ids.long()], P, D) * f).to(torch.bfloat16)
+    return (_unpack(pool[page_ids.long()], D) * f).to(torch.bfloat16)
 
 
 def _plain_store(s):
     P, D = s["case"]["P"], s["case"]["D"]
     b, t = _rows_of(s)
     page, row = s["page_table"][s["indptr"][b] + t // P].long(), t % P
-    for_rows = s["pool"][..., :P * D // 2].unflatten(-1, (P, D // 2))
-    for_scales = s["pool"][..., P * D // 2:].unflatten(-1, (P, D // GROUP))
+    codes, scales = _views(s["pool"], D)
     kb, ks = _pack(s["k_new"], s["k_scale"])
     vb, vs = _pack(s["v_new"], s["v_scale"])
-    for_rows[page, 0, :, row], for_scales[page, 0, :, row] = kb, ks
-    for_rows[page, 1, :, row], for_scales[page, 1, :, row] = vb, vs
-    return _plain_expand(s["pool"], s["page_ids"], P, D, s["k_scale"], s["v_scale"])
+    codes[page, 0, :, row // 16, row % 16], scales[page, 0, :, row // 16, row % 16] = kb, ks
+    codes[page, 1, :, row // 16, row % 16], scales[page, 1, :, row // 16, row % 16] = vb, vs
+    return _plain_expand(s["pool"], s["page_ids"], D, s["k_scale"], s["v_scale"])
 
 
 def _plain_decode4(s):
@@ -389,12 +392,11 @@ def _plain_evict(s):
     if c["bits"] == 16:
         s["pool_out"].transpose(1, 2)[page_out, head, :, row_out] = s["pool"].transpose(1, 2)[page, head, :, r]
         return s["kept"], s["pool_out"], s["weights_out"]
-    half = P * D // 2
-    for_rows = [x[..., :half].unflatten(-1, (P, D // 2)).transpose(1, 2) for x in (s["pool_out"], s["pool"])]
-    for_scales = [x[..., half:].unflatten(-1, (P, D // GROUP)).transpose(1, 2) for x in (s["pool_out"], s["pool"])]
-    for_rows[0][page_out, head, :, row_out] = for_rows[1][page, head, :, r]
-    for_scales[0][page_out, head, :, row_out] = for_scales[1][page, head, :, r]
-    back = _plain_expand(s["pool_out"], s["out_table"], P, D, s["k_scale"], s["v_scale"])
+    codes, scales = _views(s["pool"].transpose(1, 2), D)
+    codes_out, scales_out = _views(s["pool_out"].transpose(1, 2), D)
+    codes_out[page_out, head, :, row_out // 16, row_out % 16] = codes[page, head, :, r // 16, r % 16]
+    scales_out[page_out, head, :, row_out // 16, row_out % 16] = scales[page, head, :, r // 16, r % 16]
+    back = _plain_expand(s["pool_out"], s["out_table"], D, s["k_scale"], s["v_scale"])
     return s["kept"], back, s["weights_out"]
 
 
@@ -461,16 +463,17 @@ def _two_to(k):
 def _value4(block, P, D):
     """Values of one (page, K/V, head) block or several, from the bits of the two formats: fp64 [..., P, D]."""
     b = block.to(torch.int64)
-    n = b[..., :P * D // 2]
-    code = torch.stack((n % 16, n // 16), -1).reshape(*n.shape[:-1], P, D)
+    lead = b.shape[:-2]
+    n = b[..., :8 * D]
+    code = torch.stack((n % 16, n // 16), -1).reshape(*lead, P, D // GROUP, GROUP)
     e, m = (code // 2) % 4, code % 2
     mag = torch.where(e == 0, 0.5 * m.double(), (1 + 0.5 * m.double()) * _two_to(e - 1))
     val = torch.where(code >= 8, -mag, mag)
-    f = b[..., P * D // 2:].reshape(*n.shape[:-1], P, D // GROUP)
+    f = b[..., 8 * D:].reshape(*lead, P, D // GROUP)
     fe, fm = (f // 8) % 16, f % 8
     fs = torch.where(fe == 0, fm.double() / 512, (8 + fm.double()) * _two_to(fe - 10))
     fs = torch.where((fe == 15) & (fm == 7), torch.full_like(fs, float("nan")), fs) * torch.where(f >= 128, -1.0, 1.0)
-    return (val.reshape(*val.shape[:-1], D // GROUP, GROUP) * fs[..., None]).reshape(val.shape)
+    return (val * fs[..., None]).reshape(*lead, P, D)
 
 
 def _nearest4(x):
