@@ -362,6 +362,118 @@ ATTN_API attn_status attn_unpack_kv_heads(const void* buf, int64_t num_pages, in
                                           int64_t n_pages, int32_t head_begin, int32_t n_heads, void* kv_cache,
                                           int32_t* device_error, void* stream);
 
+/*
+ * The 4-bit KV cache -- the same pages, heads and tokens as kv_cache in 4 bits
+ * a value plus one 8-bit scale per 16 dims (9/32 of the bytes), for batches
+ * whose bf16 cache would not fit or whose decode waits for it.  No source
+ * describes one: attn_append_kv4 to attn_decode_kv4 are interface additions.
+ *
+ *   kv4_cache  uint8 [num_pages][2][Hkv][page_size / 16][9 * head_dim], 16-byte
+ *              aligned ([.][0] = K, [.][1] = V).  The last two dimensions are
+ *              16 tokens: 16 rows of head_dim / 2 code bytes (dim 2i in the low
+ *              nibble of byte i, dim 2i + 1 in the high one), then 16 rows of
+ *              head_dim / 16 scale bytes.
+ *   value      code * scale * g.  Code: e2m1 (sign; 0, .5, 1, 1.5, 2, 3, 4, 6);
+ *              scale: e4m3; g: k_scale for K, v_scale for V, one per pool, a
+ *              power of two in [2^-40, 2^40] (else ATTN_ERR_INVALID_ARG), so
+ *              that the block scales (2^-9 .. 448) cover the data: 1 for values
+ *              around 1.  Use one k_scale and v_scale for all calls on a pool.
+ * bf16 holds every such value exactly.
+ *
+ * attn_append_kv4 -- attn_append_kv into a 4-bit cache: each 16 dims x of a new
+ * row are stored as scale s = e4m3 round(max|x| / (6 g)) and codes
+ * e2m1 round(x / (g s)), both to nearest, ties to even, saturating (largest
+ * magnitude 6 * 448 * g).  A NaN makes its 16 values NaN.  Other rows' bytes
+ * keep their values.
+ *
+ * attn_expand_kv4 -- the listed pages' values as bf16 HND pages
+ * buf[n_pages][2][Hkv][page_size][head_dim] (whole pages, exact), for
+ * attn_prefill over a 4-bit cache: expand a request's pages into a bf16 pool
+ * and plan the prefill on that.  head_dim 64 or 128, page_size a multiple of
+ * 16 (else ATTN_ERR_UNSUPPORTED); page_ids, n_pages, device_error as in
+ * attn_pack_kv_heads.
+ *
+ * attn_decode_kv4 -- attn_decode over a 4-bit cache: the same plan, rows, sinks,
+ * out and lse (and the same workspace regions: it must not overlap attn_decode
+ * on the same plan).
+ *
+ * All three are asynchronous on `stream` and capturable (the plan's lengths are
+ * fixed; there is no form for attn_graph_plan).  Plans: host-planned paged
+ * ones (others: ATTN_ERR_INVALID_ARG).
+ */
+ATTN_API attn_status attn_append_kv4(attn_plan_t plan, const void* k_new, const void* v_new, float k_scale,
+                                     float v_scale, void* kv4_cache, void* stream);
+ATTN_API attn_status attn_expand_kv4(const void* kv4_cache, int64_t num_pages, int32_t num_kv_heads,
+                                     int32_t page_size, int32_t head_dim, const int32_t* page_ids, int64_t n_pages,
+                                     float k_scale, float v_scale, void* buf, int32_t* device_error, void* stream);
+ATTN_API attn_status attn_decode_kv4(attn_plan_t plan, const void* q, const void* kv4_cache, float k_scale,
+                                     float v_scale, const float* sinks, void* out, float* lse, void* stream);
+
+/*
+ * attn_key_weights / attn_key_weights_kv4 -- how much attention each cached key
+ * receives, the measure that eviction goes by (no source describes it: an
+ * interface addition).  For every request of the plan with query rows, every
+ * KV head g and every cached token t < kv_len:
+ *
+ *   weights[t, g] = decay * prev[t, g] + sum_{i, h} exp(sm_scale q[i,h] . k[t,g] - lse[i,h])
+ *
+ * over the request's last `window` query rows i (0: all of them) that see key
+ * t under the plan's mask and the query heads h of KV head g.  Tokens that the
+ * plan appends (t >= kv_len - qo_len) have no previous weight; with decay = 0
+ * prev is not read.  lse is what attn_decode / attn_prefill wrote for the same
+ * q (with a sink, the weights of a row and head sum to less than 1).
+ *
+ *   weights, prev  fp32 [num_pages][Hkv][page_size], device, paged like the
+ *                  cache (prev may be weights; NULL when decay = 0).  Only the
+ *                  slots of the plan's tokens are written; requests without
+ *                  query rows are left out.
+ *   lse            fp32 [total_qo_rows][Hq];   decay finite, >= 0
+ *   kv_cache       as in attn_decode;  kv4_cache, k_scale as in attn_decode_kv4
+ * Decode and prefill rows alike.  The sum's order is fixed: equal calls give
+ * equal bits.  Pages out of range set ATTN_DEVICE_ERR_PAGE_ID and their tokens
+ * are skipped.  Host-planned paged plans only.  Async on `stream`.
+ */
+ATTN_API attn_status attn_key_weights(attn_plan_t plan, const void* q, const void* kv_cache, const float* lse,
+                                      const float* prev, float decay, int32_t window, float* weights, void* stream);
+ATTN_API attn_status attn_key_weights_kv4(attn_plan_t plan, const void* q, const void* kv4_cache, float k_scale,
+                                          const float* lse, const float* prev, float decay, int32_t window,
+                                          float* weights, void* stream);
+
+/*
+ * attn_evict_kv / attn_evict_kv4 -- shrink every request of the plan to at most
+ * `budget` cached tokens per KV head, by weight (no source describes it: an
+ * interface addition).  Of a request's n = kv_len tokens each KV head keeps
+ * m = min(n, budget): the newest min(n, recent), and of the others those with
+ * the largest weights (equal ones: the older token; NaN counts as the lowest).
+ * Heads choose on their own; kept tokens stay in order and become tokens
+ * 0 .. m - 1 of the request, so that decode, key weights and eviction go on
+ * over a cache of m tokens (plan it with kv_len = m; keys carry their
+ * positional encoding with them).
+ *
+ *   weights         fp32 [num_pages][Hkv][page_size] as attn_key_weights writes it
+ *   kept            int32 [batch][Hkv][budget], device, output: the kept token
+ *                   indices in order, -1 from m on
+ *   page_table_out  device int32: pages that receive the kept tokens, request b's
+ *                   ceil(m_b / page_size) ids after those of the requests before
+ *                   it, in pools of num_pages_out pages kv_out / weights_out
+ *                   (kv_cache's and weights' layout; may be the input pools, the
+ *                   pages then distinct from every page the plan reads).
+ *                   NULL: in place, in each request's own first pages; kv_out,
+ *                   weights_out and num_pages_out are then the inputs' own, and
+ *                   no page may belong to two requests.
+ *   1 <= budget, 0 <= recent <= budget
+ * Slots of the receiving pages past the kept tokens are left as they were.
+ * Page ids out of range set ATTN_DEVICE_ERR_PAGE_ID: such a source page's
+ * tokens count as NaN weights, and what would be read from or written to such a
+ * page is skipped.  Host-planned paged plans only.  Async on `stream`.
+ */
+ATTN_API attn_status attn_evict_kv(attn_plan_t plan, const float* weights, const void* kv_cache, int32_t budget,
+                                   int32_t recent, int32_t* kept, const int32_t* page_table_out,
+                                   int32_t num_pages_out, void* kv_out, float* weights_out, void* stream);
+ATTN_API attn_status attn_evict_kv4(attn_plan_t plan, const float* weights, const void* kv4_cache, int32_t budget,
+                                    int32_t recent, int32_t* kept, const int32_t* page_table_out,
+                                    int32_t num_pages_out, void* kv4_out, float* weights_out, void* stream);
+
 /* Copy the plan's summary into *info (host only). */
 ATTN_API attn_status attn_plan_get_info(attn_plan_t plan, attn_plan_info* info);
 

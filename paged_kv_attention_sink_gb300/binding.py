@@ -58,6 +58,13 @@ def _declare(lib):
         "attn_merge_states": (st, [p, p, p, p, p, p, i32, i32, i32, p]),
         "attn_merge_states_f32": (st, [p, p, p, p, p, i32, p, i32, i32, i32, p]),
         "attn_append_kv": (st, [p, p, p, p, p]),
+        "attn_append_kv4": (st, [p, p, p, f32, f32, p, p]),
+        "attn_expand_kv4": (st, [p, i64, i32, i32, i32, p, i64, f32, f32, p, p, p]),
+        "attn_decode_kv4": (st, [p, p, p, f32, f32, p, p, p, p]),
+        "attn_key_weights": (st, [p, p, p, p, p, f32, i32, p, p]),
+        "attn_key_weights_kv4": (st, [p, p, p, f32, p, p, f32, i32, p, p]),
+        "attn_evict_kv": (st, [p, p, p, i32, i32, p, p, i32, p, p, p]),
+        "attn_evict_kv4": (st, [p, p, p, i32, i32, p, p, i32, p, p, p]),
         "attn_plan_ragged": (st, [p, p, i32, i32, i32, i32, i32, f32, i32, p, p]),
         "attn_graph_plan": (st, [i32, i32, i32, i32, i32, f32, i32, i64, p, i32, p, p]),
         "attn_decode_graph": (st, [p, p, p, p, p, p, p, p, p, p]),
@@ -126,6 +133,46 @@ def _stream_ptr(stream=None):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _check_cuda(device, **tensors):
+    """Each given tensor must be a contiguous CUDA tensor of its dtype and shape
+    on `device` (specs: name=(tensor, dtype, shape); shape None: any)."""
+    for name, (t, dt, shape) in tensors.items():
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dt and t.is_contiguous()):
+            raise TypeError(f"{name} must be a contiguous {dt} CUDA tensor")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _launch_on(device, stream, fn_name, *args):
+    """Call fn_name(*args, stream) with `device` current: a kernel runs, and the
+    current stream is looked up, on the device that holds the tensors."""
+    fn = getattr(load_library(), fn_name)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _check(fn_name, fn(*args, _stream_ptr(stream)))
+    _check(fn_name, fn(*args, _stream_ptr(stream)))
+
+
+def _empty_on(stream, shape, dtype, device):
+    """An output allocated on the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+KV4_TOKENS, KV4_GROUP = 16, 16   # tokens stored together, dims per scale
+
+
+def kv4_cache_shape(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int):
+    """Shape of a 4-bit cache (uint8): [num_pages, 2, Hkv, page_size / 16, 9 * head_dim]."""
+    if page_size % KV4_TOKENS or head_dim % KV4_GROUP:
+        raise ValueError("a 4-bit cache needs page_size and head_dim in multiples of 16")
+    return (num_pages, 2, num_kv_heads, page_size // KV4_TOKENS, KV4_TOKENS * (head_dim // 2 + head_dim // KV4_GROUP))
+
+
 class Plan:
     """A planned batch: host work lists inside the library plus the device
     workspace (a torch uint8 buffer) they were uploaded to.
@@ -162,6 +209,7 @@ class Plan:
         self.total_rows = int(qo[-1]) if len(qo) else 0
         handle = ctypes.c_void_p()
         ws_bytes = ctypes.c_size_t()
+        self._kv = kv.copy(), lpl.copy()
         _check("attn_plan", lib.attn_plan(
             qo.ctypes.data, kv.ctypes.data, _ptr(page_table), lpl.ctypes.data, self.batch, num_qo_heads,
             num_kv_heads, head_dim, page_size, int(self.causal), self.sm_scale, int(num_pages),
@@ -184,6 +232,13 @@ class Plan:
     @property
     def handle(self):
         return self._handle
+
+    @property
+    def kv_lens(self) -> np.ndarray:
+        """Cached tokens of each request."""
+        kv, lpl = self._kv
+        pages = np.diff(kv)
+        return np.where(pages > 0, (pages - 1) * self.page_size + lpl[:self.batch], 0)
 
     def info(self) -> dict:
         info = PlanInfo()
@@ -259,6 +314,113 @@ class Plan:
             self._handle, _ptr(k_new), _ptr(v_new), _ptr(kv_cache), _stream_ptr(stream)))
         return kv_cache
 
+    # -- 4-bit cache ------------------------------------------------------
+    def kv4_shape(self, num_pages: Optional[int] = None):
+        """Shape of the 4-bit cache this plan works on (uint8)."""
+        return kv4_cache_shape(self.num_pages if num_pages is None else num_pages, self.num_kv_heads, self.page_size,
+                               self.head_dim)
+
+    def append_kv4(self, k_new, v_new, kv4_cache, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+        """append_kv into a 4-bit cache (see attn_append_kv4; in place)."""
+        dev, shape = self.workspace.device, (self.total_rows, self.num_kv_heads, self.head_dim)
+        _check_cuda(dev, k_new=(k_new, torch.bfloat16, shape), v_new=(v_new, torch.bfloat16, shape),
+                    kv4_cache=(kv4_cache, torch.uint8, self.kv4_shape()))
+        _launch_on(dev, stream, "attn_append_kv4", self._handle, _ptr(k_new), _ptr(v_new), k_scale, v_scale,
+                   _ptr(kv4_cache))
+        return kv4_cache
+
+    def decode_kv4(self, q, kv4_cache, sinks=None, out=None, lse=None, k_scale: float = 1.0, v_scale: float = 1.0,
+                   stream=None):
+        """decode over a 4-bit cache; returns (out, lse)."""
+        dev, H, D = self.workspace.device, self.num_qo_heads, self.head_dim
+        out = _empty_on(stream, (self.total_rows, H, D), torch.bfloat16, dev) if out is None else out
+        _check_cuda(dev, q=(q, torch.bfloat16, (self.total_rows, H, D)), out=(out, torch.bfloat16, (self.total_rows, H, D)),
+                    kv4_cache=(kv4_cache, torch.uint8, self.kv4_shape()))
+        if sinks is not None:
+            _check_cuda(dev, sinks=(sinks, torch.float32, (H,)))
+        if lse is not None:
+            _check_cuda(dev, lse=(lse, torch.float32, (self.total_rows, H)))
+        _launch_on(dev, stream, "attn_decode_kv4", self._handle, _ptr(q), _ptr(kv4_cache), k_scale, v_scale, _ptr(sinks),
+                   _ptr(out), _ptr(lse))
+        return out, lse
+
+    # -- attention weights per cached key, and eviction by them -----------
+    def _cache_spec(self, four, num_pages):
+        if four:
+            return torch.uint8, self.kv4_shape(num_pages)
+        return torch.bfloat16, (num_pages, 2, self.num_kv_heads, self.page_size, self.head_dim)
+
+    def _key_weights(self, four, q, cache, lse, weights, prev, decay, window, k_scale, stream):
+        dev, H = self.workspace.device, self.num_qo_heads
+        paged = (self.num_pages, self.num_kv_heads, self.page_size)
+        if prev is None and decay != 0:
+            prev = weights
+        _check_cuda(dev, q=(q, torch.bfloat16, (self.total_rows, H, self.head_dim)),
+                    lse=(lse, torch.float32, (self.total_rows, H)), weights=(weights, torch.float32, paged),
+                    cache=(cache, *self._cache_spec(four, self.num_pages)))
+        if prev is not None:
+            _check_cuda(dev, prev=(prev, torch.float32, paged))
+        scale = (k_scale,) if four else ()
+        _launch_on(dev, stream, "attn_key_weights_kv4" if four else "attn_key_weights", self._handle, _ptr(q),
+                   _ptr(cache), *scale, _ptr(lse), _ptr(prev), float(decay), int(window), _ptr(weights))
+        return weights
+
+    def key_weights(self, q, kv_cache, lse, weights, prev=None, decay: float = 1.0, window: int = 0, stream=None):
+        """weights[page, g, row] of every cached key of the plan's requests:
+        decay * prev (weights itself by default; nothing for tokens this plan
+        appends) plus the attention weight the last `window` query rows (0: all)
+        give it, summed over g's query heads.  lse is the rows' log-sum-exp as
+        decode / prefill returned it.  weights, prev: fp32 [num_pages, Hkv,
+        page_size].  See attn_key_weights."""
+        return self._key_weights(False, q, kv_cache, lse, weights, prev, decay, window, 1.0, stream)
+
+    def key_weights_kv4(self, q, kv4_cache, lse, weights, prev=None, decay: float = 1.0, window: int = 0,
+                        k_scale: float = 1.0, stream=None):
+        """key_weights over a 4-bit cache."""
+        return self._key_weights(True, q, kv4_cache, lse, weights, prev, decay, window, k_scale, stream)
+
+    def _evict(self, four, weights, cache, budget, recent, kept, page_table_out, kv_out, weights_out, stream):
+        dev, Hkv, P = self.workspace.device, self.num_kv_heads, self.page_size
+        if budget < 1 or not 0 <= recent <= budget:
+            raise ValueError("eviction needs budget >= 1 and 0 <= recent <= budget")
+        _check_cuda(dev, weights=(weights, torch.float32, (self.num_pages, Hkv, P)),
+                    cache=(cache, *self._cache_spec(four, self.num_pages)))
+        if page_table_out is None and (kv_out is not None or weights_out is not None):
+            raise ValueError("kv_out / weights_out need page_table_out (without it eviction works in place)")
+        kv_out = cache if kv_out is None else kv_out
+        weights_out = weights if weights_out is None else weights_out
+        if page_table_out is not None:
+            if kv_out.dim() == 0 or weights_out.shape[0] != kv_out.shape[0]:
+                raise ValueError("kv_out and weights_out must have the same number of pages")
+            pages = sum(-(-int(n) // P) for n in self.evicted_lens(budget))
+            _check_cuda(dev, page_table_out=(page_table_out, torch.int32, (pages,)),
+                        kv_out=(kv_out, *self._cache_spec(four, kv_out.shape[0])),
+                        weights_out=(weights_out, torch.float32, (kv_out.shape[0], Hkv, P)))
+        kept = _empty_on(stream, (self.batch, Hkv, budget), torch.int32, dev) if kept is None else kept
+        _check_cuda(dev, kept=(kept, torch.int32, (self.batch, Hkv, budget)))
+        _launch_on(dev, stream, "attn_evict_kv4" if four else "attn_evict_kv", self._handle, _ptr(weights), _ptr(cache),
+                   budget, recent, _ptr(kept), _ptr(page_table_out), kv_out.shape[0], _ptr(kv_out), _ptr(weights_out))
+        return kept
+
+    def evicted_lens(self, budget: int) -> np.ndarray:
+        """Tokens each request holds after evict_kv(budget): min(kv_len, budget)."""
+        return np.minimum(self.kv_lens, budget)
+
+    def evict_kv(self, weights, kv_cache, budget: int, recent: int, kept=None, page_table_out=None, kv_out=None,
+                 weights_out=None, stream=None):
+        """Keep, per request and KV head, the newest `recent` tokens and the most
+        attended others, `budget` in all, as tokens 0 .. m - 1 of the request:
+        in place, or in the pages page_table_out (ceil(m / page_size) per request,
+        m = evicted_lens(budget)) of kv_out / weights_out (default: the same
+        pools).  Returns kept: int32 [batch, Hkv, budget], the tokens' former
+        indices, -1 from m on.  See attn_evict_kv."""
+        return self._evict(False, weights, kv_cache, budget, recent, kept, page_table_out, kv_out, weights_out, stream)
+
+    def evict_kv4(self, weights, kv4_cache, budget: int, recent: int, kept=None, page_table_out=None, kv_out=None,
+                  weights_out=None, stream=None):
+        """evict_kv over a 4-bit cache."""
+        return self._evict(True, weights, kv4_cache, budget, recent, kept, page_table_out, kv_out, weights_out, stream)
+
 
 class RaggedPlan(Plan):
     """A planned batch over contiguous K / V (no KV cache): every request runs
@@ -314,6 +476,8 @@ class RaggedPlan(Plan):
     def append_kv(self, *args, **kwargs):
         raise TypeError("a ragged plan has no KV cache")
 
+    append_kv4 = decode_kv4 = key_weights = key_weights_kv4 = evict_kv = evict_kv4 = append_kv
+
 
 class GraphPlan(Plan):
     """Decode plan for CUDA-graph capture: the work list is built on the device
@@ -368,6 +532,8 @@ class GraphPlan(Plan):
 
     def append_kv(self, *args, **kwargs):
         raise TypeError("a graph plan only decodes")
+
+    append_kv4 = decode_kv4 = key_weights = key_weights_kv4 = evict_kv = evict_kv4 = append_kv
 
 
 def attn_plan(qo_indptr, kv_indptr, page_table, last_page_len, num_qo_heads, num_kv_heads,
@@ -453,6 +619,26 @@ def attn_unpack_kv_heads(buf, page_ids, head_begin, kv_cache, device_error=None,
     [head_begin, head_begin + n_heads) of pages page_ids of the pool (in place)."""
     _head_slice("attn_unpack_kv_heads", kv_cache, page_ids, head_begin, buf.shape[2], buf, device_error, stream)
     return kv_cache
+
+
+def attn_expand_kv4(kv4_cache, page_ids, head_dim: int, buf=None, k_scale: float = 1.0, v_scale: float = 1.0,
+                    device_error=None, stream=None):
+    """Pages page_ids of a 4-bit cache as bf16 HND pages buf [n_pages, 2, Hkv,
+    page_size, head_dim] (exact; see attn_expand_kv4)."""
+    if not isinstance(kv4_cache, torch.Tensor) or kv4_cache.dim() != 5:
+        raise TypeError("kv4_cache must be a uint8 CUDA tensor [num_pages, 2, Hkv, page_size / 16, 9 * head_dim]")
+    dev, (num_pages, _, hkv, subs, _) = kv4_cache.device, kv4_cache.shape
+    P = subs * KV4_TOKENS
+    _check_cuda(dev, kv4_cache=(kv4_cache, torch.uint8, kv4_cache_shape(num_pages, hkv, P, head_dim)),
+                page_ids=(page_ids, torch.int32, None))
+    shape = (page_ids.numel(), 2, hkv, P, head_dim)
+    buf = _empty_on(stream, shape, torch.bfloat16, dev) if buf is None else buf
+    _check_cuda(dev, buf=(buf, torch.bfloat16, shape))
+    if device_error is not None:
+        _check_cuda(dev, device_error=(device_error, torch.int32, None))
+    _launch_on(dev, stream, "attn_expand_kv4", _ptr(kv4_cache), num_pages, hkv, P, head_dim, _ptr(page_ids),
+               page_ids.numel(), k_scale, v_scale, _ptr(buf), _ptr(device_error))
+    return buf
 
 
 def attn_selftest_bounded_wait(result=None, stream=None):

@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -98,11 +99,12 @@ extern "C" attn_status attn_plan_bind_workspace(attn_plan_t plan, void* workspac
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     // The work lists lie in [0, L.counters): one host image, one copy (graph
     // plans have none: their list is built on the device).
-    if (!plan->units.empty() || !plan->items.empty() || !plan->append_slots.empty()) {
+    if (!plan->units.empty() || !plan->items.empty() || !plan->requests.empty()) {
         std::vector<unsigned char> img(L.counters, 0);
         auto put = [&](size_t off, const void* src, size_t bytes) {
             if (bytes) std::memcpy(img.data() + off, src, bytes);
         };
+        put(L.requests, plan->requests.data(), plan->requests.size() * sizeof(attn::RequestInfo));
         put(L.units, plan->units.data(), plan->units.size() * sizeof(attn::DecodeUnit));
         put(L.items, plan->items.data(), plan->items.size() * sizeof(attn::PrefillItem));
         put(L.item_off, plan->item_off.data(), plan->item_off.size() * sizeof(int32_t));
@@ -286,6 +288,113 @@ extern "C" attn_status attn_unpack_kv_heads(const void* buf, int64_t num_pages, 
                                            int32_t* device_error, void* stream) {
     return head_slice(true, kv_cache, num_pages, num_kv_heads, page_size, head_dim, page_ids, n_pages, head_begin,
                       n_heads, const_cast<void*>(buf), device_error, stream);
+}
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+// A 4-bit pool's scale: a power of two between 2^-40 and 2^40, so that
+// scaling by it (and by its inverse) rounds nothing.
+bool valid_pool_scale(float s) {
+    int e = 0;
+    return std::isfinite(s) && s > 0.f && std::frexp(s, &e) == 0.5f && e - 1 >= -40 && e - 1 <= 40;
+}
+
+// A bound paged plan planned on the host (the kind that the operators on whole
+// requests and on 4-bit pages take).
+attn_status check_paged(attn_plan_t plan) {
+    if (!plan || plan->ragged || plan->graph) return ATTN_ERR_INVALID_ARG;
+    return plan->bound ? ATTN_OK : ATTN_ERR_NOT_BOUND;
+}
+
+attn_status key_weights(attn_plan_t plan, bool four, const void* q, const void* pool, float k_scale, const float* lse,
+                        const float* prev, float decay, int32_t window, float* weights, void* stream) {
+    if (attn_status st = check_paged(plan); st != ATTN_OK) return st;
+    if (!std::isfinite(decay) || decay < 0.f || window < 0 || !valid_pool_scale(k_scale)) return ATTN_ERR_INVALID_ARG;
+    if (plan->info.total_qo_rows == 0) return ATTN_OK;
+    if (!q || !pool || !lse || !weights || (decay != 0.f && !prev)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(pool) || !aligned4(lse) || !aligned4(prev) || !aligned4(weights))
+        return ATTN_ERR_INVALID_ARG;
+    return attn::launch_key_weights(plan, four, q, pool, k_scale, lse, prev, decay, window, weights,
+                                    static_cast<cudaStream_t>(stream));
+}
+
+attn_status evict(attn_plan_t plan, bool four, const float* weights, const void* pool, int32_t budget, int32_t recent,
+                  int32_t* kept, const int32_t* page_table_out, int32_t num_pages_out, void* pool_out,
+                  float* weights_out, void* stream) {
+    if (attn_status st = check_paged(plan); st != ATTN_OK) return st;
+    if (budget <= 0 || recent < 0 || recent > budget) return ATTN_ERR_INVALID_ARG;
+    if (plan->batch == 0) return ATTN_OK;
+    if (!weights || !pool || !kept || !pool_out || !weights_out) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(pool) || !aligned16(pool_out) || !aligned4(weights) || !aligned4(weights_out) || !aligned4(kept))
+        return ATTN_ERR_INVALID_ARG;
+    if (!page_table_out && (pool_out != pool || weights_out != weights || num_pages_out != plan->num_pages))
+        return ATTN_ERR_INVALID_ARG;
+    if (page_table_out && (num_pages_out <= 0 || !aligned4(page_table_out))) return ATTN_ERR_INVALID_ARG;
+    return attn::launch_evict(plan, four, weights, pool, budget, recent, kept, page_table_out, num_pages_out, pool_out,
+                              weights_out, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" attn_status attn_append_kv4(attn_plan_t plan, const void* k_new, const void* v_new, float k_scale,
+                                       float v_scale, void* kv4_cache, void* stream) {
+    if (attn_status st = check_paged(plan); st != ATTN_OK) return st;
+    if (!valid_pool_scale(k_scale) || !valid_pool_scale(v_scale)) return ATTN_ERR_INVALID_ARG;
+    if (plan->info.total_qo_rows == 0) return ATTN_OK;
+    if (!k_new || !v_new || !kv4_cache || !aligned16(k_new) || !aligned16(v_new) || !aligned16(kv4_cache))
+        return ATTN_ERR_INVALID_ARG;
+    return attn::launch_append_kv4(plan, k_new, v_new, kv4_cache, k_scale, v_scale, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" attn_status attn_expand_kv4(const void* kv4_cache, int64_t num_pages, int32_t num_kv_heads,
+                                       int32_t page_size, int32_t head_dim, const int32_t* page_ids, int64_t n_pages,
+                                       float k_scale, float v_scale, void* buf, int32_t* device_error, void* stream) {
+    if (n_pages < 0 || num_pages <= 0 || num_kv_heads <= 0 || page_size <= 0 || head_dim <= 0 ||
+        !valid_pool_scale(k_scale) || !valid_pool_scale(v_scale))
+        return ATTN_ERR_INVALID_ARG;
+    if ((head_dim != 64 && head_dim != 128) || page_size % attn::kKv4Tokens != 0) return ATTN_ERR_UNSUPPORTED;
+    if (n_pages == 0) return ATTN_OK;
+    if (!kv4_cache || !buf || !page_ids || !aligned16(kv4_cache) || !aligned16(buf) || !aligned4(page_ids))
+        return ATTN_ERR_INVALID_ARG;
+    return attn::launch_expand_kv4(kv4_cache, buf, page_ids, n_pages, num_pages, num_kv_heads, page_size, head_dim,
+                                   k_scale, v_scale, device_error, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" attn_status attn_decode_kv4(attn_plan_t plan, const void* q, const void* kv4_cache, float k_scale,
+                                       float v_scale, const float* sinks, void* out, float* lse, void* stream) {
+    if (!plan || plan->ragged || plan->graph || !valid_pool_scale(k_scale) || !valid_pool_scale(v_scale))
+        return ATTN_ERR_INVALID_ARG;
+    if (plan->bound && plan->units.empty()) return ATTN_OK;
+    if (attn_status st = check_launch(plan, q, kv4_cache, out); st != ATTN_OK) return st;
+    return attn::launch_decode_kv4(plan, q, kv4_cache, k_scale, v_scale, sinks, out, lse,
+                                   static_cast<cudaStream_t>(stream));
+}
+
+extern "C" attn_status attn_key_weights(attn_plan_t plan, const void* q, const void* kv_cache, const float* lse,
+                                        const float* prev, float decay, int32_t window, float* weights, void* stream) {
+    return key_weights(plan, false, q, kv_cache, 1.f, lse, prev, decay, window, weights, stream);
+}
+
+extern "C" attn_status attn_key_weights_kv4(attn_plan_t plan, const void* q, const void* kv4_cache, float k_scale,
+                                            const float* lse, const float* prev, float decay, int32_t window,
+                                            float* weights, void* stream) {
+    return key_weights(plan, true, q, kv4_cache, k_scale, lse, prev, decay, window, weights, stream);
+}
+
+extern "C" attn_status attn_evict_kv(attn_plan_t plan, const float* weights, const void* kv_cache, int32_t budget,
+                                     int32_t recent, int32_t* kept, const int32_t* page_table_out,
+                                     int32_t num_pages_out, void* kv_out, float* weights_out, void* stream) {
+    return evict(plan, false, weights, kv_cache, budget, recent, kept, page_table_out, num_pages_out, kv_out,
+                 weights_out, stream);
+}
+
+extern "C" attn_status attn_evict_kv4(attn_plan_t plan, const float* weights, const void* kv4_cache, int32_t budget,
+                                      int32_t recent, int32_t* kept, const int32_t* page_table_out,
+                                      int32_t num_pages_out, void* kv4_out, float* weights_out, void* stream) {
+    return evict(plan, true, weights, kv4_cache, budget, recent, kept, page_table_out, num_pages_out, kv4_out,
+                 weights_out, stream);
 }
 
 extern "C" attn_status attn_plan_device_error(attn_plan_t plan, int32_t* code, void* stream) {

@@ -59,8 +59,26 @@ struct PrefillItem {
 };
 static_assert(sizeof(PrefillItem) == 48, "prefill item is 12 int32");
 
+// One request of a paged plan, for the kernels that work on whole requests
+// (key weights, eviction).
+struct RequestInfo {
+    int32_t q_row0;     // first row in q / lse
+    int32_t qo_len;
+    int32_t page_base;  // kv_indptr[b]: first slot of the request in page_table
+    int32_t kv_len;
+};
+static_assert(sizeof(RequestInfo) == 16, "request info is one 16-byte load");
+
+// The 4-bit cache holds 16 tokens of a (page, K/V, KV head) block together:
+// 16 rows of D / 2 code bytes, then 16 rows of D / 16 scale bytes.
+constexpr int kKv4Tokens = 16;
+constexpr int kKv4Group = 16;             // dims that share an e4m3 scale
+constexpr int kv4_sub_bytes(int head_dim) { return kKv4Tokens * (head_dim / 2 + head_dim / kKv4Group); }
+
+// The requests come first: attn_decode_noalloc's static scratch holds the
+// regions from `units` on.
 struct WorkspaceLayout {
-    size_t units = 0, items = 0, item_off = 0, append = 0, counters = 0, err = 0, n_units = 0, part_lse = 0,
+    size_t requests = 0, units = 0, items = 0, item_off = 0, append = 0, counters = 0, err = 0, n_units = 0, part_lse = 0,
            part_o = 0, total = 0;
 };
 
@@ -106,6 +124,7 @@ struct attn_plan_s {
     int64_t kv_tokens = 0;                // ragged: rows of K and V (kv_indptr[batch])
     int64_t graph_kv_blocks = 0;          // graph: 16-token blocks a batch may hold in total
 
+    std::vector<attn::RequestInfo> requests;   // paged plans: every request, in order
     std::vector<attn::DecodeUnit> units;
     std::vector<attn::PrefillItem> items;
     std::vector<int32_t> append_slots;    // per query row: page-table slot, row in page

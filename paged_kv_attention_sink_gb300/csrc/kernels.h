@@ -31,6 +31,23 @@ attn_status launch_head_slice(bool unpack, void* kv_cache, void* buf, const int3
                               int64_t num_pages, int32_t Hkv, int32_t P, int32_t D, int32_t h0, int32_t nh,
                               int32_t* err, cudaStream_t stream);
 
+// 4-bit cache (kv4.cuh): quantising append, pages back to bf16, decode.
+attn_status launch_append_kv4(attn_plan_s* plan, const void* k_new, const void* v_new, void* kv4_cache, float k_scale,
+                              float v_scale, cudaStream_t stream);
+attn_status launch_expand_kv4(const void* kv4_cache, void* buf, const int32_t* page_ids, int64_t n, int64_t num_pages,
+                              int32_t Hkv, int32_t P, int32_t D, float k_scale, float v_scale, int32_t* err,
+                              cudaStream_t stream);
+attn_status launch_decode_kv4(attn_plan_s* plan, const void* q, const void* kv4_cache, float k_scale, float v_scale,
+                              const float* sinks, void* out, float* lse, cudaStream_t stream);
+// four: `pool` is a 4-bit cache (else bf16).
+attn_status launch_key_weights(attn_plan_s* plan, bool four, const void* q, const void* pool, float k_scale,
+                               const float* lse, const float* prev, float decay, int32_t window, float* weights,
+                               cudaStream_t stream);
+// page_table_out NULL: in place (pool_out / weights_out are then the inputs).
+attn_status launch_evict(attn_plan_s* plan, bool four, const float* weights, const void* pool, int32_t budget,
+                         int32_t recent, int32_t* kept, const int32_t* page_table_out, int32_t num_pages_out,
+                         void* pool_out, float* weights_out, cudaStream_t stream);
+
 }  // namespace attn
 
 namespace attn {

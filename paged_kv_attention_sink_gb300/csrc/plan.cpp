@@ -262,9 +262,14 @@ attn_status make_plan(bool ragged, const int32_t* qo_indptr, const int32_t* kv_i
         }
     }
 
+    plan->requests.resize(ragged ? 0 : (size_t)batch);
+    for (int32_t b = 0; b < batch && !ragged; ++b)
+        plan->requests[b] = {qo_indptr[b], (int32_t)qo_len[b], kv_indptr[b], (int32_t)kv_len[b]};
+
     // ---- workspace layout (every region 256-byte aligned).
     WorkspaceLayout& L = plan->layout;
     size_t off = 0;
+    L.requests = off; off = align_up(off + plan->requests.size() * sizeof(RequestInfo), 256);
     L.units = off;    off = align_up(off + plan->units.size() * sizeof(DecodeUnit), 256);
     L.items = off;    off = align_up(off + plan->items.size() * sizeof(PrefillItem), 256);
     L.append = off;   off = align_up(off + plan->append_slots.size() * sizeof(int32_t), 256);
