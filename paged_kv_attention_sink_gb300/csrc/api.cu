@@ -105,6 +105,7 @@ extern "C" attn_status attn_plan_bind_workspace(attn_plan_t plan, void* workspac
             if (bytes) std::memcpy(img.data() + off, src, bytes);
         };
         put(L.requests, plan->requests.data(), plan->requests.size() * sizeof(attn::RequestInfo));
+        put(L.weight_tiles, plan->weight_tiles.data(), plan->weight_tiles.size() * sizeof(attn::WeightTile));
         put(L.units, plan->units.data(), plan->units.size() * sizeof(attn::DecodeUnit));
         put(L.items, plan->items.data(), plan->items.size() * sizeof(attn::PrefillItem));
         put(L.item_off, plan->item_off.data(), plan->item_off.size() * sizeof(int32_t));
@@ -316,7 +317,22 @@ attn_status key_weights(attn_plan_t plan, bool four, const void* q, const void* 
     if (!q || !pool || !lse || !weights || (decay != 0.f && !prev)) return ATTN_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(pool) || !aligned4(lse) || !aligned4(prev) || !aligned4(weights))
         return ATTN_ERR_INVALID_ARG;
-    return attn::launch_key_weights(plan, four, q, pool, k_scale, lse, prev, decay, window, weights,
+    if (!four && !plan->units.empty() && plan->kv_map_decode_ptr != pool) {
+        if (!make_kv_map(plan->kv_map_decode, pool, plan, attn::kBlockTokens)) return ATTN_ERR_CUDA;
+        plan->kv_map_decode_ptr = pool;
+    }
+    if (!plan->weight_tiles.empty()) {
+        if (!four && plan->kv_map_prefill_ptr != pool) {
+            if (!make_kv_map(plan->kv_map_prefill, pool, plan, plan->P)) return ATTN_ERR_CUDA;
+            plan->kv_map_prefill_ptr = pool;
+        }
+        if (plan->q_map_prefill_ptr != q) {
+            if (!make_q_map(plan->q_map_prefill, q, plan)) return ATTN_ERR_CUDA;
+            plan->q_map_prefill_ptr = q;
+        }
+    }
+    return attn::launch_key_weights(plan, four, q, pool, k_scale, plan->kv_map_decode, plan->q_map_prefill,
+                                    plan->kv_map_prefill, lse, prev, decay, window, weights,
                                     static_cast<cudaStream_t>(stream));
 }
 

@@ -69,16 +69,22 @@ struct RequestInfo {
 };
 static_assert(sizeof(RequestInfo) == 16, "request info is one 16-byte load");
 
+// 128 keys of a prefill request: the work item of its key weights (times KV heads).
+struct WeightTile {
+    int32_t request;
+    int32_t key0;
+};
+
 // The 4-bit cache holds 16 tokens of a (page, K/V, KV head) block together:
 // 16 rows of D / 2 code bytes, then 16 rows of D / 16 scale bytes.
 constexpr int kKv4Tokens = 16;
 constexpr int kKv4Group = 16;             // dims that share an e4m3 scale
 constexpr int kv4_sub_bytes(int head_dim) { return kKv4Tokens * (head_dim / 2 + head_dim / kKv4Group); }
 
-// The requests come first: attn_decode_noalloc's static scratch holds the
+// Requests and weight tiles come first: attn_decode_noalloc's static scratch holds the
 // regions from `units` on.
 struct WorkspaceLayout {
-    size_t requests = 0, units = 0, items = 0, item_off = 0, append = 0, counters = 0, err = 0, n_units = 0, part_lse = 0,
+    size_t requests = 0, weight_tiles = 0, units = 0, items = 0, item_off = 0, append = 0, counters = 0, err = 0, n_units = 0, part_lse = 0,
            part_o = 0, total = 0;
 };
 
@@ -125,6 +131,7 @@ struct attn_plan_s {
     int64_t graph_kv_blocks = 0;          // graph: 16-token blocks a batch may hold in total
 
     std::vector<attn::RequestInfo> requests;   // paged plans: every request, in order
+    std::vector<attn::WeightTile> weight_tiles;   // prefill requests' 128-key tiles, most query rows first
     std::vector<attn::DecodeUnit> units;
     std::vector<attn::PrefillItem> items;
     std::vector<int32_t> append_slots;    // per query row: page-table slot, row in page

@@ -5,12 +5,21 @@
 //   s_ith = sm_scale * q_ih . k_tg;  tokens appended by this plan (t >= kv_len -
 //   qo_len) have no previous weight.
 //
-// One warp owns 16 keys of one KV head: their K rows are the row operand of
-// mma.sync m16n8k16 (bf16, exact for either cache), held in registers, and the
-// query rows stream past as columns (query row i, head h), eight at a time.  A
-// lane then holds the scores of two keys for two columns, exponentiates them
-// with the rows' own lse and adds them up: no max, no reduction until the end,
-// where the four lanes of a key row are summed (a fixed order).
+// With the rows' lse known there is no running max and nothing to rescale: one
+// product, one exponential and one sum per (row, head, key).  Keys are the rows
+// of every product (S^T = K Q^T), so that a key's sum stays with one thread (or
+// four lanes) and no atomics are needed: the sums' order is fixed.
+//
+// Two kernels, by the kind of request:
+//  * decode requests (one query row): bound by reading K, 2 D (bf16) or 9 D / 16
+//    (4 bits) bytes per key and head.  The plan's decode units, four warps each
+//    with a ring of 32-token stages, mma.sync with the heads as columns.
+//  * prefill requests: bound by the exponentials (MUFU: 32 a clock and SM) and
+//    the product on the tensor cores.  One CTA per 128 keys of a KV head keeps
+//    the K tile in shared memory and streams Q tiles (128 rows of one head)
+//    past it; tcgen05.mma fills one of two 128-column accumulators in TMEM
+//    while a warpgroup drains the other, one key per thread.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "attn_internal.h"
@@ -22,127 +31,534 @@ namespace attn {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWeightWarps = 4;
-constexpr int kWeightKeys = kWeightWarps * 16;   // keys per CTA
 
 struct KeyWeightArgs {
+    const DecodeUnit* units;
     const RequestInfo* requests;
+    const int2* tiles;          // prefill requests: (request, first key) of each 128-key tile
     const int32_t* page_table;
     const __nv_bfloat16* q;
     const float* lse;
-    const void* pool;
+    const uint8_t* pool4;       // 4-bit cache (the bf16 one is read through its tensor map)
     const float* prev;
     float* weights;
     int32_t* err;
-    int32_t batch, Hq, Hkv, P, num_pages, causal, window;
-    float scale_log2, decay;
+    int32_t Hq, Hkv, P, num_pages, causal, window;
+    float scale_log2, decay;    // scale_log2 = sm_scale * log2(e) * k_scale
 };
 
-// K rows of 16 keys as row operand: lane (gq, tq)'s dims of step kk are
-// tq * D / 4 + 4 kk + {0..3}; keys gq and gq + 8 (bf16) or kv4_row order.
+// ------------------------------------------------------------ decode requests
+
+// kFour: 4-bit pages, else bf16.
 template <int D, bool kFour>
-__device__ __forceinline__ void load_keys(const KeyWeightArgs& a, int64_t page, int g, int row0, int gq, int tq,
-                                          uint32_t (&ka)[D / 16][4]) {
-    if constexpr (kFour) {
-        const uint8_t* sub = static_cast<const uint8_t*>(a.pool) +
-                             kv4::sub_offset(page, 0, a.Hkv, g, a.P, row0, kv4_sub_bytes(D));
-        kv4_for_k<D>(sub, kv4_row(gq), tq, [&](int kk, const uint32_t (&x)[4]) {
+struct StepWeightCfg {
+    static constexpr int kWarps = kDecodeWarps;
+    static constexpr int kStages = 4;
+    static constexpr int kTile = 32;
+    static constexpr int kSubs = kTile / kBlockTokens;
+    static constexpr int kSub = kFour ? kv4_sub_bytes(D) : kBlockTokens * D * 2;   // K of 16 tokens
+    static constexpr int kStageBytes = kSubs * kSub;
+    static constexpr int kPipeBytes = kWarps * kStages * kStageBytes;
+    static constexpr int kPageBytes = (kDecodeMaxChunkPages * 4 + 15) / 16 * 16;
+    static constexpr int kSmem = 1024 + kPipeBytes + kPageBytes + kWarps * kStages * 8;
+};
+
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32"
+        " {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Eight query heads (head0 ..; those from n on count nothing) as column
+// operand, and per column 2 tq + e the factor and the (negated) lse in log2
+// units that turn a product into the exponent.
+template <int D, bool kFour>
+struct QueryTile {
+    uint32_t b[D / 16][2];
+    float mult[2], nl[2];
+    __device__ __forceinline__ void load(const KeyWeightArgs& a, int row, int head0, int n, int gq, int tq) {
+        const int64_t at = (int64_t)row * a.Hq + head0;
+        float inv = 1.f;
+        if constexpr (kFour) {
+            kv4_load_q<D>(gq < n ? a.q + (at + gq) * D : nullptr, tq, b, inv);
+        } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 v = kv4::f16x2_to_f32(x[j]);
-                ka[kk][j] = ptx::pack_bf16x2(v.x, v.y);   // exact
-            }
-        });
-    } else {
-        const __nv_bfloat16* k0 = static_cast<const __nv_bfloat16*>(a.pool) +
-                                  ((page * 2 * a.Hkv + g) * a.P + row0 + kv4_row(gq)) * D + tq * (D / 4);
+            for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            const uint2 x = *reinterpret_cast<const uint2*>(k0 + 4 * kk);
-            const uint2 y = *reinterpret_cast<const uint2*>(k0 + 8 * D + 4 * kk);
-            ka[kk][0] = x.x; ka[kk][1] = y.x; ka[kk][2] = x.y; ka[kk][3] = y.y;
+                for (int j = 0; j < 2; ++j)
+                    b[kk][j] = gq < n ? *reinterpret_cast<const uint32_t*>(a.q + (at + gq) * D + 16 * kk + 8 * j + 2 * tq) : 0u;
         }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int h = 2 * tq + e;
+            mult[e] = kFour ? __shfl_sync(0xffffffffu, inv, h * 4) * a.scale_log2 : a.scale_log2;
+            nl[e] = h < n ? -a.lse[at + h] * kLog2e : -INFINITY;
+        }
+    }
+};
+
+// NT: column tiles of 8 heads held in registers; 0: more than 16 heads, taken
+// from memory tile by tile.
+template <int D, bool kFour, int NT>
+__global__ void __launch_bounds__(kDecodeWarps * 32)
+key_weights_step_kernel(const __grid_constant__ CUtensorMap kv_map, const KeyWeightArgs a) {
+    using C = StepWeightCfg<D, kFour>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    int32_t* pages_s = reinterpret_cast<int32_t*>(smem + C::kPipeBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kPipeBytes + C::kPageBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int gq = lane >> 2, tq = lane & 3;
+    const DecodeUnit u = a.units[blockIdx.x];
+    const int G = a.Hq / a.Hkv, P = a.P;
+    if (u.head0 != u.kv_head * G) return;   // the unit of the first head slice takes all heads
+    if (lane == 0)
+        for (int s = 0; s < C::kStages; ++s) ptx::mbar_init(ptx::smem_u32(&bars[warp * C::kStages + s]), 1);
+    ptx::fence_mbar_init();
+    const int first_page = u.tok_begin / P;
+    const int n_pages = (u.tok_end - 1) / P - first_page + 1;
+    for (int i = tid; i < n_pages; i += blockDim.x) pages_s[i] = a.page_table[u.page_base + first_page + i];
+    __syncthreads();
+
+    const uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
+    const uint32_t ring_u32 = ptx::smem_u32(ring);
+    const uint32_t bar0 = ptx::smem_u32(&bars[warp * C::kStages]);
+    const int n_tiles = (u.tok_end - u.tok_begin + C::kTile - 1) / C::kTile;
+    const int n_it = n_tiles > warp ? (n_tiles - warp + C::kWarps - 1) / C::kWarps : 0;
+    auto tile_tok = [&](int it) { return u.tok_begin + (warp + it * C::kWarps) * C::kTile; };
+    const Kv4Source src{a.pool4, pages_s, first_page, a.num_pages, a.Hkv, u.kv_head, P, a.err};
+    auto issue = [&](int it) {
+        const int s = it % C::kStages, tok = tile_tok(it);
+        const uint32_t dst = ring_u32 + s * C::kStageBytes, bar = bar0 + s * 8;
+        if constexpr (kFour) {
+            kv4_stage_load<D, C::kTile, 1>(src, tok, u.tok_end, dst, bar, lane);
+        } else {
+            // One 16-token box per 64 dims, a lane each.
+            constexpr int kBoxes = C::kSubs * (D / 64);
+            const int t = tok + lane / (D / 64) * kBlockTokens;
+            int page = -1;
+            if (lane < kBoxes && t < u.tok_end) {
+                page = pages_s[t / P - first_page];
+                if (page < 0 || page >= a.num_pages) {
+                    atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
+                    page = -1;
+                }
+            }
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, boxes * kBlockTokens * 128);
+            __syncwarp();
+            if (page >= 0)
+                ptx::tma_load_3d_hint(dst + lane * kBlockTokens * 128, &kv_map, bar, lane % (D / 64) * 64, t % P,
+                                      page * 2 * a.Hkv + u.kv_head, ptx::policy_evict_first());
+        }
+    };
+    for (int it = 0; it < C::kStages && it < n_it; ++it) issue(it);
+
+    constexpr int kHeld = NT > 0 ? NT : 1;
+    QueryTile<D, kFour> qt[kHeld];
+    if constexpr (NT > 0)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) qt[nt].load(a, u.q_row, u.head0 + nt * 8, G - nt * 8, gq, tq);
+
+    // Scores of 16 tokens (two of them this lane's rows) against the held tiles
+    // of heads, exponentiated and added to w.
+    auto add_sub = [&](const uint8_t* sub, float (&w)[2]) {
+        float s[kHeld][4];
+#pragma unroll
+        for (int nt = 0; nt < kHeld; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        if constexpr (kFour) {
+            kv4_for_k<D>(sub, kv4_row(gq), tq, [&](int kk, const uint32_t (&ka)[4]) {
+#pragma unroll
+                for (int nt = 0; nt < kHeld; ++nt) mma_f16_16816(s[nt], ka, qt[nt].b[kk][0], qt[nt].b[kk][1]);
+            });
+        } else {
+            const uint32_t at = ptx::smem_u32(sub);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const int mi = lane >> 3, row = (mi & 1) * 8 + (lane & 7), ch = 2 * kk + (mi >> 1);
+                uint32_t ka[4];
+                ptx::ldmatrix_x4(at + (ch >> 3) * (kBlockTokens * 128) + row * 128 + (((ch & 7) ^ (lane & 7)) << 4), ka[0],
+                                 ka[1], ka[2], ka[3]);
+#pragma unroll
+                for (int nt = 0; nt < kHeld; ++nt) ptx::mma_bf16_16816(s[nt], ka, qt[nt].b[kk][0], qt[nt].b[kk][1]);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < kHeld; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e >> 1] += ptx::ex2(fmaf(s[nt][e], qt[nt].mult[e & 1], qt[nt].nl[e & 1]));
+    };
+
+    // Each lane writes one of the tile's 32 tokens: sixteen tq >> 1, row
+    // (tq & 1) * 8 + its own.
+    const int row = kFour ? kv4_row(gq) : gq;
+    const int mine = (tq >> 1) * kBlockTokens + (tq & 1) * 8 + row;
+    bool timed_out = false;
+    int it = 0;
+    for (; it < n_it; ++it) {
+        const int s = it % C::kStages, tok = tile_tok(it) + mine;
+        // This lane's slot, and its previous weight on the way while the tile arrives.
+        int64_t at = -1;
+        float before = 0.f;
+        if (tok < u.tok_end) {
+            const int page = pages_s[tok / P - first_page];
+            if (page >= 0 && page < a.num_pages) {
+                at = ((int64_t)page * a.Hkv + u.kv_head) * P + tok % P;
+                const bool is_new = u.chunk == u.n_chunks - 1 && tok == u.tok_end - 1;
+                if (a.decay != 0.f && !is_new) before = a.decay * a.prev[at];
+            }
+        }
+        if (!ptx::mbar_wait(bar0 + s * 8, (it / C::kStages) & 1)) { timed_out = true; break; }
+        const uint8_t* kt = ring + s * C::kStageBytes;
+        float w[C::kSubs][2];
+#pragma unroll
+        for (int sub = 0; sub < C::kSubs; ++sub) {
+            w[sub][0] = w[sub][1] = 0.f;
+            if constexpr (NT > 0) {
+                add_sub(kt + sub * C::kSub, w[sub]);
+            } else {
+                for (int h = 0; h < G; h += 8) {
+                    qt[0].load(a, u.q_row, u.head0 + h, G - h, gq, tq);
+                    add_sub(kt + sub * C::kSub, w[sub]);
+                }
+            }
+        }
+        __syncwarp();
+        if (it + C::kStages < n_it) {
+            ptx::fence_proxy_async_smem();
+            issue(it + C::kStages);
+        }
+#pragma unroll
+        for (int sub = 0; sub < C::kSubs; ++sub)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                w[sub][r] += __shfl_xor_sync(0xffffffffu, w[sub][r], 1);
+                w[sub][r] += __shfl_xor_sync(0xffffffffu, w[sub][r], 2);
+            }
+        const float mine_w = tq < 2 ? (tq == 0 ? w[0][0] : w[0][1]) : (tq == 2 ? w[1][0] : w[1][1]);
+        if (at >= 0) a.weights[at] = mine_w + before;
+    }
+    if (timed_out) {
+        if (lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
+        for (int j = it; j < n_it && j < it + C::kStages; ++j)
+            ptx::mbar_wait(bar0 + (j % C::kStages) * 8, (j / C::kStages) & 1);
     }
 }
 
+// ----------------------------------------------------------- prefill requests
+
+constexpr int kTileKeys = 128;   // keys per CTA: the MMA's M, a TMEM lane each
+constexpr int kTileRows = 128;   // query rows per step: the MMA's N
+
+// A wait with the same result in every lane of the warp.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity));
+}
+
+template <int D>
+struct PromptWeightCfg {
+    static constexpr int kAtom = 128 * 128;                 // 128 rows x 64 dims, 128-byte swizzle
+    static constexpr int kTile = kAtom * (D / 64);
+    // Two CTAs per SM (each 256 of the 512 TMEM columns) must fill shared
+    // memory so that a third does not fit and wait for TMEM.
+    static constexpr int kStages = D == 64 ? 4 : 2;
+    static constexpr int kEpilogueWarps = 8;
+    static constexpr int kThreads = (kEpilogueWarps + 2) * 32;
+    static constexpr int kOffQ = kTile;
+    static constexpr int kOffNl = kOffQ + kStages * kTile;  // [2 warpgroups][2][128] negated lse
+    static constexpr int kOffSum = kOffNl + 2 * 2 * kTileRows * 4;
+    static constexpr int kOffBars = kOffSum + kTileKeys * 4;
+    static constexpr int kSmem = 1024 + kOffBars + (2 * kStages + 6) * 8 + 16;
+    static_assert(3 * (kSmem + 1024) > 233472 && 2 * (kSmem + 1024) <= 233472, "exactly two CTAs per SM");
+};
+
 template <int D, bool kFour>
-__global__ void __launch_bounds__(kWeightWarps * 32)
-key_weights_kernel(const KeyWeightArgs a) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    const int b = blockIdx.z, g = blockIdx.y;
-    const RequestInfo r = a.requests[b];
-    if (r.qo_len == 0) return;
-    const int G = a.Hq / a.Hkv, prefix = r.kv_len - r.qo_len;
-    for (int64_t tile = blockIdx.x; tile * kWeightKeys < r.kv_len; tile += gridDim.x) {
-        const int t0 = (int)tile * kWeightKeys + warp * 16;
-        if (t0 >= r.kv_len) continue;
-        const int page = a.page_table[r.page_base + t0 / a.P];
-        if (page < 0 || page >= a.num_pages) {
-            if (lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
-            continue;
+__global__ void __launch_bounds__(PromptWeightCfg<D>::kThreads, 2)
+key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
+                          const KeyWeightArgs a) {
+    using C = PromptWeightCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const uint32_t q_full = sbase + C::kOffBars, q_empty = q_full + 8 * C::kStages, k_full = q_empty + 8 * C::kStages;
+    const uint32_t s_full = k_full + 8, s_free = s_full + 16, drain = s_free + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBars + (2 * C::kStages + 6) * 8);
+    float* sum_s = reinterpret_cast<float*>(smem + C::kOffSum);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int2 tile = a.tiles[blockIdx.x / a.Hkv];
+    const int g = blockIdx.x % a.Hkv, t0 = tile.y;
+    const RequestInfo r = a.requests[tile.x];
+    const int G = a.Hq / a.Hkv, P = a.P, prefix = r.kv_len - r.qo_len;
+    // First query row that counts: inside the window, and seeing the first key.
+    int i0 = a.window > 0 ? max(0, r.qo_len - a.window) : 0;
+    if (a.causal) i0 = max(i0, t0 - prefix);
+    const int n_steps = (r.qo_len - i0 + kTileRows - 1) / kTileRows * G;   // step s: rows i0 + s / G * 128, head s % G
+
+    if (tid == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            ptx::mbar_init(q_full + 8 * s, 1);
+            ptx::mbar_init(q_empty + 8 * s, 1);
         }
-        uint32_t ka[D / 16][4];
-        load_keys<D, kFour>(a, page, g, t0 % a.P, gq, tq, ka);
-        // Rows that count and can see any of these keys.
-        int i0 = a.window > 0 ? max(0, r.qo_len - a.window) : 0;
-        if (a.causal) i0 = max(i0, t0 - prefix);
-        const int key0 = t0 + kv4_row(gq);
-        float w0 = 0.f, w1 = 0.f;   // keys key0 and key0 + 8
-        const int64_t cols = (int64_t)(r.qo_len - i0) * G;
-        for (int64_t c0 = 0; c0 < cols; c0 += 8) {
-            const int64_t c = c0 + gq;
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
-            const __nv_bfloat16* q = a.q + ((int64_t)(r.q_row0 + i0 + (int)(c / G)) * a.Hq + g * G + (int)(c % G)) * D +
-                                     tq * (D / 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                uint2 x = make_uint2(0u, 0u);
-                if (c < cols) x = *reinterpret_cast<const uint2*>(q + 4 * kk);
-                ptx::mma_bf16_16816(s, ka[kk], x.x, x.y);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int64_t ce = c0 + 2 * tq + e;
-                if (ce >= cols) continue;
-                const int i = i0 + (int)(ce / G);
-                const float l2 = a.lse[(int64_t)(r.q_row0 + i) * a.Hq + g * G + (int)(ce % G)] * kLog2e;
-                const int last = a.causal ? prefix + i : r.kv_len - 1;   // last key row i sees
-                if (key0 <= last) w0 += ptx::ex2(fmaf(s[e], a.scale_log2, -l2));
-                if (key0 + 8 <= last) w1 += ptx::ex2(fmaf(s[e + 2], a.scale_log2, -l2));
-            }
+        ptx::mbar_init(k_full, kFour ? C::kEpilogueWarps : 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(s_full + 8 * i, 1);
+            ptx::mbar_init(s_free + 8 * i, 4);
         }
-        w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
-        w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
-        w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
-        w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
-        if (tq < 2) {
-            const int key = key0 + 8 * tq;
-            if (key < r.kv_len) {
-                const int64_t at = ((int64_t)page * a.Hkv + g) * a.P + key % a.P;
-                float w = tq ? w1 : w0;
-                if (a.decay != 0.f && key < prefix) w = fmaf(a.decay, a.prev[at], w);
+        ptx::mbar_init(drain, 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == C::kEpilogueWarps) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 256);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == C::kEpilogueWarps + 1) {
+        // ------------------------------------------------------------ producer
+        if (!kFour) {
+            const int n_load = (min(kTileKeys, r.kv_len - t0) + P - 1) / P;   // page boxes of the K tile
+            int page = -1;
+            if (lane < n_load) {
+                page = a.page_table[r.page_base + t0 / P + lane];
+                if (page < 0 || page >= a.num_pages) {
+                    atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
+                    page = -1;
+                }
+            }
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * (D / 64);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(k_full, boxes * P * 128);
+            __syncwarp();
+            if (page >= 0)
+                for (int c = 0; c < D / 64; ++c)
+                    ptx::tma_load_3d(sbase + c * C::kAtom + lane * P * 128, &kv_map, k_full, c * 64, 0,
+                                     page * 2 * a.Hkv + g);
+        }
+        if (lane == 0) {
+            int s = 0;
+            for (; s < n_steps; ++s) {
+                const int st = s % C::kStages;
+                if (s >= C::kStages && !ptx::mbar_wait(q_empty + 8 * st, (s / C::kStages - 1) & 1)) {
+                    atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
+                    break;
+                }
+                ptx::mbar_arrive_expect_tx(q_full + 8 * st, C::kTile);
+                for (int c = 0; c < D / 64; ++c)
+                    ptx::tma_load_3d(sbase + C::kOffQ + st * C::kTile + c * C::kAtom, &q_map, q_full + 8 * st, c * 64,
+                                     g * G + s % G, r.q_row0 + i0 + s / G * kTileRows);
+            }
+            // Copies still in flight when a wait ran out land before the CTA exits.
+            if (s < n_steps)
+                for (int k = max(0, s - C::kStages); k < s; ++k)
+                    ptx::mbar_wait(q_full + 8 * (k % C::kStages), (k / C::kStages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == C::kEpilogueWarps) {
+        // ---------------------------------------------------------- MMA issuer
+        constexpr uint32_t idesc = ptx::idesc_bf16(kTileKeys, kTileRows, false, false);
+        bool ok = wait_all(k_full, 0);
+        for (int s = 0; ok && s < n_steps; ++s) {
+            const int st = s % C::kStages, buf = s & 1;
+            ok = wait_all(q_full + 8 * st, (s / C::kStages) & 1) && (s < 2 || wait_all(s_free + 8 * buf, (s / 2 - 1) & 1));
+            if (!ok) break;
+            if (ptx::elect_one()) {
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk / 4) * C::kAtom + (kk % 4) * 32;
+                    ptx::tc_mma_ss(tmem + buf * kTileRows, ptx::smem_desc_sw128(sbase + off, 16, 1024),
+                                   ptx::smem_desc_sw128(sbase + C::kOffQ + st * C::kTile + off, 16, 1024), idesc, kk > 0);
+                }
+                ptx::tc_commit(s_full + 8 * buf);
+                ptx::tc_commit(q_empty + 8 * st);
+            }
+            __syncwarp();
+        }
+        if (!ok && lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
+        if (ptx::elect_one()) ptx::tc_commit(drain);
+        __syncwarp();
+    } else {
+        // ------------------------------------------- epilogue: one key per thread
+        const int wg = warp >> 2, key = (warp & 3) * 32 + lane;   // warpgroup wg takes steps wg, wg + 2, ...
+        if (kFour) {
+            // The K tile: codes and scales to bf16 (exact), in the swizzled
+            // layout TMA would have given a bf16 page.
+            constexpr int kGroups = D / kKv4Group;
+            for (int idx = tid; idx < kTileKeys * kGroups; idx += C::kEpilogueWarps * 32) {
+                const int k = idx / kGroups, grp = idx % kGroups, t = t0 + k;
+                if (t >= r.kv_len) break;
+                const int page = a.page_table[r.page_base + t / P];
+                if (page < 0 || page >= a.num_pages) {
+                    atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
+                    continue;
+                }
+                const uint8_t* sub = a.pool4 + kv4::sub_offset(page, 0, a.Hkv, g, P, t % P, kv4_sub_bytes(D));
+                const int in = t % kKv4Tokens;
+                const uint2 codes = *reinterpret_cast<const uint2*>(sub + in * (D / 2) + grp * 8);
+                const float sc = kv4::f16x2_to_f32(kv4::scales_to_f16x2(sub[8 * D + in * kGroups + grp])).x;
+                uint32_t h[2][4], o[8];
+                kv4::codes_to_f16x2(codes.x, h[0]);
+                kv4::codes_to_f16x2(codes.y, h[1]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 v = kv4::f16x2_to_f32(h[j >> 2][j & 3]);
+                    o[j] = ptx::pack_bf16x2(v.x * sc, v.y * sc);
+                }
+                const uint32_t at = sbase + (grp / 4) * C::kAtom + k * 128;
+                const int ch = (grp % 4) * 2;
+                ptx::st_shared_v4(at + ((ch ^ (k & 7)) << 4), o[0], o[1], o[2], o[3]);
+                ptx::st_shared_v4(at + (((ch + 1) ^ (k & 7)) << 4), o[4], o[5], o[6], o[7]);
+            }
+            ptx::fence_proxy_async_smem();   // the MMA reads it through the async proxy
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(k_full);
+        }
+        float* nl_s = reinterpret_cast<float*>(smem + C::kOffNl) + wg * 2 * kTileRows;
+        const uint32_t t_s = tmem + wg * kTileRows + ((uint32_t)((warp & 3) * 32) << 16);
+        const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+        // The (negated) lse of row `key` of step s's rows, in log2 units.
+        auto load_nl = [&](int s) {
+            const int i = i0 + s / G * kTileRows + key;
+            return s < n_steps && i < r.qo_len ? -a.lse[(int64_t)(r.q_row0 + i) * a.Hq + g * G + s % G] * kLog2e : 0.f;
+        };
+        float total = 0.f, nl = load_nl(wg);
+        bool ok = true;
+        for (int s = wg; s < n_steps; s += 2) {
+            float* nl_b = nl_s + ((s >> 1) & 1) * kTileRows;
+            nl_b[key] = nl;
+            nl = load_nl(s + 2);
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+            // After a wait that ran out the warp only keeps the barriers' count.
+            ok = ok && wait_all(s_full + 8 * wg, (s >> 1) & 1);
+            if (!ok) continue;
+            ptx::tc_fence_after();
+            const int row0 = i0 + s / G * kTileRows, n_rows = r.qo_len - row0;
+            // Columns [lo, n_rows) count: rows that see the key, of this request.
+            const int lo = a.causal ? t0 + key - (prefix + row0) : 0;
+            const bool masked = n_rows < kTileRows || (a.causal && t0 + kTileKeys - 1 > prefix + row0);
+            float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < kTileRows / 32; ++c) {
+                uint32_t v[32];
+                ptx::tmem_ld32(t_s + c * 32, v);
+                ptx::tc_wait_ld();
+                if (c == kTileRows / 32 - 1) {   // all of S is in registers: the next product may overwrite it
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(s_free + 8 * wg);
+                }
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    const float4 l4 = *reinterpret_cast<const float4*>(nl_b + c * 32 + k);
+                    const float2 x0 = ptx::fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), scale2,
+                                                make_float2(l4.x, l4.y));
+                    const float2 x1 = ptx::fma2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), scale2,
+                                                make_float2(l4.z, l4.w));
+                    float2 p0 = make_float2(ptx::ex2(x0.x), ptx::ex2(x0.y));
+                    float2 p1 = make_float2(ptx::ex2(x1.x), ptx::ex2(x1.y));
+                    if (masked) {
+                        const int col = c * 32 + k;
+                        p0.x = col >= lo && col < n_rows ? p0.x : 0.f;
+                        p0.y = col + 1 >= lo && col + 1 < n_rows ? p0.y : 0.f;
+                        p1.x = col + 2 >= lo && col + 2 < n_rows ? p1.x : 0.f;
+                        p1.y = col + 3 >= lo && col + 3 < n_rows ? p1.y : 0.f;
+                    }
+                    acc0 = ptx::add2(acc0, p0);
+                    acc1 = ptx::add2(acc1, p1);
+                }
+            }
+            total += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+        }
+        if (!ok && lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
+        // The two warpgroups' sums, in a fixed order.
+        if (wg == 1) sum_s[key] = total;
+        asm volatile("bar.sync 3, 256;" ::: "memory");
+        const int t = t0 + key;
+        if (wg == 0 && t < r.kv_len) {
+            const int page = a.page_table[r.page_base + t / P];
+            if (page >= 0 && page < a.num_pages) {
+                const int64_t at = ((int64_t)page * a.Hkv + g) * P + t % P;
+                float w = total + sum_s[key];
+                if (a.decay != 0.f && t < prefix) w = fmaf(a.decay, a.prev[at], w);
                 a.weights[at] = w;
             }
         }
     }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == C::kEpilogueWarps) {
+        ptx::mbar_wait(drain, 0);
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 256);
+    }
+}
+
+template <int D, bool kFour, int NT>
+cudaError_t launch_step(const CUtensorMap& map, const KeyWeightArgs& a, int grid, cudaStream_t stream) {
+    using C = StepWeightCfg<D, kFour>;
+    auto kernel = key_weights_step_kernel<D, kFour, NT>;
+    static std::atomic<bool> configured[kMaxDevices];
+    cudaError_t e = once_per_device(configured, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    });
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kDecodeWarps * 32, C::kSmem, stream>>>(map, a);
+    return cudaGetLastError();
+}
+
+template <int D, bool kFour>
+cudaError_t launch_prompt(const CUtensorMap& q_map, const CUtensorMap& kv_map, const KeyWeightArgs& a, int grid,
+                          cudaStream_t stream) {
+    using C = PromptWeightCfg<D>;
+    auto kernel = key_weights_prompt_kernel<D, kFour>;
+    static std::atomic<bool> configured[kMaxDevices];
+    cudaError_t e = once_per_device(configured, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    });
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, C::kThreads, C::kSmem, stream>>>(q_map, kv_map, a);
+    return cudaGetLastError();
+}
+
+template <int D, bool kFour>
+attn_status launch_all(const attn_plan_s* plan, const CUtensorMap& step_map, const CUtensorMap& q_map,
+                       const CUtensorMap& kv_map, const KeyWeightArgs& a, cudaStream_t stream) {
+    const int G = plan->Hq / plan->Hkv, units = (int)plan->units.size();
+    cudaError_t e = cudaSuccess;
+    if (units > 0)
+        e = G <= 8    ? launch_step<D, kFour, 1>(step_map, a, units, stream)
+            : G <= 16 ? launch_step<D, kFour, 2>(step_map, a, units, stream)
+                      : launch_step<D, kFour, 0>(step_map, a, units, stream);
+    if (e == cudaSuccess && !plan->weight_tiles.empty())
+        e = launch_prompt<D, kFour>(q_map, kv_map, a, (int)plan->weight_tiles.size() * plan->Hkv, stream);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace
 
 attn_status launch_key_weights(attn_plan_s* plan, bool four, const void* q, const void* pool, float k_scale,
-                               const float* lse, const float* prev, float decay, int32_t window, float* weights,
-                               cudaStream_t stream) {
-    if (plan->info.total_qo_rows == 0) return ATTN_OK;
+                               const void* step_map, const void* q_map, const void* kv_map, const float* lse,
+                               const float* prev, float decay, int32_t window, float* weights, cudaStream_t stream) {
     KeyWeightArgs a;
+    a.units = reinterpret_cast<const DecodeUnit*>(plan->ws + plan->layout.units);
     a.requests = reinterpret_cast<const RequestInfo*>(plan->ws + plan->layout.requests);
+    a.tiles = reinterpret_cast<const int2*>(plan->ws + plan->layout.weight_tiles);
     a.page_table = plan->page_table;
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.lse = lse;
-    a.pool = pool;
+    a.pool4 = static_cast<const uint8_t*>(pool);
     a.prev = prev;
     a.weights = weights;
     a.err = reinterpret_cast<int32_t*>(plan->ws + plan->layout.err);
-    a.batch = plan->batch;
     a.Hq = plan->Hq;
     a.Hkv = plan->Hkv;
     a.P = plan->P;
@@ -151,17 +567,12 @@ attn_status launch_key_weights(attn_plan_s* plan, bool four, const void* q, cons
     a.window = window;
     a.scale_log2 = plan->sm_scale * kLog2e * k_scale;
     a.decay = decay;
-    int32_t longest = 0;
-    for (const RequestInfo& r : plan->requests) longest = std::max(longest, r.kv_len);
-    const dim3 grid(std::min((longest + kWeightKeys - 1) / kWeightKeys, 4096), plan->Hkv, plan->batch);
-    if (plan->D == 64) {
-        if (four) key_weights_kernel<64, true><<<grid, kWeightWarps * 32, 0, stream>>>(a);
-        else key_weights_kernel<64, false><<<grid, kWeightWarps * 32, 0, stream>>>(a);
-    } else {
-        if (four) key_weights_kernel<128, true><<<grid, kWeightWarps * 32, 0, stream>>>(a);
-        else key_weights_kernel<128, false><<<grid, kWeightWarps * 32, 0, stream>>>(a);
-    }
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    const CUtensorMap& sm = *static_cast<const CUtensorMap*>(step_map);
+    const CUtensorMap& qm = *static_cast<const CUtensorMap*>(q_map);
+    const CUtensorMap& km = *static_cast<const CUtensorMap*>(kv_map);
+    if (plan->D == 64)
+        return four ? launch_all<64, true>(plan, sm, qm, km, a, stream) : launch_all<64, false>(plan, sm, qm, km, a, stream);
+    return four ? launch_all<128, true>(plan, sm, qm, km, a, stream) : launch_all<128, false>(plan, sm, qm, km, a, stream);
 }
 
 }  // namespace attn

@@ -265,11 +265,23 @@ attn_status make_plan(bool ragged, const int32_t* qo_indptr, const int32_t* kv_i
     plan->requests.resize(ragged ? 0 : (size_t)batch);
     for (int32_t b = 0; b < batch && !ragged; ++b)
         plan->requests[b] = {qo_indptr[b], (int32_t)qo_len[b], kv_indptr[b], (int32_t)kv_len[b]};
+    // Key weights of prefill requests: 128-key tiles, the ones that most query
+    // rows see first (the CTAs are dispatched in this order).
+    for (int32_t b = 0; b < batch && !ragged; ++b)
+        for (int64_t t0 = 0; qo_len[b] > 1 && t0 < kv_len[b]; t0 += kPrefillKeys)
+            plan->weight_tiles.push_back({b, (int32_t)t0});
+    auto rows_seeing = [&](const WeightTile& w) {
+        const int64_t n = qo_len[w.request], prefix = kv_len[w.request] - n;
+        return causal ? n - std::max<int64_t>(0, w.key0 - prefix) : n;
+    };
+    std::stable_sort(plan->weight_tiles.begin(), plan->weight_tiles.end(),
+                     [&](const WeightTile& x, const WeightTile& y) { return rows_seeing(x) > rows_seeing(y); });
 
     // ---- workspace layout (every region 256-byte aligned).
     WorkspaceLayout& L = plan->layout;
     size_t off = 0;
     L.requests = off; off = align_up(off + plan->requests.size() * sizeof(RequestInfo), 256);
+    L.weight_tiles = off; off = align_up(off + plan->weight_tiles.size() * sizeof(WeightTile), 256);
     L.units = off;    off = align_up(off + plan->units.size() * sizeof(DecodeUnit), 256);
     L.items = off;    off = align_up(off + plan->items.size() * sizeof(PrefillItem), 256);
     L.append = off;   off = align_up(off + plan->append_slots.size() * sizeof(int32_t), 256);
