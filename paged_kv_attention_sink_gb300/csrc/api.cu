@@ -317,10 +317,6 @@ attn_status key_weights(attn_plan_t plan, bool four, const void* q, const void* 
     if (!q || !pool || !lse || !weights || (decay != 0.f && !prev)) return ATTN_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(pool) || !aligned4(lse) || !aligned4(prev) || !aligned4(weights))
         return ATTN_ERR_INVALID_ARG;
-    if (!four && !plan->units.empty() && plan->kv_map_decode_ptr != pool) {
-        if (!make_kv_map(plan->kv_map_decode, pool, plan, attn::kBlockTokens)) return ATTN_ERR_CUDA;
-        plan->kv_map_decode_ptr = pool;
-    }
     if (!plan->weight_tiles.empty()) {
         if (!four && plan->kv_map_prefill_ptr != pool) {
             if (!make_kv_map(plan->kv_map_prefill, pool, plan, plan->P)) return ATTN_ERR_CUDA;
@@ -331,8 +327,8 @@ attn_status key_weights(attn_plan_t plan, bool four, const void* q, const void* 
             plan->q_map_prefill_ptr = q;
         }
     }
-    return attn::launch_key_weights(plan, four, q, pool, k_scale, plan->kv_map_decode, plan->q_map_prefill,
-                                    plan->kv_map_prefill, lse, prev, decay, window, weights,
+    return attn::launch_key_weights(plan, four, q, pool, k_scale, plan->q_map_prefill, plan->kv_map_prefill, lse,
+                                    prev, decay, window, weights,
                                     static_cast<cudaStream_t>(stream));
 }
 

@@ -24,8 +24,7 @@
 //
 // One CTA = one decode unit of the plan (request, KV head, <= 16 query heads,
 // KV chunk), four warps, each with its own ring of kTile-token stages filled
-// by cp.async.bulk (one copy per page run: sixteen tokens' codes and scales
-// lie together in the pool).
+// by its own cp.async, so that no barrier sits in the streaming loop.
 #include "attn_internal.h"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -45,9 +44,10 @@ constexpr float kShift = 7.f, kSlack = 15.f;   // log2 units
 template <int D, int NT>
 struct Decode4Cfg {
     static constexpr int kWarps = kDecodeWarps;
-    static constexpr int kStages = 3;
-    static constexpr int kTile = 32;                                  // tokens per stage
-    static constexpr int kSubs = kTile / kKv4Tokens;
+    static constexpr int kTile = 64;                                  // tokens per stage (one wait, one refill)
+    static constexpr int kStep = 32;                                  // tokens whose scores are held at a time
+    static constexpr int kStages = 2;
+    static constexpr int kSubs = kTile / kKv4Tokens, kStepSubs = kStep / kKv4Tokens;
     static constexpr int kSub = kv4_sub_bytes(D);
     static constexpr int kStageBytes = 2 * kSubs * kSub;              // K, then V
     static constexpr int kHeads = NT * 8;
@@ -55,9 +55,8 @@ struct Decode4Cfg {
     static constexpr int kWarpBytes = kStages * kStageBytes;
     static constexpr int kPipeBytes = kWarps * kWarpBytes;
     static constexpr int kPageBytes = (kDecodeMaxChunkPages * 4 + 15) / 16 * 16;
-    static constexpr int kBarBytes = kWarps * kStages * 8;
     static constexpr int kStateBytes = kWarps * 32 * 4 + 16;          // per-warp m, l (16 heads each) + flag
-    static constexpr int kSmem = 128 + kPipeBytes + kPageBytes + kBarBytes + kStateBytes;
+    static constexpr int kSmem = kPipeBytes + kPageBytes + kStateBytes;
     static_assert(kHeads * kRowStride * 4 <= kWarpBytes, "a warp's state fits its ring");
 };
 
@@ -73,7 +72,7 @@ struct Decode4Args {
     float* part_lse;
     int32_t* counters;
     int32_t* err;
-    int32_t Hq, Hkv, P, num_pages;
+    int32_t Hq, Hkv, page_log2, num_pages;
     float scale_log2;   // sm_scale * log2(e) * k_scale
     float v_scale;
 };
@@ -85,6 +84,14 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
         " {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// D = A * B
+__device__ __forceinline__ void mma_f16_16816_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32"
+        " {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
@@ -101,179 +108,177 @@ __device__ __forceinline__ void store_bf16x4(__nv_bfloat16* dst, float a, float 
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kDecodeWarps * 32)
+__global__ void __launch_bounds__(Decode4Cfg<D, NT>::kWarps * 32)
 decode4_sink_attn_kernel(const Decode4Args a) {
     using C = Decode4Cfg<D, NT>;
     constexpr int kKSteps = D / 16;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
-                                               ~static_cast<uintptr_t>(127));
-    int32_t* pages_s = reinterpret_cast<int32_t*>(smem + C::kPipeBytes);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kPipeBytes + C::kPageBytes);
-    float* ml_s = reinterpret_cast<float*>(smem + C::kPipeBytes + C::kPageBytes + C::kBarBytes);
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint32_t* first_s = reinterpret_cast<uint32_t*>(smem + C::kPipeBytes);
+    float* ml_s = reinterpret_cast<float*>(smem + C::kPipeBytes + C::kPageBytes);
     int* flag_s = reinterpret_cast<int*>(ml_s + C::kWarps * 32);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gq = lane >> 2, tq = lane & 3;
-    if (lane == 0)
-        for (int s = 0; s < C::kStages; ++s) ptx::mbar_init(ptx::smem_u32(&bars[warp * C::kStages + s]), 1);
-    ptx::fence_mbar_init();
-
     const DecodeUnit u = a.units[blockIdx.x];
-    const int P = a.P;
-    const int first_page = u.tok_begin / P;
-    const int n_pages = (u.tok_end - 1) / P - first_page + 1;
-    for (int i = tid; i < n_pages; i += blockDim.x) pages_s[i] = a.page_table[u.page_base + first_page + i];
+    const int first_page = u.tok_begin >> a.page_log2;
+    const int n_pages = ((u.tok_end - 1) >> a.page_log2) - first_page + 1;
+    load_sixteens(first_s, a.page_table + u.page_base + first_page, n_pages, a.num_pages, a.Hkv, u.kv_head, a.page_log2, a.err);
     __syncthreads();
 
     uint8_t* ring = smem + warp * C::kWarpBytes;
     const uint32_t ring_u32 = ptx::smem_u32(ring);
-    const uint32_t bar0 = ptx::smem_u32(&bars[warp * C::kStages]);
     const int n_tiles = (u.tok_end - u.tok_begin + C::kTile - 1) / C::kTile;
     const int n_it = n_tiles > warp ? (n_tiles - warp + C::kWarps - 1) / C::kWarps : 0;
-    const Kv4Source src{a.pool, pages_s, first_page, a.num_pages, a.Hkv, u.kv_head, P, a.err};
-    auto issue = [&](int it) {
-        const int s = it % C::kStages, tok = u.tok_begin + (warp + it * C::kWarps) * C::kTile;
-        kv4_stage_load<D, C::kTile, 2>(src, tok, u.tok_end, ring_u32 + s * C::kStageBytes, bar0 + s * 8, lane);
+    const TileSource src = tile_source<D, true, C::kTile>(a.pool, first_s, first_page, a.page_log2, a.Hkv, lane);
+    auto issue = [&](int it, int s) {   // one group per stage, empty past the end
+        const int tok = u.tok_begin + (warp + it * C::kWarps) * C::kTile;
+        if (it < n_it) kv4_stage_load<D, C::kTile, 2>(src, tok, u.tok_end, ring_u32 + s * C::kStageBytes, lane);
+        cp_async_commit();
     };
-    for (int it = 0; it < C::kStages && it < n_it; ++it) issue(it);
+    for (int it = 0; it < C::kStages; ++it) issue(it, it);
 
     // Q (column operand: heads), scaled per head by a power of two; heads past
-    // the slice are zero.  mult[nt][e] turns column 2 tq + e's products into
+    // the slice are zero.  mult[nt] turns columns 2 tq and 2 tq + 1's products into
     // log2 units.
     uint32_t qb[NT][kKSteps][2];
-    float mult[NT][2];
+    float2 mult[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int h = nt * 8 + gq;
         float inv = 1.f;
         kv4_load_q<D>(h < u.n_heads ? a.q + ((size_t)u.q_row * a.Hq + u.head0 + h) * D : nullptr, tq, qb[nt], inv);
-        mult[nt][0] = __shfl_sync(0xffffffffu, inv, (2 * tq) * 4) * a.scale_log2;
-        mult[nt][1] = __shfl_sync(0xffffffffu, inv, (2 * tq + 1) * 4) * a.scale_log2;
+        mult[nt].x = __shfl_sync(0xffffffffu, inv, (2 * tq) * 4) * a.scale_log2;
+        mult[nt].y = __shfl_sync(0xffffffffu, inv, (2 * tq + 1) * 4) * a.scale_log2;
     }
 
     // Online-softmax state of heads nt * 8 + 2 tq + e (log2 domain).  l is this
-    // lane's share of the row sum; the sink counts once, on lane row 0.
-    float m[NT][2], l[NT][2], o[NT][kKSteps][4];
+    // lane's share of the row sum; the sink counts once, on lane row 0.  Until
+    // the first scores come m is the sink's shift, or 0 where there is none.
+    auto sink_shift = [&](int h) {
+        return warp == 0 && u.chunk == 0 && a.sinks != nullptr && h < u.n_heads ? a.sinks[u.head0 + h] * kLog2e - kShift
+                                                                               : -INFINITY;
+    };
+    float o[NT][kKSteps][4];
+    float2 nm[NT], l[NT];   // nm: the shift, negated
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int h = nt * 8 + 2 * tq + e;
-            m[nt][e] = -INFINITY;
-            l[nt][e] = 0.f;
-            if (warp == 0 && u.chunk == 0 && a.sinks != nullptr && h < u.n_heads) {
-                m[nt][e] = a.sinks[u.head0 + h] * kLog2e - kShift;
-                l[nt][e] = gq == 0 ? exp2f(kShift) : 0.f;
-            }
+            const float s = sink_shift(nt * 8 + 2 * tq + e);
+            (e ? nm[nt].y : nm[nt].x) = s == -INFINITY ? 0.f : -s;
+            (e ? l[nt].y : l[nt].x) = s == -INFINITY || gq != 0 ? 0.f : exp2f(kShift);
         }
 #pragma unroll
         for (int i = 0; i < kKSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
+    float slack = -INFINITY;   // the first step moves every shift (a score of NaN never does)
 
     const int row = kv4_row(gq);   // tokens row and row + 8 of each sixteen are this lane's S rows
-    bool timed_out = false;
-    int it = 0;
-    for (; it < n_it; ++it) {
-        const int s = it % C::kStages;
-        if (!ptx::mbar_wait(bar0 + s * 8, (it / C::kStages) & 1)) { timed_out = true; break; }
+    for (int it = 0, s = 0; it < n_it; ++it) {
+        cp_async_wait<C::kStages - 1>();
+        __syncwarp();   // every lane's copies of this stage have landed
         const uint8_t* kt = ring + s * C::kStageBytes;
-        const uint8_t* vt = kt + C::kSubs * C::kSub;
         const int valid = min(C::kTile, u.tok_end - (u.tok_begin + (warp + it * C::kWarps) * C::kTile));
-
-        // S^T of the tile's tokens.
-        float sc[C::kSubs][NT][4];
-#pragma unroll
-        for (int sub = 0; sub < C::kSubs; ++sub) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) sc[sub][nt][0] = sc[sub][nt][1] = sc[sub][nt][2] = sc[sub][nt][3] = 0.f;
-            kv4_for_k<D>(kt + sub * C::kSub, row, tq, [&](int kk, const uint32_t (&ka)[4]) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_f16_16816(sc[sub][nt], ka, qb[nt][kk][0], qb[nt][kk][1]);
-            });
-        }
         if (valid < C::kTile) {
-            // Tokens past the end: no score, and scale 0 for their V (whatever
-            // lies there may have a NaN scale; codes are always finite).
-#pragma unroll
-            for (int sub = 0; sub < C::kSubs; ++sub)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (sub * kKv4Tokens + row + 8 * (e >> 1) >= valid) sc[sub][nt][e] = -INFINITY;
+            // Scale 0 for the V of tokens past the end (whatever their page
+            // holds there may have a NaN scale; codes are always finite).
             kv4_clear_scales<D, C::kTile>(ring + s * C::kStageBytes + C::kSubs * C::kSub, valid, lane);
             __syncwarp();
         }
-
-        // Does a score pass its shift by too much?
-        bool over = false;
+#pragma unroll 1
+        for (int t0 = 0; t0 < valid; t0 += C::kStep, kt += C::kStepSubs * C::kSub) {
+            const uint8_t* vt = kt + C::kSubs * C::kSub;
+            // S^T of the step's tokens.
+            float x[C::kStepSubs][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int sub = 0; sub < C::kStepSubs; ++sub) {
+                kv4_for_k<D>(kt + sub * C::kSub, row, tq, [&](int kk, const uint32_t (&ka)[4]) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mx = -INFINITY;
-#pragma unroll
-                for (int sub = 0; sub < C::kSubs; ++sub) mx = fmaxf(mx, fmaxf(sc[sub][nt][e], sc[sub][nt][e + 2]));
-                over = over || mx * mult[nt][e] > m[nt][e] + kSlack;
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (kk == 0) mma_f16_16816_new(x[sub][nt], ka, qb[nt][kk][0], qb[nt][kk][1]);
+                        else mma_f16_16816(x[sub][nt], ka, qb[nt][kk][0], qb[nt][kk][1]);
+                    }
+                });
             }
-        if (__any_sync(0xffffffffu, over)) {
+            if (valid < t0 + C::kStep) {   // tokens past the end have no score
+#pragma unroll
+                for (int sub = 0; sub < C::kStepSubs; ++sub)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (t0 + sub * kKv4Tokens + row + 8 * (e >> 1) >= valid) x[sub][nt][e] = -INFINITY;
+            }
+
+            // Scores above their shift, in log2 units; where one is by too
+            // much (and at the start), the shifts move.
+            float top = -INFINITY;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mx = -INFINITY;
+                for (int sub = 0; sub < C::kStepSubs; ++sub)
 #pragma unroll
-                    for (int sub = 0; sub < C::kSubs; ++sub)
-                        mx = fmaxf(mx, fmaxf(sc[sub][nt][e], sc[sub][nt][e + 2]));
-                    mx *= mult[nt][e];
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    const float mn = fmaxf(m[nt][e], mx - kShift);
-                    const float alpha = mn == -INFINITY ? 1.f : ptx::ex2(m[nt][e] - mn);
-                    m[nt][e] = mn;
-                    l[nt][e] *= alpha;
-#pragma unroll
-                    for (int i = 0; i < kKSteps; ++i) {
-                        o[nt][i][e] *= alpha;
-                        o[nt][i][e + 2] *= alpha;
+                    for (int e = 0; e < 4; e += 2) {
+                        const float2 v = ptx::fma2(make_float2(x[sub][nt][e], x[sub][nt][e + 1]), mult[nt], nm[nt]);
+                        x[sub][nt][e] = v.x;
+                        x[sub][nt][e + 1] = v.y;
+                        top = fmaxf(top, fmaxf(v.x, v.y));
                     }
-                }
-        }
-
-        // P^T as the column operand of the second product.
-        uint32_t pb[C::kSubs][NT][2];
+            if (__any_sync(0xffffffffu, top > slack)) {
 #pragma unroll
-        for (int sub = 0; sub < C::kSubs; ++sub)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float p[4];
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = ptx::ex2(fmaf(sc[sub][nt][e], mult[nt][e & 1], -m[nt][e & 1]));
-                l[nt][0] += p[0] + p[2];
-                l[nt][1] += p[1] + p[3];
-                pb[sub][nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
-                pb[sub][nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
+                        for (int sub = 0; sub < C::kStepSubs; ++sub)
+                            mx = fmaxf(mx, fmaxf(x[sub][nt][e], x[sub][nt][e + 2]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                        // How far the shift moves; at the start it holds no score
+                        // yet, only (if any) the sink's.
+                        const bool none = slack < 0.f && sink_shift(nt * 8 + 2 * tq + e) == -INFINITY;
+                        const float up = none ? mx - kShift : fmaxf(0.f, mx - kShift);
+                        const float alpha = none ? 0.f : ptx::ex2(-up);
+                        (e ? nm[nt].y : nm[nt].x) -= up;
+                        (e ? l[nt].y : l[nt].x) *= alpha;
+#pragma unroll
+                        for (int i = 0; i < kKSteps; ++i) {
+                            o[nt][i][e] *= alpha;
+                            o[nt][i][e + 2] *= alpha;
+                        }
+#pragma unroll
+                        for (int sub = 0; sub < C::kStepSubs; ++sub) {
+                            x[sub][nt][e] -= up;
+                            x[sub][nt][e + 2] -= up;
+                        }
+                    }
+                slack = kSlack;
             }
 
-        // O^T += V^T P^T.
+            // P^T as the column operand of the second product; O^T += V^T P^T.
 #pragma unroll
-        for (int sub = 0; sub < C::kSubs; ++sub)
-            kv4_for_v<D>(vt + sub * C::kSub, gq, tq, [&](int i, const uint32_t (&va)[4]) {
+            for (int sub = 0; sub < C::kStepSubs; ++sub) {
+                uint32_t pb[NT][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][i], va, pb[sub][nt][0], pb[sub][nt][1]);
-            });
-
-        __syncwarp();
-        if (it + C::kStages < n_it) {
-            ptx::fence_proxy_async_smem();   // reads (and cleared scales) before the copy rewrites the stage
-            issue(it + C::kStages);
+                for (int nt = 0; nt < NT; ++nt) {
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[e] = ptx::ex2(x[sub][nt][e]);
+                    l[nt] = ptx::add2(l[nt], ptx::add2(make_float2(p[0], p[1]), make_float2(p[2], p[3])));
+                    pb[nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
+                    pb[nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
+                }
+                kv4_for_v<D>(vt + sub * C::kSub, gq, tq, [&](int i, const uint32_t (&va)[4]) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][i], va, pb[nt][0], pb[nt][1]);
+                });
+            }
         }
-    }
-    if (timed_out) {
-        if (lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
-        for (int j = it; j < n_it && j < it + C::kStages; ++j)   // drain copies still in flight
-            ptx::mbar_wait(bar0 + (j % C::kStages) * 8, (j / C::kStages) & 1);
+
+        __syncwarp();   // every lane has read the stage
+        issue(it + C::kStages, s);
+        s = s + 1 == C::kStages ? 0 : s + 1;
     }
 
     // This warp's state into its own ring: O by head and dim.  Lane (gq, tq)
@@ -288,16 +293,17 @@ decode4_sink_attn_kernel(const Decode4Args a) {
 #pragma unroll
             for (int i = 0; i < kKSteps; ++i)
                 *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[nt][i][e], o[nt][i][e + 2]);
+            float sum = e ? l[nt].y : l[nt].x;
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+            for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             if (gq == 0) {
-                ml_s[warp * 32 + nt * 8 + 2 * tq + e] = m[nt][e];
-                ml_s[warp * 32 + 16 + nt * 8 + 2 * tq + e] = l[nt][e];
+                ml_s[warp * 32 + nt * 8 + 2 * tq + e] = n_it > 0 ? -(e ? nm[nt].y : nm[nt].x) : -INFINITY;   // no tokens: no state
+                ml_s[warp * 32 + 16 + nt * 8 + 2 * tq + e] = sum;
             }
         }
     __syncthreads();
 
-    // Merge the 4 warps: heads < n_heads, 4 dims per item.
+    // Merge the warps: heads < n_heads, 4 dims per item.
     const int items = u.n_heads * (D / 4);
     for (int idx = tid; idx < items; idx += blockDim.x) {
         const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
@@ -384,7 +390,7 @@ cudaError_t launch(const Decode4Args& args, int grid, cudaStream_t stream) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Decode4Cfg<D, NT>::kSmem);
     });
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kDecodeWarps * 32, Decode4Cfg<D, NT>::kSmem, stream>>>(args);
+    kernel<<<grid, Decode4Cfg<D, NT>::kWarps * 32, Decode4Cfg<D, NT>::kSmem, stream>>>(args);
     return cudaGetLastError();
 }
 
@@ -407,7 +413,7 @@ attn_status launch_decode_kv4(attn_plan_s* plan, const void* q, const void* kv4_
     a.err = reinterpret_cast<int32_t*>(plan->ws + plan->layout.err);
     a.Hq = plan->Hq;
     a.Hkv = plan->Hkv;
-    a.P = plan->P;
+    a.page_log2 = 31 - __builtin_clz(plan->P);
     a.num_pages = plan->num_pages;
     a.scale_log2 = plan->sm_scale * kLog2e * k_scale;
     a.v_scale = v_scale;

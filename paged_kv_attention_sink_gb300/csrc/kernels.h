@@ -39,10 +39,10 @@ attn_status launch_expand_kv4(const void* kv4_cache, void* buf, const int32_t* p
                               cudaStream_t stream);
 attn_status launch_decode_kv4(attn_plan_s* plan, const void* q, const void* kv4_cache, float k_scale, float v_scale,
                               const float* sinks, void* out, float* lse, cudaStream_t stream);
-// four: `pool` is a 4-bit cache (else bf16, read through step_map and kv_map,
-// the pool's tensor maps with 16-token boxes and with page boxes).
+// four: `pool` is a 4-bit cache (else bf16; prefill requests read it through
+// kv_map).
 attn_status launch_key_weights(attn_plan_s* plan, bool four, const void* q, const void* pool, float k_scale,
-                               const void* step_map, const void* q_map, const void* kv_map, const float* lse, const float* prev, float decay, int32_t window, float* weights,
+                               const void* q_map, const void* kv_map, const float* lse, const float* prev, float decay, int32_t window, float* weights,
                                cudaStream_t stream);
 // page_table_out NULL: in place (pool_out / weights_out are then the inputs).
 attn_status launch_evict(attn_plan_s* plan, bool four, const float* weights, const void* pool, int32_t budget,

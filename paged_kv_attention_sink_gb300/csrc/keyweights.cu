@@ -39,11 +39,11 @@ struct KeyWeightArgs {
     const int32_t* page_table;
     const __nv_bfloat16* q;
     const float* lse;
-    const uint8_t* pool4;       // 4-bit cache (the bf16 one is read through its tensor map)
+    const uint8_t* pool;
     const float* prev;
     float* weights;
     int32_t* err;
-    int32_t Hq, Hkv, P, num_pages, causal, window;
+    int32_t Hq, Hkv, P, page_log2, num_pages, causal, window;   // P = 1 << page_log2
     float scale_log2, decay;    // scale_log2 = sm_scale * log2(e) * k_scale
 };
 
@@ -53,14 +53,14 @@ struct KeyWeightArgs {
 template <int D, bool kFour>
 struct StepWeightCfg {
     static constexpr int kWarps = kDecodeWarps;
-    static constexpr int kStages = 4;
-    static constexpr int kTile = 32;
+    static constexpr int kTile = 32;                                     // tokens per stage
+    static constexpr int kStages = kFour || D == 64 ? 4 : 3;
     static constexpr int kSubs = kTile / kBlockTokens;
     static constexpr int kSub = kFour ? kv4_sub_bytes(D) : kBlockTokens * D * 2;   // K of 16 tokens
     static constexpr int kStageBytes = kSubs * kSub;
     static constexpr int kPipeBytes = kWarps * kStages * kStageBytes;
     static constexpr int kPageBytes = (kDecodeMaxChunkPages * 4 + 15) / 16 * 16;
-    static constexpr int kSmem = 1024 + kPipeBytes + kPageBytes + kWarps * kStages * 8;
+    static constexpr int kSmem = 128 + kPipeBytes + kPageBytes;
 };
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -103,59 +103,36 @@ struct QueryTile {
 // from memory tile by tile.
 template <int D, bool kFour, int NT>
 __global__ void __launch_bounds__(kDecodeWarps * 32)
-key_weights_step_kernel(const __grid_constant__ CUtensorMap kv_map, const KeyWeightArgs a) {
+key_weights_step_kernel(const KeyWeightArgs a) {
     using C = StepWeightCfg<D, kFour>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                               ~static_cast<uintptr_t>(1023));
-    int32_t* pages_s = reinterpret_cast<int32_t*>(smem + C::kPipeBytes);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kPipeBytes + C::kPageBytes);
+    uint8_t* smem = smem_raw + (-ptx::smem_u32(smem_raw) & 127u);
+    uint32_t* first_s = reinterpret_cast<uint32_t*>(smem + C::kPipeBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gq = lane >> 2, tq = lane & 3;
     const DecodeUnit u = a.units[blockIdx.x];
     const int G = a.Hq / a.Hkv, P = a.P;
     if (u.head0 != u.kv_head * G) return;   // the unit of the first head slice takes all heads
-    if (lane == 0)
-        for (int s = 0; s < C::kStages; ++s) ptx::mbar_init(ptx::smem_u32(&bars[warp * C::kStages + s]), 1);
-    ptx::fence_mbar_init();
-    const int first_page = u.tok_begin / P;
-    const int n_pages = (u.tok_end - 1) / P - first_page + 1;
-    for (int i = tid; i < n_pages; i += blockDim.x) pages_s[i] = a.page_table[u.page_base + first_page + i];
+    const int first_page = u.tok_begin >> a.page_log2;
+    const int n_pages = ((u.tok_end - 1) >> a.page_log2) - first_page + 1;
+    load_sixteens(first_s, a.page_table + u.page_base + first_page, n_pages, a.num_pages, a.Hkv, u.kv_head, a.page_log2, a.err);
     __syncthreads();
 
     const uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
     const uint32_t ring_u32 = ptx::smem_u32(ring);
-    const uint32_t bar0 = ptx::smem_u32(&bars[warp * C::kStages]);
     const int n_tiles = (u.tok_end - u.tok_begin + C::kTile - 1) / C::kTile;
     const int n_it = n_tiles > warp ? (n_tiles - warp + C::kWarps - 1) / C::kWarps : 0;
     auto tile_tok = [&](int it) { return u.tok_begin + (warp + it * C::kWarps) * C::kTile; };
-    const Kv4Source src{a.pool4, pages_s, first_page, a.num_pages, a.Hkv, u.kv_head, P, a.err};
-    auto issue = [&](int it) {
-        const int s = it % C::kStages, tok = tile_tok(it);
-        const uint32_t dst = ring_u32 + s * C::kStageBytes, bar = bar0 + s * 8;
-        if constexpr (kFour) {
-            kv4_stage_load<D, C::kTile, 1>(src, tok, u.tok_end, dst, bar, lane);
-        } else {
-            // One 16-token box per 64 dims, a lane each.
-            constexpr int kBoxes = C::kSubs * (D / 64);
-            const int t = tok + lane / (D / 64) * kBlockTokens;
-            int page = -1;
-            if (lane < kBoxes && t < u.tok_end) {
-                page = pages_s[t / P - first_page];
-                if (page < 0 || page >= a.num_pages) {
-                    atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
-                    page = -1;
-                }
-            }
-            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, boxes * kBlockTokens * 128);
-            __syncwarp();
-            if (page >= 0)
-                ptx::tma_load_3d_hint(dst + lane * kBlockTokens * 128, &kv_map, bar, lane % (D / 64) * 64, t % P,
-                                      page * 2 * a.Hkv + u.kv_head, ptx::policy_evict_first());
+    const TileSource src = tile_source<D, kFour, C::kTile>(a.pool, first_s, first_page, a.page_log2, a.Hkv, lane);
+    auto issue = [&](int it, int s) {   // one group per stage, empty past the end
+        const uint32_t dst = ring_u32 + s * C::kStageBytes;
+        if (it < n_it) {
+            if constexpr (kFour) kv4_stage_load<D, C::kTile, 1>(src, tile_tok(it), u.tok_end, dst, lane);
+            else bf16_stage_load<D, C::kTile>(src, tile_tok(it), u.tok_end, dst, lane);
         }
+        cp_async_commit();
     };
-    for (int it = 0; it < C::kStages && it < n_it; ++it) issue(it);
+    for (int it = 0; it < C::kStages; ++it) issue(it, it);
 
     constexpr int kHeld = NT > 0 ? NT : 1;
     QueryTile<D, kFour> qt[kHeld];
@@ -196,22 +173,23 @@ key_weights_step_kernel(const __grid_constant__ CUtensorMap kv_map, const KeyWei
     // (tq & 1) * 8 + its own.
     const int row = kFour ? kv4_row(gq) : gq;
     const int mine = (tq >> 1) * kBlockTokens + (tq & 1) * 8 + row;
-    bool timed_out = false;
-    int it = 0;
-    for (; it < n_it; ++it) {
-        const int s = it % C::kStages, tok = tile_tok(it) + mine;
+    for (int it = 0, s = 0; it < n_it; ++it) {
+        const int tok = tile_tok(it) + mine;
         // This lane's slot, and its previous weight on the way while the tile arrives.
         int64_t at = -1;
         float before = 0.f;
         if (tok < u.tok_end) {
-            const int page = pages_s[tok / P - first_page];
-            if (page >= 0 && page < a.num_pages) {
-                at = ((int64_t)page * a.Hkv + u.kv_head) * P + tok % P;
+            const uint32_t first = first_s[(tok >> a.page_log2) - first_page];
+            if (first != kBadPage) {
+                // weights[page][head][row]: (page * Hkv + head) * P + row, from (page * 2 Hkv + head) * P / 16.
+                const uint32_t block = first >> (a.page_log2 - 4);
+                at = ((int64_t)(block / (2 * a.Hkv) * a.Hkv + u.kv_head) << a.page_log2) + (tok & (P - 1));
                 const bool is_new = u.chunk == u.n_chunks - 1 && tok == u.tok_end - 1;
                 if (a.decay != 0.f && !is_new) before = a.decay * a.prev[at];
             }
         }
-        if (!ptx::mbar_wait(bar0 + s * 8, (it / C::kStages) & 1)) { timed_out = true; break; }
+        cp_async_wait<C::kStages - 1>();
+        __syncwarp();   // every lane's copies of this stage have landed
         const uint8_t* kt = ring + s * C::kStageBytes;
         float w[C::kSubs][2];
 #pragma unroll
@@ -226,11 +204,9 @@ key_weights_step_kernel(const __grid_constant__ CUtensorMap kv_map, const KeyWei
                 }
             }
         }
-        __syncwarp();
-        if (it + C::kStages < n_it) {
-            ptx::fence_proxy_async_smem();
-            issue(it + C::kStages);
-        }
+        __syncwarp();   // every lane has read the stage
+        issue(it + C::kStages, s);
+        s = s + 1 == C::kStages ? 0 : s + 1;
 #pragma unroll
         for (int sub = 0; sub < C::kSubs; ++sub)
 #pragma unroll
@@ -240,11 +216,6 @@ key_weights_step_kernel(const __grid_constant__ CUtensorMap kv_map, const KeyWei
             }
         const float mine_w = tq < 2 ? (tq == 0 ? w[0][0] : w[0][1]) : (tq == 2 ? w[1][0] : w[1][1]);
         if (at >= 0) a.weights[at] = mine_w + before;
-    }
-    if (timed_out) {
-        if (lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
-        for (int j = it; j < n_it && j < it + C::kStages; ++j)
-            ptx::mbar_wait(bar0 + (j % C::kStages) * 8, (j / C::kStages) & 1);
     }
 }
 
@@ -281,8 +252,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
                           const KeyWeightArgs a) {
     using C = PromptWeightCfg<D>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* smem = smem_raw + (-ptx::smem_u32(smem_raw) & 1023u);
     const uint32_t sbase = ptx::smem_u32(smem);
     const uint32_t q_full = sbase + C::kOffBars, q_empty = q_full + 8 * C::kStages, k_full = q_empty + 8 * C::kStages;
     const uint32_t s_full = k_full + 8, s_free = s_full + 16, drain = s_free + 16;
@@ -399,7 +369,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
                     atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
                     continue;
                 }
-                const uint8_t* sub = a.pool4 + kv4::sub_offset(page, 0, a.Hkv, g, P, t % P, kv4_sub_bytes(D));
+                const uint8_t* sub = a.pool + kv4::sub_offset(page, 0, a.Hkv, g, P, t % P, kv4_sub_bytes(D));
                 const int in = t % kKv4Tokens;
                 const uint2 codes = *reinterpret_cast<const uint2*>(sub + in * (D / 2) + grp * 8);
                 const float sc = kv4::f16x2_to_f32(kv4::scales_to_f16x2(sub[8 * D + in * kGroups + grp])).x;
@@ -503,7 +473,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
 }
 
 template <int D, bool kFour, int NT>
-cudaError_t launch_step(const CUtensorMap& map, const KeyWeightArgs& a, int grid, cudaStream_t stream) {
+cudaError_t launch_step(const KeyWeightArgs& a, int grid, cudaStream_t stream) {
     using C = StepWeightCfg<D, kFour>;
     auto kernel = key_weights_step_kernel<D, kFour, NT>;
     static std::atomic<bool> configured[kMaxDevices];
@@ -511,7 +481,7 @@ cudaError_t launch_step(const CUtensorMap& map, const KeyWeightArgs& a, int grid
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kDecodeWarps * 32, C::kSmem, stream>>>(map, a);
+    kernel<<<grid, kDecodeWarps * 32, C::kSmem, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -530,14 +500,14 @@ cudaError_t launch_prompt(const CUtensorMap& q_map, const CUtensorMap& kv_map, c
 }
 
 template <int D, bool kFour>
-attn_status launch_all(const attn_plan_s* plan, const CUtensorMap& step_map, const CUtensorMap& q_map,
-                       const CUtensorMap& kv_map, const KeyWeightArgs& a, cudaStream_t stream) {
+attn_status launch_all(const attn_plan_s* plan, const CUtensorMap& q_map, const CUtensorMap& kv_map,
+                       const KeyWeightArgs& a, cudaStream_t stream) {
     const int G = plan->Hq / plan->Hkv, units = (int)plan->units.size();
     cudaError_t e = cudaSuccess;
     if (units > 0)
-        e = G <= 8    ? launch_step<D, kFour, 1>(step_map, a, units, stream)
-            : G <= 16 ? launch_step<D, kFour, 2>(step_map, a, units, stream)
-                      : launch_step<D, kFour, 0>(step_map, a, units, stream);
+        e = G <= 8    ? launch_step<D, kFour, 1>(a, units, stream)
+            : G <= 16 ? launch_step<D, kFour, 2>(a, units, stream)
+                      : launch_step<D, kFour, 0>(a, units, stream);
     if (e == cudaSuccess && !plan->weight_tiles.empty())
         e = launch_prompt<D, kFour>(q_map, kv_map, a, (int)plan->weight_tiles.size() * plan->Hkv, stream);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
@@ -546,8 +516,8 @@ attn_status launch_all(const attn_plan_s* plan, const CUtensorMap& step_map, con
 }  // namespace
 
 attn_status launch_key_weights(attn_plan_s* plan, bool four, const void* q, const void* pool, float k_scale,
-                               const void* step_map, const void* q_map, const void* kv_map, const float* lse,
-                               const float* prev, float decay, int32_t window, float* weights, cudaStream_t stream) {
+                               const void* q_map, const void* kv_map, const float* lse, const float* prev,
+                               float decay, int32_t window, float* weights, cudaStream_t stream) {
     KeyWeightArgs a;
     a.units = reinterpret_cast<const DecodeUnit*>(plan->ws + plan->layout.units);
     a.requests = reinterpret_cast<const RequestInfo*>(plan->ws + plan->layout.requests);
@@ -555,24 +525,24 @@ attn_status launch_key_weights(attn_plan_s* plan, bool four, const void* q, cons
     a.page_table = plan->page_table;
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.lse = lse;
-    a.pool4 = static_cast<const uint8_t*>(pool);
+    a.pool = static_cast<const uint8_t*>(pool);
     a.prev = prev;
     a.weights = weights;
     a.err = reinterpret_cast<int32_t*>(plan->ws + plan->layout.err);
     a.Hq = plan->Hq;
     a.Hkv = plan->Hkv;
     a.P = plan->P;
+    a.page_log2 = 31 - __builtin_clz(plan->P);
     a.num_pages = plan->num_pages;
     a.causal = plan->causal;
     a.window = window;
     a.scale_log2 = plan->sm_scale * kLog2e * k_scale;
     a.decay = decay;
-    const CUtensorMap& sm = *static_cast<const CUtensorMap*>(step_map);
     const CUtensorMap& qm = *static_cast<const CUtensorMap*>(q_map);
     const CUtensorMap& km = *static_cast<const CUtensorMap*>(kv_map);
     if (plan->D == 64)
-        return four ? launch_all<64, true>(plan, sm, qm, km, a, stream) : launch_all<64, false>(plan, sm, qm, km, a, stream);
-    return four ? launch_all<128, true>(plan, sm, qm, km, a, stream) : launch_all<128, false>(plan, sm, qm, km, a, stream);
+        return four ? launch_all<64, true>(plan, qm, km, a, stream) : launch_all<64, false>(plan, qm, km, a, stream);
+    return four ? launch_all<128, true>(plan, qm, km, a, stream) : launch_all<128, false>(plan, qm, km, a, stream);
 }
 
 }  // namespace attn

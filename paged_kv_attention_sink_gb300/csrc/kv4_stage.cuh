@@ -8,49 +8,108 @@
 
 namespace attn {
 
-// Where a unit's tokens lie: page ids (shared memory, from token
-// first_page * P on) of one KV head in the pool.
-struct Kv4Source {
-    const uint8_t* pool;
-    const int32_t* pages;
-    int first_page, num_pages, Hkv, kv_head, P;
-    int32_t* err;
-};
+// A "sixteen": 16 consecutive tokens of a (page, K/V, KV head) block, which lie
+// together in either pool (P is a multiple of 16, and units start on one, so a
+// sixteen never crosses a page).  Sixteens are numbered through the pool:
+//   ((page * 2 + half) * Hkv + head) * (P / 16) + row / 16,
+// below 2^31 for any pool that fits the device.
+constexpr uint32_t kBadPage = 0x80000000u;
 
-// Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
-        ::"r"(dst), "l"(src), "r"(bytes), "r"(bar), "l"(policy) : "memory");
+// All threads of a CTA: K's first sixteen in each of a unit's pages (kBadPage,
+// recorded, for an id outside the pool) into shared memory.  A barrier follows.
+__device__ __forceinline__ void load_sixteens(uint32_t* first, const int32_t* page_table, int n_pages, int num_pages,
+                                              int Hkv, int kv_head, int page_log2, int32_t* err) {
+    for (int i = threadIdx.x; i < n_pages; i += blockDim.x) {
+        const int page = page_table[i];
+        const bool bad = page < 0 || page >= num_pages;
+        if (bad) atomicOr(err, ATTN_DEVICE_ERR_PAGE_ID);
+        first[i] = bad ? kBadPage : (uint32_t)(page * 2 * Hkv + kv_head) << (page_log2 - 4);
+    }
 }
 
-// A whole warp: start the copies of tokens [tok, min(tok + kTile, tok_end))
-// into a stage (kTile / 16 sub-blocks of K, then, for kHalves = 2, of V); tok
-// is a multiple of 16.  One copy per run of sub-blocks within a page; `bar`
-// (one arrival) completes when all have landed.  Runs of a page id outside
-// the pool are skipped and recorded.
+// A unit's tokens: its table of sixteens, the first of which holds token tok0
+// of the request rounded down to a page, and where each lane copies from.
+struct TileSource {
+    const uint8_t *pool, *pool_v;   // K's and V's sixteen 0, + this lane's 16 bytes
+    const uint8_t* pool_s;          // 4-bit: this lane's piece of its sixteen's scales (K or V)
+    const uint32_t* first;          // shared memory
+    int tok0, page_log2;
+    __device__ __forceinline__ uint32_t at(int t) const {
+        return first[(t - tok0) >> page_log2] + ((t & ((1 << page_log2) - 1)) >> 4);
+    }
+};
+
+template <int D, bool kFour, int kTile>
+__device__ __forceinline__ TileSource tile_source(const uint8_t* pool, const uint32_t* first, int first_page,
+                                                  int page_log2, int Hkv, int lane) {
+    constexpr int kSub = kFour ? kv4_sub_bytes(D) : kBlockTokens * D * 2, kPieces = kTile / kKv4Tokens * (D / 16);
+    const int64_t v = ((int64_t)Hkv << (page_log2 - 4)) * kSub;
+    return {pool + lane * 16, pool + v + lane * 16, pool + (lane >= kPieces ? v : 0) + 8 * D + lane % (D / 16) * 16, first,
+            first_page << page_log2, page_log2};
+}
+
+// 16 bytes global -> shared, asynchronously (the thread's current group), from
+// `offset` bytes into a sixteen; zeros, and no access, where it is a bad one.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* pool, uint32_t sixteen, uint32_t bytes, int offset) {
+    const uint8_t* src = pool + (uint64_t)(sixteen & ~kBadPage) * bytes + offset;
+    const uint32_t size = 16u & ~(uint32_t)((int32_t)sixteen >> 31);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// A whole warp: start the copies of tokens [tok, tok + kTile) of a 4-bit pool
+// into a stage (kTile / 16 sixteens of K, then, for kHalves = 2, of V); tok is
+// a multiple of 16.  A sixteen's codes are 16 bytes for every lane (or twice
+// that), and one copy takes the scales of eight sixteens (or four).  Sixteens
+// from tok_end on, and those of a bad page, are set to zero instead.
 template <int D, int kTile, int kHalves>
-__device__ __forceinline__ void kv4_stage_load(const Kv4Source& s, int tok, int tok_end, uint32_t dst, uint32_t bar,
-                                               int lane) {
-    constexpr int kSubs = kTile / kKv4Tokens, kSub = kv4_sub_bytes(D);
-    const int n_subs = min(kSubs, (tok_end - tok + kKv4Tokens - 1) / kKv4Tokens);
-    const int half = lane / kSubs, sub = lane % kSubs;
-    const int t = tok + sub * kKv4Tokens, off = t % s.P;
-    uint32_t bytes = 0;
-    const uint8_t* src = nullptr;
-    if (half < kHalves && sub < n_subs && (sub == 0 || off == 0)) {
-        const int page = s.pages[t / s.P - s.first_page];
-        if (page < 0 || page >= s.num_pages) {
-            atomicOr(s.err, ATTN_DEVICE_ERR_PAGE_ID);
-        } else {
-            bytes = min(n_subs - sub, (s.P - off) / kKv4Tokens) * kSub;
-            src = s.pool + kv4::sub_offset(page, half, s.Hkv, s.kv_head, s.P, off, kSub);
+__device__ __forceinline__ void kv4_stage_load(const TileSource& s, int tok, int tok_end, uint32_t dst, int lane) {
+    constexpr int kSubs = kTile / kKv4Tokens, kSub = kv4_sub_bytes(D), kScalePieces = D / 16;
+    // Lane l looks up sixteen l % kSubs.
+    const int t = tok + lane % kSubs * kKv4Tokens;
+    const uint32_t mine = t < tok_end ? s.at(t) : kBadPage;
+#pragma unroll
+    for (int sub = 0; sub < kSubs; ++sub) {
+        const uint32_t k = __shfl_sync(0xffffffffu, mine, sub);
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+                cp_async16(dst + (half * kSubs + sub) * kSub + j * 512 + lane * 16, half ? s.pool_v : s.pool, k, kSub, j * 512);
+    }
+    // Scales: lane l's piece and sixteen are the same in every stage (pool_s).
+    constexpr int kPieces = kSubs * kScalePieces;   // of one half
+#pragma unroll
+    for (int i = 0; i < (kHalves * kPieces + 31) / 32; ++i) {
+        const int idx = i * 32 + lane, block = idx / kScalePieces;
+        const uint32_t k = __shfl_sync(0xffffffffu, mine, block % kSubs);
+        const uint8_t* src = kPieces % 32 == 0 ? s.pool_s + (i * 32 / kPieces) * (s.pool_v - s.pool) : s.pool_s;
+        if (kHalves * kPieces % 32 == 0 || idx < kHalves * kPieces)
+            cp_async16(dst + block * kSub + 8 * D + idx % kScalePieces * 16, src, k, kSub, 0);
+    }
+}
+
+// The same for K of a bf16 pool: rows of 64 dims (128 bytes) apart, 16-byte
+// piece c of row r at c ^ (r % 8), as ldmatrix reads them without conflicts.
+template <int D, int kTile>
+__device__ __forceinline__ void bf16_stage_load(const TileSource& s, int tok, int tok_end, uint32_t dst, int lane) {
+    constexpr int kSubs = kTile / kBlockTokens, kSub = kBlockTokens * D * 2, kPieces = D / 8;   // pieces of a row
+    const int t = tok + lane % kSubs * kBlockTokens;
+    const uint32_t mine = t < tok_end ? s.at(t) : kBadPage;
+#pragma unroll
+    for (int sub = 0; sub < kSubs; ++sub) {
+        const uint32_t k = __shfl_sync(0xffffffffu, mine, sub);
+#pragma unroll
+        for (int j = 0; j < kSub / 512; ++j) {
+            const int idx = j * 32 + lane, r = idx / kPieces, c = idx % kPieces;
+            cp_async16(dst + sub * kSub + (c >> 3) * (kBlockTokens * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), s.pool, k,
+                       kSub, j * 512);
         }
     }
-    const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
-    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, total);
-    __syncwarp();
-    if (bytes) bulk_load(dst + (half * kSubs + sub) * kSub, src, bytes, bar, ptx::policy_evict_first());
 }
 
 // Token of a sixteen that MMA row i (0..7) stands for; row i + 8 is 8 further.
