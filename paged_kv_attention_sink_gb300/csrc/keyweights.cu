@@ -17,10 +17,12 @@
 //  * prefill requests: bound by the exponentials (MUFU: 32 a clock and SM) and
 //    the product on the tensor cores.  One CTA per 128 keys of a KV head keeps
 //    the K tile in shared memory and streams Q tiles (128 rows of one head)
-//    past it; tcgen05.mma fills one of two 128-column accumulators in TMEM
-//    while a warpgroup drains the other, one key per thread.
+//    past it; tcgen05.mma fills a ring of four 128-column accumulators in TMEM
+//    ahead of the warpgroups that drain them, one key per thread.
 #include <cuda.h>
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "attn_internal.h"
 #include "kernels.h"
@@ -233,30 +235,41 @@ template <int D>
 struct PromptWeightCfg {
     static constexpr int kAtom = 128 * 128;                 // 128 rows x 64 dims, 128-byte swizzle
     static constexpr int kTile = kAtom * (D / 64);
-    // Two CTAs per SM (each 256 of the 512 TMEM columns) must fill shared
-    // memory so that a third does not fit and wait for TMEM.
-    static constexpr int kStages = D == 64 ? 4 : 2;
-    static constexpr int kEpilogueWarps = 8;
-    static constexpr int kThreads = (kEpilogueWarps + 2) * 32;
+    // Q stages: a stage's round trip (refill noticed, copied, multiplied) is
+    // some 2,000 clocks, so many must be on their way at once.
+    static constexpr int kStages = D == 64 ? 10 : 5;
+    static constexpr int kBufs = 4;                         // S accumulators: all 512 TMEM columns
+    static constexpr int kWgs = 3;                          // epilogue warpgroups
+    static constexpr int kEpilogueWarps = 4 * kWgs;
+    // MMA warps, taking steps in turn: a step costs its warp some 650 clocks
+    // (two waits, the issue of the MMAs and a commit), a step's exponentials 515.
+    static constexpr int kMmaWarps = 2;
+    static constexpr int kThreads = (kEpilogueWarps + kMmaWarps + 2) * 32;   // + Q producer, + lse
+    static constexpr int kHeads = 8;                        // heads whose lse is staged at a time
     static constexpr int kOffQ = kTile;
-    static constexpr int kOffNl = kOffQ + kStages * kTile;  // [2 warpgroups][2][128] negated lse
-    static constexpr int kOffSum = kOffNl + 2 * 2 * kTileRows * 4;
-    static constexpr int kOffBars = kOffSum + kTileKeys * 4;
-    static constexpr int kSmem = 1024 + kOffBars + (2 * kStages + 6) * 8 + 16;
-    static_assert(3 * (kSmem + 1024) > 233472 && 2 * (kSmem + 1024) <= 233472, "exactly two CTAs per SM");
+    static constexpr int kOffNl = kOffQ + kStages * kTile;    // [2][8 heads][128 rows] negated lse
+    static constexpr int kOffSum = kOffNl + 2 * kHeads * kTileRows * 4;
+    static constexpr int kOffBars = kOffSum + kWgs * kTileKeys * 4;
+    static constexpr int kSmem = 1024 + kOffBars + (2 * kStages + kBufs + 6) * 8 + 16;
+    // One CTA per SM: it holds all of an SM's TMEM, and a second one would wait for it.
+    static_assert(2 * (kSmem + 1024) > 233472 && kSmem <= 232448, "one CTA per SM");
 };
 
 template <int D, bool kFour>
-__global__ void __launch_bounds__(PromptWeightCfg<D>::kThreads, 2)
+__global__ void __launch_bounds__(PromptWeightCfg<D>::kThreads, 1)
 key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
                           const KeyWeightArgs a) {
     using C = PromptWeightCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-ptx::smem_u32(smem_raw) & 1023u);
     const uint32_t sbase = ptx::smem_u32(smem);
-    const uint32_t q_full = sbase + C::kOffBars, q_empty = q_full + 8 * C::kStages, k_full = q_empty + 8 * C::kStages;
-    const uint32_t s_full = k_full + 8, s_free = s_full + 16, drain = s_free + 16;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBars + (2 * C::kStages + 6) * 8);
+    // Step s uses Q stage s % kStages and S accumulator s % kBufs.  s_full (by
+    // stage): the product is done, S may be read and the stage refilled; s_free
+    // (by accumulator): S has been read.
+    const uint32_t q_full = sbase + C::kOffBars, s_full = q_full + 8 * C::kStages, s_free = s_full + 8 * C::kStages;
+    const uint32_t l_full = s_free + 8 * C::kBufs, l_free = l_full + 16, k_full = l_free + 16, drain = k_full + 8;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBars + (2 * C::kStages + C::kBufs + 6) * 8);
+    float* nl_s = reinterpret_cast<float*>(smem + C::kOffNl);
     float* sum_s = reinterpret_cast<float*>(smem + C::kOffSum);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -268,22 +281,24 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
     int i0 = a.window > 0 ? max(0, r.qo_len - a.window) : 0;
     if (a.causal) i0 = max(i0, t0 - prefix);
     const int n_steps = (r.qo_len - i0 + kTileRows - 1) / kTileRows * G;   // step s: rows i0 + s / G * 128, head s % G
+    const int n_groups = n_steps / G * ((G + C::kHeads - 1) / C::kHeads);
 
     if (tid == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
-            ptx::mbar_init(q_full + 8 * s, 1);
-            ptx::mbar_init(q_empty + 8 * s, 1);
+        for (int i = 0; i < C::kStages; ++i) {
+            ptx::mbar_init(q_full + 8 * i, 1);
+            ptx::mbar_init(s_full + 8 * i, 1);
+        }
+        for (int i = 0; i < C::kBufs; ++i) ptx::mbar_init(s_free + 8 * i, 4);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(l_full + 8 * i, 1);
+            ptx::mbar_init(l_free + 8 * i, C::kEpilogueWarps);
         }
         ptx::mbar_init(k_full, kFour ? C::kEpilogueWarps : 1);
-        for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(s_full + 8 * i, 1);
-            ptx::mbar_init(s_free + 8 * i, 4);
-        }
-        ptx::mbar_init(drain, 1);
+        ptx::mbar_init(drain, C::kMmaWarps);
         ptx::fence_mbar_init();
     }
     if (warp == C::kEpilogueWarps) {
-        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 256);
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
@@ -291,7 +306,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == C::kEpilogueWarps + 1) {
+    if (warp == C::kEpilogueWarps + C::kMmaWarps) {
         // ------------------------------------------------------------ producer
         if (!kFour) {
             const int n_load = (min(kTileKeys, r.kv_len - t0) + P - 1) / P;   // page boxes of the K tile
@@ -313,16 +328,20 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
         }
         if (lane == 0) {
             int s = 0;
-            for (; s < n_steps; ++s) {
+            for (int head = 0, row0 = r.q_row0 + i0; s < n_steps; ++s) {
                 const int st = s % C::kStages;
-                if (s >= C::kStages && !ptx::mbar_wait(q_empty + 8 * st, (s / C::kStages - 1) & 1)) {
+                if (s >= C::kStages && !ptx::mbar_wait(s_full + 8 * st, (s / C::kStages - 1) & 1)) {
                     atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
                     break;
                 }
                 ptx::mbar_arrive_expect_tx(q_full + 8 * st, C::kTile);
                 for (int c = 0; c < D / 64; ++c)
                     ptx::tma_load_3d(sbase + C::kOffQ + st * C::kTile + c * C::kAtom, &q_map, q_full + 8 * st, c * 64,
-                                     g * G + s % G, r.q_row0 + i0 + s / G * kTileRows);
+                                     g * G + head, row0);
+                if (++head == G) {
+                    head = 0;
+                    row0 += kTileRows;
+                }
             }
             // Copies still in flight when a wait ran out land before the CTA exits.
             if (s < n_steps)
@@ -330,13 +349,46 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
                     ptx::mbar_wait(q_full + 8 * (k % C::kStages), (k / C::kStages) & 1);
         }
         __syncwarp();
-    } else if (warp == C::kEpilogueWarps) {
-        // ---------------------------------------------------------- MMA issuer
+    } else if (warp == C::kEpilogueWarps + C::kMmaWarps + 1) {
+        // ----------------------------------------------------------------- lse
+        // Steps come in groups, the same 128 rows and up to 8 heads; this warp
+        // stages a group's lse (negated, in log2 units, by head) ahead of them.
+        int row0 = i0, h0 = 0;
+        for (int grp = 0; grp < n_groups; ++grp) {
+            float* dst = nl_s + (grp & 1) * C::kHeads * kTileRows + lane;
+            const int n = min(C::kHeads, G - h0);
+            float v[kTileRows / 32][C::kHeads];   // every load on its way before the first is used
+#pragma unroll
+            for (int k = 0; k < kTileRows / 32; ++k) {
+                const int row = row0 + k * 32 + lane;
+                const float* src = a.lse + (int64_t)(r.q_row0 + row) * a.Hq + g * G + h0;
+#pragma unroll
+                for (int h = 0; h < C::kHeads; ++h) v[k][h] = h < n && row < r.qo_len ? __ldg(src + h) : 0.f;
+            }
+            if (grp >= 2 && !wait_all(l_free + 8 * (grp & 1), ((grp >> 1) - 1) & 1)) {
+                if (lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
+                break;
+            }
+#pragma unroll
+            for (int k = 0; k < kTileRows / 32; ++k)
+#pragma unroll
+                for (int h = 0; h < C::kHeads; ++h) dst[h * kTileRows + k * 32] = -v[k][h] * kLog2e;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(l_full + 8 * (grp & 1));
+            h0 += C::kHeads;
+            if (h0 >= G) {
+                h0 = 0;
+                row0 += kTileRows;
+            }
+        }
+    } else if (warp >= C::kEpilogueWarps) {
+        // --------------------------------------------------------- MMA issuers
         constexpr uint32_t idesc = ptx::idesc_bf16(kTileKeys, kTileRows, false, false);
         bool ok = wait_all(k_full, 0);
-        for (int s = 0; ok && s < n_steps; ++s) {
-            const int st = s % C::kStages, buf = s & 1;
-            ok = wait_all(q_full + 8 * st, (s / C::kStages) & 1) && (s < 2 || wait_all(s_free + 8 * buf, (s / 2 - 1) & 1));
+        for (int s = warp - C::kEpilogueWarps; ok && s < n_steps; s += C::kMmaWarps) {
+            const int st = s % C::kStages, buf = s % C::kBufs;
+            ok = wait_all(q_full + 8 * st, (s / C::kStages) & 1) &&
+                 (s < C::kBufs || wait_all(s_free + 8 * buf, (s / C::kBufs - 1) & 1));
             if (!ok) break;
             if (ptx::elect_one()) {
                 ptx::tc_fence_after();
@@ -346,8 +398,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
                     ptx::tc_mma_ss(tmem + buf * kTileRows, ptx::smem_desc_sw128(sbase + off, 16, 1024),
                                    ptx::smem_desc_sw128(sbase + C::kOffQ + st * C::kTile + off, 16, 1024), idesc, kk > 0);
                 }
-                ptx::tc_commit(s_full + 8 * buf);
-                ptx::tc_commit(q_empty + 8 * st);
+                ptx::tc_commit(s_full + 8 * st);
             }
             __syncwarp();
         }
@@ -356,7 +407,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
         __syncwarp();
     } else {
         // ------------------------------------------- epilogue: one key per thread
-        const int wg = warp >> 2, key = (warp & 3) * 32 + lane;   // warpgroup wg takes steps wg, wg + 2, ...
+        const int wg = warp >> 2, key = (warp & 3) * 32 + lane;   // warpgroup wg takes steps wg, wg + kWgs, ...
         if (kFour) {
             // The K tile: codes and scales to bf16 (exact), in the swizzled
             // layout TMA would have given a bf16 page.
@@ -390,72 +441,103 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(k_full);
         }
-        float* nl_s = reinterpret_cast<float*>(smem + C::kOffNl) + wg * 2 * kTileRows;
-        const uint32_t t_s = tmem + wg * kTileRows + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
-        // The (negated) lse of row `key` of step s's rows, in log2 units.
-        auto load_nl = [&](int s) {
-            const int i = i0 + s / G * kTileRows + key;
-            return s < n_steps && i < r.qo_len ? -a.lse[(int64_t)(r.q_row0 + i) * a.Hq + g * G + s % G] * kLog2e : 0.f;
-        };
-        float total = 0.f, nl = load_nl(wg);
-        bool ok = true;
-        for (int s = wg; s < n_steps; s += 2) {
-            float* nl_b = nl_s + ((s >> 1) & 1) * kTileRows;
-            nl_b[key] = nl;
-            nl = load_nl(s + 2);
-            asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
-            // After a wait that ran out the warp only keeps the barriers' count.
-            ok = ok && wait_all(s_full + 8 * wg, (s >> 1) & 1);
-            if (!ok) continue;
-            ptx::tc_fence_after();
-            const int row0 = i0 + s / G * kTileRows, n_rows = r.qo_len - row0;
-            // Columns [lo, n_rows) count: rows that see the key, of this request.
-            const int lo = a.causal ? t0 + key - (prefix + row0) : 0;
-            const bool masked = n_rows < kTileRows || (a.causal && t0 + kTileKeys - 1 > prefix + row0);
-            float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+        // Adds 2^(s scale - lse) over 32 columns; masked: over those in [lo, hi) alone.
+        auto add_columns = [&](auto masked, const uint32_t (&v)[32], uint32_t nl_at, int lo, int hi) {
 #pragma unroll
-            for (int c = 0; c < kTileRows / 32; ++c) {
-                uint32_t v[32];
-                ptx::tmem_ld32(t_s + c * 32, v);
-                ptx::tc_wait_ld();
-                if (c == kTileRows / 32 - 1) {   // all of S is in registers: the next product may overwrite it
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(s_free + 8 * wg);
+            for (int k = 0; k < 32; k += 4) {
+                float4 l4;
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(l4.x), "=f"(l4.y), "=f"(l4.z), "=f"(l4.w) : "r"(nl_at + k * 4));
+                const float2 x0 = ptx::fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), scale2,
+                                            make_float2(l4.x, l4.y));
+                const float2 x1 = ptx::fma2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), scale2,
+                                            make_float2(l4.z, l4.w));
+                float2 p0 = make_float2(ptx::ex2(x0.x), ptx::ex2(x0.y));
+                float2 p1 = make_float2(ptx::ex2(x1.x), ptx::ex2(x1.y));
+                if constexpr (decltype(masked)::value) {
+                    const uint32_t n = (uint32_t)(hi - lo);   // unsigned: one comparison for both ends
+                    p0.x = (uint32_t)(k - lo) < n ? p0.x : 0.f;
+                    p0.y = (uint32_t)(k + 1 - lo) < n ? p0.y : 0.f;
+                    p1.x = (uint32_t)(k + 2 - lo) < n ? p1.x : 0.f;
+                    p1.y = (uint32_t)(k + 3 - lo) < n ? p1.y : 0.f;
                 }
-#pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    const float4 l4 = *reinterpret_cast<const float4*>(nl_b + c * 32 + k);
-                    const float2 x0 = ptx::fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), scale2,
-                                                make_float2(l4.x, l4.y));
-                    const float2 x1 = ptx::fma2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), scale2,
-                                                make_float2(l4.z, l4.w));
-                    float2 p0 = make_float2(ptx::ex2(x0.x), ptx::ex2(x0.y));
-                    float2 p1 = make_float2(ptx::ex2(x1.x), ptx::ex2(x1.y));
-                    if (masked) {
-                        const int col = c * 32 + k;
-                        p0.x = col >= lo && col < n_rows ? p0.x : 0.f;
-                        p0.y = col + 1 >= lo && col + 1 < n_rows ? p0.y : 0.f;
-                        p1.x = col + 2 >= lo && col + 2 < n_rows ? p1.x : 0.f;
-                        p1.y = col + 3 >= lo && col + 3 < n_rows ? p1.y : 0.f;
-                    }
-                    acc0 = ptx::add2(acc0, p0);
-                    acc1 = ptx::add2(acc1, p1);
-                }
+                acc0 = ptx::add2(acc0, p0);
+                acc1 = ptx::add2(acc1, p1);
             }
-            total += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+        };
+
+        float total = 0.f;
+        bool ok = true;
+        int s = wg, h = wg;   // this warpgroup's next step, and its head counted from the group's first
+        auto released = [&](int buf) {   // all of S has been read: a later product may overwrite it
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(s_free + 8 * buf);
+        };
+        for (int grp = 0, row0 = i0, h0 = 0; grp < n_groups; ++grp) {
+            ok = ok && wait_all(l_full + 8 * (grp & 1), (grp >> 1) & 1);
+            const int n = min(C::kHeads, G - h0), hi = min(kTileRows, r.qo_len - row0);
+            // Columns [lo, hi) count: rows that see the key, of this request.
+            // Over the warp's keys lo rises by 31.
+            const int lo = a.causal ? t0 + key - (prefix + row0) : 0;
+            const int lo0 = a.causal ? lo - lane : 0, lo31 = a.causal ? lo0 + 31 : 0;
+            for (; h < n; h += C::kWgs, s += C::kWgs) {
+                // After a wait that ran out the warp only keeps the barriers' count.
+                const int buf = s % C::kBufs;
+                ok = ok && wait_all(s_full + 8 * (s % C::kStages), (s / C::kStages) & 1);
+                if (!ok) continue;
+                ptx::tc_fence_after();
+                const uint32_t nl_at = ptx::smem_u32(nl_s) + (((grp & 1) * C::kHeads + h) * kTileRows) * 4;
+                const uint32_t t_s = t_lane + buf * kTileRows;
+                if (lo31 <= 0 && hi == kTileRows) {
+                    uint32_t v[2][32];   // 32 columns at a time, the next ones on their way
+                    ptx::tmem_ld32(t_s, v[0]);
+                    ptx::tc_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < kTileRows / 32; ++c) {
+                        if (c + 1 < kTileRows / 32) ptx::tmem_ld32(t_s + (c + 1) * 32, v[(c + 1) & 1]);
+                        add_columns(std::false_type{}, v[c & 1], nl_at + c * 128, 0, 32);
+                        if (c + 1 < kTileRows / 32) ptx::tc_wait_ld();
+                        if (c + 2 == kTileRows / 32) released(buf);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < kTileRows; c += 32) {
+                        if (c + 32 < kTileRows && c + 31 < lo0) continue;   // no key of the warp is seen
+                        uint32_t v[32];
+                        ptx::tmem_ld32(t_s + c, v);
+                        ptx::tc_wait_ld();
+                        if (c + 32 == kTileRows) released(buf);
+                        add_columns(std::true_type{}, v, nl_at + c * 4, max(0, lo - c), max(max(0, lo - c), min(32, hi - c)));
+                    }
+                }
+                total += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+                acc0 = acc1 = make_float2(0.f, 0.f);
+            }
+            h -= n;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(l_free + 8 * (grp & 1));
+            h0 += C::kHeads;
+            if (h0 >= G) {
+                h0 = 0;
+                row0 += kTileRows;
+            }
         }
         if (!ok && lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
-        // The two warpgroups' sums, in a fixed order.
-        if (wg == 1) sum_s[key] = total;
-        asm volatile("bar.sync 3, 256;" ::: "memory");
+        // The warpgroups' sums, in a fixed order.
+        sum_s[wg * kTileKeys + key] = total;
+        asm volatile("bar.sync 3, %0;" ::"n"(C::kEpilogueWarps * 32) : "memory");
         const int t = t0 + key;
         if (wg == 0 && t < r.kv_len) {
             const int page = a.page_table[r.page_base + t / P];
             if (page >= 0 && page < a.num_pages) {
                 const int64_t at = ((int64_t)page * a.Hkv + g) * P + t % P;
-                float w = total + sum_s[key];
+                float w = 0.f;
+#pragma unroll
+                for (int i = 0; i < C::kWgs; ++i) w += sum_s[i * kTileKeys + key];
                 if (a.decay != 0.f && t < prefix) w = fmaf(a.decay, a.prev[at], w);
                 a.weights[at] = w;
             }
@@ -468,7 +550,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
         ptx::mbar_wait(drain, 0);
         __syncwarp();
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 256);
+        ptx::tmem_dealloc(tmem, 512);
     }
 }
 
