@@ -450,7 +450,8 @@ ATTN_API attn_status attn_key_weights_kv4(attn_plan_t plan, const void* q, const
  * over a cache of m tokens (plan it with kv_len = m; keys carry their
  * positional encoding with them).
  *
- *   weights         fp32 [num_pages][Hkv][page_size] as attn_key_weights writes it
+ *   weights         fp32 [num_pages][Hkv][page_size] as attn_key_weights writes it,
+ *                   16-byte aligned
  *   kept            int32 [batch][Hkv][budget], device, output: the kept token
  *                   indices in order, -1 from m on
  *   page_table_out  device int32: pages that receive the kept tokens, request b's

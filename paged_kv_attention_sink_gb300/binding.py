@@ -209,7 +209,7 @@ class Plan:
         self.total_rows = int(qo[-1]) if len(qo) else 0
         handle = ctypes.c_void_p()
         ws_bytes = ctypes.c_size_t()
-        self._kv = kv.copy(), lpl.copy()
+        self._kv, self._kv_lens = (kv.copy(), lpl.copy()), None
         _check("attn_plan", lib.attn_plan(
             qo.ctypes.data, kv.ctypes.data, _ptr(page_table), lpl.ctypes.data, self.batch, num_qo_heads,
             num_kv_heads, head_dim, page_size, int(self.causal), self.sm_scale, int(num_pages),
@@ -236,9 +236,12 @@ class Plan:
     @property
     def kv_lens(self) -> np.ndarray:
         """Cached tokens of each request."""
-        kv, lpl = self._kv
-        pages = np.diff(kv)
-        return np.where(pages > 0, (pages - 1) * self.page_size + lpl[:self.batch], 0)
+        if self._kv_lens is None:
+            kv, lpl = self._kv
+            pages = np.diff(kv)
+            self._kv_lens = np.where(pages > 0, (pages - 1) * self.page_size + lpl[:self.batch], 0)
+            self._kv_lens.flags.writeable = False
+        return self._kv_lens
 
     def info(self) -> dict:
         info = PlanInfo()
@@ -392,7 +395,7 @@ class Plan:
         if page_table_out is not None:
             if kv_out.dim() == 0 or weights_out.shape[0] != kv_out.shape[0]:
                 raise ValueError("kv_out and weights_out must have the same number of pages")
-            pages = sum(-(-int(n) // P) for n in self.evicted_lens(budget))
+            pages = int(((self.evicted_lens(budget) + (P - 1)) // P).sum())
             _check_cuda(dev, page_table_out=(page_table_out, torch.int32, (pages,)),
                         kv_out=(kv_out, *self._cache_spec(four, kv_out.shape[0])),
                         weights_out=(weights_out, torch.float32, (kv_out.shape[0], Hkv, P)))

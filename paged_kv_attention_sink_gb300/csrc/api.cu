@@ -339,7 +339,7 @@ attn_status evict(attn_plan_t plan, bool four, const float* weights, const void*
     if (budget <= 0 || recent < 0 || recent > budget) return ATTN_ERR_INVALID_ARG;
     if (plan->batch == 0) return ATTN_OK;
     if (!weights || !pool || !kept || !pool_out || !weights_out) return ATTN_ERR_INVALID_ARG;
-    if (!aligned16(pool) || !aligned16(pool_out) || !aligned4(weights) || !aligned4(weights_out) || !aligned4(kept))
+    if (!aligned16(pool) || !aligned16(pool_out) || !aligned16(weights) || !aligned4(weights_out) || !aligned4(kept))
         return ATTN_ERR_INVALID_ARG;
     if (!page_table_out && (pool_out != pool || weights_out != weights || num_pages_out != plan->num_pages))
         return ATTN_ERR_INVALID_ARG;

@@ -6,18 +6,25 @@
 // Heads choose independently; kept tokens stay in order and become tokens
 // 0 .. keep - 1 of the request, in new pages or in place.
 //
-// Select: one CTA per (request, KV head).  Weights map to unsigned keys of the
-// same order; a radix selection, a byte of the key at a time, finds the
-// threshold key and how many tokens that equal it are kept, and one ordered
-// scan then writes the kept indices (and moves the weights).  Move: copies the
-// kept tokens' K and V rows.  Both are bound by memory: 4 bytes per token and
-// head are read, and the kept rows once read and once written.
+// Select: one CTA per (request, KV head).  The weights are read into shared
+// memory once (in chunks, again for each pass, where a row does not fit) and map
+// to unsigned keys of the same order; a radix selection, 11 bits of the key at
+// a time, finds the threshold key and how many tokens that equal it are kept.
+// Then every warp counts the kept tokens of its own range of tokens and, from
+// the sum of the ranges before it, writes their indices in order (and moves
+// their weights).  Move: a warp looks up 32 kept tokens at a time, one per lane,
+// and copies their K and V rows with all loads on their way at once.  Both are
+// bound by memory: 4 bytes per token and head are read, and the kept rows once
+// read and once written.
 //
 // In place, token j comes from index kept[j] >= j.  A CTA owns one (request,
 // head, K/V) and moves the rows in ascending order, a chunk at a time, all of
 // a chunk read before any of it is written: every row it overwrites has been
-// read before.
+// read before.  The weights are moved the same way, chunk by chunk.
 #include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "attn_internal.h"
 #include "kernels.h"
@@ -26,9 +33,8 @@
 namespace attn {
 namespace {
 
-constexpr int kSelectThreads = 512;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 4;   // 16-byte pieces a thread holds between a chunk's reads and its writes
+constexpr int kDigitBits = 11, kDigits = 1 << kDigitBits;   // radix passes over 11, 11 and 10 bits
 
 struct EvictArgs {
     const RequestInfo* requests;
@@ -40,7 +46,8 @@ struct EvictArgs {
     float* weights_out;
     int32_t* kept;                   // [batch][Hkv][budget]
     int32_t* err;
-    int32_t batch, Hkv, P, D, budget, recent, num_pages, num_pages_out;
+    int32_t batch, Hkv, page_log2, budget, recent, num_pages, num_pages_out;
+    int32_t chunk;                   // select: tokens held in shared memory at a time
 };
 
 // Unsigned keys in the weights' order: NaN lowest, -0 equal to +0.
@@ -50,198 +57,322 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// First output page slot of request b (pages of the requests before it); all
-// threads of the block take part.
-__device__ int64_t out_page_base(const EvictArgs& a, int b, int64_t* sh) {
+constexpr uint32_t kZeroKey = 0x80000000u;   // of a weight of 0
+
+// First output page slot of request b (pages of the requests before it); the
+// lanes of a warp share the work.
+__device__ int64_t out_page_base(const EvictArgs& a, int b, int lane) {
+    if (!a.page_table_out) return 0;
     int64_t n = 0;
-    for (int i = threadIdx.x; i < b; i += blockDim.x)
-        n += (min(a.requests[i].kv_len, a.budget) + a.P - 1) / a.P;
+    const int P = 1 << a.page_log2;
+    for (int i = lane; i < b; i += 32) n += (min(a.requests[i].kv_len, a.budget) + P - 1) >> a.page_log2;
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = n;
-    __syncthreads();
-    n = 0;
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) n += sh[w];
-    __syncthreads();
     return n;
 }
 
 // Output page id of token j of request r; -1 (recorded) when out of range.
 __device__ __forceinline__ int out_page(const EvictArgs& a, const RequestInfo& r, int64_t base, int j) {
-    const int page = a.page_table_out ? a.page_table_out[base + j / a.P] : a.page_table[r.page_base + j / a.P];
+    const int slot = j >> a.page_log2;
+    const int page = a.page_table_out ? a.page_table_out[base + slot] : a.page_table[r.page_base + slot];
     if (page >= 0 && page < a.num_pages_out) return page;
     atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
     return -1;
 }
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictArgs a) {
-    constexpr int kWarps = kSelectThreads / 32;
-    __shared__ int hist[256];
-    __shared__ int64_t sh_base[kWarps];
-    __shared__ uint32_t sh_scan[kWarps];
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a) {
+    constexpr int kWarps = kThreads / 32;
+    extern __shared__ __align__(16) float w_s[];   // [chunk] weights
+    __shared__ int hist[kDigits];
+    __shared__ int2 sh_count[kWarps];     // a warp's range: larger keys, equal keys
+    __shared__ int sh_total[kWarps];
     __shared__ int sh_bucket, sh_above;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // The move kernel may be launched now; it waits for this grid to finish.
+    asm volatile("griddepcontrol.launch_dependents;");
     const int b = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv;
     const RequestInfo r = a.requests[b];
-    const int n = r.kv_len, keep = min(n, a.budget);
+    const int n = r.kv_len, keep = min(n, a.budget), P = 1 << a.page_log2;
     int32_t* kept = a.kept + ((int64_t)b * a.Hkv + g) * a.budget;
-    for (int j = keep + tid; j < a.budget; j += kSelectThreads) kept[j] = -1;
+    for (int j = keep + tid; j < a.budget; j += kThreads) kept[j] = -1;
     if (n == 0) return;
-    const int64_t base = a.page_table_out ? out_page_base(a, b, sh_base) : 0;
+    const int64_t base = out_page_base(a, b, lane);
 
     const int old = n - min(n, a.recent);        // tokens [0, old) compete
-    int want = keep - (n - old);                 // that many of them are kept
-    auto weight = [&](int t) {
-        const int page = a.page_table[r.page_base + t / a.P];
-        if (page < 0 || page >= a.num_pages) {
-            atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
-            return __uint_as_float(0x7FC00000u);
-        }
-        return a.weights[((int64_t)page * a.Hkv + g) * a.P + t % a.P];
-    };
+    const int want = keep - (n - old);           // that many of them are kept
+    const bool select = want > 0 && want < old;  // else all of them are, or none
 
-    // Threshold: the want-th largest key of the old tokens, byte by byte.
+    // Tokens [t0, t1) into shared memory, four (of one page) at a time; t0 is a
+    // multiple of 4, and so is the chunk.
+    auto load = [&](int t0, int t1) {
+        constexpr int kBatch = 4;   // lookups, then loads, on their way together
+        __syncthreads();            // the last chunk's readers are done
+        for (int q0 = t0 + tid * 4; q0 < t1; q0 += kBatch * kThreads * 4) {
+            int page[kBatch];
+            float4 w[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int t = q0 + k * kThreads * 4;
+                page[k] = t < t1 ? a.page_table[r.page_base + (t >> a.page_log2)] : 0;
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int t = q0 + k * kThreads * 4;
+                w[k] = make_float4(nanf(""), nanf(""), nanf(""), nanf(""));
+                if (t >= t1) continue;
+                if (page[k] >= 0 && page[k] < a.num_pages)
+                    w[k] = *reinterpret_cast<const float4*>(a.weights + ((int64_t)page[k] * a.Hkv + g) * P + (t & (P - 1)));
+                else atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (q0 + k * kThreads * 4 < t1) *reinterpret_cast<float4*>(w_s + q0 + k * kThreads * 4 - t0) = w[k];
+        }
+        __syncthreads();
+    };
+    const bool fits = n <= a.chunk;
+    if (fits) load(0, n);
+
+    // Threshold: the want-th largest key of the old tokens, digit by digit.
     uint32_t prefix = 0;
     int ties = want;                             // of the tokens that match the prefix, still to be kept
-    if (want > 0 && want < old) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
+    if (select) {
+        for (int shift = 32 - kDigitBits;; shift = max(0, shift - kDigitBits)) {
+            const int bits = shift == 0 ? 32 - 2 * kDigitBits : kDigitBits;
+            for (int i = tid; i < kDigits; i += kThreads) hist[i] = 0;
             __syncthreads();
-            for (int t = tid; t < old; t += kSelectThreads) {
-                const uint32_t k = order_key(weight(t));
-                if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
+            for (int t0 = 0; t0 < old; t0 += a.chunk) {
+                const int t1 = min(old, t0 + a.chunk);
+                if (!fits) load(t0, t1);
+                const uint32_t mask = (1u << bits) - 1, want_high = shift + bits == 32 ? 0 : prefix >> (shift + bits);
+                int zeros = 0;   // weights of exactly 0 (keys never attended to) are many: one addition for all of a warp's
+                for (int t = t0 + tid * 4; t < t1; t += kThreads * 4) {
+                    const float4 w = *reinterpret_cast<const float4*>(w_s + t - t0);
+                    const float v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t k = order_key(v[e]);
+                        if (t + e >= t1 || (shift + bits < 32 && k >> (shift + bits) != want_high)) continue;
+                        if (k == kZeroKey) ++zeros;
+                        else atomicAdd(&hist[(k >> shift) & mask], 1);
+                    }
+                }
+                zeros = __reduce_add_sync(0xffffffffu, zeros);
+                if (lane == 0 && zeros) atomicAdd(&hist[(kZeroKey >> shift) & mask], zeros);
             }
             __syncthreads();
-            if (warp == 0) {   // the bucket the ties-th largest falls into; 8 buckets a lane, from the top
-                int c[8], sum = 0;
+            // The bucket that the ties-th largest falls into: each thread sums a
+            // run of buckets, from the top; then the runs before it.
+            constexpr int kRun = (kDigits + kThreads - 1) / kThreads;
+            int c[kRun], sum = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - (lane * 8 + i)];
-                int inc = sum;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += v;
-                }
-                int above = inc - sum;
-                if (above < ties && inc >= ties) {
+            for (int i = 0; i < kRun; ++i) {
+                const int d = kDigits - 1 - (tid * kRun + i);
+                sum += c[i] = d >= 0 ? hist[d] : 0;
+            }
+            int inc = sum;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (lane == 31) sh_total[warp] = inc;
+            __syncthreads();
+            int above = inc - sum;
+            for (int w = 0; w < warp; ++w) above += sh_total[w];
+            if (above < ties && above + sum >= ties) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (above < ties && above + c[i] >= ties) {
-                            sh_bucket = 255 - (lane * 8 + i);
-                            sh_above = above;
-                            break;
-                        }
-                        above += c[i];
+                for (int i = 0; i < kRun; ++i) {
+                    if (above < ties && above + c[i] >= ties) {
+                        sh_bucket = kDigits - 1 - (tid * kRun + i);
+                        sh_above = above;
+                        break;
                     }
+                    above += c[i];
                 }
             }
             __syncthreads();
             prefix |= (uint32_t)sh_bucket << shift;
             ties -= sh_above;
+            if (shift == 0) break;
+            __syncthreads();
         }
     }
-    // keys > prefix are kept, of those equal to it the first `ties`; all old
-    // tokens when want == old, none when want == 0.
-    const bool all = want == old, none = want == 0;
-
-    // Ordered scan: ranks of the kept tokens, chunk by chunk; low half counts
-    // larger keys, high half equal ones.
+    // Kept: keys > prefix, and of those equal to it the first `ties`.
+    const int all_ties = select ? ties : 0;
     int greater = 0, equal = 0;
-    for (int t0 = 0; t0 < n; t0 += kSelectThreads) {
-        const int t = t0 + tid;
-        const float w = t < n ? weight(t) : 0.f;
-        uint32_t gt = 0, eq = 0;
-        if (t >= old) {
-            gt = t < n;
-        } else if (all) {
-            gt = 1;
-        } else if (!none) {
-            const uint32_t k = order_key(w);
-            gt = k > prefix;
-            eq = k == prefix;
-        }
-        uint32_t inc = gt | (eq << 16);
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        if (lane == 31) sh_scan[warp] = inc;
-        __syncthreads();                          // also: the whole chunk's weights are read
-        uint32_t before = inc - (gt | (eq << 16)), total = 0;
+    for (int t0 = 0; t0 < n; t0 += a.chunk) {
+        const int t1 = min(n, t0 + a.chunk);
+        if (!fits) load(t0, t1);
+        // This warp's range of the chunk, in whole steps of 128 tokens, four a lane.
+        const int per = ((t1 - t0 + 127) / 128 + kWarps - 1) / kWarps * 128;
+        const int r0 = min(t1, t0 + warp * per), r1 = min(t1, r0 + per);
+        // Bits 0-3: token t + e is kept by its key; 4-7: its key equals the threshold.
+        auto classify = [&](int t, const float (&v)[4]) {
+            uint32_t c = 0;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) before += sh_scan[i];
-            total += sh_scan[i];
+            for (int e = 0; e < 4; ++e) {
+                if (t + e >= r1) continue;
+                if (t + e >= old || want == old) {
+                    c |= 1u << e;
+                } else if (select) {
+                    const uint32_t k = order_key(v[e]);
+                    c |= k > prefix ? 1u << e : k == prefix ? 16u << e : 0u;
+                }
+            }
+            return c;
+        };
+        auto four = [&](int t, float (&v)[4]) {
+            const float4 w = t < r1 ? *reinterpret_cast<const float4*>(w_s + t - t0) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+        };
+        int n_gt = 0, n_eq = 0;
+        for (int t = r0 + lane * 4; t < r1; t += 128) {
+            float v[4];
+            four(t, v);
+            const uint32_t c = classify(t, v);
+            n_gt += __popc(c & 15u);
+            n_eq += __popc(c >> 4);
         }
-        const int gt_before = greater + (int)(before & 0xFFFF), eq_before = equal + (int)(before >> 16);
-        if (gt || (eq && eq_before < ties)) {
-            const int j = gt_before + min(eq_before, all || none ? 0 : ties);
-            kept[j] = t;
-            const int page = out_page(a, r, base, j);
-            if (page >= 0) a.weights_out[((int64_t)page * a.Hkv + g) * a.P + j % a.P] = w;
-        }
-        greater += (int)(total & 0xFFFF);
-        equal += (int)(total >> 16);
+        n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+        n_eq = __reduce_add_sync(0xffffffffu, n_eq);
+        if (lane == 0) sh_count[warp] = make_int2(n_gt, n_eq);
         __syncthreads();
+        int before_gt = greater, before_eq = equal;
+        for (int w = 0; w < kWarps; ++w) {
+            const int2 c = sh_count[w];
+            if (w < warp) {
+                before_gt += c.x;
+                before_eq += c.y;
+            }
+            greater += c.x;
+            equal += c.y;
+        }
+        for (int s = r0; s < r1; s += 128) {
+            const int t = s + lane * 4;
+            float v[4];
+            four(t, v);
+            const uint32_t c = classify(t, v);
+            uint32_t inc = __popc(c & 15u) | __popc(c >> 4) << 16;
+            const uint32_t own = inc;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += u;
+            }
+            int gt = before_gt + (int)((inc - own) & 0xFFFF), eq = before_eq + (int)((inc - own) >> 16);
+            int j[4], page[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool is_gt = c >> e & 1, is_eq = c >> (4 + e) & 1;
+                j[e] = is_gt || (is_eq && eq < all_ties) ? gt + min(eq, all_ties) : -1;
+                gt += is_gt;
+                eq += is_eq;
+                page[e] = j[e] >= 0 ? out_page(a, r, base, j[e]) : -1;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (j[e] < 0) continue;
+                kept[j[e]] = t + e;
+                if (page[e] >= 0) a.weights_out[((int64_t)page[e] * a.Hkv + g) * P + (j[e] & (P - 1))] = v[e];
+            }
+            const uint32_t total = __shfl_sync(0xffffffffu, inc, 31);
+            before_gt += (int)(total & 0xFFFF);
+            before_eq += (int)(total >> 16);
+        }
+        __syncthreads();   // sh_count is written again
     }
 }
 
-// grid (requests x KV heads x K/V, splits); a split takes every gridDim.y-th
-// chunk of rows (one split in place).  kRowPieces: 16-byte pieces of a row's
-// values; kFour: the rows also have D / 16 scale bytes.
-template <int D, bool kFour>
+// grid (requests x KV heads x K/V, splits): the warps of a split's CTAs take
+// every gridDim.y-th run of 32 kept tokens per warp (one split in place).
+// kFour: the rows also have D / 16 scale bytes.
+template <int D, bool kFour, bool kInPlace>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
-    constexpr int kPieces = (kFour ? D / 2 : D * 2) / 16;
-    constexpr int kChunk = kMoveThreads * kMoveUnroll / kPieces;   // rows
-    __shared__ int64_t sh_base[kMoveThreads / 32];
+    constexpr int kPieces = (kFour ? D / 2 : D * 2) / 16;   // 16-byte pieces of a row's values
+    constexpr int kRows = 32 / kPieces;                     // rows a warp copies per instruction
+    using Scales = std::conditional_t<D == 64, uint32_t, uint2>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // kept is complete and visible
     const int half = blockIdx.x & 1, g = (blockIdx.x >> 1) % a.Hkv, b = (blockIdx.x >> 1) / a.Hkv;
     const RequestInfo r = a.requests[b];
-    const int keep = min(r.kv_len, a.budget);
+    const int keep = min(r.kv_len, a.budget), P = 1 << a.page_log2;
     if (keep == 0) return;
-    const int64_t base = a.page_table_out ? out_page_base(a, b, sh_base) : 0;
+    const int64_t base = out_page_base(a, b, lane);
     const int32_t* kept = a.kept + ((int64_t)b * a.Hkv + g) * a.budget;
 
     auto row_at = [&](int64_t page, int row) -> int64_t {   // byte offset of a row's values
+        const int64_t block = (page * 2 + half) * a.Hkv + g;
         if constexpr (kFour)
-            return kv4::sub_offset(page, half, a.Hkv, g, a.P, row, kv4_sub_bytes(D)) + (row % kKv4Tokens) * (D / 2);
+            return ((block << (a.page_log2 - 4)) + row / kKv4Tokens) * kv4_sub_bytes(D) + (row % kKv4Tokens) * (D / 2);
         else
-            return ((((page * 2 + half) * a.Hkv + g) * a.P) + row) * (D * 2);
+            return ((block << a.page_log2) + row) * (D * 2);
     };
-    for (int j0 = blockIdx.y * kChunk; j0 < keep; j0 += gridDim.y * kChunk) {
-        uint4 x[kMoveUnroll];
-        uint32_t sc[kMoveUnroll];
-        int64_t dst[kMoveUnroll], dst_sc[kMoveUnroll];
-#pragma unroll
-        for (int k = 0; k < kMoveUnroll; ++k) {
-            const int idx = k * kMoveThreads + threadIdx.x;
-            const int j = j0 + idx / kPieces, piece = idx % kPieces;
-            dst[k] = -1;
-            if (j >= keep) continue;
+    constexpr int kChunk = kMoveThreads;                    // rows of a CTA's step, 32 a warp
+    for (int c0 = blockIdx.y * kChunk; c0 < keep; c0 += gridDim.y * kChunk) {
+        // Lane l looks up row l of the warp's 32.
+        const int j = c0 + warp * 32 + lane;
+        int64_t src = -1, dst = -1;
+        Scales sc = {};
+        int64_t dst_sc = -1;
+        if (j < keep) {
             const int t = kept[j];
-            const int page = a.page_table[r.page_base + t / a.P];
+            const int page = a.page_table[r.page_base + (t >> a.page_log2)];
             const int to = out_page(a, r, base, j);
             if (page < 0 || page >= a.num_pages || to < 0) {
                 atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
-                continue;
+            } else {
+                const int from_row = t & (P - 1), to_row = j & (P - 1);
+                src = row_at(page, from_row);
+                dst = row_at(to, to_row);
+                if constexpr (kFour) {
+                    const int in = from_row % kKv4Tokens, out = to_row % kKv4Tokens;
+                    sc = *reinterpret_cast<const Scales*>(a.pool + src - in * (D / 2) + 8 * D + in * (D / 16));
+                    dst_sc = dst - out * (D / 2) + 8 * D + out * (D / 16);
+                }
             }
-            const int64_t src = row_at(page, t % a.P);
-            x[k] = *reinterpret_cast<const uint4*>(a.pool + src + piece * 16);
-            dst[k] = row_at(to, j % a.P);
-            if constexpr (kFour) {
-                // 16 code bytes are two groups: their two scales go along.
-                const int in = t % kKv4Tokens, out = j % kKv4Tokens;
-                sc[k] = *reinterpret_cast<const uint16_t*>(a.pool + src - in * (D / 2) + 8 * D + in * (D / 16) + 2 * piece);
-                dst_sc[k] = dst[k] - out * (D / 2) + 8 * D + out * (D / 16) + 2 * piece;
-            }
-            dst[k] += piece * 16;
         }
-        __syncthreads();
+        uint4 x[kPieces];
+        int64_t to[kPieces];
 #pragma unroll
-        for (int k = 0; k < kMoveUnroll; ++k) {
-            if (dst[k] < 0) continue;
-            *reinterpret_cast<uint4*>(a.pool_out + dst[k]) = x[k];
-            if constexpr (kFour) *reinterpret_cast<uint16_t*>(a.pool_out + dst_sc[k]) = (uint16_t)sc[k];
+        for (int k = 0; k < kPieces; ++k) {
+            const int row = k * kRows + lane / kPieces;
+            const int64_t from = __shfl_sync(0xffffffffu, src, row);
+            to[k] = __shfl_sync(0xffffffffu, dst, row);
+            if (from >= 0) x[k] = *reinterpret_cast<const uint4*>(a.pool + from + lane % kPieces * 16);
         }
-        __syncthreads();   // in place: the next chunk may read what this one wrote over only after it is done
+        if (kInPlace) __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k)
+            if (to[k] >= 0) *reinterpret_cast<uint4*>(a.pool_out + to[k] + lane % kPieces * 16) = x[k];
+        if (kFour && dst_sc >= 0) *reinterpret_cast<Scales*>(a.pool_out + dst_sc) = sc;
+        if (kInPlace) __syncthreads();   // the next step may read what this one wrote over only after it is done
     }
+}
+
+template <int kThreads>
+attn_status launch_select(const EvictArgs& a, int longest, int most, cudaStream_t stream) {
+    EvictArgs x = a;
+    x.chunk = std::max(32, std::min((longest + 31) / 32 * 32, most));
+    static std::atomic<bool> configured[kMaxDevices];
+    if (once_per_device(configured, [&] {
+            return cudaFuncSetAttribute(evict_select_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, most * 4);
+        }) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+    evict_select_kernel<kThreads><<<a.batch * a.Hkv, kThreads, x.chunk * 4, stream>>>(x);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+template <int D, bool kFour, bool kInPlace>
+attn_status launch_move(const EvictArgs& a, int splits, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.batch * a.Hkv * 2, splits);
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see griddepcontrol in both kernels
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel<D, kFour, kInPlace>, a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace
@@ -262,23 +393,33 @@ attn_status launch_evict(attn_plan_s* plan, bool four, const float* weights, con
     a.err = reinterpret_cast<int32_t*>(plan->ws + plan->layout.err);
     a.batch = plan->batch;
     a.Hkv = plan->Hkv;
-    a.P = plan->P;
-    a.D = plan->D;
+    a.page_log2 = 31 - __builtin_clz(plan->P);
     a.budget = budget;
     a.recent = recent;
     a.num_pages = plan->num_pages;
     a.num_pages_out = num_pages_out;
-    evict_select_kernel<<<plan->batch * plan->Hkv, kSelectThreads, 0, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-    const dim3 grid(plan->batch * plan->Hkv * 2, page_table_out ? 8 : 1);
+    a.chunk = 0;
+    int32_t longest = 0;
+    for (const RequestInfo& r : plan->requests) longest = std::max(longest, r.kv_len);
+    // With at most a CTA per SM, each takes all of an SM's threads and shared
+    // memory; with more, a fourth of it.
+    int32_t sms = 0;
+    if (!current_sm_count(&sms)) return ATTN_ERR_CUDA;
+    const bool few = (int64_t)plan->batch * plan->Hkv <= sms;
+    const attn_status st = few ? launch_select<1024>(a, longest, 48 * 1024, stream)
+                               : launch_select<512>(a, longest, 11 * 1024, stream);
+    if (st != ATTN_OK) return st;
+    // Out of place, enough CTAs for some eight per SM.
+    const int64_t rows = std::min<int64_t>(longest, budget), most = (rows + kMoveThreads - 1) / kMoveThreads;
+    const int64_t want = std::max<int64_t>(1, (int64_t)sms * 8 / ((int64_t)plan->batch * plan->Hkv * 2));
+    const int splits = page_table_out ? (int)std::max<int64_t>(1, std::min(most, want)) : 1;
+    const bool in_place = !page_table_out;
     if (plan->D == 64) {
-        if (four) evict_move_kernel<64, true><<<grid, kMoveThreads, 0, stream>>>(a);
-        else evict_move_kernel<64, false><<<grid, kMoveThreads, 0, stream>>>(a);
-    } else {
-        if (four) evict_move_kernel<128, true><<<grid, kMoveThreads, 0, stream>>>(a);
-        else evict_move_kernel<128, false><<<grid, kMoveThreads, 0, stream>>>(a);
+        if (four) return in_place ? launch_move<64, true, true>(a, splits, stream) : launch_move<64, true, false>(a, splits, stream);
+        return in_place ? launch_move<64, false, true>(a, splits, stream) : launch_move<64, false, false>(a, splits, stream);
     }
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    if (four) return in_place ? launch_move<128, true, true>(a, splits, stream) : launch_move<128, true, false>(a, splits, stream);
+    return in_place ? launch_move<128, false, true>(a, splits, stream) : launch_move<128, false, false>(a, splits, stream);
 }
 
 }  // namespace attn
