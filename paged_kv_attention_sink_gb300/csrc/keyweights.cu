@@ -59,10 +59,11 @@ struct StepWeightCfg {
     static constexpr int kStages = kFour || D == 64 ? 4 : 3;
     static constexpr int kSubs = kTile / kBlockTokens;
     static constexpr int kSub = kFour ? kv4_sub_bytes(D) : kBlockTokens * D * 2;   // K of 16 tokens
-    static constexpr int kStageBytes = kSubs * kSub;
+    static constexpr int kPrev = kSubs * kSub;                           // then the tokens' previous weights
+    static constexpr int kStageBytes = kPrev + kTile * 4;
     static constexpr int kPipeBytes = kWarps * kStages * kStageBytes;
     static constexpr int kPageBytes = (kDecodeMaxChunkPages * 4 + 15) / 16 * 16;
-    static constexpr int kSmem = 128 + kPipeBytes + kPageBytes;
+    static constexpr int kSmem = 128 + kPipeBytes + 2 * kPageBytes;
 };
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -118,6 +119,11 @@ key_weights_step_kernel(const KeyWeightArgs a) {
     const int first_page = u.tok_begin >> a.page_log2;
     const int n_pages = ((u.tok_end - 1) >> a.page_log2) - first_page + 1;
     load_sixteens(first_s, a.page_table + u.page_base + first_page, n_pages, a.num_pages, a.Hkv, u.kv_head, a.page_log2, a.err);
+    uint32_t* block_s = first_s + C::kPageBytes / 4;   // (page, head) block of the weights
+    for (int i = tid; i < n_pages; i += blockDim.x) {
+        const int page = a.page_table[u.page_base + first_page + i];
+        block_s[i] = page < 0 || page >= a.num_pages ? kBadPage : (uint32_t)(page * a.Hkv + u.kv_head);
+    }
     __syncthreads();
 
     const uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
@@ -126,9 +132,23 @@ key_weights_step_kernel(const KeyWeightArgs a) {
     const int n_it = n_tiles > warp ? (n_tiles - warp + C::kWarps - 1) / C::kWarps : 0;
     auto tile_tok = [&](int it) { return u.tok_begin + (warp + it * C::kWarps) * C::kTile; };
     const TileSource src = tile_source<D, kFour, C::kTile>(a.pool, first_s, first_page, a.page_log2, a.Hkv, lane);
+    // Each lane takes one of a tile's 32 tokens: sixteen tq >> 1, row
+    // (tq & 1) * 8 + its own.  slot: where its weight lies, or -1.
+    const int row = kFour ? kv4_row(gq) : gq;
+    const int mine = (tq >> 1) * kBlockTokens + (tq & 1) * 8 + row;
+    auto slot = [&](int tok) -> int64_t {
+        const uint32_t block = tok < u.tok_end ? block_s[(tok >> a.page_log2) - first_page] : kBadPage;
+        return block == kBadPage ? -1 : ((int64_t)block << a.page_log2) + (tok & (P - 1));
+    };
+    // The one new token of a decode request, its last, has no previous weight.
+    const int prev_end = a.decay == 0.f ? 0 : u.tok_end - (u.chunk == u.n_chunks - 1);
     auto issue = [&](int it, int s) {   // one group per stage, empty past the end
         const uint32_t dst = ring_u32 + s * C::kStageBytes;
         if (it < n_it) {
+            const int64_t at = slot(tile_tok(it) + mine);
+            const bool old = at >= 0 && tile_tok(it) + mine < prev_end;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                         ::"r"(dst + C::kPrev + lane * 4), "l"(a.prev + (old ? at : 0)), "r"(old ? 4 : 0) : "memory");
             if constexpr (kFour) kv4_stage_load<D, C::kTile, 1>(src, tile_tok(it), u.tok_end, dst, lane);
             else bf16_stage_load<D, C::kTile>(src, tile_tok(it), u.tok_end, dst, lane);
         }
@@ -171,25 +191,7 @@ key_weights_step_kernel(const KeyWeightArgs a) {
             for (int e = 0; e < 4; ++e) w[e >> 1] += ptx::ex2(fmaf(s[nt][e], qt[nt].mult[e & 1], qt[nt].nl[e & 1]));
     };
 
-    // Each lane writes one of the tile's 32 tokens: sixteen tq >> 1, row
-    // (tq & 1) * 8 + its own.
-    const int row = kFour ? kv4_row(gq) : gq;
-    const int mine = (tq >> 1) * kBlockTokens + (tq & 1) * 8 + row;
     for (int it = 0, s = 0; it < n_it; ++it) {
-        const int tok = tile_tok(it) + mine;
-        // This lane's slot, and its previous weight on the way while the tile arrives.
-        int64_t at = -1;
-        float before = 0.f;
-        if (tok < u.tok_end) {
-            const uint32_t first = first_s[(tok >> a.page_log2) - first_page];
-            if (first != kBadPage) {
-                // weights[page][head][row]: (page * Hkv + head) * P + row, from (page * 2 Hkv + head) * P / 16.
-                const uint32_t block = first >> (a.page_log2 - 4);
-                at = ((int64_t)(block / (2 * a.Hkv) * a.Hkv + u.kv_head) << a.page_log2) + (tok & (P - 1));
-                const bool is_new = u.chunk == u.n_chunks - 1 && tok == u.tok_end - 1;
-                if (a.decay != 0.f && !is_new) before = a.decay * a.prev[at];
-            }
-        }
         cp_async_wait<C::kStages - 1>();
         __syncwarp();   // every lane's copies of this stage have landed
         const uint8_t* kt = ring + s * C::kStageBytes;
@@ -206,18 +208,21 @@ key_weights_step_kernel(const KeyWeightArgs a) {
                 }
             }
         }
+        const float before = *reinterpret_cast<const float*>(kt + C::kPrev + lane * 4);
         __syncwarp();   // every lane has read the stage
         issue(it + C::kStages, s);
         s = s + 1 == C::kStages ? 0 : s + 1;
+        // Sums over the four lanes of a key row, each of which ends with one token's.
+        float v[C::kSubs];
 #pragma unroll
-        for (int sub = 0; sub < C::kSubs; ++sub)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                w[sub][r] += __shfl_xor_sync(0xffffffffu, w[sub][r], 1);
-                w[sub][r] += __shfl_xor_sync(0xffffffffu, w[sub][r], 2);
-            }
-        const float mine_w = tq < 2 ? (tq == 0 ? w[0][0] : w[0][1]) : (tq == 2 ? w[1][0] : w[1][1]);
-        if (at >= 0) a.weights[at] = mine_w + before;
+        for (int sub = 0; sub < C::kSubs; ++sub) {
+            const float keep = tq & 1 ? w[sub][1] : w[sub][0], give = tq & 1 ? w[sub][0] : w[sub][1];
+            v[sub] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+        }
+        const float keep = tq & 2 ? v[1] : v[0], give = tq & 2 ? v[0] : v[1];
+        const float sum = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+        const int64_t at = slot(tile_tok(it) + mine);
+        if (at >= 0) a.weights[at] = fmaf(a.decay, before, sum);
     }
 }
 
@@ -608,7 +613,7 @@ attn_status launch_key_weights(attn_plan_s* plan, bool four, const void* q, cons
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.lse = lse;
     a.pool = static_cast<const uint8_t*>(pool);
-    a.prev = prev;
+    a.prev = prev ? prev : weights;   // a valid address; not read when decay is 0
     a.weights = weights;
     a.err = reinterpret_cast<int32_t*>(plan->ws + plan->layout.err);
     a.Hq = plan->Hq;
