@@ -133,23 +133,22 @@ def _stream_ptr(stream=None):
     return torch.cuda.current_stream().cuda_stream
 
 
-def _check_cuda(device, **tensors):
-    """Each given tensor must be a contiguous CUDA tensor of its dtype and shape
-    on `device` (specs: name=(tensor, dtype, shape); shape None: any)."""
-    for name, (t, dt, shape) in tensors.items():
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dt and t.is_contiguous()):
-            raise TypeError(f"{name} must be a contiguous {dt} CUDA tensor")
-        if shape is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {list(shape)}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _check_cuda(device, name, t, dtype, shape=None):
+    """t must be a contiguous CUDA tensor of dtype (and shape) on `device`, an ordinal."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous {dtype} CUDA tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
 
 
 def _launch_on(device, stream, fn_name, *args):
-    """Call fn_name(*args, stream) with `device` current: a kernel runs, and the
-    current stream is looked up, on the device that holds the tensors."""
-    fn = getattr(load_library(), fn_name)
-    if device.index != torch.cuda.current_device():
+    """Call fn_name(*args, stream) with `device` (an ordinal) current: a kernel
+    runs, and the current stream is looked up, on the device that holds the
+    tensors."""
+    fn = getattr(_lib, fn_name)
+    if device != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _check(fn_name, fn(*args, _stream_ptr(stream)))
     _check(fn_name, fn(*args, _stream_ptr(stream)))
@@ -323,11 +322,18 @@ class Plan:
         return kv4_cache_shape(self.num_pages if num_pages is None else num_pages, self.num_kv_heads, self.page_size,
                                self.head_dim)
 
+    def _cache_spec(self, four, num_pages=None):
+        n = self.num_pages if num_pages is None else num_pages
+        if four:
+            return torch.uint8, kv4_cache_shape(n, self.num_kv_heads, self.page_size, self.head_dim)
+        return torch.bfloat16, (n, 2, self.num_kv_heads, self.page_size, self.head_dim)
+
     def append_kv4(self, k_new, v_new, kv4_cache, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
         """append_kv into a 4-bit cache (see attn_append_kv4; in place)."""
-        dev, shape = self.workspace.device, (self.total_rows, self.num_kv_heads, self.head_dim)
-        _check_cuda(dev, k_new=(k_new, torch.bfloat16, shape), v_new=(v_new, torch.bfloat16, shape),
-                    kv4_cache=(kv4_cache, torch.uint8, self.kv4_shape()))
+        dev, shape = self.workspace.get_device(), (self.total_rows, self.num_kv_heads, self.head_dim)
+        _check_cuda(dev, "k_new", k_new, torch.bfloat16, shape)
+        _check_cuda(dev, "v_new", v_new, torch.bfloat16, shape)
+        _check_cuda(dev, "kv4_cache", kv4_cache, *self._cache_spec(True))
         _launch_on(dev, stream, "attn_append_kv4", self._handle, _ptr(k_new), _ptr(v_new), k_scale, v_scale,
                    _ptr(kv4_cache))
         return kv4_cache
@@ -335,34 +341,31 @@ class Plan:
     def decode_kv4(self, q, kv4_cache, sinks=None, out=None, lse=None, k_scale: float = 1.0, v_scale: float = 1.0,
                    stream=None):
         """decode over a 4-bit cache; returns (out, lse)."""
-        dev, H, D = self.workspace.device, self.num_qo_heads, self.head_dim
-        out = _empty_on(stream, (self.total_rows, H, D), torch.bfloat16, dev) if out is None else out
-        _check_cuda(dev, q=(q, torch.bfloat16, (self.total_rows, H, D)), out=(out, torch.bfloat16, (self.total_rows, H, D)),
-                    kv4_cache=(kv4_cache, torch.uint8, self.kv4_shape()))
+        dev, H, shape = self.workspace.get_device(), self.num_qo_heads, (self.total_rows, self.num_qo_heads, self.head_dim)
+        out = _empty_on(stream, shape, torch.bfloat16, self.workspace.device) if out is None else out
+        _check_cuda(dev, "q", q, torch.bfloat16, shape)
+        _check_cuda(dev, "out", out, torch.bfloat16, shape)
+        _check_cuda(dev, "kv4_cache", kv4_cache, *self._cache_spec(True))
         if sinks is not None:
-            _check_cuda(dev, sinks=(sinks, torch.float32, (H,)))
+            _check_cuda(dev, "sinks", sinks, torch.float32, (H,))
         if lse is not None:
-            _check_cuda(dev, lse=(lse, torch.float32, (self.total_rows, H)))
+            _check_cuda(dev, "lse", lse, torch.float32, (self.total_rows, H))
         _launch_on(dev, stream, "attn_decode_kv4", self._handle, _ptr(q), _ptr(kv4_cache), k_scale, v_scale, _ptr(sinks),
                    _ptr(out), _ptr(lse))
         return out, lse
 
     # -- attention weights per cached key, and eviction by them -----------
-    def _cache_spec(self, four, num_pages):
-        if four:
-            return torch.uint8, self.kv4_shape(num_pages)
-        return torch.bfloat16, (num_pages, 2, self.num_kv_heads, self.page_size, self.head_dim)
-
     def _key_weights(self, four, q, cache, lse, weights, prev, decay, window, k_scale, stream):
-        dev, H = self.workspace.device, self.num_qo_heads
+        dev, H = self.workspace.get_device(), self.num_qo_heads
         paged = (self.num_pages, self.num_kv_heads, self.page_size)
         if prev is None and decay != 0:
             prev = weights
-        _check_cuda(dev, q=(q, torch.bfloat16, (self.total_rows, H, self.head_dim)),
-                    lse=(lse, torch.float32, (self.total_rows, H)), weights=(weights, torch.float32, paged),
-                    cache=(cache, *self._cache_spec(four, self.num_pages)))
+        _check_cuda(dev, "q", q, torch.bfloat16, (self.total_rows, H, self.head_dim))
+        _check_cuda(dev, "lse", lse, torch.float32, (self.total_rows, H))
+        _check_cuda(dev, "weights", weights, torch.float32, paged)
+        _check_cuda(dev, "kv4_cache" if four else "kv_cache", cache, *self._cache_spec(four))
         if prev is not None:
-            _check_cuda(dev, prev=(prev, torch.float32, paged))
+            _check_cuda(dev, "prev", prev, torch.float32, paged)
         scale = (k_scale,) if four else ()
         _launch_on(dev, stream, "attn_key_weights_kv4" if four else "attn_key_weights", self._handle, _ptr(q),
                    _ptr(cache), *scale, _ptr(lse), _ptr(prev), float(decay), int(window), _ptr(weights))
@@ -383,24 +386,25 @@ class Plan:
         return self._key_weights(True, q, kv4_cache, lse, weights, prev, decay, window, k_scale, stream)
 
     def _evict(self, four, weights, cache, budget, recent, kept, page_table_out, kv_out, weights_out, stream):
-        dev, Hkv, P = self.workspace.device, self.num_kv_heads, self.page_size
+        dev, Hkv, P = self.workspace.get_device(), self.num_kv_heads, self.page_size
         if budget < 1 or not 0 <= recent <= budget:
             raise ValueError("eviction needs budget >= 1 and 0 <= recent <= budget")
-        _check_cuda(dev, weights=(weights, torch.float32, (self.num_pages, Hkv, P)),
-                    cache=(cache, *self._cache_spec(four, self.num_pages)))
+        _check_cuda(dev, "weights", weights, torch.float32, (self.num_pages, Hkv, P))
+        _check_cuda(dev, "kv4_cache" if four else "kv_cache", cache, *self._cache_spec(four))
         if page_table_out is None and (kv_out is not None or weights_out is not None):
             raise ValueError("kv_out / weights_out need page_table_out (without it eviction works in place)")
         kv_out = cache if kv_out is None else kv_out
         weights_out = weights if weights_out is None else weights_out
         if page_table_out is not None:
-            if kv_out.dim() == 0 or weights_out.shape[0] != kv_out.shape[0]:
+            if kv_out.dim() == 0 or weights_out.dim() == 0 or weights_out.shape[0] != kv_out.shape[0]:
                 raise ValueError("kv_out and weights_out must have the same number of pages")
             pages = int(((self.evicted_lens(budget) + (P - 1)) // P).sum())
-            _check_cuda(dev, page_table_out=(page_table_out, torch.int32, (pages,)),
-                        kv_out=(kv_out, *self._cache_spec(four, kv_out.shape[0])),
-                        weights_out=(weights_out, torch.float32, (kv_out.shape[0], Hkv, P)))
-        kept = _empty_on(stream, (self.batch, Hkv, budget), torch.int32, dev) if kept is None else kept
-        _check_cuda(dev, kept=(kept, torch.int32, (self.batch, Hkv, budget)))
+            _check_cuda(dev, "page_table_out", page_table_out, torch.int32, (pages,))
+            _check_cuda(dev, "kv_out", kv_out, *self._cache_spec(four, kv_out.shape[0]))
+            _check_cuda(dev, "weights_out", weights_out, torch.float32, (kv_out.shape[0], Hkv, P))
+        shape = (self.batch, Hkv, budget)
+        kept = _empty_on(stream, shape, torch.int32, self.workspace.device) if kept is None else kept
+        _check_cuda(dev, "kept", kept, torch.int32, shape)
         _launch_on(dev, stream, "attn_evict_kv4" if four else "attn_evict_kv", self._handle, _ptr(weights), _ptr(cache),
                    budget, recent, _ptr(kept), _ptr(page_table_out), kv_out.shape[0], _ptr(kv_out), _ptr(weights_out))
         return kept
@@ -630,15 +634,17 @@ def attn_expand_kv4(kv4_cache, page_ids, head_dim: int, buf=None, k_scale: float
     page_size, head_dim] (exact; see attn_expand_kv4)."""
     if not isinstance(kv4_cache, torch.Tensor) or kv4_cache.dim() != 5:
         raise TypeError("kv4_cache must be a uint8 CUDA tensor [num_pages, 2, Hkv, page_size / 16, 9 * head_dim]")
-    dev, (num_pages, _, hkv, subs, _) = kv4_cache.device, kv4_cache.shape
+    dev, (num_pages, _, hkv, subs, _) = kv4_cache.get_device(), kv4_cache.shape
     P = subs * KV4_TOKENS
-    _check_cuda(dev, kv4_cache=(kv4_cache, torch.uint8, kv4_cache_shape(num_pages, hkv, P, head_dim)),
-                page_ids=(page_ids, torch.int32, None))
+    _check_cuda(dev, "kv4_cache", kv4_cache, torch.uint8, kv4_cache_shape(num_pages, hkv, P, head_dim))
+    _check_cuda(dev, "page_ids", page_ids, torch.int32)
     shape = (page_ids.numel(), 2, hkv, P, head_dim)
-    buf = _empty_on(stream, shape, torch.bfloat16, dev) if buf is None else buf
-    _check_cuda(dev, buf=(buf, torch.bfloat16, shape))
+    buf = _empty_on(stream, shape, torch.bfloat16, kv4_cache.device) if buf is None else buf
+    _check_cuda(dev, "buf", buf, torch.bfloat16, shape)
     if device_error is not None:
-        _check_cuda(dev, device_error=(device_error, torch.int32, None))
+        _check_cuda(dev, "device_error", device_error, torch.int32)
+        if device_error.numel() == 0:
+            raise ValueError("device_error must hold an int32")
     _launch_on(dev, stream, "attn_expand_kv4", _ptr(kv4_cache), num_pages, hkv, P, head_dim, _ptr(page_ids),
                page_ids.numel(), k_scale, v_scale, _ptr(buf), _ptr(device_error))
     return buf

@@ -8,9 +8,10 @@
 // 6 is e2m1's largest magnitude.  A NaN in a group makes the scale NaN, and
 // with it the whole group; an infinity saturates (448 * 6 * g).
 //
-// Both kernels are HBM-bound copies with a few instructions per value; a
-// thread owns one group of 16 dims (32 bytes of bf16, 8 code bytes and a
-// scale byte).
+// Both kernels are HBM-bound copies as long as they spend few instructions on
+// a value: packed fp32 arithmetic, and each thread finds its place by a
+// division once and then steps (a 64-bit division per item alone cost 20 us of
+// the 73 that appending 57K rows of 8 heads x 128 dims took).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,8 +25,15 @@ namespace {
 
 constexpr int kKv4Threads = 256;
 
-// Quantise 16 bf16 values (w: pairs): the scale byte, and 8 code bytes.
-__device__ __forceinline__ uint32_t quantise16(const uint32_t (&w)[8], float inv_pool_scale, uint2& codes) {
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(ptx::f2_bits(a)), "l"(ptx::f2_bits(b)));
+    return ptx::bits_f2(r);
+}
+
+// Quantise 16 bf16 values (w: pairs): the scale byte, and 8 code bytes.  g: the
+// pool's scale, a power of two.
+__device__ __forceinline__ uint32_t quantise16(const uint32_t (&w)[8], float g, float inv_g, uint2& codes) {
     // max |x| on the bits: bf16 magnitudes order like integers, NaN above infinity.
     uint32_t hi = 0, lo = 0;
 #pragma unroll
@@ -33,97 +41,127 @@ __device__ __forceinline__ uint32_t quantise16(const uint32_t (&w)[8], float inv
         hi = max(hi, w[i] & 0x7FFF0000u);
         lo = max(lo, w[i] & 0x00007FFFu);
     }
-    const float amax = __uint_as_float(max(hi, lo << 16)) * inv_pool_scale;
+    const float amax = __uint_as_float(max(hi, lo << 16)) * inv_g;
     // amax has 8 significant bits and a border between two e4m3 values 5, so
     // that amax * fl(1/6) falls on the same side of (or onto) each border as
     // amax / 6: fl(1/6)'s relative error 2^-25 is below half an ulp of a tie
     // and far below the distance of anything else.
     const uint32_t sb = kv4::scale_byte(amax * (1.f / 6.f));
     const float s = kv4::f16x2_to_f32(kv4::scales_to_f16x2(sb)).x;
-    const float inv = s > 0.f ? 1.f / s : 0.f;
-    // x / s correctly rounded (one Newton step on the quotient), so that a
+    const float inv = s > 0.f ? 1.f / s : 0.f;      // a scale that underflowed to 0: all codes 0
+    // x / (s g) correctly rounded (a Newton step on the quotient), so that a
     // quotient on a border between two codes lands on it and goes to the even
-    // code.  0 * inf (a scale that underflowed to 0) cannot occur: inv = 0.
-    auto div = [&](float x) {
-        const float q = x * inv;
-        const float q1 = fmaf(fmaf(-q, s, x), inv, q);
-        return fabsf(q) < 16.f ? q1 : q;   // saturates either way; keeps an infinite x from turning NaN
-    };
+    // code.  Groups far beyond the largest scale saturate either way; there the
+    // step is left out, for it would turn an infinity into NaN.
+    const float2 d = make_float2(inv * inv_g, inv * inv_g), m = make_float2(-s * g, -s * g);
+    const bool far = amax * inv >= 16.f;
     uint32_t c[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float2 x = ptx::unpack_bf16x2(w[i]);
-        c[i >> 2] |= kv4::code_pair(div(x.x * inv_pool_scale), div(x.y * inv_pool_scale)) << (8 * (i & 3));
+        float2 q = mul2(x, d);
+        if (!far) q = ptx::fma2(ptx::fma2(q, m, x), d, q);
+        c[i >> 2] |= kv4::code_pair(q.x, q.y) << (8 * (i & 3));
     }
     codes = make_uint2(c[0], c[1]);
     return sb;
 }
 
-// One thread per (row, K/V, KV head, group of 16 dims).
+// One thread per (row, K/V, KV head, group of 16 dims), stepping through the
+// items (a row's are per_row = 2 * Hkv * D / 16).
 template <int D>
 __global__ void __launch_bounds__(kKv4Threads)
 append_kv4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, uint8_t* __restrict__ pool,
                   const int2* __restrict__ slots, const int32_t* __restrict__ page_table, int64_t rows, int32_t Hkv,
-                  int32_t P, int32_t num_pages, float inv_k, float inv_v, int32_t* err) {
-    constexpr int kGroups = D / kKv4Group;
-    const int32_t per_half = Hkv * kGroups;   // groups of one row's K (or V)
-    const int64_t total = rows * 2 * per_half;
-    for (int64_t i = (int64_t)blockIdx.x * kKv4Threads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kKv4Threads) {
-        const int64_t r = i / (2 * per_half);
-        const int32_t in_row = (int32_t)(i - r * (2 * per_half));
+                  int32_t page_log2, int32_t num_pages, float k_scale, float inv_k, float v_scale, float inv_v,
+                  int32_t* err) {
+    constexpr int kGroups = D / kKv4Group, kSub = kv4_sub_bytes(D);
+    const int32_t per_half = Hkv * kGroups, per_row = 2 * per_half;
+    const int64_t i = (int64_t)blockIdx.x * kKv4Threads + threadIdx.x, step = (int64_t)gridDim.x * kKv4Threads;
+    const int64_t step_rows = step / per_row;
+    const int32_t step_in = (int32_t)(step - step_rows * per_row);
+    int64_t r = i / per_row;
+    int32_t in_row = (int32_t)(i - r * per_row);
+    // The next item's values and slot are on their way while this one is worked on.
+    uint4 next_a, next_b;
+    int2 next_slot;
+    auto fetch = [&] {
+        if (r >= rows) return;
         const int half = in_row >= per_half;
-        const int32_t in_half = in_row - half * per_half;
+        const uint4* src = (half ? v_new : k_new) + (r * per_half + in_row - half * per_half) * 2;
+        next_a = __ldg(src);
+        next_b = __ldg(src + 1);
+        next_slot = slots[r];
+    };
+    fetch();
+    while (r < rows) {
+        const int half = in_row >= per_half;
+        const int32_t in_half = in_row - half * per_half, in_row0 = in_row;
         const int g = in_half / kGroups, grp = in_half % kGroups;
-        const int2 slot = slots[r];
+        const uint4 a = next_a, b = next_b;
+        const int2 slot = next_slot;
         const int32_t page = page_table[slot.x];
-        if (page < 0 || page >= num_pages) {
-            if (in_row == 0) atomicOr(err, ATTN_DEVICE_ERR_PAGE_ID);
-            continue;
+        r += step_rows;
+        in_row += step_in;
+        if (in_row >= per_row) {
+            in_row -= per_row;
+            ++r;
         }
-        const uint4* src = (half ? v_new : k_new) + (r * per_half + in_half) * 2;
-        const uint4 a = __ldg(src), b = __ldg(src + 1);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint2 codes;
-        const uint32_t sb = quantise16(w, half ? inv_v : inv_k, codes);
-        uint8_t* sub = pool + kv4::sub_offset(page, half, Hkv, g, P, slot.y, kv4_sub_bytes(D));
-        const int t = slot.y % kKv4Tokens;
-        *reinterpret_cast<uint2*>(sub + t * (D / 2) + grp * 8) = codes;
-        sub[8 * D + t * kGroups + grp] = (uint8_t)sb;
+        fetch();
+        if (page >= 0 && page < num_pages) {
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            uint2 codes;
+            const uint32_t sb = quantise16(w, half ? v_scale : k_scale, half ? inv_v : inv_k, codes);
+            const int64_t block = ((int64_t)page * 2 + half) * Hkv + g;
+            uint8_t* sub = pool + ((block << (page_log2 - 4)) + (slot.y >> 4)) * kSub;
+            const int t = slot.y & (kKv4Tokens - 1);
+            *reinterpret_cast<uint2*>(sub + t * (D / 2) + grp * 8) = codes;
+            sub[8 * D + t * kGroups + grp] = (uint8_t)sb;
+        } else if (in_row0 == 0) {
+            atomicOr(err, ATTN_DEVICE_ERR_PAGE_ID);
+        }
     }
 }
 
-// One thread per (listed page, K/V, KV head, token, group of 16 dims).
+// One thread per 8 values: (listed page, K/V, KV head, token, 8 dims), so that
+// a warp writes 512 consecutive bytes; stepping as above (a (page, K/V) half
+// has per_half = Hkv * P * D / 8 of them).
 template <int D>
 __global__ void __launch_bounds__(kKv4Threads)
 expand_kv4_kernel(const uint8_t* __restrict__ pool, uint4* __restrict__ buf, const int32_t* __restrict__ page_ids,
                   int64_t n, int32_t Hkv, int32_t P, int64_t num_pages, float k_scale, float v_scale, int32_t* err) {
-    constexpr int kGroups = D / kKv4Group, kSub = kv4_sub_bytes(D);
-    const int64_t per_half = (int64_t)Hkv * P * kGroups;
-    const int64_t total = n * 2 * per_half;
-    for (int64_t i = (int64_t)blockIdx.x * kKv4Threads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kKv4Threads) {
-        const int64_t blk = i / per_half;                 // (page in the list, K/V)
-        const int64_t in_half = i - blk * per_half;       // ((head, sixteen tokens), token, group)
+    constexpr int kOctets = D / 8, kSub = kv4_sub_bytes(D), kPerSub = kKv4Tokens * kOctets;
+    const int32_t per_half = Hkv * P * kOctets, half_subs = Hkv * (P / kKv4Tokens);
+    const int64_t step = (int64_t)gridDim.x * kKv4Threads, step_halves = step / per_half;
+    const int32_t step_in = (int32_t)(step - step_halves * per_half);
+    int64_t i = (int64_t)blockIdx.x * kKv4Threads + threadIdx.x, blk = i / per_half;   // blk: (page in the list, K/V)
+    int32_t in_half = (int32_t)(i - blk * per_half);   // ((head, sixteen tokens), token, 8 dims)
+    while (blk < 2 * n) {
         const int32_t page = page_ids[blk >> 1];
-        if (page < 0 || page >= num_pages) {
-            if (in_half == 0 && (blk & 1) == 0 && err) atomicOr(err, ATTN_DEVICE_ERR_PAGE_ID);
-            continue;
-        }
-        const int64_t sub_idx = in_half / (kKv4Tokens * kGroups);
-        const int tg = (int)(in_half % (kKv4Tokens * kGroups));   // token * kGroups + group
-        const uint8_t* sub = pool + (((int64_t)page * 2 + (blk & 1)) * Hkv * (P / kKv4Tokens) + sub_idx) * kSub;
-        const uint2 codes = *reinterpret_cast<const uint2*>(sub + tg * 8);
-        const float pool_scale = (blk & 1) ? v_scale : k_scale;
-        const float s = kv4::f16x2_to_f32(kv4::scales_to_f16x2(sub[8 * D + tg])).x * pool_scale;
-        uint32_t h[2][4], o[8];
-        kv4::codes_to_f16x2(codes.x, h[0]);
-        kv4::codes_to_f16x2(codes.y, h[1]);
+        if (page >= 0 && page < num_pages) {
+            const int32_t sub_idx = in_half / kPerSub, at = in_half % kPerSub;
+            const uint8_t* sub = pool + (((int64_t)page * 2 + (blk & 1)) * half_subs + sub_idx) * kSub;
+            const uint32_t codes = *reinterpret_cast<const uint32_t*>(sub + at * 4);
+            const uint32_t sb = sub[8 * D + at / 2];
+            const float s = kv4::f16x2_to_f32(kv4::scales_to_f16x2(sb)).x * ((blk & 1) ? v_scale : k_scale);
+            uint32_t h[4], o[4];
+            kv4::codes_to_f16x2(codes, h);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float2 v = kv4::f16x2_to_f32(h[k >> 2][k & 3]);
-            o[k] = ptx::pack_bf16x2(v.x * s, v.y * s);    // exact: see kv4.cuh
+            for (int k = 0; k < 4; ++k) {
+                const float2 v = mul2(kv4::f16x2_to_f32(h[k]), make_float2(s, s));
+                o[k] = ptx::pack_bf16x2(v.x, v.y);    // exact: see kv4.cuh
+            }
+            buf[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        } else if (in_half == 0 && (blk & 1) == 0 && err) {
+            atomicOr(err, ATTN_DEVICE_ERR_PAGE_ID);
         }
-        buf[i * 2] = make_uint4(o[0], o[1], o[2], o[3]);
-        buf[i * 2 + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+        i += step;
+        blk += step_halves;
+        in_half += step_in;
+        if (in_half >= per_half) {
+            in_half -= per_half;
+            ++blk;
+        }
     }
 }
 
@@ -140,13 +178,16 @@ attn_status launch_append_kv4(attn_plan_s* plan, const void* k_new, const void* 
                               float v_scale, cudaStream_t stream) {
     const int64_t rows = plan->info.total_qo_rows;
     if (rows == 0) return ATTN_OK;
-    const int grid = kv4_grid(rows * 2 * plan->Hkv * (plan->D / kKv4Group), 8);
+    // As many CTAs as stay resident (48 registers a thread): a grid of 8 per SM
+    // left a third of the last wave idle.
+    const int grid = kv4_grid(rows * 2 * plan->Hkv * (plan->D / kKv4Group), 5);
     if (grid == 0) return ATTN_ERR_CUDA;
     auto run = [&](auto kernel) {
         kernel<<<grid, kKv4Threads, 0, stream>>>(
             static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), static_cast<uint8_t*>(kv4_cache),
-            reinterpret_cast<const int2*>(plan->ws + plan->layout.append), plan->page_table, rows, plan->Hkv, plan->P,
-            plan->num_pages, 1.f / k_scale, 1.f / v_scale, reinterpret_cast<int32_t*>(plan->ws + plan->layout.err));
+            reinterpret_cast<const int2*>(plan->ws + plan->layout.append), plan->page_table, rows, plan->Hkv,
+            31 - __builtin_clz(plan->P), plan->num_pages, k_scale, 1.f / k_scale, v_scale, 1.f / v_scale,
+            reinterpret_cast<int32_t*>(plan->ws + plan->layout.err));
     };
     if (plan->D == 64) run(append_kv4_kernel<64>);
     else run(append_kv4_kernel<128>);
@@ -157,7 +198,7 @@ attn_status launch_expand_kv4(const void* kv4_cache, void* buf, const int32_t* p
                               int32_t Hkv, int32_t P, int32_t D, float k_scale, float v_scale, int32_t* err,
                               cudaStream_t stream) {
     if (n == 0) return ATTN_OK;
-    const int grid = kv4_grid(n * 2 * Hkv * P * (D / kKv4Group), 8);
+    const int grid = kv4_grid(n * 2 * Hkv * P * (D / 8), 8);
     if (grid == 0) return ATTN_ERR_CUDA;
     auto run = [&](auto kernel) {
         kernel<<<grid, kKv4Threads, 0, stream>>>(static_cast<const uint8_t*>(kv4_cache), static_cast<uint4*>(buf),
