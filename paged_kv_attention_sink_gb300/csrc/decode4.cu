@@ -44,10 +44,13 @@ constexpr float kShift = 7.f, kSlack = 15.f;   // log2 units
 template <int D, int NT>
 struct Decode4Cfg {
     static constexpr int kWarps = kDecodeWarps;
-    static constexpr int kTile = 64;                                  // tokens per stage (one wait, one refill)
-    static constexpr int kStep = 32;                                  // tokens whose scores are held at a time
+    // Tokens per stage, all of whose scores are held at once: independent
+    // products hide more than further warps do (256 requests of 0.5K-16K tokens,
+    // D = 64: 242 us with 32 tokens at a time and 20 warps per SM, 228 with 64,
+    // 236 with 128 and 12 warps).
+    static constexpr int kTile = 64;
     static constexpr int kStages = 2;
-    static constexpr int kSubs = kTile / kKv4Tokens, kStepSubs = kStep / kKv4Tokens;
+    static constexpr int kSubs = kTile / kKv4Tokens;
     static constexpr int kSub = kv4_sub_bytes(D);
     static constexpr int kStageBytes = 2 * kSubs * kSub;              // K, then V
     static constexpr int kHeads = NT * 8;
@@ -185,95 +188,92 @@ decode4_sink_attn_kernel(const Decode4Args a) {
             kv4_clear_scales<D, C::kTile>(ring + s * C::kStageBytes + C::kSubs * C::kSub, valid, lane);
             __syncwarp();
         }
-#pragma unroll 1
-        for (int t0 = 0; t0 < valid; t0 += C::kStep, kt += C::kStepSubs * C::kSub) {
-            const uint8_t* vt = kt + C::kSubs * C::kSub;
-            // S^T of the step's tokens.
-            float x[C::kStepSubs][NT][4];
+        const uint8_t* vt = kt + C::kSubs * C::kSub;
+        // S^T of the stage's tokens.
+        float x[C::kSubs][NT][4];
 #pragma unroll
-            for (int sub = 0; sub < C::kStepSubs; ++sub) {
-                kv4_for_k<D>(kt + sub * C::kSub, row, tq, [&](int kk, const uint32_t (&ka)[4]) {
+        for (int sub = 0; sub < C::kSubs; ++sub) {
+            kv4_for_k<D>(kt + sub * C::kSub, row, tq, [&](int kk, const uint32_t (&ka)[4]) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if (kk == 0) mma_f16_16816_new(x[sub][nt], ka, qb[nt][kk][0], qb[nt][kk][1]);
-                        else mma_f16_16816(x[sub][nt], ka, qb[nt][kk][0], qb[nt][kk][1]);
-                    }
-                });
-            }
-            if (valid < t0 + C::kStep) {   // tokens past the end have no score
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (kk == 0) mma_f16_16816_new(x[sub][nt], ka, qb[nt][kk][0], qb[nt][kk][1]);
+                    else mma_f16_16816(x[sub][nt], ka, qb[nt][kk][0], qb[nt][kk][1]);
+                }
+            });
+        }
+        if (valid < C::kTile) {   // tokens past the end have no score
 #pragma unroll
-                for (int sub = 0; sub < C::kStepSubs; ++sub)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (t0 + sub * kKv4Tokens + row + 8 * (e >> 1) >= valid) x[sub][nt][e] = -INFINITY;
-            }
-
-            // Scores above their shift, in log2 units; where one is by too
-            // much (and at the start), the shifts move.
-            float top = -INFINITY;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int sub = 0; sub < C::kStepSubs; ++sub)
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const float2 v = ptx::fma2(make_float2(x[sub][nt][e], x[sub][nt][e + 1]), mult[nt], nm[nt]);
-                        x[sub][nt][e] = v.x;
-                        x[sub][nt][e + 1] = v.y;
-                        top = fmaxf(top, fmaxf(v.x, v.y));
-                    }
-            if (__any_sync(0xffffffffu, top > slack)) {
+            for (int sub = 0; sub < C::kSubs; ++sub)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float mx = -INFINITY;
-#pragma unroll
-                        for (int sub = 0; sub < C::kStepSubs; ++sub)
-                            mx = fmaxf(mx, fmaxf(x[sub][nt][e], x[sub][nt][e + 2]));
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                        // How far the shift moves; at the start it holds no score
-                        // yet, only (if any) the sink's.
-                        const bool none = slack < 0.f && sink_shift(nt * 8 + 2 * tq + e) == -INFINITY;
-                        const float up = none ? mx - kShift : fmaxf(0.f, mx - kShift);
-                        const float alpha = none ? 0.f : ptx::ex2(-up);
-                        (e ? nm[nt].y : nm[nt].x) -= up;
-                        (e ? l[nt].y : l[nt].x) *= alpha;
-#pragma unroll
-                        for (int i = 0; i < kKSteps; ++i) {
-                            o[nt][i][e] *= alpha;
-                            o[nt][i][e + 2] *= alpha;
-                        }
-#pragma unroll
-                        for (int sub = 0; sub < C::kStepSubs; ++sub) {
-                            x[sub][nt][e] -= up;
-                            x[sub][nt][e + 2] -= up;
-                        }
-                    }
-                slack = kSlack;
-            }
+                    for (int e = 0; e < 4; ++e)
+                        if (sub * kKv4Tokens + row + 8 * (e >> 1) >= valid) x[sub][nt][e] = -INFINITY;
+        }
 
-            // P^T as the column operand of the second product; O^T += V^T P^T.
+        // Scores above their shift, in log2 units; where one is by too
+        // much (and at the start), the shifts move.
+        float top = -INFINITY;
 #pragma unroll
-            for (int sub = 0; sub < C::kStepSubs; ++sub) {
-                uint32_t pb[NT][2];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float p[4];
+            for (int sub = 0; sub < C::kSubs; ++sub)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = ptx::ex2(x[sub][nt][e]);
-                    l[nt] = ptx::add2(l[nt], ptx::add2(make_float2(p[0], p[1]), make_float2(p[2], p[3])));
-                    pb[nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
-                    pb[nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
+                for (int e = 0; e < 4; e += 2) {
+                    const float2 v = ptx::fma2(make_float2(x[sub][nt][e], x[sub][nt][e + 1]), mult[nt], nm[nt]);
+                    x[sub][nt][e] = v.x;
+                    x[sub][nt][e + 1] = v.y;
+                    top = fmaxf(top, fmaxf(v.x, v.y));
                 }
-                kv4_for_v<D>(vt + sub * C::kSub, gq, tq, [&](int i, const uint32_t (&va)[4]) {
+        if (__any_sync(0xffffffffu, top > slack)) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][i], va, pb[nt][0], pb[nt][1]);
-                });
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int sub = 0; sub < C::kSubs; ++sub)
+                        mx = fmaxf(mx, fmaxf(x[sub][nt][e], x[sub][nt][e + 2]));
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    // How far the shift moves; at the start it holds no score
+                    // yet, only (if any) the sink's.
+                    const bool none = slack < 0.f && sink_shift(nt * 8 + 2 * tq + e) == -INFINITY;
+                    const float up = none ? mx - kShift : fmaxf(0.f, mx - kShift);
+                    const float alpha = none ? 0.f : ptx::ex2(-up);
+                    (e ? nm[nt].y : nm[nt].x) -= up;
+                    (e ? l[nt].y : l[nt].x) *= alpha;
+#pragma unroll
+                    for (int i = 0; i < kKSteps; ++i) {
+                        o[nt][i][e] *= alpha;
+                        o[nt][i][e + 2] *= alpha;
+                    }
+#pragma unroll
+                    for (int sub = 0; sub < C::kSubs; ++sub) {
+                        x[sub][nt][e] -= up;
+                        x[sub][nt][e + 2] -= up;
+                    }
+                }
+            slack = kSlack;
+        }
+
+        // P^T as the column operand of the second product; O^T += V^T P^T.
+#pragma unroll
+        for (int sub = 0; sub < C::kSubs; ++sub) {
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] = ptx::ex2(x[sub][nt][e]);
+                l[nt] = ptx::add2(l[nt], ptx::add2(make_float2(p[0], p[1]), make_float2(p[2], p[3])));
+                pb[nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
+                pb[nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
             }
+            kv4_for_v<D>(vt + sub * C::kSub, gq, tq, [&](int i, const uint32_t (&va)[4]) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][i], va, pb[nt][0], pb[nt][1]);
+            });
         }
 
         __syncwarp();   // every lane has read the stage

@@ -55,8 +55,8 @@ struct KeyWeightArgs {
 template <int D, bool kFour>
 struct StepWeightCfg {
     static constexpr int kWarps = kDecodeWarps;
-    static constexpr int kTile = 32;                                     // tokens per stage
-    static constexpr int kStages = kFour || D == 64 ? 4 : 3;
+    static constexpr int kTile = kFour ? 64 : 32;                        // tokens per stage
+    static constexpr int kStages = kFour ? 2 : D == 64 ? 4 : 3;
     static constexpr int kSubs = kTile / kBlockTokens;
     static constexpr int kSub = kFour ? kv4_sub_bytes(D) : kBlockTokens * D * 2;   // K of 16 tokens
     static constexpr int kPrev = kSubs * kSub;                           // then the tokens' previous weights
@@ -132,8 +132,8 @@ key_weights_step_kernel(const KeyWeightArgs a) {
     const int n_it = n_tiles > warp ? (n_tiles - warp + C::kWarps - 1) / C::kWarps : 0;
     auto tile_tok = [&](int it) { return u.tok_begin + (warp + it * C::kWarps) * C::kTile; };
     const TileSource src = tile_source<D, kFour, C::kTile>(a.pool, first_s, first_page, a.page_log2, a.Hkv, lane);
-    // Each lane takes one of a tile's 32 tokens: sixteen tq >> 1, row
-    // (tq & 1) * 8 + its own.  slot: where its weight lies, or -1.
+    // Each lane takes one of every 32 of a tile's tokens: sixteen tq >> 1, row
+    // (tq & 1) * 8 + its own.  slot: where a token's weight lies, or -1.
     const int row = kFour ? kv4_row(gq) : gq;
     const int mine = (tq >> 1) * kBlockTokens + (tq & 1) * 8 + row;
     auto slot = [&](int tok) -> int64_t {
@@ -145,10 +145,13 @@ key_weights_step_kernel(const KeyWeightArgs a) {
     auto issue = [&](int it, int s) {   // one group per stage, empty past the end
         const uint32_t dst = ring_u32 + s * C::kStageBytes;
         if (it < n_it) {
-            const int64_t at = slot(tile_tok(it) + mine);
-            const bool old = at >= 0 && tile_tok(it) + mine < prev_end;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
-                         ::"r"(dst + C::kPrev + lane * 4), "l"(a.prev + (old ? at : 0)), "r"(old ? 4 : 0) : "memory");
+#pragma unroll
+            for (int t = 0; t < C::kTile; t += 32) {
+                const int64_t at = slot(tile_tok(it) + t + mine);
+                const bool old = at >= 0 && tile_tok(it) + t + mine < prev_end;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                             ::"r"(dst + C::kPrev + (t + lane) * 4), "l"(a.prev + (old ? at : 0)), "r"(old ? 4 : 0) : "memory");
+            }
             if constexpr (kFour) kv4_stage_load<D, C::kTile, 1>(src, tile_tok(it), u.tok_end, dst, lane);
             else bf16_stage_load<D, C::kTile>(src, tile_tok(it), u.tok_end, dst, lane);
         }
@@ -208,21 +211,28 @@ key_weights_step_kernel(const KeyWeightArgs a) {
                 }
             }
         }
-        const float before = *reinterpret_cast<const float*>(kt + C::kPrev + lane * 4);
+        float before[C::kTile / 32];
+#pragma unroll
+        for (int t = 0; t < C::kTile / 32; ++t)
+            before[t] = *reinterpret_cast<const float*>(kt + C::kPrev + (t * 32 + lane) * 4);
         __syncwarp();   // every lane has read the stage
         issue(it + C::kStages, s);
         s = s + 1 == C::kStages ? 0 : s + 1;
         // Sums over the four lanes of a key row, each of which ends with one token's.
-        float v[C::kSubs];
 #pragma unroll
-        for (int sub = 0; sub < C::kSubs; ++sub) {
-            const float keep = tq & 1 ? w[sub][1] : w[sub][0], give = tq & 1 ? w[sub][0] : w[sub][1];
-            v[sub] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+        for (int t = 0; t < C::kTile / 32; ++t) {
+            float v[2];
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+                const float(&x)[2] = w[2 * t + sub];
+                const float keep = tq & 1 ? x[1] : x[0], give = tq & 1 ? x[0] : x[1];
+                v[sub] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+            }
+            const float keep = tq & 2 ? v[1] : v[0], give = tq & 2 ? v[0] : v[1];
+            const float sum = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+            const int64_t at = slot(tile_tok(it) + t * 32 + mine);
+            if (at >= 0) a.weights[at] = fmaf(a.decay, before[t], sum);
         }
-        const float keep = tq & 2 ? v[1] : v[0], give = tq & 2 ? v[0] : v[1];
-        const float sum = keep + __shfl_xor_sync(0xffffffffu, give, 2);
-        const int64_t at = slot(tile_tok(it) + mine);
-        if (at >= 0) a.weights[at] = fmaf(a.decay, before, sum);
     }
 }
 
