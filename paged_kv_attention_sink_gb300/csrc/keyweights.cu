@@ -256,10 +256,7 @@ struct PromptWeightCfg {
     static constexpr int kBufs = 4;                         // S accumulators: all 512 TMEM columns
     static constexpr int kWgs = 3;                          // epilogue warpgroups
     static constexpr int kEpilogueWarps = 4 * kWgs;
-    // MMA warps, taking steps in turn: a step costs its warp some 650 clocks
-    // (two waits, the issue of the MMAs and a commit), a step's exponentials 515.
-    static constexpr int kMmaWarps = 2;
-    static constexpr int kThreads = (kEpilogueWarps + kMmaWarps + 2) * 32;   // + Q producer, + lse
+    static constexpr int kThreads = (kEpilogueWarps + 3) * 32;   // + MMA issuer, + Q producer, + lse
     static constexpr int kHeads = 8;                        // heads whose lse is staged at a time
     static constexpr int kOffQ = kTile;
     static constexpr int kOffNl = kOffQ + kStages * kTile;    // [2][8 heads][128 rows] negated lse
@@ -268,6 +265,10 @@ struct PromptWeightCfg {
     static constexpr int kSmem = 1024 + kOffBars + (2 * kStages + kBufs + 6) * 8 + 16;
     // One CTA per SM: it holds all of an SM's TMEM, and a second one would wait for it.
     static_assert(2 * (kSmem + 1024) > 233472 && kSmem <= 232448, "one CTA per SM");
+    // s_full is waited on by stage: step s + kStages must not complete before
+    // step s's S has been read.  The one MMA warp takes the steps in order, and
+    // step s + kBufs needs the accumulator of step s.
+    static_assert(kStages >= kBufs, "s_full phases");
 };
 
 template <int D, bool kFour>
@@ -309,7 +310,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
             ptx::mbar_init(l_free + 8 * i, C::kEpilogueWarps);
         }
         ptx::mbar_init(k_full, kFour ? C::kEpilogueWarps : 1);
-        ptx::mbar_init(drain, C::kMmaWarps);
+        ptx::mbar_init(drain, 1);
         ptx::fence_mbar_init();
     }
     if (warp == C::kEpilogueWarps) {
@@ -321,7 +322,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == C::kEpilogueWarps + C::kMmaWarps) {
+    if (warp == C::kEpilogueWarps + 1) {
         // ------------------------------------------------------------ producer
         if (!kFour) {
             const int n_load = (min(kTileKeys, r.kv_len - t0) + P - 1) / P;   // page boxes of the K tile
@@ -364,7 +365,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
                     ptx::mbar_wait(q_full + 8 * (k % C::kStages), (k / C::kStages) & 1);
         }
         __syncwarp();
-    } else if (warp == C::kEpilogueWarps + C::kMmaWarps + 1) {
+    } else if (warp == C::kEpilogueWarps + 2) {
         // ----------------------------------------------------------------- lse
         // Steps come in groups, the same 128 rows and up to 8 heads; this warp
         // stages a group's lse (negated, in log2 units, by head) ahead of them.
@@ -396,11 +397,11 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
                 row0 += kTileRows;
             }
         }
-    } else if (warp >= C::kEpilogueWarps) {
-        // --------------------------------------------------------- MMA issuers
+    } else if (warp == C::kEpilogueWarps) {
+        // ---------------------------------------------------------- MMA issuer
         constexpr uint32_t idesc = ptx::idesc_bf16(kTileKeys, kTileRows, false, false);
         bool ok = wait_all(k_full, 0);
-        for (int s = warp - C::kEpilogueWarps; ok && s < n_steps; s += C::kMmaWarps) {
+        for (int s = 0; ok && s < n_steps; ++s) {
             const int st = s % C::kStages, buf = s % C::kBufs;
             ok = wait_all(q_full + 8 * st, (s / C::kStages) & 1) &&
                  (s < C::kBufs || wait_all(s_free + 8 * buf, (s / C::kBufs - 1) & 1));
