@@ -63,6 +63,48 @@ def test_key_weights_match_reference(four, G, D, P, causal):
         assert np.all(np.abs(got[here] - want[here]) <= tol[here] + 1e-37), (decay, window)
 
 
+@pytest.mark.parametrize("four,D,G,P", [(False, 64, 8, 16), (True, 128, 5, 64), (False, 128, 16, 32)])
+def test_key_weights_of_longer_prompts(four, D, G, P):
+    """Enough rows and heads that every ring of the kernel wraps several times,
+    with a prefix, a window, and rows that end inside a tile."""
+    batch = batch_of([600, 129, 333], [600, 400, 334], G, 1, D, P, seed=D + G)
+    _, pool, vals = pools(batch, four, seed=3)
+    plan = make_plan(batch, dev(batch.page_table))
+    lse = some_lse(batch, vals)
+    prev = np.random.default_rng(5).exponential(size=(batch.num_pages, 1, P)).astype(np.float32)
+    for window in (0, 200):
+        out = torch.full(prev.shape, -5.0, device="cuda")
+        run_weights(plan, four, dev_bf16(batch.q), pool, dev(lse), out, prev=dev(prev), window=window)
+        assert plan.device_error() == 0
+        want, tol = ref.key_weights(batch, vals, lse, prev, 1.0, window)
+        got, here = out.double().cpu().numpy(), ~np.isnan(want)
+        assert np.all(got[~here] == -5.0)
+        assert np.all(np.abs(got[here] - want[here]) <= tol[here] + 1e-37), window
+
+
+def test_key_weights_mask_foreign_rows_and_keys():
+    """Query rows of a neighbour that are NaN, NaN keys past the end, and a NaN
+    key among the request's own, which spoils its own weight alone."""
+    batch = batch_of([40, 70], [40, 75], 4, 2, 64, 16, seed=9)
+    _, pool, vals = pools(batch, False, 4)
+    lse, q = some_lse(batch, vals), batch.q.copy()
+    q[:40] = 0x7FC0                                              # request 0's rows
+    own = batch.page_table[batch.kv_indptr[1]]                   # request 1's tokens 0..15
+    pool = pool.clone()
+    pool[own, 0, 1, 3] = float("nan")
+    vals = pool.double().cpu().numpy()
+    plan = make_plan(batch, dev(batch.page_table))
+    w = plan.key_weights(dev_bf16(q), pool, dev(lse), torch.zeros(batch.num_pages, 2, 16, device="cuda"), decay=0.0)
+    batch.q = batch.q.copy()
+    want, tol = ref.key_weights(batch, np.where(np.isnan(vals), 0, vals), lse, np.zeros(w.shape), 0.0, 0)
+    pages = batch.page_table[batch.kv_indptr[1]:batch.kv_indptr[2]]
+    got = w.double().cpu().numpy()
+    assert np.isnan(got[own, 1, 3])
+    got[own, 1, 3] = want[own, 1, 3]
+    here = ~np.isnan(want[pages])
+    assert np.all(np.abs(got[pages] - want[pages])[here] <= tol[pages][here] + 1e-37)
+
+
 def test_key_weights_in_place_and_again():
     """weights is its own prev: two steps add up, the new token starts at zero,
     and equal calls give equal bits."""
@@ -207,6 +249,45 @@ def test_evict_long_rows_and_equal_weights():
     host[batch.page_table[t // 128], 0, t % 128] = flat
     kept = plan.evict_kv(dev(host), pool, budget, 0).cpu().numpy()[0, 0]
     np.testing.assert_array_equal(kept, ref.evict(flat, n, budget, 0))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("kv,Hkv,budget,recent", [([50001, 40], 1, 20011, 100), ([12003] + [17] * 89, 2, 5000, 7)])
+def test_evict_rows_longer_than_shared_memory(in_place, kv, Hkv, budget, recent):
+    """Rows whose weights are read in chunks, for few rows (a CTA takes a whole
+    SM) and for many."""
+    P, D = 64, 64
+    batch = batch_of([0] * len(kv), kv, 1, Hkv, D, P, seed=len(kv))
+    weights = weights_like(np.random.default_rng(3), (batch.num_pages, Hkv, P))
+    plan = make_plan(batch, dev(batch.page_table))
+    pool = torch.arange(batch.num_pages * 2 * Hkv * P, device="cuda", dtype=torch.int32)   # every row its number
+    pool = pool.view(-1, 1).expand(-1, D // 2).contiguous().view(torch.bfloat16).view(batch.num_pages, 2, Hkv, P, D)
+    before, d_w = pool.clone(), dev(weights)
+    if in_place:
+        kept, out, w_out = plan.evict_kv(d_w, pool, budget, recent), pool, d_w
+        tables = [batch.page_table[batch.kv_indptr[b]:] for b in range(len(kv))]
+    else:
+        need = -(-plan.evicted_lens(budget) // P)
+        table = np.random.default_rng(7).permutation(int(need.sum())).astype(np.int32)
+        tables = np.split(table, np.cumsum(need)[:-1])
+        out = torch.zeros(len(table), 2, Hkv, P, D, dtype=torch.bfloat16, device="cuda")
+        w_out = torch.zeros(len(table), Hkv, P, device="cuda")
+        kept = plan.evict_kv(d_w, pool, budget, recent, page_table_out=dev(table), kv_out=out, weights_out=w_out)
+    assert plan.device_error() == 0
+    kept, out, before = kept.cpu().numpy(), out.view(torch.int32).cpu().numpy(), before.view(torch.int32).cpu().numpy()
+    w_out = w_out.cpu().numpy()
+    for b in range(len(kv)):
+        pages = batch.page_table[batch.kv_indptr[b]:batch.kv_indptr[b + 1]]
+        for g in range(Hkv):
+            w = weights[pages, g].reshape(-1)[:kv[b]]
+            want = ref.evict(w, kv[b], budget, recent)
+            np.testing.assert_array_equal(kept[b, g, :len(want)], want)
+            assert np.all(kept[b, g, len(want):] == -1)
+            j = np.arange(len(want))
+            to = np.asarray(tables[b])[j // P]
+            np.testing.assert_array_equal(w_out[to, g, j % P].view(np.uint32), w[want].view(np.uint32))
+            for half in (0, 1):
+                np.testing.assert_array_equal(out[to, half, g, j % P], before[pages[want // P], half, g, want % P])
 
 
 def test_evict_bad_pages():

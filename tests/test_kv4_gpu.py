@@ -186,6 +186,62 @@ def test_decode_split_sequences(D, P, num_sms):
     assert plan.device_error() == 0
 
 
+def test_decode_very_low_scores():
+    """All scores far below zero: the softmax shift follows them down, in every
+    warp, also in those that have no tokens; and rows whose scores rise or fall
+    by hundreds along the sequence."""
+    batch = batch_of([1, 1, 1], [33, 700, 700], 8, 1, 64, 16, seed=13, with_sinks=False)
+    rng = np.random.default_rng(1)
+    pool = ref.random_pool(rng, batch.num_pages, 1, 16, 64, spread=0.3)
+    codes = pool[..., :8 * 64]
+    codes[:, 0] = (codes[:, 0] & 0x77) | 0x00                      # K positive
+    q = np.abs(syn.bf16_to_float(batch.q))
+    q[0] *= -40                                                    # scores around -700
+    batch.q = syn.bf16_bits(q)
+    t = np.arange(700)
+    for b, up in ((1, 1), (2, -1)):
+        page = batch.page_table[batch.kv_indptr[b] + t // 16]
+        level = (20 + t * 50 // 700) if up > 0 else (70 - t * 50 // 700)
+        for k in range(4):
+            pool[page, 0, :, 0, 8 * 64 + (t % 16) * 4 + k] = level[:, None].astype(np.uint8)
+    ref.poison_unused(pool, batch)
+    plan = make_plan(batch, dev(batch.page_table))
+    lse = torch.empty(3, 8, device="cuda")
+    out, _ = plan.decode_kv4(dev_bf16(batch.q), dev(pool), lse=lse)
+    vals = ref.values(pool, 64)
+    want, want_lse, mag = ref.attention(batch, vals)
+    qf = syn.bf16_to_float(batch.q).astype(np.float64)
+    # 68 roundings of 2^-24 of sum |q k| in the exponent (all products have one sign here).
+    size = np.stack([np.abs(ref.gather(batch, vals, b, 0)[0] @ qf[b].T).max(0) for b in range(3)]) / 8
+    slack = 68 * 2.0 ** -24 * size
+    err = np.abs(out.double().cpu().numpy() - want)
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -12 + 2 * slack[..., None]) * mag + \
+        2.0 ** -32 * ref.value_sums(batch, vals) + 1e-30
+    assert np.all(err <= tol), float((err / tol).max())
+    assert np.all(np.abs(lse.double().cpu().numpy() - want_lse) <= 2.0 ** -12 + slack + 2.0 ** -22 * np.abs(want_lse))
+
+
+def test_decode_nan_stays_in_its_request_and_head():
+    """A NaN scale among a request's keys or values reaches that request's heads
+    of that KV head (for V, the 16 dims) and nothing else."""
+    batch = batch_of([1, 1], [100, 90], 4, 2, 64, 16, seed=17)
+    pool = ref.random_pool(np.random.default_rng(6), batch.num_pages, 2, 16, 64)
+    clean = pool.copy()
+    p0 = batch.page_table[batch.kv_indptr[0]]
+    pool[p0, 0, 0, 0, 8 * 64 + 5] = 0x7F                            # a K scale of head 0
+    pool[p0, 1, 1, 0, 8 * 64 + 4 * 3 + 2] = 0x7F                    # a V scale of head 1: dims 32..47
+    plan = make_plan(batch, dev(batch.page_table))
+    a, _ = plan.decode_kv4(dev_bf16(batch.q), dev(pool), dev(batch.sinks))
+    b, _ = plan.decode_kv4(dev_bf16(batch.q), dev(clean), dev(batch.sinks))
+    bad = torch.isnan(a)
+    assert torch.all(bad[0, :4]) and torch.all(bad[0, 4:, 32:48])
+    bad[0, :4], bad[0, 4:, 32:48] = False, False
+    assert not torch.any(bad)
+    same = torch.ones_like(bad)
+    same[0, :4], same[0, 4:, 32:48] = False, False
+    assert torch.equal(a[same], b[same])
+
+
 def test_decode_large_scores_and_sinks():
     """Scores that grow along the sequence (the running max moves again and
     again), sinks above and below everything, and heads of very different size."""
