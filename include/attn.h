@@ -426,7 +426,9 @@ ATTN_API attn_status attn_decode_kv4(attn_plan_t plan, const void* q, const void
  *   weights, prev  fp32 [num_pages][Hkv][page_size], device, paged like the
  *                  cache (prev may be weights; NULL when decay = 0).  Only the
  *                  slots of the plan's tokens are written; requests without
- *                  query rows are left out.
+ *                  query rows are left out.  A weight belongs to a page's slot:
+ *                  on a page that two requests of the plan share, which of
+ *                  the two requests' weights a slot holds is not defined.
  *   lse            fp32 [total_qo_rows][Hq];   decay finite, >= 0
  *   kv_cache       as in attn_decode;  kv4_cache, k_scale as in attn_decode_kv4
  * Decode and prefill rows alike.  The sum's order is fixed: equal calls give
@@ -490,6 +492,10 @@ ATTN_API attn_status attn_plan_get_info(attn_plan_t plan, attn_plan_info* info);
  */
 ATTN_API attn_status attn_plan_get_decode_units(attn_plan_t plan, int32_t* units, int64_t capacity);
 ATTN_API attn_status attn_plan_get_prefill_items(attn_plan_t plan, int32_t* items, int64_t capacity);
+
+/* The requests' kv_len (attn_plan's paged plans), at most `capacity` of them:
+ * what attn_evict_kv's page_table_out is sized by. */
+ATTN_API attn_status attn_plan_get_kv_lens(attn_plan_t plan, int32_t* kv_lens, int64_t capacity);
 
 /*
  * attn_plan_device_error -- wait for `stream`, then read and clear the plan's

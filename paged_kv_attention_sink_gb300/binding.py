@@ -75,6 +75,7 @@ def _declare(lib):
         "attn_plan_get_info": (st, [p, p]),
         "attn_plan_get_decode_units": (st, [p, p, i64]),
         "attn_plan_get_prefill_items": (st, [p, p, i64]),
+        "attn_plan_get_kv_lens": (st, [p, p, i64]),
         "attn_plan_device_error": (st, [p, p, p]),
         "attn_plan_destroy": (None, [p]),
         "attn_status_string": (ctypes.c_char_p, [st]),
@@ -208,7 +209,7 @@ class Plan:
         self.total_rows = int(qo[-1]) if len(qo) else 0
         handle = ctypes.c_void_p()
         ws_bytes = ctypes.c_size_t()
-        self._kv, self._kv_lens = (kv.copy(), lpl.copy()), None
+        self._kv_lens = None
         _check("attn_plan", lib.attn_plan(
             qo.ctypes.data, kv.ctypes.data, _ptr(page_table), lpl.ctypes.data, self.batch, num_qo_heads,
             num_kv_heads, head_dim, page_size, int(self.causal), self.sm_scale, int(num_pages),
@@ -234,12 +235,12 @@ class Plan:
 
     @property
     def kv_lens(self) -> np.ndarray:
-        """Cached tokens of each request."""
+        """Cached tokens of each request (read-only)."""
         if self._kv_lens is None:
-            kv, lpl = self._kv
-            pages = np.diff(kv)
-            self._kv_lens = np.where(pages > 0, (pages - 1) * self.page_size + lpl[:self.batch], 0)
-            self._kv_lens.flags.writeable = False
+            lens = np.zeros(self.batch, dtype=np.int32)
+            _check("attn_plan_get_kv_lens", load_library().attn_plan_get_kv_lens(self._handle, lens.ctypes.data, self.batch))
+            lens.flags.writeable = False
+            self._kv_lens = lens
         return self._kv_lens
 
     def info(self) -> dict:

@@ -354,6 +354,13 @@ extern "C" attn_status attn_plan_get_prefill_items(attn_plan_t plan, int32_t* it
     return ATTN_OK;
 }
 
+extern "C" attn_status attn_plan_get_kv_lens(attn_plan_t plan, int32_t* kv_lens, int64_t capacity) {
+    if (!plan || plan->ragged || plan->graph || (!kv_lens && capacity > 0) || capacity < 0) return ATTN_ERR_INVALID_ARG;
+    const int64_t n = std::min<int64_t>(capacity, (int64_t)plan->requests.size());
+    for (int64_t b = 0; b < n; ++b) kv_lens[b] = plan->requests[b].kv_len;
+    return ATTN_OK;
+}
+
 extern "C" void attn_plan_destroy(attn_plan_t plan) { delete plan; }
 
 extern "C" const char* attn_status_string(attn_status status) {

@@ -43,6 +43,17 @@ def test_unbound_null_ragged_and_graph_plans_are_refused(lib):
         lib.attn_plan_destroy(h)
 
 
+def test_kv_lens(lib):
+    st, h, _ = plan(lib, [1, 0, 5, 0], [3, 0, 1, 7], [4, 0, 16, 1])
+    lens = np.full(5, -9, dtype=np.int32)
+    assert lib.attn_plan_get_kv_lens(h, lens.ctypes.data, 4) == OK
+    assert lens.tolist() == [36, 0, 16, 97, -9]
+    assert lib.attn_plan_get_kv_lens(h, lens.ctypes.data, -1) == INVALID
+    assert lib.attn_plan_get_kv_lens(h, None, 2) == INVALID
+    assert lib.attn_plan_get_kv_lens(None, lens.ctypes.data, 2) == INVALID
+    lib.attn_plan_destroy(h)
+
+
 @pytest.mark.parametrize("bad", [0.0, -1.0, 1.5, float("nan"), float("inf"), 2.0 ** 41, 2.0 ** -41])
 def test_pool_scales_are_powers_of_two(lib, bad):
     st, h, _ = plan(lib, [1], [2], [4])
