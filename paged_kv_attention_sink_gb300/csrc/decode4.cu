@@ -122,7 +122,8 @@ decode4_sink_attn_kernel(const Decode4Args a) {
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gq = lane >> 2, tq = lane & 3;
-    const DecodeUnit u = a.units[blockIdx.x];
+    const DecodeUnit u = a.units[blockIdx.x];   // uploaded before the kernels this one may overlap
+    ptx::grid_dependency_wait();
     const int first_page = u.tok_begin >> a.page_log2;
     const int n_pages = ((u.tok_end - 1) >> a.page_log2) - first_page + 1;
     load_sixteens(first_s, a.page_table + u.page_base + first_page, n_pages, a.num_pages, a.Hkv, u.kv_head, a.page_log2, a.err);
@@ -281,6 +282,10 @@ decode4_sink_attn_kernel(const Decode4Args a) {
         s = s + 1 == C::kStages ? 0 : s + 1;
     }
 
+    // Only now: CTAs of the next grid that start while this one is in its loop
+    // crowd onto the SMs that are done first.
+    ptx::grid_dependents_go();
+
     // This warp's state into its own ring: O by head and dim.  Lane (gq, tq)
     // holds dims gq * D / 8 + {0 .. D / 8 - 1} of heads 2 tq and 2 tq + 1.
     __syncwarp();
@@ -390,8 +395,7 @@ cudaError_t launch(const Decode4Args& args, int grid, cudaStream_t stream) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Decode4Cfg<D, NT>::kSmem);
     });
     if (e != cudaSuccess) return e;
-    kernel<<<grid, Decode4Cfg<D, NT>::kWarps * 32, Decode4Cfg<D, NT>::kSmem, stream>>>(args);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3(grid), Decode4Cfg<D, NT>::kWarps * 32, Decode4Cfg<D, NT>::kSmem, stream, args);
 }
 
 }  // namespace

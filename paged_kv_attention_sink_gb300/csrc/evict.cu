@@ -29,6 +29,7 @@
 #include "attn_internal.h"
 #include "kernels.h"
 #include "kv4.cuh"
+#include "ptx.cuh"
 
 namespace attn {
 namespace {
@@ -88,10 +89,10 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     __shared__ int sh_total[kWarps];
     __shared__ int sh_bucket, sh_above;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // The move kernel may be launched now; it waits for this grid to finish.
-    asm volatile("griddepcontrol.launch_dependents;");
+    ptx::grid_dependents_go();
     const int b = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv;
-    const RequestInfo r = a.requests[b];
+    const RequestInfo r = a.requests[b];   // uploaded before the kernels this one may overlap
+    ptx::grid_dependency_wait();
     const int n = r.kv_len, keep = min(n, a.budget), P = 1 << a.page_log2;
     int32_t* kept = a.kept + ((int64_t)b * a.Hkv + g) * a.budget;
     for (int j = keep + tid; j < a.budget; j += kThreads) kept[j] = -1;
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     constexpr int kRows = 32 / kPieces;                     // rows a warp copies per instruction
     using Scales = std::conditional_t<D == 64, uint32_t, uint2>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");      // kept is complete and visible
+    ptx::grid_dependency_wait();                            // kept is complete and visible
     const int half = blockIdx.x & 1, g = (blockIdx.x >> 1) % a.Hkv, b = (blockIdx.x >> 1) / a.Hkv;
     const RequestInfo r = a.requests[b];
     const int keep = min(r.kv_len, a.budget), P = 1 << a.page_log2;
@@ -346,6 +347,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
         if (kFour && dst_sc >= 0) *reinterpret_cast<Scales*>(a.pool_out + dst_sc) = sc;
         if (kInPlace) __syncthreads();   // the next step may read what this one wrote over only after it is done
     }
+    ptx::grid_dependents_go();
 }
 
 template <int kThreads>
@@ -357,22 +359,14 @@ attn_status launch_select(const EvictArgs& a, int longest, int most, cudaStream_
             return cudaFuncSetAttribute(evict_select_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, most * 4);
         }) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    evict_select_kernel<kThreads><<<a.batch * a.Hkv, kThreads, x.chunk * 4, stream>>>(x);
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return launch_dependent(evict_select_kernel<kThreads>, dim3(a.batch * a.Hkv), kThreads, x.chunk * 4, stream, x) == cudaSuccess
+               ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 template <int D, bool kFour, bool kInPlace>
 attn_status launch_move(const EvictArgs& a, int splits, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.batch * a.Hkv * 2, splits);
-    cfg.blockDim = dim3(kMoveThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see griddepcontrol in both kernels
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_move_kernel<D, kFour, kInPlace>, a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return launch_dependent(evict_move_kernel<D, kFour, kInPlace>, dim3(a.batch * a.Hkv * 2, splits), kMoveThreads, 0, stream,
+                            a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace

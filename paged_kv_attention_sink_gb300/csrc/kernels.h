@@ -3,9 +3,32 @@
 
 #include <cuda_runtime.h>
 
+#include <utility>
+
 #include "attn_internal.h"
 
 namespace attn {
+
+// Launches a kernel as the programmatic dependent of the one before it on the
+// stream: its CTAs may start while that one's last are running.  Every CTA of
+// such a kernel calls ptx::grid_dependency_wait() before it reads or writes
+// anything that other kernels do, and before it exits; ptx::grid_dependents_go()
+// lets the kernel after it start in the same way.
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
 
 // kv_map / q_map point at CUtensorMap objects built by the API layer.
 attn_status launch_decode(attn_plan_s* plan, const void* q, const void* kv_map, const float* sinks,

@@ -113,7 +113,8 @@ key_weights_step_kernel(const KeyWeightArgs a) {
     uint32_t* first_s = reinterpret_cast<uint32_t*>(smem + C::kPipeBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gq = lane >> 2, tq = lane & 3;
-    const DecodeUnit u = a.units[blockIdx.x];
+    const DecodeUnit u = a.units[blockIdx.x];   // uploaded before the kernels this one may overlap
+    ptx::grid_dependency_wait();
     const int G = a.Hq / a.Hkv, P = a.P;
     if (u.head0 != u.kv_head * G) return;   // the unit of the first head slice takes all heads
     const int first_page = u.tok_begin >> a.page_log2;
@@ -234,6 +235,9 @@ key_weights_step_kernel(const KeyWeightArgs a) {
             if (at >= 0) a.weights[at] = fmaf(a.decay, before[t], sum);
         }
     }
+    // Only now: CTAs of the next grid that start while this one is in its loop
+    // crowd onto the SMs that are done first.
+    ptx::grid_dependents_go();
 }
 
 // ----------------------------------------------------------- prefill requests
@@ -321,6 +325,8 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    ptx::grid_dependents_go();     // with this grid's TMEM in hand: a dependent that allocates too waits for it
+    ptx::grid_dependency_wait();   // up to here only the plan's own lists were read
 
     if (warp == C::kEpilogueWarps + 1) {
         // ------------------------------------------------------------ producer
@@ -579,8 +585,7 @@ cudaError_t launch_step(const KeyWeightArgs& a, int grid, cudaStream_t stream) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kDecodeWarps * 32, C::kSmem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3(grid), kDecodeWarps * 32, C::kSmem, stream, a);
 }
 
 template <int D, bool kFour>
@@ -593,8 +598,7 @@ cudaError_t launch_prompt(const CUtensorMap& q_map, const CUtensorMap& kv_map, c
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (e != cudaSuccess) return e;
-    kernel<<<grid, C::kThreads, C::kSmem, stream>>>(q_map, kv_map, a);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3(grid), C::kThreads, C::kSmem, stream, q_map, kv_map, a);
 }
 
 template <int D, bool kFour>

@@ -75,6 +75,8 @@ append_kv4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_n
                   const int2* __restrict__ slots, const int32_t* __restrict__ page_table, int64_t rows, int32_t Hkv,
                   int32_t page_log2, int32_t num_pages, float k_scale, float inv_k, float v_scale, float inv_v,
                   int32_t* err) {
+    ptx::grid_dependents_go();
+    ptx::grid_dependency_wait();
     constexpr int kGroups = D / kKv4Group, kSub = kv4_sub_bytes(D);
     const int32_t per_half = Hkv * kGroups, per_row = 2 * per_half;
     const int64_t i = (int64_t)blockIdx.x * kKv4Threads + threadIdx.x, step = (int64_t)gridDim.x * kKv4Threads;
@@ -130,6 +132,8 @@ template <int D>
 __global__ void __launch_bounds__(kKv4Threads)
 expand_kv4_kernel(const uint8_t* __restrict__ pool, uint4* __restrict__ buf, const int32_t* __restrict__ page_ids,
                   int64_t n, int32_t Hkv, int32_t P, int64_t num_pages, float k_scale, float v_scale, int32_t* err) {
+    ptx::grid_dependents_go();
+    ptx::grid_dependency_wait();
     constexpr int kOctets = D / 8, kSub = kv4_sub_bytes(D), kPerSub = kKv4Tokens * kOctets;
     const int32_t per_half = Hkv * P * kOctets, half_subs = Hkv * (P / kKv4Tokens);
     const int64_t step = (int64_t)gridDim.x * kKv4Threads, step_halves = step / per_half;
@@ -182,16 +186,13 @@ attn_status launch_append_kv4(attn_plan_s* plan, const void* k_new, const void* 
     // left a third of the last wave idle.
     const int grid = kv4_grid(rows * 2 * plan->Hkv * (plan->D / kKv4Group), 5);
     if (grid == 0) return ATTN_ERR_CUDA;
-    auto run = [&](auto kernel) {
-        kernel<<<grid, kKv4Threads, 0, stream>>>(
-            static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), static_cast<uint8_t*>(kv4_cache),
-            reinterpret_cast<const int2*>(plan->ws + plan->layout.append), plan->page_table, rows, plan->Hkv,
-            31 - __builtin_clz(plan->P), plan->num_pages, k_scale, 1.f / k_scale, v_scale, 1.f / v_scale,
-            reinterpret_cast<int32_t*>(plan->ws + plan->layout.err));
-    };
-    if (plan->D == 64) run(append_kv4_kernel<64>);
-    else run(append_kv4_kernel<128>);
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    const cudaError_t e = launch_dependent(
+        plan->D == 64 ? append_kv4_kernel<64> : append_kv4_kernel<128>, dim3(grid), kKv4Threads, 0, stream,
+        static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), static_cast<uint8_t*>(kv4_cache),
+        reinterpret_cast<const int2*>(plan->ws + plan->layout.append), plan->page_table, rows, plan->Hkv,
+        31 - __builtin_clz(plan->P), plan->num_pages, k_scale, 1.f / k_scale, v_scale, 1.f / v_scale,
+        reinterpret_cast<int32_t*>(plan->ws + plan->layout.err));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 attn_status launch_expand_kv4(const void* kv4_cache, void* buf, const int32_t* page_ids, int64_t n, int64_t num_pages,
@@ -200,13 +201,10 @@ attn_status launch_expand_kv4(const void* kv4_cache, void* buf, const int32_t* p
     if (n == 0) return ATTN_OK;
     const int grid = kv4_grid(n * 2 * Hkv * P * (D / 8), 8);
     if (grid == 0) return ATTN_ERR_CUDA;
-    auto run = [&](auto kernel) {
-        kernel<<<grid, kKv4Threads, 0, stream>>>(static_cast<const uint8_t*>(kv4_cache), static_cast<uint4*>(buf),
-                                                 page_ids, n, Hkv, P, num_pages, k_scale, v_scale, err);
-    };
-    if (D == 64) run(expand_kv4_kernel<64>);
-    else run(expand_kv4_kernel<128>);
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    const cudaError_t e = launch_dependent(D == 64 ? expand_kv4_kernel<64> : expand_kv4_kernel<128>, dim3(grid), kKv4Threads,
+                                           0, stream, static_cast<const uint8_t*>(kv4_cache), static_cast<uint4*>(buf),
+                                           page_ids, n, Hkv, P, num_pages, k_scale, v_scale, err);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace attn

@@ -86,6 +86,12 @@ __device__ __forceinline__ bool elect_one() {
     return pred != 0;
 }
 
+// --------------------------------------------------- programmatic dependents
+// All memory operations of the kernels before this one are visible after it.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel on the stream may start once every CTA has called this.
+__device__ __forceinline__ void grid_dependents_go() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // ------------------------------------------------------------------- fences
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

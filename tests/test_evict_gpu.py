@@ -485,3 +485,58 @@ def test_another_stream():
     s.synchronize()
     check_decode(batch, pool, out, lse)
     assert int(kept[0, 0, -1]) == 299 and int(kept[1, 1, -1]) == 49
+
+
+def test_captured_branches():
+    """Kernels of two branches of one graph, with copies and fills between them,
+    each after what it reads: equal to the same calls one after the other."""
+    batch = batch_of([1, 1, 1], [700, 33, 1500], 8, 2, 64, 16, seed=33)
+    pool, d_pool, _ = pools(batch, True, 9)
+    plan = make_plan(batch, dev(batch.page_table))
+    q, q_next = dev_bf16(batch.q), torch.empty_like(dev_bf16(batch.q))
+    k_new, v_new = (dev_bf16(x) for x in syn.new_kv_rows(batch, 1))
+    sinks, budget = dev(batch.sinks), 40
+    pages = dev(batch.page_table)
+    bufs = dict(out=torch.empty_like(q), lse=torch.empty(3, 16, device="cuda"),
+                weights=torch.zeros(batch.num_pages, 2, 16, device="cuda"),
+                kept=torch.empty(3, 2, budget, dtype=torch.int32, device="cuda"),
+                back=torch.empty(len(pages), 2, 2, 16, 64, dtype=torch.bfloat16, device="cuda"))
+
+    def calls(side):
+        main = torch.cuda.current_stream()
+        bufs["weights"].zero_()
+        plan.append_kv4(k_new, v_new, d_pool)
+        if side is not None:
+            side.wait_stream(main)
+        with torch.cuda.stream(side if side is not None else main):
+            q_next.copy_(q)
+            binding().attn_expand_kv4(d_pool, pages, 64, buf=bufs["back"])
+            q_next.mul_(0.5)
+        plan.decode_kv4(q, d_pool, sinks, bufs["out"], bufs["lse"])
+        plan.key_weights_kv4(q, d_pool, bufs["lse"], bufs["weights"], prev=bufs["weights"], decay=0.5)
+        if side is not None:
+            main.wait_stream(side)
+        plan.decode_kv4(q_next, d_pool, sinks, bufs["out"], bufs["lse"])
+        plan.key_weights_kv4(q_next, d_pool, bufs["lse"], bufs["weights"], prev=bufs["weights"], decay=0.5)
+        plan.evict_kv4(bufs["weights"], d_pool, budget, 8, kept=bufs["kept"])
+
+    first_pool = d_pool.clone()
+    calls(None)
+    torch.cuda.synchronize()
+    want, want_pool = {k: t.clone() for k, t in bufs.items()}, d_pool.clone()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(main):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=main):
+            calls(side)
+    for _ in range(3):
+        d_pool.copy_(first_pool)
+        for t in bufs.values():
+            t.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(d_pool, want_pool)
+        for k, t in bufs.items():
+            assert torch.equal(t.view(torch.uint8), want[k].view(torch.uint8)), k
+    assert plan.device_error() == 0
