@@ -53,12 +53,16 @@ struct EvictArgs {
 
 // Unsigned keys in the weights' order: NaN lowest, -0 equal to +0.
 __device__ __forceinline__ uint32_t order_key(float w) {
-    if (w != w) return 0;
-    const uint32_t u = w == 0.f ? 0u : __float_as_uint(w);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    const int32_t u = __float_as_int(w + 0.f);   // -0 + 0 = +0
+    return w == w ? (uint32_t)u ^ ((uint32_t)(u >> 31) | 0x80000000u) : 0u;
 }
 
-constexpr uint32_t kZeroKey = 0x80000000u;   // of a weight of 0
+// The weight of a key.
+__device__ __forceinline__ float key_weight(uint32_t k) {
+    return __uint_as_float(k ^ (~(uint32_t)((int32_t)k >> 31) | 0x80000000u));
+}
+
+constexpr uint32_t kZeroKey = 0x80000000u, kLowestKey = 0x007FFFFFu, kInfKey = 0xFF800000u;   // of 0, -inf and +inf
 
 // First output page slot of request b (pages of the requests before it); the
 // lanes of a warp share the work.
@@ -84,7 +88,7 @@ template <int kThreads>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a) {
     constexpr int kWarps = kThreads / 32;
     extern __shared__ __align__(16) float w_s[];   // [chunk] weights
-    __shared__ int hist[kDigits];
+    __shared__ __align__(16) int hist[kDigits];
     __shared__ int2 sh_count[kWarps];     // a warp's range: larger keys, equal keys
     __shared__ int sh_total[kWarps];
     __shared__ int sh_bucket, sh_above;
@@ -131,6 +135,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
         }
         __syncthreads();
     };
+    for (int i = tid; i < kDigits; i += kThreads) hist[i] = 0;   // a barrier follows in load()
     const bool fits = n <= a.chunk;
     if (fits) load(0, n);
 
@@ -140,20 +145,28 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     if (select) {
         for (int shift = 32 - kDigitBits;; shift = max(0, shift - kDigitBits)) {
             const int bits = shift == 0 ? 32 - 2 * kDigitBits : kDigitBits;
-            for (int i = tid; i < kDigits; i += kThreads) hist[i] = 0;
-            __syncthreads();
             for (int t0 = 0; t0 < old; t0 += a.chunk) {
                 const int t1 = min(old, t0 + a.chunk);
                 if (!fits) load(t0, t1);
-                const uint32_t mask = (1u << bits) - 1, want_high = shift + bits == 32 ? 0 : prefix >> (shift + bits);
+                const uint32_t mask = (1u << bits) - 1;
+                // Of the digits above this one the weight must have the prefix's:
+                // it lies in a range of weights.  The range test is by value and
+                // lets a zero of either sign into the range next to it; the few
+                // weights that pass are tested by their keys.  (Below -inf there
+                // are only NaNs, above +inf nothing.)
+                const int high = shift + bits;
+                const uint32_t above_mask = high == 32 ? 0u : ~0u << high;
+                const bool all = high == 32 || prefix < kLowestKey;
+                const float least = key_weight(prefix), most = key_weight(min(prefix | ~above_mask, kInfKey));
                 int zeros = 0;   // weights of exactly 0 (keys never attended to) are many: one addition for all of a warp's
                 for (int t = t0 + tid * 4; t < t1; t += kThreads * 4) {
                     const float4 w = *reinterpret_cast<const float4*>(w_s + t - t0);
                     const float v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
+                        if (!(all || (v[e] >= least && v[e] <= most))) continue;
                         const uint32_t k = order_key(v[e]);
-                        if (t + e >= t1 || (shift + bits < 32 && k >> (shift + bits) != want_high)) continue;
+                        if (((k ^ prefix) & above_mask) || t + e >= t1) continue;
                         if (k == kZeroKey) ++zeros;
                         else atomicAdd(&hist[(k >> shift) & mask], 1);
                     }
@@ -162,14 +175,17 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
                 if (lane == 0 && zeros) atomicAdd(&hist[(kZeroKey >> shift) & mask], zeros);
             }
             __syncthreads();
-            // The bucket that the ties-th largest falls into: each thread sums a
-            // run of buckets, from the top; then the runs before it.
-            constexpr int kRun = (kDigits + kThreads - 1) / kThreads;
+            // The bucket that the ties-th largest falls into: each thread sums (and
+            // clears) a run of buckets, from the top; then the runs before it.
+            constexpr int kRun = kDigits / kThreads;
             int c[kRun], sum = 0;
 #pragma unroll
-            for (int i = 0; i < kRun; ++i) {
-                const int d = kDigits - 1 - (tid * kRun + i);
-                sum += c[i] = d >= 0 ? hist[d] : 0;
+            for (int i = 0; i < kRun; i += 2) {
+                int2* at = reinterpret_cast<int2*>(hist + kDigits - 2 - (tid * kRun + i));
+                c[i] = at->y;
+                c[i + 1] = at->x;
+                *at = make_int2(0, 0);
+                sum += c[i] + c[i + 1];
             }
             int inc = sum;
             for (int o = 1; o < 32; o <<= 1) {
@@ -178,8 +194,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
             }
             if (lane == 31) sh_total[warp] = inc;
             __syncthreads();
-            int above = inc - sum;
-            for (int w = 0; w < warp; ++w) above += sh_total[w];
+            const int above_warp = __reduce_add_sync(0xffffffffu, lane < warp ? sh_total[lane] : 0);
+            int above = above_warp + inc - sum;
             if (above < ties && above + sum >= ties) {
 #pragma unroll
                 for (int i = 0; i < kRun; ++i) {
@@ -195,7 +211,6 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
             prefix |= (uint32_t)sh_bucket << shift;
             ties -= sh_above;
             if (shift == 0) break;
-            __syncthreads();
         }
     }
     // Kept: keys > prefix, and of those equal to it the first `ties`.
@@ -208,19 +223,25 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
         const int per = ((t1 - t0 + 127) / 128 + kWarps - 1) / kWarps * 128;
         const int r0 = min(t1, t0 + warp * per), r1 = min(t1, r0 + per);
         // Bits 0-3: token t + e is kept by its key; 4-7: its key equals the threshold.
+        // (By value, as the keys are ordered; below -inf there are only NaNs.)
+        const float threshold = key_weight(prefix);
+        const bool of_nans = prefix < kLowestKey;
         auto classify = [&](int t, const float (&v)[4]) {
             uint32_t c = 0;
+            if (select && !of_nans) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (t + e >= r1) continue;
-                if (t + e >= old || want == old) {
-                    c |= 1u << e;
-                } else if (select) {
-                    const uint32_t k = order_key(v[e]);
-                    c |= k > prefix ? 1u << e : k == prefix ? 16u << e : 0u;
-                }
+                for (int e = 0; e < 4; ++e) c |= v[e] > threshold ? 1u << e : v[e] == threshold ? 16u << e : 0u;
+            } else if (select) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c |= v[e] == v[e] ? 1u << e : 16u << e;
+            } else if (want == old) {
+                c = 15u;
             }
-            return c;
+            if (t + 4 > old) {   // the newest are kept
+                const uint32_t newest = 15u & ~0u << max(0, old - t);
+                c = (c & ~(newest * 17u)) | newest;
+            }
+            return t + 4 > r1 ? c & (17u * ((1u << max(0, r1 - t)) - 1)) : c;
         };
         auto four = [&](int t, float (&v)[4]) {
             const float4 w = t < r1 ? *reinterpret_cast<const float4*>(w_s + t - t0) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -238,16 +259,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
         n_eq = __reduce_add_sync(0xffffffffu, n_eq);
         if (lane == 0) sh_count[warp] = make_int2(n_gt, n_eq);
         __syncthreads();
-        int before_gt = greater, before_eq = equal;
-        for (int w = 0; w < kWarps; ++w) {
-            const int2 c = sh_count[w];
-            if (w < warp) {
-                before_gt += c.x;
-                before_eq += c.y;
-            }
-            greater += c.x;
-            equal += c.y;
-        }
+        const int2 count = lane < kWarps ? sh_count[lane] : make_int2(0, 0);
+        int before_gt = greater + __reduce_add_sync(0xffffffffu, lane < warp ? count.x : 0);
+        int before_eq = equal + __reduce_add_sync(0xffffffffu, lane < warp ? count.y : 0);
+        greater += __reduce_add_sync(0xffffffffu, count.x);
+        equal += __reduce_add_sync(0xffffffffu, count.y);
         for (int s = r0; s < r1; s += 128) {
             const int t = s + lane * 4;
             float v[4];

@@ -540,3 +540,30 @@ def test_captured_branches():
         for k, t in bufs.items():
             assert torch.equal(t.view(torch.uint8), want[k].view(torch.uint8)), k
     assert plan.device_error() == 0
+
+
+@pytest.mark.parametrize("n,budget,recent", [(700, 1, 0), (700, 130, 3), (700, 350, 0), (700, 520, 64), (700, 699, 0),
+                                             (20000, 9000, 100), (20000, 17000, 1)])
+def test_evict_orders_all_values(n, budget, recent):
+    """Weights of either sign and size, zeros of either sign, infinities and
+    NaNs, each many times; and no others but one value."""
+    rng = np.random.default_rng(n + budget)
+    some = np.array([-np.inf, -3e38, -1.0, -1e-38, -1e-45, -0.0, 0.0, 1e-45, 1e-38, 1.0, np.nextafter(np.float32(1), 2),
+                     3e38, np.inf, np.nan], dtype=np.float32)
+    Hkv, P = len(some) + 3, 16
+    pages = -(-n // P)
+    flat = np.full((Hkv, pages * P), np.nan, dtype=np.float32)
+    flat[:3, :n] = rng.choice(some, (3, n))
+    flat[3:, :n] = some[:, None]
+    batch = batch_of([1], [n], 1, Hkv, 64, P)
+    plan = make_plan(batch, dev(batch.page_table))
+    host = np.zeros((batch.num_pages, Hkv, P), dtype=np.float32)
+    host[batch.page_table] = flat.reshape(Hkv, pages, P).transpose(1, 0, 2)
+    pool = torch.zeros(batch.num_pages, 2, Hkv, P, 64, dtype=torch.bfloat16, device="cuda")
+    w = dev(host)
+    kept = plan.evict_kv(w, pool, budget, recent).cpu().numpy()[0]
+    moved = w.cpu().numpy()[batch.page_table].transpose(1, 0, 2).reshape(Hkv, -1)
+    for g in range(Hkv):
+        want = ref.evict(flat[g], n, budget, recent)
+        np.testing.assert_array_equal(kept[g], want, err_msg=str(g))
+        np.testing.assert_array_equal(moved[g, :budget].view(np.uint32), flat[g, want].view(np.uint32), err_msg=str(g))
