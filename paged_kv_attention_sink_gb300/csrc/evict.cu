@@ -34,7 +34,8 @@
 namespace attn {
 namespace {
 
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 256, kBothThreads = 512;
+constexpr int kBothChunk = 11 * 1024;
 constexpr int kDigitBits = 11, kDigits = 1 << kDigitBits;   // radix passes over 11, 11 and 10 bits
 
 struct EvictArgs {
@@ -84,8 +85,9 @@ __device__ __forceinline__ int out_page(const EvictArgs& a, const RequestInfo& r
     return -1;
 }
 
+// One request and KV head, by all threads of a CTA.
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a) {
+__device__ __forceinline__ void select_tokens(const EvictArgs& a, const RequestInfo& r, int b, int g) {
     constexpr int kWarps = kThreads / 32;
     extern __shared__ __align__(16) float w_s[];   // [chunk] weights
     __shared__ __align__(16) int hist[kDigits];
@@ -93,10 +95,6 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     __shared__ int sh_total[kWarps];
     __shared__ int sh_bucket, sh_above;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    ptx::grid_dependents_go();
-    const int b = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv;
-    const RequestInfo r = a.requests[b];   // uploaded before the kernels this one may overlap
-    ptx::grid_dependency_wait();
     const int n = r.kv_len, keep = min(n, a.budget), P = 1 << a.page_log2;
     int32_t* kept = a.kept + ((int64_t)b * a.Hkv + g) * a.budget;
     for (int j = keep + tid; j < a.budget; j += kThreads) kept[j] = -1;
@@ -299,18 +297,19 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     }
 }
 
-// grid (requests x KV heads x K/V, splits): the warps of a split's CTAs take
-// every gridDim.y-th run of 32 kept tokens per warp (one split in place).
+// Kept rows of one request, KV head and K/V half, by `warps` warps of which this
+// is number `warp`: 32 at a time per warp, `skip` from one step to the next, the
+// copies of kBatch instructions on their way together.  In place all warps of
+// the CTA take part and a step's rows are read before any is written.
 // kFour: the rows also have D / 16 scale bytes.
-template <int D, bool kFour, bool kInPlace>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
+template <int D, bool kFour, bool kInPlace, int kBatch = (kFour ? D / 2 : D * 2) / 16>
+__device__ __forceinline__ void move_rows(const EvictArgs& a, const RequestInfo& r, int b, int g, int half, int warp,
+                                          int first, int skip) {
     constexpr int kPieces = (kFour ? D / 2 : D * 2) / 16;   // 16-byte pieces of a row's values
     constexpr int kRows = 32 / kPieces;                     // rows a warp copies per instruction
+    static_assert(kPieces % kBatch == 0 && (!kInPlace || kBatch == kPieces), "whole batches");
     using Scales = std::conditional_t<D == 64, uint32_t, uint2>;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    ptx::grid_dependency_wait();                            // kept is complete and visible
-    const int half = blockIdx.x & 1, g = (blockIdx.x >> 1) % a.Hkv, b = (blockIdx.x >> 1) / a.Hkv;
-    const RequestInfo r = a.requests[b];
+    const int lane = threadIdx.x & 31;
     const int keep = min(r.kv_len, a.budget), P = 1 << a.page_log2;
     if (keep == 0) return;
     const int64_t base = out_page_base(a, b, lane);
@@ -323,8 +322,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
         else
             return ((block << a.page_log2) + row) * (D * 2);
     };
-    constexpr int kChunk = kMoveThreads;                    // rows of a CTA's step, 32 a warp
-    for (int c0 = blockIdx.y * kChunk; c0 < keep; c0 += gridDim.y * kChunk) {
+    for (int c0 = first; c0 < keep; c0 += skip) {
         // Lane l looks up row l of the warp's 32.
         const int j = c0 + warp * 32 + lane;
         int64_t src = -1, dst = -1;
@@ -347,22 +345,57 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
                 }
             }
         }
-        uint4 x[kPieces];
-        int64_t to[kPieces];
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-            const int row = k * kRows + lane / kPieces;
-            const int64_t from = __shfl_sync(0xffffffffu, src, row);
-            to[k] = __shfl_sync(0xffffffffu, dst, row);
-            if (from >= 0) x[k] = *reinterpret_cast<const uint4*>(a.pool + from + lane % kPieces * 16);
+        for (int k0 = 0; k0 < kPieces; k0 += kBatch) {
+            uint4 x[kBatch];
+            int64_t to[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int row = (k0 + k) * kRows + lane / kPieces;
+                const int64_t from = __shfl_sync(0xffffffffu, src, row);
+                to[k] = __shfl_sync(0xffffffffu, dst, row);
+                if (from >= 0) x[k] = *reinterpret_cast<const uint4*>(a.pool + from + lane % kPieces * 16);
+            }
+            if (kInPlace) __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (to[k] >= 0) *reinterpret_cast<uint4*>(a.pool_out + to[k] + lane % kPieces * 16) = x[k];
         }
-        if (kInPlace) __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k)
-            if (to[k] >= 0) *reinterpret_cast<uint4*>(a.pool_out + to[k] + lane % kPieces * 16) = x[k];
         if (kFour && dst_sc >= 0) *reinterpret_cast<Scales*>(a.pool_out + dst_sc) = sc;
         if (kInPlace) __syncthreads();   // the next step may read what this one wrote over only after it is done
     }
+}
+
+// grid: requests x KV heads
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a) {
+    ptx::grid_dependents_go();
+    const int b = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv;
+    const RequestInfo r = a.requests[b];   // uploaded before the kernels this one may overlap
+    ptx::grid_dependency_wait();
+    select_tokens<kThreads>(a, r, b, g);
+}
+
+// grid (requests x KV heads x K/V, splits; one split in place)
+template <int D, bool kFour, bool kInPlace>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
+    const int half = blockIdx.x & 1, g = (blockIdx.x >> 1) % a.Hkv, b = (blockIdx.x >> 1) / a.Hkv;
+    const RequestInfo r = a.requests[b];
+    ptx::grid_dependency_wait();           // kept is complete and visible
+    move_rows<D, kFour, kInPlace>(a, r, b, g, half, threadIdx.x >> 5, blockIdx.y * kMoveThreads, gridDim.y * kMoveThreads);
+    ptx::grid_dependents_go();
+}
+
+// Both for the same request and head, out of place; grid: requests x KV heads.
+// Half of the warps move K, the others V.
+template <int D, bool kFour>
+__global__ void __launch_bounds__(kBothThreads, 3) evict_both_kernel(const EvictArgs a) {
+    const int b = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv, warp = threadIdx.x >> 5;
+    const RequestInfo r = a.requests[b];   // uploaded before the kernels this one may overlap
+    ptx::grid_dependency_wait();
+    select_tokens<kBothThreads>(a, r, b, g);
+    __syncthreads();                       // kept is complete
+    move_rows<D, kFour, false, (kFour ? D / 2 : D * 2) / 16 < 4 ? 2 : 4>(a, r, b, g, warp & 1, warp >> 1, 0, kBothThreads / 2);
     ptx::grid_dependents_go();
 }
 
@@ -377,6 +410,19 @@ attn_status launch_select(const EvictArgs& a, int longest, int most, cudaStream_
         return ATTN_ERR_CUDA;
     return launch_dependent(evict_select_kernel<kThreads>, dim3(a.batch * a.Hkv), kThreads, x.chunk * 4, stream, x) == cudaSuccess
                ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+template <int D, bool kFour>
+attn_status launch_both(const EvictArgs& a, int longest, cudaStream_t stream) {
+    EvictArgs x = a;
+    x.chunk = std::max(32, std::min((longest + 31) / 32 * 32, kBothChunk));
+    static std::atomic<bool> configured[kMaxDevices];
+    if (once_per_device(configured, [&] {
+            return cudaFuncSetAttribute(evict_both_kernel<D, kFour>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBothChunk * 4);
+        }) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+    return launch_dependent(evict_both_kernel<D, kFour>, dim3(a.batch * a.Hkv), kBothThreads, x.chunk * 4, stream, x) ==
+                   cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 template <int D, bool kFour, bool kInPlace>
@@ -416,14 +462,18 @@ attn_status launch_evict(attn_plan_s* plan, bool four, const float* weights, con
     int32_t sms = 0;
     if (!current_sm_count(&sms)) return ATTN_ERR_CUDA;
     const bool few = (int64_t)plan->batch * plan->Hkv <= sms;
+    const bool in_place = !page_table_out;
+    if (!few && !in_place) {
+        if (plan->D == 64) return four ? launch_both<64, true>(a, longest, stream) : launch_both<64, false>(a, longest, stream);
+        return four ? launch_both<128, true>(a, longest, stream) : launch_both<128, false>(a, longest, stream);
+    }
     const attn_status st = few ? launch_select<1024>(a, longest, 48 * 1024, stream)
                                : launch_select<512>(a, longest, 11 * 1024, stream);
     if (st != ATTN_OK) return st;
     // Out of place, enough CTAs for some eight per SM.
     const int64_t rows = std::min<int64_t>(longest, budget), most = (rows + kMoveThreads - 1) / kMoveThreads;
     const int64_t want = std::max<int64_t>(1, (int64_t)sms * 8 / ((int64_t)plan->batch * plan->Hkv * 2));
-    const int splits = page_table_out ? (int)std::max<int64_t>(1, std::min(most, want)) : 1;
-    const bool in_place = !page_table_out;
+    const int splits = in_place ? 1 : (int)std::max<int64_t>(1, std::min(most, want));
     if (plan->D == 64) {
         if (four) return in_place ? launch_move<64, true, true>(a, splits, stream) : launch_move<64, true, false>(a, splits, stream);
         return in_place ? launch_move<64, false, true>(a, splits, stream) : launch_move<64, false, false>(a, splits, stream);
