@@ -13,9 +13,19 @@
 // Then every warp counts the kept tokens of its own range of tokens and, from
 // the sum of the ranges before it, writes their indices in order (and moves
 // their weights).  Move: a warp looks up 32 kept tokens at a time, one per lane,
-// and copies their K and V rows with all loads on their way at once.  Both are
-// bound by memory: 4 bytes per token and head are read, and the kept rows once
-// read and once written.
+// and copies their K and V rows with many loads on their way at once.
+//
+// What has to be moved is 4 bytes per token and head, and the kept rows twice;
+// but the selection's passes are a chain of barriers and shared-memory work that
+// a row's CTA cannot shorten, while the memory idles.  With more rows than SMs
+// one kernel does both, so that some CTAs copy while others select: 512 rows of
+// 1K-8K tokens, 64 dims in bf16, down to 1024 each (283 MB) take 64 us (4.4 TB/s)
+// instead of 32 + 39 in two.  With fewer rows the copies need all SMs and stay a
+// kernel of their own: 128 rows of 2K-32K tokens, 128 dims in 4 bits, down to
+// 4000 each, 35 + 32 us (176 in all instead of 133, the read-back included, when
+// a row's CTA also copies).  The longest row sets the selection's time there;
+// clusters of CTAs that share a row's histogram over distributed shared memory
+// were slower (157 us with two or four 256-thread CTAs, 260 with eight).
 //
 // In place, token j comes from index kept[j] >= j.  A CTA owns one (request,
 // head, K/V) and moves the rows in ascending order, a chunk at a time, all of
@@ -35,7 +45,7 @@ namespace attn {
 namespace {
 
 constexpr int kMoveThreads = 256, kBothThreads = 512;
-constexpr int kBothChunk = 11 * 1024;
+constexpr int kBothChunk = 11 * 1024;   // weights of a row at a time: three CTAs per SM
 constexpr int kDigitBits = 11, kDigits = 1 << kDigitBits;   // radix passes over 11, 11 and 10 bits
 
 struct EvictArgs {
@@ -387,7 +397,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 }
 
 // Both for the same request and head, out of place; grid: requests x KV heads.
-// Half of the warps move K, the others V.
+// Half of the warps move K, the others V.  Three CTAs per SM: 64 us where 256
+// threads and five took 87 and four CTAs of 512 (of 32 registers) 74; the rows
+// in order of length, 70, for then all CTAs select, and all copy, at once.
 template <int D, bool kFour>
 __global__ void __launch_bounds__(kBothThreads, 3) evict_both_kernel(const EvictArgs a) {
     const int b = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv, warp = threadIdx.x >> 5;
@@ -458,7 +470,7 @@ attn_status launch_evict(attn_plan_s* plan, bool four, const float* weights, con
     int32_t longest = 0;
     for (const RequestInfo& r : plan->requests) longest = std::max(longest, r.kv_len);
     // With at most a CTA per SM, each takes all of an SM's threads and shared
-    // memory; with more, a fourth of it.
+    // memory; with more, a part of it.
     int32_t sms = 0;
     if (!current_sm_count(&sms)) return ATTN_ERR_CUDA;
     const bool few = (int64_t)plan->batch * plan->Hkv <= sms;

@@ -8,10 +8,13 @@
 // 6 is e2m1's largest magnitude.  A NaN in a group makes the scale NaN, and
 // with it the whole group; an infinity saturates (448 * 6 * g).
 //
-// Both kernels are HBM-bound copies as long as they spend few instructions on
-// a value: packed fp32 arithmetic, and each thread finds its place by a
-// division once and then steps (a 64-bit division per item alone cost 20 us of
-// the 73 that appending 57K rows of 8 heads x 128 dims took).
+// Both kernels are copies that must spend few instructions on a value: packed
+// fp32 arithmetic, and each thread finds its place by a division once and then
+// steps.  Append also fetches its next item while it works on one.  57K rows of
+// 8 heads x 128 dims (301 MB each way): append 62 us (73 with a division per
+// item and nothing fetched ahead), 4.8 TB/s, bound by instruction issue (71% of
+// its slots); expand 58 us, 5.2 TB/s, four of five bytes written: two items per
+// thread at a time gain 2% more, four or eight nothing.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
