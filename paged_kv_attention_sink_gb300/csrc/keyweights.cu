@@ -273,7 +273,8 @@ struct PromptWeightCfg {
     static constexpr int kHeads = 8;                        // heads whose lse is staged at a time
     static constexpr int kOffQ = kTile;
     static constexpr int kOffNl = kOffQ + kStages * kTile;    // [2][8 heads][128 rows] negated lse
-    static constexpr int kOffSum = kOffNl + 2 * kHeads * kTileRows * 4;
+    static constexpr int kLseRow = kTileRows + 4;           // floats of a head's; the 4 spread a store over the banks
+    static constexpr int kOffSum = kOffNl + 2 * kHeads * kLseRow * 4;
     static constexpr int kOffBars = kOffSum + kWgs * kTileKeys * 4;
     static constexpr int kSmem = 1024 + kOffBars + (2 * kStages + kBufs + 6) * 8 + 16;
     // One CTA per SM: it holds all of an SM's TMEM, and a second one would wait for it.
@@ -386,24 +387,21 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
         // stages a group's lse (negated, in log2 units, by head) ahead of them.
         int row0 = i0, h0 = 0;
         for (int grp = 0; grp < n_groups; ++grp) {
-            float* dst = nl_s + (grp & 1) * C::kHeads * kTileRows + lane;
-            const int n = min(C::kHeads, G - h0);
-            float v[kTileRows / 32][C::kHeads];   // every load on its way before the first is used
+            // A load takes four rows' heads: whole 32-byte sectors.
+            const int h = lane % C::kHeads, first = lane / C::kHeads;
+            float* dst = nl_s + ((grp & 1) * C::kHeads + h) * C::kLseRow + first;
+            const bool there = h0 + h < G;
+            const float* src = a.lse + (int64_t)(r.q_row0 + row0 + first) * a.Hq + g * G + h0 + h;
+            float v[kTileRows / 4];   // every load on its way before the first is used
 #pragma unroll
-            for (int k = 0; k < kTileRows / 32; ++k) {
-                const int row = row0 + k * 32 + lane;
-                const float* src = a.lse + (int64_t)(r.q_row0 + row) * a.Hq + g * G + h0;
-#pragma unroll
-                for (int h = 0; h < C::kHeads; ++h) v[k][h] = h < n && row < r.qo_len ? __ldg(src + h) : 0.f;
-            }
+            for (int k = 0; k < kTileRows / 4; ++k)
+                v[k] = there && row0 + first + 4 * k < r.qo_len ? __ldg(src + (int64_t)4 * k * a.Hq) : 0.f;
             if (grp >= 2 && !wait_all(l_free + 8 * (grp & 1), ((grp >> 1) - 1) & 1)) {
                 if (lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
                 break;
             }
 #pragma unroll
-            for (int k = 0; k < kTileRows / 32; ++k)
-#pragma unroll
-                for (int h = 0; h < C::kHeads; ++h) dst[h * kTileRows + k * 32] = -v[k][h] * kLog2e;
+            for (int k = 0; k < kTileRows / 4; ++k) dst[4 * k] = -v[k] * kLog2e;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(l_full + 8 * (grp & 1));
             h0 += C::kHeads;
@@ -414,27 +412,37 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
         }
     } else if (warp == C::kEpilogueWarps) {
         // ---------------------------------------------------------- MMA issuer
+        // One thread, with the descriptors made beforehand: its loop lies between
+        // an S that is released and the next one that is ready.
         constexpr uint32_t idesc = ptx::idesc_bf16(kTileKeys, kTileRows, false, false);
-        bool ok = wait_all(k_full, 0);
-        for (int s = 0; ok && s < n_steps; ++s) {
-            const int st = s % C::kStages, buf = s % C::kBufs;
-            ok = wait_all(q_full + 8 * st, (s / C::kStages) & 1) &&
-                 (s < C::kBufs || wait_all(s_free + 8 * buf, (s / C::kBufs - 1) & 1));
-            if (!ok) break;
-            if (ptx::elect_one()) {
+        if (lane == 0) {
+            const uint64_t a0 = ptx::smem_desc_sw128(sbase, 16, 1024), b0 = ptx::smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
+            bool ok = ptx::mbar_wait(k_full, 0);
+            int st = 0, buf = 0;
+            uint32_t full = 0, free = 1;   // phases: of Q's stages, and of the accumulators (first use: none to wait for)
+            for (int s = 0; ok && s < n_steps; ++s) {
+                ok = ptx::mbar_wait(q_full + 8 * st, full) && ptx::mbar_wait(s_free + 8 * buf, free);
+                if (!ok) break;
                 ptx::tc_fence_after();
+                const uint64_t b = b0 + (uint32_t)(st * (C::kTile >> 4));
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk / 4) * C::kAtom + (kk % 4) * 32;
-                    ptx::tc_mma_ss(tmem + buf * kTileRows, ptx::smem_desc_sw128(sbase + off, 16, 1024),
-                                   ptx::smem_desc_sw128(sbase + C::kOffQ + st * C::kTile + off, 16, 1024), idesc, kk > 0);
+                    const uint32_t off = kk / 4 * (C::kAtom >> 4) + kk % 4 * 2;   // in 16 bytes
+                    ptx::tc_mma_ss(tmem + buf * kTileRows, a0 + off, b + off, idesc, kk > 0);
                 }
                 ptx::tc_commit(s_full + 8 * st);
+                if (++st == C::kStages) {
+                    st = 0;
+                    full ^= 1;
+                }
+                if (++buf == C::kBufs) {
+                    buf = 0;
+                    free ^= 1;
+                }
             }
-            __syncwarp();
+            if (!ok) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
+            ptx::tc_commit(drain);
         }
-        if (!ok && lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
-        if (ptx::elect_one()) ptx::tc_commit(drain);
         __syncwarp();
     } else {
         // ------------------------------------------- epilogue: one key per thread
@@ -521,7 +529,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
                 ok = ok && wait_all(s_full + 8 * (s % C::kStages), (s / C::kStages) & 1);
                 if (!ok) continue;
                 ptx::tc_fence_after();
-                const uint32_t nl_at = ptx::smem_u32(nl_s) + (((grp & 1) * C::kHeads + h) * kTileRows) * 4;
+                const uint32_t nl_at = ptx::smem_u32(nl_s) + ((grp & 1) * C::kHeads + h) * C::kLseRow * 4;
                 const uint32_t t_s = t_lane + buf * kTileRows;
                 if (lo31 <= 0 && hi == kTileRows) {
                     uint32_t v[2][32];   // 32 columns at a time, the next ones on their way
@@ -542,7 +550,8 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
                         ptx::tmem_ld32(t_s + c, v);
                         ptx::tc_wait_ld();
                         if (c + 32 == kTileRows) released(buf);
-                        add_columns(std::true_type{}, v, nl_at + c * 4, max(0, lo - c), max(max(0, lo - c), min(32, hi - c)));
+                        if (lo31 <= c && hi >= c + 32) add_columns(std::false_type{}, v, nl_at + c * 4, 0, 32);
+                        else add_columns(std::true_type{}, v, nl_at + c * 4, max(0, lo - c), max(max(0, lo - c), min(32, hi - c)));
                     }
                 }
                 total += (acc0.x + acc0.y) + (acc1.x + acc1.y);
