@@ -23,11 +23,15 @@
 //    the K tile in shared memory and streams Q tiles (128 rows of one head)
 //    past it; tcgen05.mma fills a ring of four 128-column accumulators in TMEM
 //    ahead of the warpgroups that drain them, one key per thread.  Four prompts
-//    of 0.5K-4K tokens, 64 query heads of 64 dims: 205 us, where the exponentials
-//    of whole tiles take 119 us at the MUFU's rate and the products 73 us; the
-//    rest is the barriers between producer, MMA and epilogue.  Two warpgroups
-//    measured 223 us and four 252 (fewer registers each); a query row per thread,
-//    a column sum of 128 keys in registers, 297.
+//    of 0.5K-4K tokens, 64 query heads of 64 dims: 200 us, where the exponentials
+//    of whole tiles take 119 us at the MUFU's rate and the products 73 us.  A CTA
+//    starts for some 5,000 clocks (TMEM, K, the first lse), 4.2 times per SM; its
+//    steps take 800 instead of the MUFU's 512: the barriers and TMEM loads alone
+//    measure 600, and overlap with the exponentials in part.  Two warpgroups
+//    measured 223 us and four 252 (fewer registers each); steps of two heads
+//    (N = 256) with four warpgroups on 64 columns each 228; the next step's first
+//    columns loaded ahead 209; a query row per thread, a column sum of 128 keys
+//    in registers, 297.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
