@@ -567,3 +567,39 @@ def test_evict_orders_all_values(n, budget, recent):
         want = ref.evict(flat[g], n, budget, recent)
         np.testing.assert_array_equal(kept[g], want, err_msg=str(g))
         np.testing.assert_array_equal(moved[g, :budget].view(np.uint32), flat[g, want].view(np.uint32), err_msg=str(g))
+
+
+def test_after_another_streams_event():
+    """A call behind an event of another stream, and behind a call of the same
+    kind, waits for both: its rows, its weights and its plan's lists arrive late."""
+    first, second = (batch_of([1, 1], kv, 8, 2, 64, 16, seed=41) for kv in ([900, 60], [60, 900]))
+    pool, d_pool, _ = pools(first, True, 9)
+    table = dev(first.page_table)
+    q = dev_bf16(second.q)
+    want_plan = make_plan(second, table)
+    want, want_lse = want_plan.decode_kv4(q, d_pool, lse=torch.empty(2, 16, device="cuda"))
+    want_w = want_plan.key_weights_kv4(q, d_pool, want_lse, torch.zeros(first.num_pages, 2, 16, device="cuda"), decay=0.0)
+    want_kept = want_plan.evict_kv4(want_w.clone(), d_pool.clone(), 20, 4)
+    plan = make_plan(first, table)
+    torch.cuda.synchronize()
+    side, late = torch.cuda.Stream(), torch.zeros_like(q)
+    for _ in range(3):
+        late.zero_()
+        weights, lse = torch.zeros_like(want_w), torch.empty_like(want_lse)
+        torch.cuda.synchronize()
+        plan.decode_kv4(late, d_pool, lse=torch.empty_like(lse))
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(4_000_000)
+            late.copy_(q)
+            next_plan = binding().Plan(second.qo_indptr, second.kv_indptr, table, second.last_page_len, 16, 2, 64, 16,
+                                       causal=second.causal, sm_scale=second.sm_scale, num_pages=second.num_pages)
+            torch.cuda._sleep(2_000_000)
+        torch.cuda.current_stream().wait_stream(side)
+        out, _ = next_plan.decode_kv4(late, d_pool, lse=lse)
+        next_plan.key_weights_kv4(late, d_pool, lse, weights, decay=0.0)
+        with torch.cuda.stream(side):
+            side.wait_stream(torch.cuda.default_stream())
+            kept = next_plan.evict_kv4(weights.clone(), d_pool.clone(), 20, 4)
+        torch.cuda.synchronize()
+        for got, expect in ((out, want), (lse, want_lse), (weights, want_w), (kept, want_kept)):
+            assert torch.equal(got.view(torch.uint8), expect.view(torch.uint8))
