@@ -603,3 +603,42 @@ def test_after_another_streams_event():
         torch.cuda.synchronize()
         for got, expect in ((out, want), (lse, want_lse), (weights, want_w), (kept, want_kept)):
             assert torch.equal(got.view(torch.uint8), expect.view(torch.uint8))
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("D,P,budget,recent", [(64, 16, 48, 5), (128, 16, 33, 0), (128, 64, 90, 90), (64, 32, 1, 1)])
+def test_evict_many_rows(four, D, P, budget, recent):
+    """More rows than SMs, out of place, with pages outside the pools among them."""
+    rng = np.random.default_rng(budget)
+    kv = [0, 1, 1200] + [int(n) for n in rng.integers(0, 150, 87)]
+    batch = batch_of([0] * len(kv), kv, 1, 2, D, P, seed=budget)
+    pool, d_pool, _ = pools(batch, four, 1)
+    weights = weights_like(rng, (batch.num_pages, 2, P))
+    plan = make_plan(batch, dev(batch.page_table))
+    need = -(-plan.evicted_lens(budget) // P)
+    n_out = int(need.sum()) + 2
+    table = rng.permutation(n_out)[:need.sum()].astype(np.int32)
+    out_pages = np.split(table, np.cumsum(need)[:-1])
+    want_pool = np.full((n_out,) + pool.shape[1:], 99, dtype=pool.dtype)
+    want_w = np.full((n_out, 2, P), 5.0, dtype=np.float32)
+    call, pool0, w0 = plan.evict_kv4 if four else plan.evict_kv, want_pool.copy(), want_w.copy()
+    out = lambda: (dev(pool0) if four else dev_bf16(pool0), dev(w0))
+    host = lambda t: t.cpu().numpy() if four else t.view(torch.int16).cpu().numpy().view(np.uint16)
+    got_pool, got_w = out()
+    kept = call(dev(weights), d_pool, budget, recent, page_table_out=dev(table), kv_out=got_pool, weights_out=got_w)
+    want_kept = evict_reference(batch, pool, weights, budget, recent, out_pages, want_pool, want_w, four)
+    assert plan.device_error() == 0
+    np.testing.assert_array_equal(kept.cpu().numpy(), want_kept)
+    np.testing.assert_array_equal(host(got_pool), want_pool)
+    np.testing.assert_array_equal(got_w.cpu().numpy().view(np.uint32), want_w.view(np.uint32))
+    # Request 2's first receiving page lies outside: it alone stays as it was.
+    first = int(need[:2].sum())
+    bad = table.copy()
+    bad[first] = n_out
+    got_pool, got_w = out()
+    kept = call(dev(weights), d_pool, budget, recent, page_table_out=dev(bad), kv_out=got_pool, weights_out=got_w)
+    assert plan.device_error() == 1
+    want_pool[table[first]], want_w[table[first]] = pool0[table[first]], w0[table[first]]
+    np.testing.assert_array_equal(kept.cpu().numpy(), want_kept)
+    np.testing.assert_array_equal(host(got_pool), want_pool)
+    np.testing.assert_array_equal(got_w.cpu().numpy().view(np.uint32), want_w.view(np.uint32))
