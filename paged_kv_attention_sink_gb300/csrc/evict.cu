@@ -11,21 +11,23 @@
 // to unsigned keys of the same order; a radix selection, 11 bits of the key at
 // a time, finds the threshold key and how many tokens that equal it are kept.
 // Then every warp counts the kept tokens of its own range of tokens and, from
-// the sum of the ranges before it, writes their indices in order (and moves
-// their weights).  Move: a warp looks up 32 kept tokens at a time, one per lane,
-// and copies their K and V rows with many loads on their way at once.
+// the sum of the ranges before it, writes their indices in order; the listed
+// tokens' weights are moved after that, a thread each.  Move: a warp looks up 32
+// kept tokens at a time, one per lane, and copies their K and V rows with many
+// loads on their way at once.
 //
 // What has to be moved is 4 bytes per token and head, and the kept rows twice;
 // but the selection's passes are a chain of barriers and shared-memory work that
 // a row's CTA cannot shorten, while the memory idles.  With more rows than SMs
 // one kernel does both, so that some CTAs copy while others select: 512 rows of
-// 1K-8K tokens, 64 dims in bf16, down to 1024 each (283 MB) take 64 us (4.4 TB/s)
-// instead of 32 + 39 in two.  With fewer rows the copies need all SMs and stay a
+// 1K-8K tokens, 64 dims in bf16, down to 1024 each (283 MB) take 63 us (4.5 TB/s)
+// where two kernels took 76.  With fewer rows the copies need all SMs and stay a
 // kernel of their own: 128 rows of 2K-32K tokens, 128 dims in 4 bits, down to
-// 4000 each, 35 + 32 us (176 in all instead of 133, the read-back included, when
-// a row's CTA also copies).  The longest row sets the selection's time there;
-// clusters of CTAs that share a row's histogram over distributed shared memory
-// were slower (157 us with two or four 256-thread CTAs, 260 with eight).
+// 4000 each, 31 + 32 us, set by the longest row's 32768 tokens (its weights
+// arrive after 10,000 clocks; 23,000 for the three digits, 24,000 for counting
+// and listing).  A row's CTA copying there too made the case 176 us instead of
+// 133; clusters of CTAs that shared a row's histogram over distributed shared
+// memory 157 (two or four of 256 threads) and 260 (eight).
 //
 // In place, token j comes from index kept[j] >= j.  A CTA owns one (request,
 // head, K/V) and moves the rows in ascending order, a chunk at a time, all of
@@ -131,15 +133,20 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& a, const RequestI
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int t = q0 + k * kThreads * 4;
-                w[k] = make_float4(nanf(""), nanf(""), nanf(""), nanf(""));
-                if (t >= t1) continue;
-                if (page[k] >= 0 && page[k] < a.num_pages)
-                    w[k] = *reinterpret_cast<const float4*>(a.weights + ((int64_t)page[k] * a.Hkv + g) * P + (t & (P - 1)));
-                else atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
+                const int from = page[k] >= 0 && page[k] < a.num_pages ? page[k] : 0;   // no branch between the loads
+                if (t < t1)
+                    w[k] = *reinterpret_cast<const float4*>(a.weights + ((int64_t)from * a.Hkv + g) * P + (t & (P - 1)));
             }
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (q0 + k * kThreads * 4 < t1) *reinterpret_cast<float4*>(w_s + q0 + k * kThreads * 4 - t0) = w[k];
+            for (int k = 0; k < kBatch; ++k) {
+                const int t = q0 + k * kThreads * 4;
+                if (t >= t1) continue;
+                if (page[k] < 0 || page[k] >= a.num_pages) {
+                    atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
+                    w[k] = make_float4(nanf(""), nanf(""), nanf(""), nanf(""));
+                }
+                *reinterpret_cast<float4*>(w_s + t - t0) = w[k];
+            }
         }
         __syncthreads();
     };
@@ -223,7 +230,7 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& a, const RequestI
     }
     // Kept: keys > prefix, and of those equal to it the first `ties`.
     const int all_ties = select ? ties : 0;
-    int greater = 0, equal = 0;
+    int greater = 0, equal = 0, moved = 0;
     for (int t0 = 0; t0 < n; t0 += a.chunk) {
         const int t1 = min(n, t0 + a.chunk);
         if (!fits) load(t0, t1);
@@ -284,25 +291,26 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& a, const RequestI
                 if (lane >= o) inc += u;
             }
             int gt = before_gt + (int)((inc - own) & 0xFFFF), eq = before_eq + (int)((inc - own) >> 16);
-            int j[4], page[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const bool is_gt = c >> e & 1, is_eq = c >> (4 + e) & 1;
-                j[e] = is_gt || (is_eq && eq < all_ties) ? gt + min(eq, all_ties) : -1;
+                if (is_gt || (is_eq && eq < all_ties)) kept[gt + min(eq, all_ties)] = t + e;
                 gt += is_gt;
                 eq += is_eq;
-                page[e] = j[e] >= 0 ? out_page(a, r, base, j[e]) : -1;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (j[e] < 0) continue;
-                kept[j[e]] = t + e;
-                if (page[e] >= 0) a.weights_out[((int64_t)page[e] * a.Hkv + g) * P + (j[e] & (P - 1))] = v[e];
             }
             const uint32_t total = __shfl_sync(0xffffffffu, inc, 31);
             before_gt += (int)(total & 0xFFFF);
             before_eq += (int)(total >> 16);
         }
+        // The weights of the tokens just listed, while they are in shared memory.
+        __syncthreads();
+        const int listed = greater + min(equal, all_ties);
+        for (int j = moved + tid; j < listed; j += kThreads) {
+            const int page = out_page(a, r, base, j);
+            const float v = w_s[kept[j] - t0];
+            if (page >= 0) a.weights_out[((int64_t)page * a.Hkv + g) * P + (j & (P - 1))] = v;
+        }
+        moved = listed;
         __syncthreads();   // sh_count is written again
     }
 }
