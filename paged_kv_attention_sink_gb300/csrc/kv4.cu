@@ -13,8 +13,8 @@
 // steps.  Append also fetches its next item while it works on one.  57K rows of
 // 8 heads x 128 dims (301 MB each way): append 62 us (73 with a division per
 // item and nothing fetched ahead), 4.8 TB/s, bound by instruction issue (71% of
-// its slots); expand 58 us, 5.2 TB/s, four of five bytes written: two items per
-// thread at a time gain 2% more, four or eight nothing.
+// its slots); expand 56 us, 5.4 TB/s, four of five bytes written (58 with one
+// item per thread at a time instead of two, 64 with four).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -137,37 +137,58 @@ expand_kv4_kernel(const uint8_t* __restrict__ pool, uint4* __restrict__ buf, con
                   int64_t n, int32_t Hkv, int32_t P, int64_t num_pages, float k_scale, float v_scale, int32_t* err) {
     ptx::grid_dependents_go();
     ptx::grid_dependency_wait();
-    constexpr int kOctets = D / 8, kSub = kv4_sub_bytes(D), kPerSub = kKv4Tokens * kOctets;
+    constexpr int kOctets = D / 8, kSub = kv4_sub_bytes(D), kPerSub = kKv4Tokens * kOctets, kBatch = 2;
     const int32_t per_half = Hkv * P * kOctets, half_subs = Hkv * (P / kKv4Tokens);
     const int64_t step = (int64_t)gridDim.x * kKv4Threads, step_halves = step / per_half;
     const int32_t step_in = (int32_t)(step - step_halves * per_half);
     int64_t i = (int64_t)blockIdx.x * kKv4Threads + threadIdx.x, blk = i / per_half;   // blk: (page in the list, K/V)
     int32_t in_half = (int32_t)(i - blk * per_half);   // ((head, sixteen tokens), token, 8 dims)
     while (blk < 2 * n) {
-        const int32_t page = page_ids[blk >> 1];
-        if (page >= 0 && page < num_pages) {
-            const int32_t sub_idx = in_half / kPerSub, at = in_half % kPerSub;
-            const uint8_t* sub = pool + (((int64_t)page * 2 + (blk & 1)) * half_subs + sub_idx) * kSub;
-            const uint32_t codes = *reinterpret_cast<const uint32_t*>(sub + at * 4);
-            const uint32_t sb = sub[8 * D + at / 2];
-            const float s = kv4::f16x2_to_f32(kv4::scales_to_f16x2(sb)).x * ((blk & 1) ? v_scale : k_scale);
+        // kBatch items: their pages, then their codes and scales, on the way together.
+        int32_t page[kBatch], item[kBatch];
+        bool v_half[kBatch];
+        const int64_t i0 = i;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            page[u] = -1;
+            item[u] = in_half;
+            v_half[u] = blk & 1;
+            if (blk < 2 * n) {
+                page[u] = page_ids[blk >> 1];
+                if (page[u] < 0 || page[u] >= num_pages) {
+                    if (in_half == 0 && (blk & 1) == 0 && err) atomicOr(err, ATTN_DEVICE_ERR_PAGE_ID);
+                    page[u] = -1;
+                }
+            }
+            i += step;
+            blk += step_halves;
+            in_half += step_in;
+            if (in_half >= per_half) {
+                in_half -= per_half;
+                ++blk;
+            }
+        }
+        uint32_t codes[kBatch], sb[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (page[u] < 0) continue;
+            const int32_t sub_idx = item[u] / kPerSub, at = item[u] % kPerSub;
+            const uint8_t* sub = pool + (((int64_t)page[u] * 2 + v_half[u]) * half_subs + sub_idx) * kSub;
+            codes[u] = *reinterpret_cast<const uint32_t*>(sub + at * 4);
+            sb[u] = sub[8 * D + at / 2];
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (page[u] < 0) continue;
+            const float s = kv4::f16x2_to_f32(kv4::scales_to_f16x2(sb[u])).x * (v_half[u] ? v_scale : k_scale);
             uint32_t h[4], o[4];
-            kv4::codes_to_f16x2(codes, h);
+            kv4::codes_to_f16x2(codes[u], h);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float2 v = mul2(kv4::f16x2_to_f32(h[k]), make_float2(s, s));
                 o[k] = ptx::pack_bf16x2(v.x, v.y);    // exact: see kv4.cuh
             }
-            buf[i] = make_uint4(o[0], o[1], o[2], o[3]);
-        } else if (in_half == 0 && (blk & 1) == 0 && err) {
-            atomicOr(err, ATTN_DEVICE_ERR_PAGE_ID);
-        }
-        i += step;
-        blk += step_halves;
-        in_half += step_in;
-        if (in_half >= per_half) {
-            in_half -= per_half;
-            ++blk;
+            buf[i0 + u * step] = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
