@@ -63,13 +63,14 @@ bool make_ragged_map(void* map, const void* x, const attn_plan_s* p) {
 // q (or out) [rows][Hq][D] as a 3-D tensor {dim, head, row}: one box is 128
 // rows x 64 dims of one head; rows past the end read as zero (and are not
 // written by a store).
-bool make_q_map(void* map, const void* q, const attn_plan_s* p, uint32_t box_rows = attn::kPrefillRows) {
+bool make_q_map(void* map, const void* q, const attn_plan_s* p, uint32_t box_rows = attn::kPrefillRows,
+                uint32_t box_heads = 1) {
     auto fn = encode_fn();
     if (!fn) return false;
     const int64_t rows = p->info.total_qo_rows;
     cuuint64_t dims[3] = {(cuuint64_t)p->D, (cuuint64_t)p->Hq, (cuuint64_t)rows};
     cuuint64_t strides[2] = {(cuuint64_t)p->D * 2, (cuuint64_t)p->Hq * p->D * 2};
-    cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
     cuuint32_t elem[3] = {1, 1, 1};
     return fn(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
               const_cast<void*>(q), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -322,12 +323,13 @@ attn_status key_weights(attn_plan_t plan, bool four, const void* q, const void* 
             if (!make_kv_map(plan->kv_map_prefill, pool, plan, plan->P)) return ATTN_ERR_CUDA;
             plan->kv_map_prefill_ptr = pool;
         }
-        if (plan->q_map_prefill_ptr != q) {
-            if (!make_q_map(plan->q_map_prefill, q, plan)) return ATTN_ERR_CUDA;
-            plan->q_map_prefill_ptr = q;
+        if (plan->q_map_weights_ptr != q) {   // some rows' heads of one KV head (128 in all at most)
+            const int heads = std::min(plan->Hq / plan->Hkv, 128);
+            if (!make_q_map(plan->q_map_weights, q, plan, 128 / heads, heads)) return ATTN_ERR_CUDA;
+            plan->q_map_weights_ptr = q;
         }
     }
-    return attn::launch_key_weights(plan, four, q, pool, k_scale, plan->q_map_prefill, plan->kv_map_prefill, lse,
+    return attn::launch_key_weights(plan, four, q, pool, k_scale, plan->q_map_weights, plan->kv_map_prefill, lse,
                                     prev, decay, window, weights,
                                     static_cast<cudaStream_t>(stream));
 }

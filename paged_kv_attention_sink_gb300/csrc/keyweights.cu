@@ -274,11 +274,10 @@ struct PromptWeightCfg {
     static constexpr int kWgs = 3;                          // epilogue warpgroups
     static constexpr int kEpilogueWarps = 4 * kWgs;
     static constexpr int kThreads = (kEpilogueWarps + 3) * 32;   // + MMA issuer, + Q producer, + lse
-    static constexpr int kHeads = 8;                        // heads whose lse is staged at a time
+    static constexpr int kGroup = 8;                        // steps whose lse is staged at a time
     static constexpr int kOffQ = kTile;
-    static constexpr int kOffNl = kOffQ + kStages * kTile;    // [2][8 heads][128 rows] negated lse
-    static constexpr int kLseRow = kTileRows + 4;           // floats of a head's; the 4 spread a store over the banks
-    static constexpr int kOffSum = kOffNl + 2 * kHeads * kLseRow * 4;
+    static constexpr int kOffNl = kOffQ + kStages * kTile;    // [2][8 steps][128 columns] negated lse
+    static constexpr int kOffSum = kOffNl + 2 * kGroup * kTileRows * 4;
     static constexpr int kOffBars = kOffSum + kWgs * kTileKeys * 4;
     static constexpr int kSmem = 1024 + kOffBars + (2 * kStages + kBufs + 6) * 8 + 16;
     // One CTA per SM: it holds all of an SM's TMEM, and a second one would wait for it.
@@ -314,9 +313,20 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
     // First query row that counts: inside the window, and seeing the first key.
     int i0 = a.window > 0 ? max(0, r.qo_len - a.window) : 0;
     if (a.causal) i0 = max(i0, t0 - prefix);
-    const int n_steps = (r.qo_len - i0 + kTileRows - 1) / kTileRows * G;   // step s: rows i0 + s / G * 128, head s % G
-    const int n_groups = n_steps / G * ((G + C::kHeads - 1) / C::kHeads);
+    // A step's 128 columns: `rows` query rows, `heads` heads of each side by side
+    // (a row's heads lie together in q and in lse); more than 128 heads in slices.
+    const int heads = min(G, kTileRows), rows = kTileRows / heads, used = rows * heads;
+    const int slices = (G + heads - 1) / heads;
+    const int n_steps = (r.qo_len - i0 + rows - 1) / rows * slices;
+    const int n_groups = (n_steps + C::kGroup - 1) / C::kGroup;
 
+    // Columns that no copy writes hold zeros, and their lse makes them 0.
+    if (used < kTileRows) {
+        const int per = (kTileRows - used) * 8;   // 16-byte pieces of an atom's rest
+        for (int i = tid; i < C::kStages * (D / 64) * per; i += C::kThreads)
+            ptx::st_shared_v4(sbase + C::kOffQ + i / per * C::kAtom + used * 128 + i % per * 16, 0u, 0u, 0u, 0u);
+        ptx::fence_proxy_async_smem();
+    }
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             ptx::mbar_init(q_full + 8 * i, 1);
@@ -364,19 +374,20 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
         }
         if (lane == 0) {
             int s = 0;
-            for (int head = 0, row0 = r.q_row0 + i0; s < n_steps; ++s) {
+            for (int h0 = 0, row = r.q_row0 + i0; s < n_steps; ++s) {
                 const int st = s % C::kStages;
                 if (s >= C::kStages && !ptx::mbar_wait(s_full + 8 * st, (s / C::kStages - 1) & 1)) {
                     atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
                     break;
                 }
-                ptx::mbar_arrive_expect_tx(q_full + 8 * st, C::kTile);
+                ptx::mbar_arrive_expect_tx(q_full + 8 * st, used * 128 * (D / 64));
                 for (int c = 0; c < D / 64; ++c)
                     ptx::tma_load_3d(sbase + C::kOffQ + st * C::kTile + c * C::kAtom, &q_map, q_full + 8 * st, c * 64,
-                                     g * G + head, row0);
-                if (++head == G) {
-                    head = 0;
-                    row0 += kTileRows;
+                                     g * G + h0, row);
+                h0 += heads;
+                if (h0 >= G) {
+                    h0 = 0;
+                    row += rows;
                 }
             }
             // Copies still in flight when a wait ran out land before the CTA exits.
@@ -387,32 +398,43 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
         __syncwarp();
     } else if (warp == C::kEpilogueWarps + 2) {
         // ----------------------------------------------------------------- lse
-        // Steps come in groups, the same 128 rows and up to 8 heads; this warp
-        // stages a group's lse (negated, in log2 units, by head) ahead of them.
+        // This warp stages eight steps' lse (negated, in log2 units) at a time, ahead of them.
+        // Of this lane's columns: row within the step (huge: none), head, index in lse
+        // (below 2^31: the plan's rows times heads are).
+        int row_of[kTileRows / 32], head_of[kTileRows / 32], at[kTileRows / 32];
+#pragma unroll
+        for (int q = 0; q < kTileRows / 32; ++q) {
+            const int col = q * 32 + lane;
+            row_of[q] = col < used ? col / heads : 1 << 30;
+            head_of[q] = col % heads;
+            at[q] = col < used ? (r.q_row0 + col / heads) * a.Hq + g * G + head_of[q] : 0;
+        }
         int row0 = i0, h0 = 0;
         for (int grp = 0; grp < n_groups; ++grp) {
-            // A load takes four rows' heads: whole 32-byte sectors.
-            const int h = lane % C::kHeads, first = lane / C::kHeads;
-            float* dst = nl_s + ((grp & 1) * C::kHeads + h) * C::kLseRow + first;
-            const bool there = h0 + h < G;
-            const float* src = a.lse + (int64_t)(r.q_row0 + row0 + first) * a.Hq + g * G + h0 + h;
-            float v[kTileRows / 4];   // every load on its way before the first is used
+            float* dst = nl_s + (grp & 1) * C::kGroup * kTileRows + lane;
+            float v[C::kGroup][kTileRows / 32];   // every load on its way before the first is used
 #pragma unroll
-            for (int k = 0; k < kTileRows / 4; ++k)
-                v[k] = there && row0 + first + 4 * k < r.qo_len ? __ldg(src + (int64_t)4 * k * a.Hq) : 0.f;
+            for (int k = 0; k < C::kGroup; ++k) {
+#pragma unroll
+                for (int q = 0; q < kTileRows / 32; ++q)
+                    v[k][q] = row_of[q] < r.qo_len - row0 && head_of[q] < G - h0 ? __ldg(a.lse + at[q] + (row0 * a.Hq + h0))
+                                                                                : INFINITY;
+                h0 += heads;
+                if (h0 >= G) {
+                    h0 = 0;
+                    row0 += rows;
+                }
+            }
             if (grp >= 2 && !wait_all(l_free + 8 * (grp & 1), ((grp >> 1) - 1) & 1)) {
                 if (lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
                 break;
             }
 #pragma unroll
-            for (int k = 0; k < kTileRows / 4; ++k) dst[4 * k] = -v[k] * kLog2e;
+            for (int k = 0; k < C::kGroup; ++k)
+#pragma unroll
+                for (int q = 0; q < kTileRows / 32; ++q) dst[k * kTileRows + q * 32] = -v[k][q] * kLog2e;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(l_full + 8 * (grp & 1));
-            h0 += C::kHeads;
-            if (h0 >= G) {
-                h0 = 0;
-                row0 += kTileRows;
-            }
         }
     } else if (warp == C::kEpilogueWarps) {
         // ---------------------------------------------------------- MMA issuer
@@ -514,28 +536,28 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
 
         float total = 0.f;
         bool ok = true;
-        int s = wg, h = wg;   // this warpgroup's next step, and its head counted from the group's first
+        int s = wg;   // this warpgroup's next step
         auto released = [&](int buf) {   // all of S has been read: a later product may overwrite it
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(s_free + 8 * buf);
         };
-        for (int grp = 0, row0 = i0, h0 = 0; grp < n_groups; ++grp) {
+        // Row seen0 is the first that sees the warp's first key.  Steps [clear, whole)
+        // count in full: rows that see all of the warp's keys, and are the request's.
+        const int seen0 = t0 + (key - lane) - prefix;
+        const int clear = a.causal ? (max(0, seen0 + 31 - i0) + rows - 1) / rows : 0;
+        const int whole = slices == 1 ? (r.qo_len - i0) / rows : 0;
+        for (int grp = 0; grp < n_groups; ++grp) {
             ok = ok && wait_all(l_full + 8 * (grp & 1), (grp >> 1) & 1);
-            const int n = min(C::kHeads, G - h0), hi = min(kTileRows, r.qo_len - row0);
-            // Columns [lo, hi) count: rows that see the key, of this request.
-            // Over the warp's keys lo rises by 31.
-            const int lo = a.causal ? t0 + key - (prefix + row0) : 0;
-            const int lo0 = a.causal ? lo - lane : 0, lo31 = a.causal ? lo0 + 31 : 0;
-            for (; h < n; h += C::kWgs, s += C::kWgs) {
+            for (const int end = min(n_steps, (grp + 1) * C::kGroup); s < end; s += C::kWgs) {
                 // After a wait that ran out the warp only keeps the barriers' count.
                 const int buf = s % C::kBufs;
                 ok = ok && wait_all(s_full + 8 * (s % C::kStages), (s / C::kStages) & 1);
                 if (!ok) continue;
                 ptx::tc_fence_after();
-                const uint32_t nl_at = ptx::smem_u32(nl_s) + ((grp & 1) * C::kHeads + h) * C::kLseRow * 4;
+                const uint32_t nl_at = ptx::smem_u32(nl_s) + s % (2 * C::kGroup) * kTileRows * 4;
                 const uint32_t t_s = t_lane + buf * kTileRows;
-                if (lo31 <= 0 && hi == kTileRows) {
+                if (s >= clear && s < whole) {
                     uint32_t v[2][32];   // 32 columns at a time, the next ones on their way
                     ptx::tmem_ld32(t_s, v[0]);
                     ptx::tc_wait_ld();
@@ -547,6 +569,13 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
                         if (c + 2 == kTileRows / 32) released(buf);
                     }
                 } else {
+                    // Columns [lo, hi) count: rows that see the key, of this request, and
+                    // heads of this KV head.  Over the warp's keys lo rises by 31 rows.
+                    const int block = s / slices, row0 = i0 + block * rows;
+                    const int hi = slices == 1 ? min(rows, r.qo_len - row0) * heads : min(heads, G - (s - block * slices) * heads);
+                    const int seen = a.causal ? seen0 - row0 : -32;
+                    const int lo = max(0, seen + (a.causal ? lane : 0)) * heads;
+                    const int lo0 = max(0, seen) * heads, lo31 = max(0, seen + 31) * heads;
 #pragma unroll 1
                     for (int c = 0; c < kTileRows; c += 32) {
                         if (c + 32 < kTileRows && c + 31 < lo0) continue;   // no key of the warp is seen
@@ -561,14 +590,8 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
                 total += (acc0.x + acc0.y) + (acc1.x + acc1.y);
                 acc0 = acc1 = make_float2(0.f, 0.f);
             }
-            h -= n;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(l_free + 8 * (grp & 1));
-            h0 += C::kHeads;
-            if (h0 >= G) {
-                h0 = 0;
-                row0 += kTileRows;
-            }
         }
         if (!ok && lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
         // The warpgroups' sums, in a fixed order.
