@@ -20,21 +20,23 @@
 //    codes into operands takes over half of the issue slots.
 //  * prefill requests: bound by the exponentials (MUFU: 32 a clock and SM) and
 //    the product on the tensor cores.  One CTA per 128 keys of a KV head keeps
-//    the K tile in shared memory and streams Q tiles (128 rows of one head)
-//    past it; tcgen05.mma fills a ring of four 128-column accumulators in TMEM
-//    ahead of the warpgroups that drain them, one key per thread.  Four prompts
-//    of 0.5K-4K tokens, 64 query heads of 64 dims: 200 us, where the exponentials
-//    of whole tiles take 119 us at the MUFU's rate and the products 73 us.  A CTA
-//    starts for some 5,000 clocks (TMEM, K, the first lse), 4.2 times per SM; its
-//    steps take 800 instead of the MUFU's 512: the barriers and TMEM loads alone
-//    measure 600, and overlap with the exponentials in part.  Two warpgroups
-//    measured 223 us and four 252 (fewer registers each); steps of two heads
-//    (N = 256) with four warpgroups on 64 columns each 228; the next step's first
-//    columns loaded ahead 209; a query row per thread, a column sum of 128 keys
-//    in registers, 297.
+//    the K tile in shared memory and streams Q tiles past it, 128 columns of some
+//    rows' heads (so that few rows with many heads fill them); tcgen05.mma fills
+//    a ring of 128-column accumulators in TMEM ahead of the warpgroups that drain
+//    them, one key per thread.  Four prompts of 0.5K-4K tokens, 64 query heads of
+//    64 dims: 193 us, where the exponentials of whole tiles take 119 us at the
+//    MUFU's rate and the products 73 us.  A CTA starts for some 5,000 clocks
+//    (TMEM, K, the first lse), 4.2 times per SM; its steps take 770 instead of
+//    the MUFU's 512: the barriers and TMEM loads alone measure 600, and overlap
+//    with the exponentials in part.  Steps of 128 rows of one head measured 200
+//    us; so built, two warpgroups 223 and four 252 (fewer registers each), steps
+//    of two heads (N = 256) with four warpgroups on 64 columns each 228, the next
+//    step's first columns loaded ahead 209, and a query row per thread with a sum
+//    of 128 keys in registers 297.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attn_internal.h"
@@ -205,7 +207,11 @@ key_weights_step_kernel(const KeyWeightArgs a) {
 #pragma unroll
         for (int nt = 0; nt < kHeld; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e >> 1] += ptx::ex2(fmaf(s[nt][e], qt[nt].mult[e & 1], qt[nt].nl[e & 1]));
+            for (int e = 0; e < 4; ++e) {
+                const float nl = qt[nt].nl[e & 1], p = ptx::ex2(fmaf(s[nt][e], qt[nt].mult[e & 1], nl));
+                // A column without a head is 0 also where the key holds infinities (4 bits cannot).
+                w[e >> 1] += !kFour && nl == -INFINITY ? 0.f : p;
+            }
     };
 
     for (int it = 0, s = 0; it < n_it; ++it) {
@@ -256,43 +262,54 @@ key_weights_step_kernel(const KeyWeightArgs a) {
 // ----------------------------------------------------------- prefill requests
 
 constexpr int kTileKeys = 128;   // keys per CTA: the MMA's M, a TMEM lane each
-constexpr int kTileRows = 128;   // query rows per step: the MMA's N
+constexpr int kTileRows = 128;   // columns per step: the MMA's N
 
 // A wait with the same result in every lane of the warp.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity));
 }
 
-template <int D>
+// Two forms.  The long one has an SM for itself and hides a step's latencies by
+// steps in flight; a CTA of few steps is mostly start and end, which the short
+// one hides by more CTAs per SM.  By the mean steps of a tile (causality not
+// counted): 76 requests of 40 rows on 15K-20K tokens, two KV heads with 8 query
+// heads each (3 steps) 838 us long and 357 short; 512 rows (32 steps) 460 and 390;
+// 1024 rows (64) 784 and 751; the prompts above (some 230) 193 and 300.
+constexpr int kShortSteps = 64;
+
+template <int D, bool kShort>
 struct PromptWeightCfg {
     static constexpr int kAtom = 128 * 128;                 // 128 rows x 64 dims, 128-byte swizzle
     static constexpr int kTile = kAtom * (D / 64);
     // Q stages: a stage's round trip (refill noticed, copied, multiplied) is
     // some 2,000 clocks, so many must be on their way at once.
-    static constexpr int kStages = D == 64 ? 10 : 5;
-    static constexpr int kBufs = 4;                         // S accumulators: all 512 TMEM columns
-    static constexpr int kWgs = 3;                          // epilogue warpgroups
+    static constexpr int kStages = kShort ? 2 : D == 64 ? 10 : 5;
+    static constexpr int kBufs = kShort ? 1 : 4;            // S accumulators: 128 of the 512 TMEM columns each
+    static constexpr int kWgs = kShort ? 1 : 3;             // epilogue warpgroups
+    static constexpr int kCtas = kShort ? (D == 64 ? 4 : 2) : 1;   // per SM
     static constexpr int kEpilogueWarps = 4 * kWgs;
     static constexpr int kThreads = (kEpilogueWarps + 3) * 32;   // + MMA issuer, + Q producer, + lse
-    static constexpr int kGroup = 8;                        // steps whose lse is staged at a time
+    static constexpr int kGroup = kShort ? 4 : 8;           // steps whose lse is staged at a time
     static constexpr int kOffQ = kTile;
-    static constexpr int kOffNl = kOffQ + kStages * kTile;    // [2][8 steps][128 columns] negated lse
+    static constexpr int kOffNl = kOffQ + kStages * kTile;    // [2][kGroup steps][128 columns] negated lse
     static constexpr int kOffSum = kOffNl + 2 * kGroup * kTileRows * 4;
     static constexpr int kOffBars = kOffSum + kWgs * kTileKeys * 4;
     static constexpr int kSmem = 1024 + kOffBars + (2 * kStages + kBufs + 6) * 8 + 16;
-    // One CTA per SM: it holds all of an SM's TMEM, and a second one would wait for it.
-    static_assert(2 * (kSmem + 1024) > 233472 && kSmem <= 232448, "one CTA per SM");
+    static_assert(kCtas * (kSmem + 1024) <= 233472 && kSmem <= 232448 && kCtas * kBufs * kTileRows <= 512, "CTAs per SM");
+    // The long form holds all of an SM's TMEM, and a second CTA would wait for it.
+    static_assert(kShort || 2 * (kSmem + 1024) > 233472, "one CTA per SM");
     // s_full is waited on by stage: step s + kStages must not complete before
     // step s's S has been read.  The one MMA warp takes the steps in order, and
     // step s + kBufs needs the accumulator of step s.
     static_assert(kStages >= kBufs, "s_full phases");
 };
 
-template <int D, bool kFour>
-__global__ void __launch_bounds__(PromptWeightCfg<D>::kThreads, 1)
+// kRagged: a number of heads that leaves some of a step's last 32 columns empty.
+template <int D, bool kFour, bool kShort, bool kRagged>
+__global__ void __launch_bounds__(PromptWeightCfg<D, kShort>::kThreads, PromptWeightCfg<D, kShort>::kCtas)
 key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
                           const KeyWeightArgs a) {
-    using C = PromptWeightCfg<D>;
+    using C = PromptWeightCfg<D, kShort>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-ptx::smem_u32(smem_raw) & 1023u);
     const uint32_t sbase = ptx::smem_u32(smem);
@@ -320,13 +337,6 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
     const int n_steps = (r.qo_len - i0 + rows - 1) / rows * slices;
     const int n_groups = (n_steps + C::kGroup - 1) / C::kGroup;
 
-    // Columns that no copy writes hold zeros, and their lse makes them 0.
-    if (used < kTileRows) {
-        const int per = (kTileRows - used) * 8;   // 16-byte pieces of an atom's rest
-        for (int i = tid; i < C::kStages * (D / 64) * per; i += C::kThreads)
-            ptx::st_shared_v4(sbase + C::kOffQ + i / per * C::kAtom + used * 128 + i % per * 16, 0u, 0u, 0u, 0u);
-        ptx::fence_proxy_async_smem();
-    }
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             ptx::mbar_init(q_full + 8 * i, 1);
@@ -342,7 +352,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
         ptx::fence_mbar_init();
     }
     if (warp == C::kEpilogueWarps) {
-        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::kBufs * kTileRows);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
@@ -398,7 +408,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
         __syncwarp();
     } else if (warp == C::kEpilogueWarps + 2) {
         // ----------------------------------------------------------------- lse
-        // This warp stages eight steps' lse (negated, in log2 units) at a time, ahead of them.
+        // This warp stages kGroup steps' lse (negated, in log2 units) at a time, ahead of them.
         // Of this lane's columns: row within the step (huge: none), head, index in lse
         // (below 2^31: the plan's rows times heads are).
         int row_of[kTileRows / 32], head_of[kTileRows / 32], at[kTileRows / 32];
@@ -543,10 +553,11 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
             if (lane == 0) ptx::mbar_arrive(s_free + 8 * buf);
         };
         // Row seen0 is the first that sees the warp's first key.  Steps [clear, whole)
-        // count in full: rows that see all of the warp's keys, and are the request's.
+        // count in full: all columns, of rows that see all of the warp's keys and are
+        // the request's.
         const int seen0 = t0 + (key - lane) - prefix;
         const int clear = a.causal ? (max(0, seen0 + 31 - i0) + rows - 1) / rows : 0;
-        const int whole = slices == 1 ? (r.qo_len - i0) / rows : 0;
+        const int whole = slices == 1 && (kRagged ? used > 96 : used == kTileRows) ? (r.qo_len - i0) / rows : 0;
         for (int grp = 0; grp < n_groups; ++grp) {
             ok = ok && wait_all(l_full + 8 * (grp & 1), (grp >> 1) & 1);
             for (const int end = min(n_steps, (grp + 1) * C::kGroup); s < end; s += C::kWgs) {
@@ -564,7 +575,8 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
 #pragma unroll
                     for (int c = 0; c < kTileRows / 32; ++c) {
                         if (c + 1 < kTileRows / 32) ptx::tmem_ld32(t_s + (c + 1) * 32, v[(c + 1) & 1]);
-                        add_columns(std::false_type{}, v[c & 1], nl_at + c * 128, 0, 32);
+                        if (kRagged && c == 3) add_columns(std::true_type{}, v[1], nl_at + 3 * 128, 0, used - 96);
+                        else add_columns(std::false_type{}, v[c & 1], nl_at + c * 128, 0, 32);
                         if (c + 1 < kTileRows / 32) ptx::tc_wait_ld();
                         if (c + 2 == kTileRows / 32) released(buf);
                     }
@@ -617,7 +629,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
         ptx::mbar_wait(drain, 0);
         __syncwarp();
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 512);
+        ptx::tmem_dealloc(tmem, C::kBufs * kTileRows);
     }
 }
 
@@ -633,11 +645,11 @@ cudaError_t launch_step(const KeyWeightArgs& a, int grid, cudaStream_t stream) {
     return launch_dependent(kernel, dim3(grid), kDecodeWarps * 32, C::kSmem, stream, a);
 }
 
-template <int D, bool kFour>
+template <int D, bool kFour, bool kShort, bool kRagged>
 cudaError_t launch_prompt(const CUtensorMap& q_map, const CUtensorMap& kv_map, const KeyWeightArgs& a, int grid,
                           cudaStream_t stream) {
-    using C = PromptWeightCfg<D>;
-    auto kernel = key_weights_prompt_kernel<D, kFour>;
+    using C = PromptWeightCfg<D, kShort>;
+    auto kernel = key_weights_prompt_kernel<D, kFour, kShort, kRagged>;
     static std::atomic<bool> configured[kMaxDevices];
     cudaError_t e = once_per_device(configured, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -655,8 +667,20 @@ attn_status launch_all(const attn_plan_s* plan, const CUtensorMap& q_map, const 
         e = G <= 8    ? launch_step<D, kFour, 1>(a, units, stream)
             : G <= 16 ? launch_step<D, kFour, 2>(a, units, stream)
                       : launch_step<D, kFour, 0>(a, units, stream);
-    if (e == cudaSuccess && !plan->weight_tiles.empty())
-        e = launch_prompt<D, kFour>(q_map, kv_map, a, (int)plan->weight_tiles.size() * plan->Hkv, stream);
+    if (e == cudaSuccess && !plan->weight_tiles.empty()) {
+        const int heads = std::min(G, kTileRows), rows = kTileRows / heads, slices = (G + heads - 1) / heads;
+        int64_t steps = 0;
+        for (const RequestInfo& r : plan->requests)
+            if (r.qo_len > 1) {
+                const int n = a.window > 0 ? std::min(a.window, r.qo_len) : r.qo_len;
+                steps += ((int64_t)r.kv_len + kTileKeys - 1) / kTileKeys * ((n + rows - 1) / rows) * slices;
+            }
+        const int grid = (int)plan->weight_tiles.size() * plan->Hkv;
+        const bool ragged = rows * heads < kTileRows;
+        e = steps <= kShortSteps * (int64_t)plan->weight_tiles.size() ? launch_prompt<D, kFour, true, false>(q_map, kv_map, a, grid, stream)
+            : ragged ? launch_prompt<D, kFour, false, true>(q_map, kv_map, a, grid, stream)
+                     : launch_prompt<D, kFour, false, false>(q_map, kv_map, a, grid, stream);
+    }
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -642,3 +642,47 @@ def test_evict_many_rows(four, D, P, budget, recent):
     np.testing.assert_array_equal(kept.cpu().numpy(), want_kept)
     np.testing.assert_array_equal(host(got_pool), want_pool)
     np.testing.assert_array_equal(got_w.cpu().numpy().view(np.uint32), want_w.view(np.uint32))
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("G,D,P,n,causal", [(32, 64, 16, 400, True), (20, 128, 64, 410, True), (128, 64, 32, 75, False),
+                                            (130, 64, 16, 60, True), (130, 128, 16, 9, True)])
+def test_key_weights_of_many_heads(four, G, D, P, n, causal):
+    """Few rows of many heads to a step, more than a step's columns among them;
+    long and short lists of steps."""
+    batch = batch_of([n, 3], [n + 37, 130], G, 1, D, P, seed=G + n, causal=causal)
+    _, pool, vals = pools(batch, four, seed=3)
+    plan = make_plan(batch, dev(batch.page_table))
+    lse = some_lse(batch, vals)
+    prev = np.random.default_rng(5).exponential(size=(batch.num_pages, 1, P)).astype(np.float32)
+    for window in (0, 50):
+        out = torch.full(prev.shape, -5.0, device="cuda")
+        run_weights(plan, four, dev_bf16(batch.q), pool, dev(lse), out, prev=dev(prev), window=window)
+        assert plan.device_error() == 0
+        want, tol = ref.key_weights(batch, vals, lse, prev, 1.0, window)
+        got, here = out.double().cpu().numpy(), ~np.isnan(want)
+        assert np.all(got[~here] == -5.0)
+        assert np.all(np.abs(got[here] - want[here]) <= tol[here] + 1e-37), window
+
+
+@pytest.mark.parametrize("G", [1, 3, 8, 12, 20])
+def test_key_weights_of_infinite_keys(G):
+    """A key at minus infinity receives nothing, whatever heads a tile leaves
+    empty; the others are as without it."""
+    batch = batch_of([1, 40, 1], [50, 70, 40], G, 2, 64, 16, seed=G)
+    _, pool, vals = pools(batch, False, 4)
+    lse = some_lse(batch, vals)
+    q = syn.bf16_to_float(batch.q).copy()
+    q[..., 0] = np.abs(q[..., 0]) + 1
+    q = torch.from_numpy(q).to(torch.bfloat16).cuda()
+    plan = make_plan(batch, dev(batch.page_table))
+    zeros = lambda: torch.zeros(batch.num_pages, 2, 16, device="cuda")
+    without = plan.key_weights(q, pool, dev(lse), zeros(), decay=0.0).cpu().numpy()
+    pool = pool.clone()
+    at = [(batch.page_table[batch.kv_indptr[b] + t // 16], t % 16)
+          for b, t in ((0, 3), (1, 20), (2, 33))]
+    for page, row in at:
+        pool[int(page), 0, :, row, 0] = -float("inf")
+        without[int(page), :, row] = 0
+    got = plan.key_weights(q, pool, dev(lse), zeros(), decay=0.0).cpu().numpy()
+    np.testing.assert_array_equal(got, without)
