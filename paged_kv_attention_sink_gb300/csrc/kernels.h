@@ -13,7 +13,11 @@ namespace attn {
 // stream: its CTAs may start while that one's last are running.  Every CTA of
 // such a kernel calls ptx::grid_dependency_wait() before it reads or writes
 // anything that other kernels do, and before it exits; ptx::grid_dependents_go()
-// lets the kernel after it start in the same way.
+// lets the kernel after it start in the same way.  Such a kernel is resident
+// while what it will read is still being written, so it reads through plain
+// loads (or asynchronous copies) alone: neither __ldg nor a const __restrict__
+// parameter, whose loads may take the read-only path and be moved before the
+// wait, for they promise that the data does not change while the kernel runs.
 template <class... Params, class... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                              Args&&... args) {

@@ -420,21 +420,24 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
             at[q] = col < used ? (r.q_row0 + col / heads) * a.Hq + g * G + head_of[q] : 0;
         }
         int row0 = i0, h0 = 0;
-        for (int grp = 0; grp < n_groups; ++grp) {
-            float* dst = nl_s + (grp & 1) * C::kGroup * kTileRows + lane;
-            float v[C::kGroup][kTileRows / 32];   // every load on its way before the first is used
+        auto fetch = [&](float (&v)[C::kGroup][kTileRows / 32]) {   // the next group's; past the last step nothing is read
 #pragma unroll
             for (int k = 0; k < C::kGroup; ++k) {
 #pragma unroll
                 for (int q = 0; q < kTileRows / 32; ++q)
-                    v[k][q] = row_of[q] < r.qo_len - row0 && head_of[q] < G - h0 ? __ldg(a.lse + at[q] + (row0 * a.Hq + h0))
-                                                                                : INFINITY;
+                    v[k][q] = row_of[q] < r.qo_len - row0 && head_of[q] < G - h0 ? a.lse[at[q] + (row0 * a.Hq + h0)] : INFINITY;
                 h0 += heads;
                 if (h0 >= G) {
                     h0 = 0;
                     row0 += rows;
                 }
             }
+        };
+        float v[C::kGroup][kTileRows / 32], next[C::kGroup][kTileRows / 32];   // two groups' loads on their way
+        fetch(v);
+        for (int grp = 0; grp < n_groups; ++grp) {
+            float* dst = nl_s + (grp & 1) * C::kGroup * kTileRows + lane;
+            fetch(next);
             if (grp >= 2 && !wait_all(l_free + 8 * (grp & 1), ((grp >> 1) - 1) & 1)) {
                 if (lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
                 break;
@@ -442,7 +445,10 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
 #pragma unroll
             for (int k = 0; k < C::kGroup; ++k)
 #pragma unroll
-                for (int q = 0; q < kTileRows / 32; ++q) dst[k * kTileRows + q * 32] = -v[k][q] * kLog2e;
+                for (int q = 0; q < kTileRows / 32; ++q) {
+                    dst[k * kTileRows + q * 32] = -v[k][q] * kLog2e;
+                    v[k][q] = next[k][q];
+                }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(l_full + 8 * (grp & 1));
         }

@@ -74,10 +74,9 @@ __device__ __forceinline__ uint32_t quantise16(const uint32_t (&w)[8], float g, 
 // items (a row's are per_row = 2 * Hkv * D / 16).
 template <int D>
 __global__ void __launch_bounds__(kKv4Threads)
-append_kv4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, uint8_t* __restrict__ pool,
-                  const int2* __restrict__ slots, const int32_t* __restrict__ page_table, int64_t rows, int32_t Hkv,
-                  int32_t page_log2, int32_t num_pages, float k_scale, float inv_k, float v_scale, float inv_v,
-                  int32_t* err) {
+append_kv4_kernel(const uint4* k_new, const uint4* v_new, uint8_t* pool, const int2* slots, const int32_t* page_table,
+                  int64_t rows, int32_t Hkv, int32_t page_log2, int32_t num_pages, float k_scale, float inv_k,
+                  float v_scale, float inv_v, int32_t* err) {
     ptx::grid_dependents_go();
     ptx::grid_dependency_wait();
     constexpr int kGroups = D / kKv4Group, kSub = kv4_sub_bytes(D);
@@ -94,8 +93,8 @@ append_kv4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_n
         if (r >= rows) return;
         const int half = in_row >= per_half;
         const uint4* src = (half ? v_new : k_new) + (r * per_half + in_row - half * per_half) * 2;
-        next_a = __ldg(src);
-        next_b = __ldg(src + 1);
+        next_a = src[0];
+        next_b = src[1];
         next_slot = slots[r];
     };
     fetch();
@@ -133,8 +132,8 @@ append_kv4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_n
 // has per_half = Hkv * P * D / 8 of them).
 template <int D>
 __global__ void __launch_bounds__(kKv4Threads)
-expand_kv4_kernel(const uint8_t* __restrict__ pool, uint4* __restrict__ buf, const int32_t* __restrict__ page_ids,
-                  int64_t n, int32_t Hkv, int32_t P, int64_t num_pages, float k_scale, float v_scale, int32_t* err) {
+expand_kv4_kernel(const uint8_t* pool, uint4* buf, const int32_t* page_ids, int64_t n, int32_t Hkv, int32_t P,
+                  int64_t num_pages, float k_scale, float v_scale, int32_t* err) {
     ptx::grid_dependents_go();
     ptx::grid_dependency_wait();
     constexpr int kOctets = D / 8, kSub = kv4_sub_bytes(D), kPerSub = kKv4Tokens * kOctets, kBatch = 2;
