@@ -390,8 +390,8 @@ ATTN_API attn_status attn_unpack_kv_heads(const void* buf, int64_t num_pages, in
  * buf[n_pages][2][Hkv][page_size][head_dim] (whole pages, exact), for
  * attn_prefill over a 4-bit cache: expand a request's pages into a bf16 pool
  * and plan the prefill on that.  head_dim 64 or 128, page_size a multiple of
- * 16 (else ATTN_ERR_UNSUPPORTED); page_ids, n_pages, device_error as in
- * attn_pack_kv_heads.
+ * 16, num_kv_heads * page_size * head_dim below 2^33 (else ATTN_ERR_UNSUPPORTED);
+ * page_ids, n_pages, device_error as in attn_pack_kv_heads.
  *
  * attn_decode_kv4 -- attn_decode over a 4-bit cache: the same plan, rows, sinks,
  * out and lse (and the same workspace regions: it must not overlap attn_decode

@@ -369,6 +369,8 @@ extern "C" attn_status attn_expand_kv4(const void* kv4_cache, int64_t num_pages,
         !valid_pool_scale(k_scale) || !valid_pool_scale(v_scale))
         return ATTN_ERR_INVALID_ARG;
     if ((head_dim != 64 && head_dim != 128) || page_size % attn::kKv4Tokens != 0) return ATTN_ERR_UNSUPPORTED;
+    // The kernel's index into a page's K or V half, and its sum with a step, are int32.
+    if ((int64_t)num_kv_heads * page_size >= (int64_t{1} << 33) / head_dim) return ATTN_ERR_UNSUPPORTED;
     if (n_pages == 0) return ATTN_OK;
     if (!kv4_cache || !buf || !page_ids || !aligned16(kv4_cache) || !aligned16(buf) || !aligned4(page_ids))
         return ATTN_ERR_INVALID_ARG;
