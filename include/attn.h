@@ -238,7 +238,8 @@ ATTN_API attn_status attn_merge_states_f32(const float* va, const float* lsea, c
  * error word live in a static 16 MiB device array inside the library.  A GPU
  * holds that array from the moment the library's device code is loaded there
  * (with lazy module loading, the first use of it on that GPU) until the
- * process exits.  Plans whose workspace_bytes exceed 16 MiB are rejected with
+ * process exits.  Plans that need more than that (their workspace_bytes without
+ * the lists that only other calls read) are rejected with
  * ATTN_ERR_WORKSPACE_TOO_SMALL.  It allocates nothing (no cudaMalloc /
  * cudaFree): each call uploads the work list with cudaMemcpyAsync from the
  * plan's host memory (pageable, so the call returns once the copy has been

@@ -95,27 +95,30 @@ extern "C" attn_status attn_plan_bind_workspace(attn_plan_t plan, void* workspac
     if (!plan) return ATTN_ERR_INVALID_ARG;
     const attn::WorkspaceLayout& L = plan->layout;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return ATTN_ERR_INVALID_ARG;
-    if (bytes < L.total) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+    const attn::ListLayout& A = plan->lists_layout;
+    if (bytes < A.total + L.total) return ATTN_ERR_WORKSPACE_TOO_SMALL;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
-    // The work lists lie in [0, L.counters): one host image, one copy (graph
-    // plans have none: their list is built on the device).
+    unsigned char* lists = static_cast<unsigned char*>(workspace);
+    unsigned char* ws = lists + A.total;
+    // The lists and, after them, the work lists in [0, L.counters): one host
+    // image, one copy (graph plans have none: their list is built on the device).
     if (!plan->units.empty() || !plan->items.empty() || !plan->requests.empty()) {
-        std::vector<unsigned char> img(L.counters, 0);
+        std::vector<unsigned char> img(A.total + L.counters, 0);
         auto put = [&](size_t off, const void* src, size_t bytes) {
             if (bytes) std::memcpy(img.data() + off, src, bytes);
         };
-        put(L.requests, plan->requests.data(), plan->requests.size() * sizeof(attn::RequestInfo));
-        put(L.weight_tiles, plan->weight_tiles.data(), plan->weight_tiles.size() * sizeof(attn::WeightTile));
-        put(L.units, plan->units.data(), plan->units.size() * sizeof(attn::DecodeUnit));
-        put(L.items, plan->items.data(), plan->items.size() * sizeof(attn::PrefillItem));
-        put(L.item_off, plan->item_off.data(), plan->item_off.size() * sizeof(int32_t));
-        put(L.append, plan->append_slots.data(), plan->append_slots.size() * sizeof(int32_t));
-        if (cudaMemcpyAsync(ws, img.data(), img.size(), cudaMemcpyHostToDevice, s) != cudaSuccess)
+        put(A.requests, plan->requests.data(), plan->requests.size() * sizeof(attn::RequestInfo));
+        put(A.weight_tiles, plan->weight_tiles.data(), plan->weight_tiles.size() * sizeof(attn::WeightTile));
+        put(A.total + L.units, plan->units.data(), plan->units.size() * sizeof(attn::DecodeUnit));
+        put(A.total + L.items, plan->items.data(), plan->items.size() * sizeof(attn::PrefillItem));
+        put(A.total + L.item_off, plan->item_off.data(), plan->item_off.size() * sizeof(int32_t));
+        put(A.total + L.append, plan->append_slots.data(), plan->append_slots.size() * sizeof(int32_t));
+        if (cudaMemcpyAsync(lists, img.data(), img.size(), cudaMemcpyHostToDevice, s) != cudaSuccess)
             return ATTN_ERR_CUDA;
     }
     // counters and the error word are adjacent: clear both.
     if (cudaMemsetAsync(ws + L.counters, 0, L.part_lse - L.counters, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    plan->lists = lists;
     plan->ws = ws;
     plan->ws_bytes = bytes;
     plan->bound = true;

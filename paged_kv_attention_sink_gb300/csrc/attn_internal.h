@@ -81,11 +81,15 @@ constexpr int kKv4Tokens = 16;
 constexpr int kKv4Group = 16;             // dims that share an e4m3 scale
 constexpr int kv4_sub_bytes(int head_dim) { return kKv4Tokens * (head_dim / 2 + head_dim / kKv4Group); }
 
-// Requests and weight tiles come first: attn_decode_noalloc's static scratch holds the
-// regions from `units` on.
 struct WorkspaceLayout {
-    size_t requests = 0, weight_tiles = 0, units = 0, items = 0, item_off = 0, append = 0, counters = 0, err = 0, n_units = 0, part_lse = 0,
-           part_o = 0, total = 0;
+    size_t units = 0, items = 0, item_off = 0, append = 0, counters = 0, err = 0, n_units = 0, part_lse = 0, part_o = 0,
+           total = 0;
+};
+
+// The lists of whole requests (key weights, eviction) lie in the workspace in
+// front of those regions, and are no part of attn_decode_noalloc's static scratch.
+struct ListLayout {
+    size_t requests = 0, weight_tiles = 0, total = 0;   // total: a multiple of 256
 };
 
 // CTAs of the decode kernel resident per SM for a head dim (matches its
@@ -141,8 +145,10 @@ struct attn_plan_s {
     int32_t n_partials = 0;
     attn_plan_info info{};
     attn::WorkspaceLayout layout;
+    attn::ListLayout lists_layout;
 
-    unsigned char* ws = nullptr;  // device, caller-owned
+    unsigned char* lists = nullptr;  // device, caller-owned: the lists ...
+    unsigned char* ws = nullptr;     // ... and after them the regions of `layout`
     size_t ws_bytes = 0;
     bool bound = false;
 

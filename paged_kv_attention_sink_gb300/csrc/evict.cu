@@ -458,7 +458,7 @@ attn_status launch_evict(attn_plan_s* plan, bool four, const float* weights, con
                          void* pool_out, float* weights_out, cudaStream_t stream) {
     if (plan->batch == 0) return ATTN_OK;
     EvictArgs a;
-    a.requests = reinterpret_cast<const RequestInfo*>(plan->ws + plan->layout.requests);
+    a.requests = reinterpret_cast<const RequestInfo*>(plan->lists + plan->lists_layout.requests);
     a.page_table = plan->page_table;
     a.weights = weights;
     a.pool = static_cast<const uint8_t*>(pool);

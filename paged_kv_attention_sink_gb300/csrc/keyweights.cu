@@ -697,8 +697,8 @@ attn_status launch_key_weights(attn_plan_s* plan, bool four, const void* q, cons
                                float decay, int32_t window, float* weights, cudaStream_t stream) {
     KeyWeightArgs a;
     a.units = reinterpret_cast<const DecodeUnit*>(plan->ws + plan->layout.units);
-    a.requests = reinterpret_cast<const RequestInfo*>(plan->ws + plan->layout.requests);
-    a.tiles = reinterpret_cast<const int2*>(plan->ws + plan->layout.weight_tiles);
+    a.requests = reinterpret_cast<const RequestInfo*>(plan->lists + plan->lists_layout.requests);
+    a.tiles = reinterpret_cast<const int2*>(plan->lists + plan->lists_layout.weight_tiles);
     a.page_table = plan->page_table;
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.lse = lse;

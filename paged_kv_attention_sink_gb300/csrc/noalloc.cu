@@ -66,10 +66,9 @@ extern "C" attn_status attn_decode_noalloc(attn_plan_t plan, const void* q, cons
          reinterpret_cast<uintptr_t>(out)) & 15)
         return ATTN_ERR_INVALID_ARG;
     const attn::WorkspaceLayout& L = plan->layout;
-    if (L.total - L.units > kNoAllocScratchBytes) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+    if (L.total > kNoAllocScratchBytes) return ATTN_ERR_WORKSPACE_TOO_SMALL;
     unsigned char* scratch = scratch_on_current_device();
     if (!scratch) return ATTN_ERR_CUDA;
-    scratch -= L.units;   // the array holds the regions from `units` on
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // The array keeps the previous call's contents: upload this plan's work
@@ -89,10 +88,9 @@ extern "C" attn_status attn_decode_noalloc(attn_plan_t plan, const void* q, cons
 extern "C" attn_status attn_decode_noalloc_device_error(attn_plan_t plan, int32_t* code, void* stream) {
     if (!plan || !code || plan->graph) return ATTN_ERR_INVALID_ARG;
     const attn::WorkspaceLayout& L = plan->layout;
-    if (L.total - L.units > kNoAllocScratchBytes) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+    if (L.total > kNoAllocScratchBytes) return ATTN_ERR_WORKSPACE_TOO_SMALL;
     unsigned char* scratch = scratch_on_current_device();
     if (!scratch) return ATTN_ERR_CUDA;
-    scratch -= L.units;   // the array holds the regions from `units` on
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
     int32_t v = 0;
     if (cudaMemcpy(&v, scratch + L.err, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return ATTN_ERR_CUDA;

@@ -278,10 +278,11 @@ attn_status make_plan(bool ragged, const int32_t* qo_indptr, const int32_t* kv_i
                      [&](const WeightTile& x, const WeightTile& y) { return rows_seeing(x) > rows_seeing(y); });
 
     // ---- workspace layout (every region 256-byte aligned).
+    ListLayout& A = plan->lists_layout;
+    A.weight_tiles = align_up(plan->requests.size() * sizeof(RequestInfo), 256);
+    A.total = align_up(A.weight_tiles + plan->weight_tiles.size() * sizeof(WeightTile), 256);
     WorkspaceLayout& L = plan->layout;
     size_t off = 0;
-    L.requests = off; off = align_up(off + plan->requests.size() * sizeof(RequestInfo), 256);
-    L.weight_tiles = off; off = align_up(off + plan->weight_tiles.size() * sizeof(WeightTile), 256);
     L.units = off;    off = align_up(off + plan->units.size() * sizeof(DecodeUnit), 256);
     L.items = off;    off = align_up(off + plan->items.size() * sizeof(PrefillItem), 256);
     L.append = off;   off = align_up(off + plan->append_slots.size() * sizeof(int32_t), 256);
@@ -306,10 +307,10 @@ attn_status make_plan(bool ragged, const int32_t* qo_indptr, const int32_t* kv_i
     I.num_sms = num_sms;
     I.decode_kv_tokens = decode_tokens;
     I.prefill_pairs = prefill_pairs;
-    I.workspace_bytes = L.total;
+    I.workspace_bytes = A.total + L.total;
 
     *plan_out = plan;
-    *workspace_bytes_out = L.total;
+    *workspace_bytes_out = I.workspace_bytes;
     return ATTN_OK;
 }
 
