@@ -23,11 +23,11 @@
 //    a reduction over its lanes.
 //
 // Measured, inputs beyond the L2: 64 requests of 1K-8K tokens, 8 KV heads of 64
-// dims (181 MB) 42.5 us, 4.3 TB/s; 256 of 0.5K-16K (1.29 GB) 224 us, 5.7 TB/s,
-// 0.85 of a copy's rate; 32 of 2K-32K, 4 KV heads of 128 dims with 16 query heads
-// each (293 MB) 77 us, 3.8 TB/s.  A large batch is bound by memory and the issue
+// dims (181 MB) 42.4 us, 4.3 TB/s; 256 of 0.5K-16K (1.29 GB) 220 us, 5.9 TB/s,
+// 0.86 of a copy's rate; 32 of 2K-32K, 4 KV heads of 128 dims with 16 query heads
+// each (293 MB) 76.8 us, 3.8 TB/s.  A large batch is bound by memory and the issue
 // slots alike; a small one by what a unit does before and after its loop (page
-// ids, first tile, merge) and the last wave; the 16-head form, with 208 registers
+// ids, first tile, merge) and the last wave; the 16-head form, with 230 registers
 // and so eight warps per SM, by the latency of a warp's chain of products.
 //
 // One CTA = one decode unit of the plan (request, KV head, <= 16 query heads,
@@ -44,6 +44,9 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// P is rounded to f16, as the tensor cores take V's exact values there: half a
+// step is 2^-11 of a weight, an eighth of what rounding the output to bf16 may
+// cost; the row sum takes P unrounded, in fp32.
 // The softmax shift m lies kShift below the running max, so that P's largest is
 // 2^7 and f16 is normal down to 2^-21 of it (its subnormals then cost 2^-32 of
 // it at most); m moves when a score passes it by kSlack (P stays below 2^15).
@@ -58,6 +61,12 @@ struct Decode4Cfg {
     // 236 with 128 and 12 warps).
     static constexpr int kTile = 64;
     static constexpr int kStages = 2;
+    // CTAs per SM, for the registers: with a bound the compiler spends what is
+    // left on loads ahead.  Without one it took 96 where 123 fit (64 dims, up to
+    // 8 heads): 44.7 us instead of 42.4 for 64 requests of 1K-8K; 16 heads of 128
+    // dims 78.6 instead of 76.8 (204 registers, 230), 8 heads of 128 dims, 256
+    // requests of 0.5K-8K, 190.5 instead of 185.8.
+    static constexpr int kCtas = D == 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
     static constexpr int kSubs = kTile / kKv4Tokens;
     static constexpr int kSub = kv4_sub_bytes(D);
     static constexpr int kStageBytes = 2 * kSubs * kSub;              // K, then V
@@ -66,7 +75,7 @@ struct Decode4Cfg {
     static constexpr int kWarpBytes = kStages * kStageBytes;
     static constexpr int kPipeBytes = kWarps * kWarpBytes;
     static constexpr int kPageBytes = (kDecodeMaxChunkPages * 4 + 15) / 16 * 16;
-    static constexpr int kStateBytes = kWarps * 32 * 4 + 16;          // per-warp m, l (16 heads each) + flag
+    static constexpr int kStateBytes = (kWarps * 32 + kMaxSliceHeads) * 4 + 16;   // per-warp m, l (16 heads each), sinks, flag
     static constexpr int kSmem = kPipeBytes + kPageBytes + kStateBytes;
     static_assert(kHeads * kRowStride * 4 <= kWarpBytes, "a warp's state fits its ring");
 };
@@ -114,19 +123,22 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// 2^(m - top) of a state at shift m (log2 units): 0 for one without weight (m = -inf).
+__device__ __forceinline__ float weight_at(float m, float top) { return m == -INFINITY ? 0.f : ptx::ex2(m - top); }
 __device__ __forceinline__ void store_bf16x4(__nv_bfloat16* dst, float a, float b, float c, float d) {
     *reinterpret_cast<uint2*>(dst) = make_uint2(ptx::pack_bf16x2(a, b), ptx::pack_bf16x2(c, d));
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(Decode4Cfg<D, NT>::kWarps * 32)
+__global__ void __launch_bounds__(Decode4Cfg<D, NT>::kWarps * 32, Decode4Cfg<D, NT>::kCtas)
 decode4_sink_attn_kernel(const Decode4Args a) {
     using C = Decode4Cfg<D, NT>;
     constexpr int kKSteps = D / 16;
     extern __shared__ __align__(16) uint8_t smem[];
     uint32_t* first_s = reinterpret_cast<uint32_t*>(smem + C::kPipeBytes);
     float* ml_s = reinterpret_cast<float*>(smem + C::kPipeBytes + C::kPageBytes);
-    int* flag_s = reinterpret_cast<int*>(ml_s + C::kWarps * 32);
+    float* sink_s = ml_s + C::kWarps * 32;
+    int* flag_s = reinterpret_cast<int*>(sink_s + kMaxSliceHeads);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gq = lane >> 2, tq = lane & 3;
@@ -134,7 +146,12 @@ decode4_sink_attn_kernel(const Decode4Args a) {
     ptx::grid_dependency_wait();
     const int first_page = u.tok_begin >> a.page_log2;
     const int n_pages = ((u.tok_end - 1) >> a.page_log2) - first_page + 1;
+    // The sinks (log2 units) of a request's first chunk, for the merge; read here,
+    // in the shadow of the page ids.
+    float sink = -INFINITY;
+    if (tid < u.n_heads && u.chunk == 0 && a.sinks != nullptr) sink = a.sinks[u.head0 + tid] * kLog2e;
     load_sixteens(first_s, a.page_table + u.page_base + first_page, n_pages, a.num_pages, a.Hkv, u.kv_head, a.page_log2, a.err);
+    if (tid < kMaxSliceHeads) sink_s[tid] = sink;
     __syncthreads();
 
     uint8_t* ring = smem + warp * C::kWarpBytes;
@@ -164,22 +181,13 @@ decode4_sink_attn_kernel(const Decode4Args a) {
     }
 
     // Online-softmax state of heads nt * 8 + 2 tq + e (log2 domain).  l is this
-    // lane's share of the row sum; the sink counts once, on lane row 0.  Until
-    // the first scores come m is the sink's shift, or 0 where there is none.
-    auto sink_shift = [&](int h) {
-        return warp == 0 && u.chunk == 0 && a.sinks != nullptr && h < u.n_heads ? a.sinks[u.head0 + h] * kLog2e - kShift
-                                                                               : -INFINITY;
-    };
+    // lane's share of the row sum.  The sink joins at the merge: a shift that
+    // followed it would leave the keys beside a large sink no bits in f16.
     float o[NT][kKSteps][4];
     float2 nm[NT], l[NT];   // nm: the shift, negated
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float s = sink_shift(nt * 8 + 2 * tq + e);
-            (e ? nm[nt].y : nm[nt].x) = s == -INFINITY ? 0.f : -s;
-            (e ? l[nt].y : l[nt].x) = s == -INFINITY || gq != 0 ? 0.f : exp2f(kShift);
-        }
+        nm[nt] = l[nt] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kKSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
@@ -245,10 +253,10 @@ decode4_sink_attn_kernel(const Decode4Args a) {
                         mx = fmaxf(mx, fmaxf(x[sub][nt][e], x[sub][nt][e + 2]));
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    // How far the shift moves; at the start it holds no score
-                    // yet, only (if any) the sink's.
-                    const bool none = slack < 0.f && sink_shift(nt * 8 + 2 * tq + e) == -INFINITY;
-                    const float up = none ? mx - kShift : fmaxf(0.f, mx - kShift);
+                    // How far the shift moves: up alone, but at the start, where it holds
+                    // no score yet (nor now, if all of them are -inf).
+                    const bool none = slack < 0.f;
+                    const float up = none && mx != -INFINITY ? mx - kShift : fmaxf(0.f, mx - kShift);
                     const float alpha = none ? 0.f : ptx::ex2(-up);
                     (e ? nm[nt].y : nm[nt].x) -= up;
                     (e ? l[nt].y : l[nt].x) *= alpha;
@@ -310,31 +318,32 @@ decode4_sink_attn_kernel(const Decode4Args a) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             if (gq == 0) {
-                ml_s[warp * 32 + nt * 8 + 2 * tq + e] = n_it > 0 ? -(e ? nm[nt].y : nm[nt].x) : -INFINITY;   // no tokens: no state
+                ml_s[warp * 32 + nt * 8 + 2 * tq + e] = sum == 0.f ? -INFINITY : -(e ? nm[nt].y : nm[nt].x);   // no weight: no state
                 ml_s[warp * 32 + 16 + nt * 8 + 2 * tq + e] = sum;
             }
         }
     __syncthreads();
 
-    // Merge the warps: heads < n_heads, 4 dims per item.
+    // Merge the warps, and in a request's first chunk the sink, a state of value
+    // 0 and weight 1 at its own shift: heads < n_heads, 4 dims per item.
     const int items = u.n_heads * (D / 4);
     for (int idx = tid; idx < items; idx += blockDim.x) {
         const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
-        float ms = -INFINITY;
+        float ms = fmaxf(sink_s[r], -INFINITY);   // -inf also where the sink is NaN
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) ms = fmaxf(ms, ml_s[w * 32 + r]);
-        float L = 0.f;
+        float L = weight_at(sink_s[r], ms);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) {
             const float mw = ml_s[w * 32 + r];
-            const float f = mw == -INFINITY ? 0.f : ptx::ex2(mw - ms);
+            const float f = weight_at(mw, ms);
             L += f * ml_s[w * 32 + 16 + r];
             const float4 ow = *reinterpret_cast<const float4*>(
                 reinterpret_cast<const float*>(smem + w * C::kWarpBytes) + r * C::kRowStride + d);
             if (f > 0.f) { acc.x += f * ow.x; acc.y += f * ow.y; acc.z += f * ow.z; acc.w += f * ow.w; }
         }
-        const float inv = (u.n_chunks == 1 ? a.v_scale : 1.f) / L;
+        const float inv = L == 0.f ? 0.f : (u.n_chunks == 1 ? a.v_scale : 1.f) / L;   // no weight at all: 0, lse -inf
         const float lse2 = ms + log2f(L);
         if (u.n_chunks == 1) {
             store_bf16x4(a.out + ((size_t)u.q_row * a.Hq + u.head0 + r) * D + d, acc.x * inv, acc.y * inv, acc.z * inv,
@@ -376,18 +385,18 @@ decode4_sink_attn_kernel(const Decode4Args a) {
             float mb = M;
 #pragma unroll
             for (int k = 0; k < kMergeBatch; ++k) mb = fmaxf(mb, lc[k]);
-            const float sc = M == -INFINITY ? 0.f : ptx::ex2(M - mb);
+            const float sc = weight_at(M, mb);
             W *= sc;
             acc.x *= sc; acc.y *= sc; acc.z *= sc; acc.w *= sc;
 #pragma unroll
             for (int k = 0; k < kMergeBatch; ++k) {
-                const float w = lc[k] == -INFINITY ? 0.f : ptx::ex2(lc[k] - mb);
+                const float w = weight_at(lc[k], mb);
                 W += w;
                 acc.x += w * oc[k].x; acc.y += w * oc[k].y; acc.z += w * oc[k].z; acc.w += w * oc[k].w;
             }
             M = mb;
         }
-        const float inv = a.v_scale / W;
+        const float inv = W == 0.f ? 0.f : a.v_scale / W;
         store_bf16x4(a.out + ((size_t)u.q_row * a.Hq + u.head0 + r) * D + d, acc.x * inv, acc.y * inv, acc.z * inv,
                      acc.w * inv);
         if (d == 0 && a.lse) a.lse[(size_t)u.q_row * a.Hq + u.head0 + r] = (M + log2f(W)) * kLn2;
