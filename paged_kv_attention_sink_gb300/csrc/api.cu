@@ -108,7 +108,8 @@ extern "C" attn_status attn_plan_bind_workspace(attn_plan_t plan, void* workspac
             if (bytes) std::memcpy(img.data() + off, src, bytes);
         };
         put(A.requests, plan->requests.data(), plan->requests.size() * sizeof(attn::RequestInfo));
-        put(A.weight_tiles, plan->weight_tiles.data(), plan->weight_tiles.size() * sizeof(attn::WeightTile));
+        put(A.weight_runs, plan->weight_runs.data(), plan->weight_runs.size() * sizeof(attn::WeightRun));
+        put(A.weight_hints, plan->weight_hints.data(), plan->weight_hints.size() * sizeof(int32_t));
         put(A.total + L.units, plan->units.data(), plan->units.size() * sizeof(attn::DecodeUnit));
         put(A.total + L.items, plan->items.data(), plan->items.size() * sizeof(attn::PrefillItem));
         put(A.total + L.item_off, plan->item_off.data(), plan->item_off.size() * sizeof(int32_t));
@@ -321,7 +322,7 @@ attn_status key_weights(attn_plan_t plan, bool four, const void* q, const void* 
     if (!q || !pool || !lse || !weights || (decay != 0.f && !prev)) return ATTN_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(pool) || !aligned4(lse) || !aligned4(prev) || !aligned4(weights))
         return ATTN_ERR_INVALID_ARG;
-    if (!plan->weight_tiles.empty()) {
+    if (plan->weight_tiles > 0) {
         if (!four && plan->kv_map_prefill_ptr != pool) {
             if (!make_kv_map(plan->kv_map_prefill, pool, plan, plan->P)) return ATTN_ERR_CUDA;
             plan->kv_map_prefill_ptr = pool;

@@ -69,11 +69,21 @@ struct RequestInfo {
 };
 static_assert(sizeof(RequestInfo) == 16, "request info is one 16-byte load");
 
-// 128 keys of a prefill request: the work item of its key weights (times KV heads).
-struct WeightTile {
-    int32_t request;
-    int32_t key0;
+// 128 keys of a prefill request are the work item of its key weights (times KV
+// heads).  A run is consecutive such tiles of one request that equally many query
+// rows see: all of those under its prefix, or a single one on the diagonal.
+// Tiles are numbered through the runs.
+constexpr int kWeightTileKeys = 128;
+struct WeightRun {
+    int32_t tile0;      // number of its first tile
+    int32_t key0;       // first key of that
+    RequestInfo request;
+    int32_t reserved[2];
 };
+static_assert(sizeof(WeightRun) == 32, "weight run is one sector");
+// A tile's run is found from a table that has the run of every 32nd tile: it is
+// that one or one of the 31 after it.
+constexpr int kWeightHintTiles = 32;
 
 // The 4-bit cache holds 16 tokens of a (page, K/V, KV head) block together:
 // 16 rows of D / 2 code bytes, then 16 rows of D / 16 scale bytes.
@@ -89,7 +99,7 @@ struct WorkspaceLayout {
 // The lists of whole requests (key weights, eviction) lie in the workspace in
 // front of those regions, and are no part of attn_decode_noalloc's static scratch.
 struct ListLayout {
-    size_t requests = 0, weight_tiles = 0, total = 0;   // total: a multiple of 256
+    size_t requests = 0, weight_runs = 0, weight_hints = 0, total = 0;   // total: a multiple of 256
 };
 
 // CTAs of the decode kernel resident per SM for a head dim (matches its
@@ -135,7 +145,9 @@ struct attn_plan_s {
     int64_t graph_kv_blocks = 0;          // graph: 16-token blocks a batch may hold in total
 
     std::vector<attn::RequestInfo> requests;   // paged plans: every request, in order
-    std::vector<attn::WeightTile> weight_tiles;   // prefill requests' 128-key tiles, most query rows first
+    std::vector<attn::WeightRun> weight_runs;  // prefill requests' 128-key tiles, most query rows first
+    std::vector<int32_t> weight_hints;         // the run of every 32nd tile
+    int32_t weight_tiles = 0;
     std::vector<attn::DecodeUnit> units;
     std::vector<attn::PrefillItem> items;
     std::vector<int32_t> append_slots;    // per query row: page-table slot, row in page

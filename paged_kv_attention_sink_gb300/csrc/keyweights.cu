@@ -51,8 +51,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct KeyWeightArgs {
     const DecodeUnit* units;
-    const RequestInfo* requests;
-    const int2* tiles;          // prefill requests: (request, first key) of each 128-key tile
+    const WeightRun* runs;      // prefill requests: runs of 128-key tiles,
+    const int32_t* hints;       // and the run of every 32nd tile
     const int32_t* page_table;
     const __nv_bfloat16* q;
     const float* lse;
@@ -60,7 +60,7 @@ struct KeyWeightArgs {
     const float* prev;
     float* weights;
     int32_t* err;
-    int32_t Hq, Hkv, P, page_log2, num_pages, causal, window;   // P = 1 << page_log2
+    int32_t Hq, Hkv, P, page_log2, num_pages, causal, window, n_runs;   // P = 1 << page_log2
     float scale_log2, decay;    // scale_log2 = sm_scale * log2(e) * k_scale
 };
 
@@ -261,7 +261,7 @@ key_weights_step_kernel(const KeyWeightArgs a) {
 
 // ----------------------------------------------------------- prefill requests
 
-constexpr int kTileKeys = 128;   // keys per CTA: the MMA's M, a TMEM lane each
+constexpr int kTileKeys = kWeightTileKeys;   // 128 keys per CTA: the MMA's M, a TMEM lane each
 constexpr int kTileRows = 128;   // columns per step: the MMA's N
 
 // A wait with the same result in every lane of the warp.
@@ -323,9 +323,13 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
     float* sum_s = reinterpret_cast<float*>(smem + C::kOffSum);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int2 tile = a.tiles[blockIdx.x / a.Hkv];
-    const int g = blockIdx.x % a.Hkv, t0 = tile.y;
-    const RequestInfo r = a.requests[tile.x];
+    // The tile's run: the last that begins at or before it, of the 32 from the hint on.
+    const int tile = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv;
+    const int hint = a.hints[tile / kWeightHintTiles];
+    const bool begun = hint + lane < a.n_runs && a.runs[min(hint + lane, a.n_runs - 1)].tile0 <= tile;
+    const WeightRun run = a.runs[hint + __popc(__ballot_sync(0xffffffffu, begun)) - 1];
+    const int t0 = run.key0 + (tile - run.tile0) * kTileKeys;
+    const RequestInfo r = run.request;
     const int G = a.Hq / a.Hkv, P = a.P, prefix = r.kv_len - r.qo_len;
     // First query row that counts: inside the window, and seeing the first key.
     int i0 = a.window > 0 ? max(0, r.qo_len - a.window) : 0;
@@ -673,7 +677,7 @@ attn_status launch_all(const attn_plan_s* plan, const CUtensorMap& q_map, const 
         e = G <= 8    ? launch_step<D, kFour, 1>(a, units, stream)
             : G <= 16 ? launch_step<D, kFour, 2>(a, units, stream)
                       : launch_step<D, kFour, 0>(a, units, stream);
-    if (e == cudaSuccess && !plan->weight_tiles.empty()) {
+    if (e == cudaSuccess && plan->weight_tiles > 0) {
         const int heads = std::min(G, kTileRows), rows = kTileRows / heads, slices = (G + heads - 1) / heads;
         int64_t steps = 0;
         for (const RequestInfo& r : plan->requests)
@@ -681,9 +685,9 @@ attn_status launch_all(const attn_plan_s* plan, const CUtensorMap& q_map, const 
                 const int n = a.window > 0 ? std::min(a.window, r.qo_len) : r.qo_len;
                 steps += ((int64_t)r.kv_len + kTileKeys - 1) / kTileKeys * ((n + rows - 1) / rows) * slices;
             }
-        const int grid = (int)plan->weight_tiles.size() * plan->Hkv;
+        const int grid = plan->weight_tiles * plan->Hkv;
         const bool ragged = rows * heads < kTileRows;
-        e = steps <= kShortSteps * (int64_t)plan->weight_tiles.size() ? launch_prompt<D, kFour, true, false>(q_map, kv_map, a, grid, stream)
+        e = steps <= kShortSteps * (int64_t)plan->weight_tiles ? launch_prompt<D, kFour, true, false>(q_map, kv_map, a, grid, stream)
             : ragged ? launch_prompt<D, kFour, false, true>(q_map, kv_map, a, grid, stream)
                      : launch_prompt<D, kFour, false, false>(q_map, kv_map, a, grid, stream);
     }
@@ -697,8 +701,9 @@ attn_status launch_key_weights(attn_plan_s* plan, bool four, const void* q, cons
                                float decay, int32_t window, float* weights, cudaStream_t stream) {
     KeyWeightArgs a;
     a.units = reinterpret_cast<const DecodeUnit*>(plan->ws + plan->layout.units);
-    a.requests = reinterpret_cast<const RequestInfo*>(plan->lists + plan->lists_layout.requests);
-    a.tiles = reinterpret_cast<const int2*>(plan->lists + plan->lists_layout.weight_tiles);
+    a.runs = reinterpret_cast<const WeightRun*>(plan->lists + plan->lists_layout.weight_runs);
+    a.hints = reinterpret_cast<const int32_t*>(plan->lists + plan->lists_layout.weight_hints);
+    a.n_runs = (int32_t)plan->weight_runs.size();
     a.page_table = plan->page_table;
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.lse = lse;

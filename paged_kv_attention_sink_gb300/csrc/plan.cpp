@@ -265,22 +265,36 @@ attn_status make_plan(bool ragged, const int32_t* qo_indptr, const int32_t* kv_i
     plan->requests.resize(ragged ? 0 : (size_t)batch);
     for (int32_t b = 0; b < batch && !ragged; ++b)
         plan->requests[b] = {qo_indptr[b], (int32_t)qo_len[b], kv_indptr[b], (int32_t)kv_len[b]};
-    // Key weights of prefill requests: 128-key tiles, the ones that most query
-    // rows see first (the CTAs are dispatched in this order).
-    for (int32_t b = 0; b < batch && !ragged; ++b)
-        for (int64_t t0 = 0; qo_len[b] > 1 && t0 < kv_len[b]; t0 += kPrefillKeys)
-            plan->weight_tiles.push_back({b, (int32_t)t0});
-    auto rows_seeing = [&](const WeightTile& w) {
-        const int64_t n = qo_len[w.request], prefix = kv_len[w.request] - n;
-        return causal ? n - std::max<int64_t>(0, w.key0 - prefix) : n;
+    // Key weights of prefill requests: runs of 128-key tiles, the ones that most
+    // query rows see first (the CTAs are dispatched in this order).
+    for (int32_t b = 0; b < batch && !ragged; ++b) {
+        if (qo_len[b] <= 1) continue;
+        const int64_t prefix = kv_len[b] - qo_len[b];
+        plan->weight_runs.push_back({0, 0, plan->requests[b], {0, 0}});
+        if (causal)
+            for (int64_t t0 = (prefix / kWeightTileKeys + 1) * kWeightTileKeys; t0 < kv_len[b]; t0 += kWeightTileKeys)
+                plan->weight_runs.push_back({0, (int32_t)t0, plan->requests[b], {0, 0}});
+    }
+    auto rows_seeing = [&](const WeightRun& w) {
+        const int32_t n = w.request.qo_len;
+        return causal ? n - std::max(0, w.key0 - (w.request.kv_len - n)) : n;
     };
-    std::stable_sort(plan->weight_tiles.begin(), plan->weight_tiles.end(),
-                     [&](const WeightTile& x, const WeightTile& y) { return rows_seeing(x) > rows_seeing(y); });
+    std::stable_sort(plan->weight_runs.begin(), plan->weight_runs.end(),
+                     [&](const WeightRun& x, const WeightRun& y) { return rows_seeing(x) > rows_seeing(y); });
+    for (size_t i = 0; i < plan->weight_runs.size(); ++i) {
+        WeightRun& w = plan->weight_runs[i];
+        const int32_t n = w.request.qo_len, prefix = w.request.kv_len - n;
+        const int32_t last = w.key0 > 0 ? w.key0 : causal ? prefix : w.request.kv_len - 1;   // in the run's last tile
+        w.tile0 = plan->weight_tiles;
+        plan->weight_tiles += (last - w.key0) / kWeightTileKeys + 1;
+        plan->weight_hints.resize(((size_t)plan->weight_tiles + kWeightHintTiles - 1) / kWeightHintTiles, (int32_t)i);
+    }
 
     // ---- workspace layout (every region 256-byte aligned).
     ListLayout& A = plan->lists_layout;
-    A.weight_tiles = align_up(plan->requests.size() * sizeof(RequestInfo), 256);
-    A.total = align_up(A.weight_tiles + plan->weight_tiles.size() * sizeof(WeightTile), 256);
+    A.weight_runs = align_up(plan->requests.size() * sizeof(RequestInfo), 256);
+    A.weight_hints = align_up(A.weight_runs + plan->weight_runs.size() * sizeof(WeightRun), 256);
+    A.total = align_up(A.weight_hints + plan->weight_hints.size() * sizeof(int32_t), 256);
     WorkspaceLayout& L = plan->layout;
     size_t off = 0;
     L.units = off;    off = align_up(off + plan->units.size() * sizeof(DecodeUnit), 256);
