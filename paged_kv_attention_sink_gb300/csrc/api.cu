@@ -109,7 +109,8 @@ extern "C" attn_status attn_plan_bind_workspace(attn_plan_t plan, void* workspac
         };
         put(A.requests, plan->requests.data(), plan->requests.size() * sizeof(attn::RequestInfo));
         put(A.weight_runs, plan->weight_runs.data(), plan->weight_runs.size() * sizeof(attn::WeightRun));
-        put(A.weight_hints, plan->weight_hints.data(), plan->weight_hints.size() * sizeof(int32_t));
+        put(A.weight_starts, plan->weight_starts.data(), plan->weight_starts.size() * sizeof(int32_t));
+        put(A.weight_hints, plan->weight_hints.data(), plan->weight_hints.size() * sizeof(uint32_t));
         put(A.total + L.units, plan->units.data(), plan->units.size() * sizeof(attn::DecodeUnit));
         put(A.total + L.items, plan->items.data(), plan->items.size() * sizeof(attn::PrefillItem));
         put(A.total + L.item_off, plan->item_off.data(), plan->item_off.size() * sizeof(int32_t));

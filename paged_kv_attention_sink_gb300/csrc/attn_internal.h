@@ -82,8 +82,42 @@ struct WeightRun {
 };
 static_assert(sizeof(WeightRun) == 32, "weight run is one sector");
 // A tile's run is found from a table that has the run of every 32nd tile: it is
-// that one or one of the 31 after it.
+// that one or one of the 31 after it (that one, where kWeightHintAll is set).
 constexpr int kWeightHintTiles = 32;
+constexpr uint32_t kWeightHintAll = 0x80000000u;
+
+// A step of a tile is 128 (row, head) pairs: 128 / G query rows with their G
+// heads of the KV head, or, beyond 128 heads, one row in slices.
+constexpr int kWeightTileRows = 128;
+inline int64_t weight_steps(int64_t rows, int G) {
+    const int heads = G < kWeightTileRows ? G : kWeightTileRows, per = kWeightTileRows / heads;
+    return (rows + per - 1) / per * ((G + heads - 1) / heads);
+}
+
+// Two forms of the kernel, for tiles of many steps and for many tiles of few.
+constexpr int kWeightShortSteps = 64;
+constexpr int weight_short_ctas(int head_dim) { return head_dim == 64 ? 4 : 2; }   // short form, per SM
+
+// Tiles of some prefill requests, and their steps (the last `window` rows alone,
+// 0: all; causality not counted).
+struct WeightLoad {
+    int64_t tiles = 0, steps = 0, longest = 0;   // longest: most steps of one tile
+    void add(const RequestInfo& r, int G, int32_t window) {
+        const int64_t n = ((int64_t)r.kv_len + kWeightTileKeys - 1) / kWeightTileKeys;
+        const int64_t s = weight_steps(window > 0 && window < r.qo_len ? window : r.qo_len, G);
+        tiles += n;
+        steps += n * s;
+        longest = longest > s ? longest : s;
+    }
+    // Whether the short form takes them; what the rule goes by is in keyweights.cu.
+    bool takes_short_form(int Hkv, int sms, int head_dim) const {
+        const int64_t ctas = tiles * Hkv;
+        return ctas > sms && steps <= kWeightShortSteps * tiles &&
+               2 * steps * sms <= 3 * weight_short_ctas(head_dim) * ctas * tiles;
+    }
+    // Whether the short form's longest CTA ends within the time that all of them take.
+    bool even(int Hkv, int sms) const { return 8 * longest * sms <= 5 * steps * Hkv; }
+};
 
 // The 4-bit cache holds 16 tokens of a (page, K/V, KV head) block together:
 // 16 rows of D / 2 code bytes, then 16 rows of D / 16 scale bytes.
@@ -99,7 +133,7 @@ struct WorkspaceLayout {
 // The lists of whole requests (key weights, eviction) lie in the workspace in
 // front of those regions, and are no part of attn_decode_noalloc's static scratch.
 struct ListLayout {
-    size_t requests = 0, weight_runs = 0, weight_hints = 0, total = 0;   // total: a multiple of 256
+    size_t requests = 0, weight_runs = 0, weight_starts = 0, weight_hints = 0, total = 0;   // total: a multiple of 256
 };
 
 // CTAs of the decode kernel resident per SM for a head dim (matches its
@@ -146,8 +180,10 @@ struct attn_plan_s {
 
     std::vector<attn::RequestInfo> requests;   // paged plans: every request, in order
     std::vector<attn::WeightRun> weight_runs;  // prefill requests' 128-key tiles, most query rows first
-    std::vector<int32_t> weight_hints;         // the run of every 32nd tile
+    std::vector<int32_t> weight_starts;        // the runs' first tiles once more
+    std::vector<uint32_t> weight_hints;        // the run of every 32nd tile
     int32_t weight_tiles = 0;
+    int32_t weight_long_tiles = 0;             // > 0: requests of many steps come first, this many tiles
     std::vector<attn::DecodeUnit> units;
     std::vector<attn::PrefillItem> items;
     std::vector<int32_t> append_slots;    // per query row: page-table slot, row in page

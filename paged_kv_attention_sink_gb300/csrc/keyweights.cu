@@ -24,12 +24,14 @@
 //    rows' heads (so that few rows with many heads fill them); tcgen05.mma fills
 //    a ring of 128-column accumulators in TMEM ahead of the warpgroups that drain
 //    them, one key per thread.  Four prompts of 0.5K-4K tokens, 64 query heads of
-//    64 dims: 193 us, where the exponentials of whole tiles take 119 us at the
+//    64 dims: 190 us, where the exponentials of whole tiles take 119 us at the
 //    MUFU's rate and the products 73 us.  A CTA starts for some 5,000 clocks
 //    (TMEM, K, the first lse), 4.2 times per SM; its steps take 770 instead of
 //    the MUFU's 512: the barriers and TMEM loads alone measure 600, and overlap
 //    with the exponentials in part.  Steps of 128 rows of one head measured 200
-//    us; so built, two warpgroups 223 and four 252 (fewer registers each), steps
+//    us where this form then took 193, but lost less with head counts that leave
+//    columns of these steps empty (two prompts, 12 heads per KV head 302 us
+//    instead of 313, 5 heads 135 instead of 138); so built, two warpgroups 223 and four 252 (fewer registers each), steps
 //    of two heads (N = 256) with four warpgroups on 64 columns each 228, the next
 //    step's first columns loaded ahead 209, and a query row per thread with a sum
 //    of 128 keys in registers 297.
@@ -51,8 +53,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct KeyWeightArgs {
     const DecodeUnit* units;
-    const WeightRun* runs;      // prefill requests: runs of 128-key tiles,
-    const int32_t* hints;       // and the run of every 32nd tile
     const int32_t* page_table;
     const __nv_bfloat16* q;
     const float* lse;
@@ -60,8 +60,16 @@ struct KeyWeightArgs {
     const float* prev;
     float* weights;
     int32_t* err;
-    int32_t Hq, Hkv, P, page_log2, num_pages, causal, window, n_runs;   // P = 1 << page_log2
+    int32_t Hq, Hkv, P, page_log2, num_pages, causal, window;   // P = 1 << page_log2
     float scale_log2, decay;    // scale_log2 = sm_scale * log2(e) * k_scale
+};
+
+// The 128-key tiles of the prefill requests.
+struct WeightTiles {
+    const WeightRun* runs;
+    const int32_t* starts;      // the runs' first tiles
+    const uint32_t* hints;      // the run of every 32nd tile
+    int32_t n_runs, tile0;      // tile0: the first tile of this launch
 };
 
 // ------------------------------------------------------------ decode requests
@@ -262,7 +270,7 @@ key_weights_step_kernel(const KeyWeightArgs a) {
 // ----------------------------------------------------------- prefill requests
 
 constexpr int kTileKeys = kWeightTileKeys;   // 128 keys per CTA: the MMA's M, a TMEM lane each
-constexpr int kTileRows = 128;   // columns per step: the MMA's N
+constexpr int kTileRows = kWeightTileRows;   // 128 columns per step: the MMA's N
 
 // A wait with the same result in every lane of the warp.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
@@ -271,12 +279,7 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
 
 // Two forms.  The long one has an SM for itself and hides a step's latencies by
 // steps in flight; a CTA of few steps is mostly start and end, which the short
-// one hides by more CTAs per SM.  By the mean steps of a tile (causality not
-// counted): 76 requests of 40 rows on 15K-20K tokens, two KV heads with 8 query
-// heads each (3 steps) 838 us long and 357 short; 512 rows (32 steps) 460 and 390;
-// 1024 rows (64) 784 and 751; the prompts above (some 230) 193 and 300.
-constexpr int kShortSteps = 64;
-
+// one hides by its several CTAs per SM, where there are that many.
 template <int D, bool kShort>
 struct PromptWeightCfg {
     static constexpr int kAtom = 128 * 128;                 // 128 rows x 64 dims, 128-byte swizzle
@@ -286,7 +289,7 @@ struct PromptWeightCfg {
     static constexpr int kStages = kShort ? 2 : D == 64 ? 10 : 5;
     static constexpr int kBufs = kShort ? 1 : 4;            // S accumulators: 128 of the 512 TMEM columns each
     static constexpr int kWgs = kShort ? 1 : 3;             // epilogue warpgroups
-    static constexpr int kCtas = kShort ? (D == 64 ? 4 : 2) : 1;   // per SM
+    static constexpr int kCtas = kShort ? weight_short_ctas(D) : 1;   // per SM
     static constexpr int kEpilogueWarps = 4 * kWgs;
     static constexpr int kThreads = (kEpilogueWarps + 3) * 32;   // + MMA issuer, + Q producer, + lse
     static constexpr int kGroup = kShort ? 4 : 8;           // steps whose lse is staged at a time
@@ -308,7 +311,7 @@ struct PromptWeightCfg {
 template <int D, bool kFour, bool kShort, bool kRagged>
 __global__ void __launch_bounds__(PromptWeightCfg<D, kShort>::kThreads, PromptWeightCfg<D, kShort>::kCtas)
 key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
-                          const KeyWeightArgs a) {
+                          const KeyWeightArgs a, const WeightTiles w) {
     using C = PromptWeightCfg<D, kShort>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-ptx::smem_u32(smem_raw) & 1023u);
@@ -323,11 +326,15 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
     float* sum_s = reinterpret_cast<float*>(smem + C::kOffSum);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // The tile's run: the last that begins at or before it, of the 32 from the hint on.
-    const int tile = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv;
-    const int hint = a.hints[tile / kWeightHintTiles];
-    const bool begun = hint + lane < a.n_runs && a.runs[min(hint + lane, a.n_runs - 1)].tile0 <= tile;
-    const WeightRun run = a.runs[hint + __popc(__ballot_sync(0xffffffffu, begun)) - 1];
+    // The tile's run: the hint's, or the last of the 32 from there on that begins at or before it.
+    const int tile = w.tile0 + blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv;
+    const uint32_t hint = w.hints[tile / kWeightHintTiles];
+    int at_run = (int)(hint & ~kWeightHintAll);
+    if (!(hint & kWeightHintAll)) {
+        const bool begun = at_run + lane < w.n_runs && w.starts[min(at_run + lane, w.n_runs - 1)] <= tile;
+        at_run += __popc(__ballot_sync(0xffffffffu, begun)) - 1;
+    }
+    const WeightRun run = w.runs[at_run];
     const int t0 = run.key0 + (tile - run.tile0) * kTileKeys;
     const RequestInfo r = run.request;
     const int G = a.Hq / a.Hkv, P = a.P, prefix = r.kv_len - r.qo_len;
@@ -441,7 +448,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
         fetch(v);
         for (int grp = 0; grp < n_groups; ++grp) {
             float* dst = nl_s + (grp & 1) * C::kGroup * kTileRows + lane;
-            fetch(next);
+            if (grp + 1 < n_groups) fetch(next);
             if (grp >= 2 && !wait_all(l_free + 8 * (grp & 1), ((grp >> 1) - 1) & 1)) {
                 if (lane == 0) atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
                 break;
@@ -624,11 +631,11 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
             const int page = a.page_table[r.page_base + t / P];
             if (page >= 0 && page < a.num_pages) {
                 const int64_t at = ((int64_t)page * a.Hkv + g) * P + t % P;
-                float w = 0.f;
+                float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < C::kWgs; ++i) w += sum_s[i * kTileKeys + key];
-                if (a.decay != 0.f && t < prefix) w = fmaf(a.decay, a.prev[at], w);
-                a.weights[at] = w;
+                for (int i = 0; i < C::kWgs; ++i) sum += sum_s[i * kTileKeys + key];
+                if (a.decay != 0.f && t < prefix) sum = fmaf(a.decay, a.prev[at], sum);
+                a.weights[at] = sum;
             }
         }
     }
@@ -656,8 +663,8 @@ cudaError_t launch_step(const KeyWeightArgs& a, int grid, cudaStream_t stream) {
 }
 
 template <int D, bool kFour, bool kShort, bool kRagged>
-cudaError_t launch_prompt(const CUtensorMap& q_map, const CUtensorMap& kv_map, const KeyWeightArgs& a, int grid,
-                          cudaStream_t stream) {
+cudaError_t launch_prompt(const CUtensorMap& q_map, const CUtensorMap& kv_map, const KeyWeightArgs& a,
+                          const WeightTiles& w, int grid, cudaStream_t stream) {
     using C = PromptWeightCfg<D, kShort>;
     auto kernel = key_weights_prompt_kernel<D, kFour, kShort, kRagged>;
     static std::atomic<bool> configured[kMaxDevices];
@@ -665,9 +672,32 @@ cudaError_t launch_prompt(const CUtensorMap& q_map, const CUtensorMap& kv_map, c
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (e != cudaSuccess) return e;
-    return launch_dependent(kernel, dim3(grid), C::kThreads, C::kSmem, stream, q_map, kv_map, a);
+    return launch_dependent(kernel, dim3(grid), C::kThreads, C::kSmem, stream, q_map, kv_map, a, w);
 }
 
+// Which form (WeightLoad::takes_short_form).  Short / long time of some last rows
+// on one context, 8 KV heads with 8 query heads each, bf16, by CTAs (down) and
+// steps per tile:
+//             D = 64:   4     16    32    64      D = 128:  4     16    32    64
+//     64              1.24  1.78  1.81  1.84              1.22  1.80  1.71  1.64
+//    152              1.26  1.72  1.78  1.81              1.25  1.58  1.54  1.55
+//    304              0.84  1.10  1.18  1.25              0.84  1.05  1.08  1.09
+//    456              0.75  1.05  1.23  1.38              0.94  1.18  1.20  1.20
+//    608              0.61  0.84  0.95  1.05              0.79  0.96  1.01  1.05
+//   1216              0.53  0.78  0.90  1.00              0.72  0.90  0.98  1.02
+//   3000              0.47  0.70  0.83  0.94              0.65  0.84  0.91  0.98
+// With no more CTAs than SMs the long form is ahead (its three warpgroups against
+// one); with more the short one, for the more steps the more of its CTAs share an
+// SM; beyond 64 steps it is behind in any number (128 steps, 1000 CTAs: 1.05 and
+// 1.03).  With 4 bits the ratios are up to 0.15 higher.
+//
+// A batch goes by its mean, in one launch, but where the few tiles of a prompt
+// would outlast all the others of the short form (WeightLoad::even; a lone short
+// CTA takes 0.72 us a step, an SM full of them 0.46): there each kind is a launch.
+// Microseconds in short form, long form, and apart, 2 KV heads with 8 query heads
+// of 64 dims: a prompt of 8K beside 40 rows on 17K in 76 requests 445, 807, 479;
+// in 30 requests 403, 370, 311; in 10, 395, 191, 235; in 2 (94 steps by the mean),
+// 366, 192, 205; a prompt of 2K beside the 76 291, 731, 337.
 template <int D, bool kFour>
 attn_status launch_all(const attn_plan_s* plan, const CUtensorMap& q_map, const CUtensorMap& kv_map,
                        const KeyWeightArgs& a, cudaStream_t stream) {
@@ -678,18 +708,26 @@ attn_status launch_all(const attn_plan_s* plan, const CUtensorMap& q_map, const 
             : G <= 16 ? launch_step<D, kFour, 2>(a, units, stream)
                       : launch_step<D, kFour, 0>(a, units, stream);
     if (e == cudaSuccess && plan->weight_tiles > 0) {
-        const int heads = std::min(G, kTileRows), rows = kTileRows / heads, slices = (G + heads - 1) / heads;
-        int64_t steps = 0;
+        const int all = plan->weight_tiles, split = plan->weight_long_tiles;
+        WeightLoad load[2];   // the tiles before `split`, and from there on
         for (const RequestInfo& r : plan->requests)
-            if (r.qo_len > 1) {
-                const int n = a.window > 0 ? std::min(a.window, r.qo_len) : r.qo_len;
-                steps += ((int64_t)r.kv_len + kTileKeys - 1) / kTileKeys * ((n + rows - 1) / rows) * slices;
-            }
-        const int grid = plan->weight_tiles * plan->Hkv;
-        const bool ragged = rows * heads < kTileRows;
-        e = steps <= kShortSteps * (int64_t)plan->weight_tiles ? launch_prompt<D, kFour, true, false>(q_map, kv_map, a, grid, stream)
-            : ragged ? launch_prompt<D, kFour, false, true>(q_map, kv_map, a, grid, stream)
-                     : launch_prompt<D, kFour, false, false>(q_map, kv_map, a, grid, stream);
+            if (r.qo_len > 1) load[split == 0 || weight_steps(r.qo_len, G) <= kWeightShortSteps].add(r, G, a.window);
+        bool is_short[2];
+        for (int i = 0; i < 2; ++i) is_short[i] = load[i].takes_short_form(plan->Hkv, plan->num_sms, D);
+        if (split == 0) is_short[0] = is_short[1];
+        const bool ragged = kTileRows % std::min(G, kTileRows) != 0;
+        WeightTiles w;
+        w.runs = reinterpret_cast<const WeightRun*>(plan->lists + plan->lists_layout.weight_runs);
+        w.starts = reinterpret_cast<const int32_t*>(plan->lists + plan->lists_layout.weight_starts);
+        w.hints = reinterpret_cast<const uint32_t*>(plan->lists + plan->lists_layout.weight_hints);
+        w.n_runs = (int32_t)plan->weight_runs.size();
+        w.tile0 = 0;
+        for (int end = is_short[0] == is_short[1] ? all : split; e == cudaSuccess && w.tile0 < all; w.tile0 = end, end = all) {
+            const int grid = (end - w.tile0) * plan->Hkv;
+            e = is_short[w.tile0 >= split] ? launch_prompt<D, kFour, true, false>(q_map, kv_map, a, w, grid, stream)
+                : ragged                   ? launch_prompt<D, kFour, false, true>(q_map, kv_map, a, w, grid, stream)
+                                           : launch_prompt<D, kFour, false, false>(q_map, kv_map, a, w, grid, stream);
+        }
     }
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
@@ -701,9 +739,6 @@ attn_status launch_key_weights(attn_plan_s* plan, bool four, const void* q, cons
                                float decay, int32_t window, float* weights, cudaStream_t stream) {
     KeyWeightArgs a;
     a.units = reinterpret_cast<const DecodeUnit*>(plan->ws + plan->layout.units);
-    a.runs = reinterpret_cast<const WeightRun*>(plan->lists + plan->lists_layout.weight_runs);
-    a.hints = reinterpret_cast<const int32_t*>(plan->lists + plan->lists_layout.weight_hints);
-    a.n_runs = (int32_t)plan->weight_runs.size();
     a.page_table = plan->page_table;
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.lse = lse;

@@ -267,34 +267,52 @@ attn_status make_plan(bool ragged, const int32_t* qo_indptr, const int32_t* kv_i
         plan->requests[b] = {qo_indptr[b], (int32_t)qo_len[b], kv_indptr[b], (int32_t)kv_len[b]};
     // Key weights of prefill requests: runs of 128-key tiles, the ones that most
     // query rows see first (the CTAs are dispatched in this order).
+    WeightLoad load[2], all;   // requests of few steps and of many
     for (int32_t b = 0; b < batch && !ragged; ++b) {
         if (qo_len[b] <= 1) continue;
+        const RequestInfo& r = plan->requests[b];
+        load[weight_steps(r.qo_len, G) > kWeightShortSteps].add(r, G, 0);
+        all.add(r, G, 0);
         const int64_t prefix = kv_len[b] - qo_len[b];
-        plan->weight_runs.push_back({0, 0, plan->requests[b], {0, 0}});
+        plan->weight_runs.push_back({0, 0, r, {0, 0}});
         if (causal)
             for (int64_t t0 = (prefix / kWeightTileKeys + 1) * kWeightTileKeys; t0 < kv_len[b]; t0 += kWeightTileKeys)
-                plan->weight_runs.push_back({0, (int32_t)t0, plan->requests[b], {0, 0}});
+                plan->weight_runs.push_back({0, (int32_t)t0, r, {0, 0}});
     }
+    // Requests of many steps among tiles that the short form would take, too few to
+    // hide theirs: they come first, so that each kind can be a launch of its own.
+    const bool apart = load[0].tiles > 0 && load[1].tiles > 0 &&
+                       all.takes_short_form(num_kv_heads, num_sms, head_dim) && !all.even(num_kv_heads, num_sms);
+    auto first = [&](const WeightRun& w) { return apart && weight_steps(w.request.qo_len, G) > kWeightShortSteps; };
     auto rows_seeing = [&](const WeightRun& w) {
         const int32_t n = w.request.qo_len;
         return causal ? n - std::max(0, w.key0 - (w.request.kv_len - n)) : n;
     };
-    std::stable_sort(plan->weight_runs.begin(), plan->weight_runs.end(),
-                     [&](const WeightRun& x, const WeightRun& y) { return rows_seeing(x) > rows_seeing(y); });
+    std::stable_sort(plan->weight_runs.begin(), plan->weight_runs.end(), [&](const WeightRun& x, const WeightRun& y) {
+        return first(x) != first(y) ? first(x) : rows_seeing(x) > rows_seeing(y);
+    });
     for (size_t i = 0; i < plan->weight_runs.size(); ++i) {
         WeightRun& w = plan->weight_runs[i];
         const int32_t n = w.request.qo_len, prefix = w.request.kv_len - n;
         const int32_t last = w.key0 > 0 ? w.key0 : causal ? prefix : w.request.kv_len - 1;   // in the run's last tile
         w.tile0 = plan->weight_tiles;
+        plan->weight_starts.push_back(w.tile0);
         plan->weight_tiles += (last - w.key0) / kWeightTileKeys + 1;
-        plan->weight_hints.resize(((size_t)plan->weight_tiles + kWeightHintTiles - 1) / kWeightHintTiles, (int32_t)i);
+        if (first(w)) plan->weight_long_tiles = plan->weight_tiles;
+        plan->weight_hints.resize(((size_t)plan->weight_tiles + kWeightHintTiles - 1) / kWeightHintTiles, (uint32_t)i);
+    }
+    for (size_t i = 0; i < plan->weight_hints.size(); ++i) {
+        const size_t run = plan->weight_hints[i], next = run + 1;
+        if (next == plan->weight_starts.size() || plan->weight_starts[next] >= (int64_t)(i + 1) * kWeightHintTiles)
+            plan->weight_hints[i] |= kWeightHintAll;
     }
 
     // ---- workspace layout (every region 256-byte aligned).
     ListLayout& A = plan->lists_layout;
     A.weight_runs = align_up(plan->requests.size() * sizeof(RequestInfo), 256);
-    A.weight_hints = align_up(A.weight_runs + plan->weight_runs.size() * sizeof(WeightRun), 256);
-    A.total = align_up(A.weight_hints + plan->weight_hints.size() * sizeof(int32_t), 256);
+    A.weight_starts = align_up(A.weight_runs + plan->weight_runs.size() * sizeof(WeightRun), 256);
+    A.weight_hints = align_up(A.weight_starts + plan->weight_starts.size() * sizeof(int32_t), 256);
+    A.total = align_up(A.weight_hints + plan->weight_hints.size() * sizeof(uint32_t), 256);
     WorkspaceLayout& L = plan->layout;
     size_t off = 0;
     L.units = off;    off = align_up(off + plan->units.size() * sizeof(DecodeUnit), 256);
