@@ -18,8 +18,8 @@
 //
 // What has to be moved is 4 bytes per token and head, and the kept rows twice;
 // but the selection's passes are a chain of barriers and shared-memory work that
-// a row's CTA cannot shorten, while the memory idles.  With more rows than SMs
-// one kernel does both, so that some CTAs copy while others select: 512 rows of
+// a row's CTA cannot shorten, while the memory idles.  With many rows one kernel
+// does both, so that some CTAs copy while others select: 512 rows of
 // 1K-8K tokens, 64 dims in bf16, down to 1024 each (283 MB) take 63 us (4.5 TB/s)
 // where two kernels took 76.  With fewer rows the copies need all SMs and stay a
 // kernel of their own: 128 rows of 2K-32K tokens, 128 dims in 4 bits, down to
@@ -48,6 +48,7 @@ namespace {
 
 constexpr int kMoveThreads = 256, kBothThreads = 512;
 constexpr int kBothChunk = 11 * 1024;   // weights of a row at a time: three CTAs per SM
+constexpr int kWholeChunk = 48 * 1024;  // a CTA that has an SM for itself
 constexpr int kDigitBits = 11, kDigits = 1 << kDigitBits;   // radix passes over 11, 11 and 10 bits
 
 struct EvictArgs {
@@ -477,18 +478,27 @@ attn_status launch_evict(attn_plan_s* plan, bool four, const float* weights, con
     a.chunk = 0;
     int32_t longest = 0;
     for (const RequestInfo& r : plan->requests) longest = std::max(longest, r.kv_len);
-    // With at most a CTA per SM, each takes all of an SM's threads and shared
-    // memory; with more, a part of it.
+    // A CTA takes all of an SM's threads and shared memory where there are few rows,
+    // else a part of it.  Up to two rows per SM are few if that is what holds the
+    // longest at once: in part of an SM it would be read four times.  Rows of
+    // 64 dims in bf16 down to an eighth, part of an SM / all of it, us, out of place
+    // and in place: 152 rows of 8K 28 / 21 and 21 / 25, of 32K 136 / 83 and 117 / 97;
+    // 160 rows of 8K 30 / 31 and 30 / 30, of 12K 59 / 46 and 52 / 41, of 32K 145 / 112 and
+    // 146 / 119, one of 32K among 8K 130 / 95 and 129 / 103, all of 64K 286 / 261 and
+    // 291 / 326; 304 rows of 32K 197 / 162 and 192 / 176, of 2K-16K 77 / 83 and 91 / 84;
+    // 456 of 32K 240 / 242 and 282 / 261, of 1K-32K 196 / 222 and 263 / 245.  (152 rows
+    // of 2K: 14 / 16 and 10 / 11.)
     int32_t sms = 0;
     if (!current_sm_count(&sms)) return ATTN_ERR_CUDA;
-    const bool few = (int64_t)plan->batch * plan->Hkv <= sms;
+    const int64_t all_rows = (int64_t)plan->batch * plan->Hkv;
+    const bool few = all_rows <= sms || (all_rows <= 2 * sms && longest > kBothChunk && longest <= kWholeChunk);
     const bool in_place = !page_table_out;
     if (!few && !in_place) {
         if (plan->D == 64) return four ? launch_both<64, true>(a, longest, stream) : launch_both<64, false>(a, longest, stream);
         return four ? launch_both<128, true>(a, longest, stream) : launch_both<128, false>(a, longest, stream);
     }
-    const attn_status st = few ? launch_select<1024>(a, longest, 48 * 1024, stream)
-                               : launch_select<512>(a, longest, 11 * 1024, stream);
+    const attn_status st = few ? launch_select<1024>(a, longest, kWholeChunk, stream)
+                               : launch_select<512>(a, longest, kBothChunk, stream);
     if (st != ATTN_OK) return st;
     // Out of place, enough CTAs for some eight per SM.
     const int64_t rows = std::min<int64_t>(longest, budget), most = (rows + kMoveThreads - 1) / kMoveThreads;
