@@ -484,7 +484,8 @@ class RaggedPlan(Plan):
     def append_kv(self, *args, **kwargs):
         raise TypeError("a ragged plan has no KV cache")
 
-    append_kv4 = decode_kv4 = key_weights = key_weights_kv4 = evict_kv = evict_kv4 = append_kv
+    append_kv4 = decode_kv4 = key_weights = key_weights_kv4 = evict_kv = evict_kv4 = kv4_shape = append_kv
+    kv_lens = property(append_kv)
 
 
 class GraphPlan(Plan):
@@ -542,6 +543,7 @@ class GraphPlan(Plan):
         raise TypeError("a graph plan only decodes")
 
     append_kv4 = decode_kv4 = key_weights = key_weights_kv4 = evict_kv = evict_kv4 = append_kv
+    kv_lens = property(append_kv)   # (they are on the device, and change between replays)
 
 
 def attn_plan(qo_indptr, kv_indptr, page_table, last_page_len, num_qo_heads, num_kv_heads,
