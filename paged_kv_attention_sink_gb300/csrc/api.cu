@@ -7,7 +7,9 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <exception>
 #include <mutex>
+#include <vector>
 
 #include "attn_internal.h"
 #include "kernels.h"
@@ -103,7 +105,12 @@ extern "C" attn_status attn_plan_bind_workspace(attn_plan_t plan, void* workspac
     // The lists and, after them, the work lists in [0, L.counters): one host
     // image, one copy (graph plans have none: their list is built on the device).
     if (!plan->units.empty() || !plan->items.empty() || !plan->requests.empty()) {
-        std::vector<unsigned char> img(A.total + L.counters, 0);
+        std::vector<unsigned char> img;
+        try {
+            img.assign(A.total + L.counters, 0);
+        } catch (const std::exception&) {
+            return ATTN_ERR_INVALID_ARG;   // no host memory for it
+        }
         auto put = [&](size_t off, const void* src, size_t bytes) {
             if (bytes) std::memcpy(img.data() + off, src, bytes);
         };

@@ -10,6 +10,8 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <exception>
+#include <memory>
 #include <new>
 
 #include <cuda_runtime.h>
@@ -56,12 +58,12 @@ namespace {
 // comes from the page count and last_page_len.  Ragged: kv_indptr is the token
 // CSR into contiguous K / V arrays, every request becomes prefill work items
 // (there is no cache to split decode over), and page_table / last_page_len /
-// num_pages_in_pool are unused.
-attn_status make_plan(bool ragged, const int32_t* qo_indptr, const int32_t* kv_indptr,
-                      const int32_t* page_table, const int32_t* last_page_len, int32_t batch,
-                      int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
-                      int32_t causal, float sm_scale, int32_t num_pages_in_pool, int32_t num_sms,
-                      attn_plan_t* plan_out, size_t* workspace_bytes_out) {
+// num_pages_in_pool are unused.  Its vectors throw where host memory runs out.
+attn_status build_plan(bool ragged, const int32_t* qo_indptr, const int32_t* kv_indptr,
+                       const int32_t* page_table, const int32_t* last_page_len, int32_t batch,
+                       int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                       int32_t causal, float sm_scale, int32_t num_pages_in_pool, int32_t num_sms,
+                       attn_plan_t* plan_out, size_t* workspace_bytes_out) {
     using namespace attn;
     if (!plan_out || !workspace_bytes_out || batch < 0) return ATTN_ERR_INVALID_ARG;
     if (batch > 0 && (!qo_indptr || !kv_indptr || (!ragged && !last_page_len))) return ATTN_ERR_INVALID_ARG;
@@ -100,7 +102,7 @@ attn_status make_plan(bool ragged, const int32_t* qo_indptr, const int32_t* kv_i
 
     if (num_sms == 0 && !current_sm_count(&num_sms)) return ATTN_ERR_CUDA;
 
-    attn_plan_s* plan = new (std::nothrow) attn_plan_s();
+    std::unique_ptr<attn_plan_s> plan(new (std::nothrow) attn_plan_s());
     if (!plan) return ATTN_ERR_INVALID_ARG;
     plan->batch = batch;
     plan->Hq = num_qo_heads;
@@ -341,9 +343,19 @@ attn_status make_plan(bool ragged, const int32_t* qo_indptr, const int32_t* kv_i
     I.prefill_pairs = prefill_pairs;
     I.workspace_bytes = A.total + L.total;
 
-    *plan_out = plan;
     *workspace_bytes_out = I.workspace_bytes;
+    *plan_out = plan.release();
     return ATTN_OK;
+}
+
+// No exception leaves a C entry point.
+template <class... Args>
+attn_status make_plan(Args... args) {
+    try {
+        return build_plan(args...);
+    } catch (const std::exception&) {
+        return ATTN_ERR_INVALID_ARG;   // as where the plan itself finds no memory
+    }
 }
 
 }  // namespace
