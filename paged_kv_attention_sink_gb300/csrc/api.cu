@@ -384,7 +384,8 @@ extern "C" attn_status attn_expand_kv4(const void* kv4_cache, int64_t num_pages,
     // The kernel's index into a page's K or V half, and its sum with a step, are int32.
     if ((int64_t)num_kv_heads * page_size >= (int64_t{1} << 33) / head_dim) return ATTN_ERR_UNSUPPORTED;
     if (n_pages == 0) return ATTN_OK;
-    if (!kv4_cache || !buf || !page_ids || !aligned16(kv4_cache) || !aligned16(buf) || !aligned4(page_ids))
+    if (!kv4_cache || !buf || !page_ids || !aligned16(kv4_cache) || !aligned16(buf) || !aligned4(page_ids) ||
+        !aligned4(device_error))
         return ATTN_ERR_INVALID_ARG;
     return attn::launch_expand_kv4(kv4_cache, buf, page_ids, n_pages, num_pages, num_kv_heads, page_size, head_dim,
                                    k_scale, v_scale, device_error, static_cast<cudaStream_t>(stream));
@@ -396,6 +397,7 @@ extern "C" attn_status attn_decode_kv4(attn_plan_t plan, const void* q, const vo
         return ATTN_ERR_INVALID_ARG;
     if (plan->bound && plan->units.empty()) return ATTN_OK;
     if (attn_status st = check_launch(plan, q, kv4_cache, out); st != ATTN_OK) return st;
+    if (!aligned4(sinks) || !aligned4(lse)) return ATTN_ERR_INVALID_ARG;
     return attn::launch_decode_kv4(plan, q, kv4_cache, k_scale, v_scale, sinks, out, lse,
                                    static_cast<cudaStream_t>(stream));
 }

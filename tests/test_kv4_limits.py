@@ -5,7 +5,7 @@ import ctypes
 
 import pytest
 
-from test_abi import OK, UNSUPPORTED, lib   # noqa: F401  (lib: the built library's fixture)
+from test_abi import INVALID, OK, UNSUPPORTED, lib   # noqa: F401  (lib: the built library's fixture)
 
 P = ctypes.c_void_p(0x10000)
 
@@ -19,3 +19,10 @@ def test_expand_refuses_pages_beyond_32_bit_indices(lib, Hkv, page, D, want):   
     index below it: under 2^30 both fit."""
     assert (Hkv * page * D // 8 >= 1 << 30) == (want == UNSUPPORTED)
     assert lib.attn_expand_kv4(P, 4, Hkv, page, D, P, 0, 1.0, 1.0, P, None, None) == want
+
+
+ODD2 = ctypes.c_void_p(0x10002)
+
+
+def test_expand_refuses_a_misaligned_error_word(lib):   # noqa: F811
+    assert lib.attn_expand_kv4(P, 4, 2, 16, 64, P, 1, 1.0, 1.0, P, ODD2, None) == INVALID

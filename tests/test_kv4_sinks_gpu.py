@@ -83,3 +83,20 @@ def test_scores_of_minus_infinity():
     _, want, want_lse = run(batch, pool, batch.sinks)
     for h in (0, 2, 3):
         assert torch.equal(out[:, h], want[:, h]) and torch.equal(lse[:, h], want_lse[:, h])
+
+
+def test_misaligned_sinks_and_lse_are_refused():
+    import ctypes
+    batch = batch_of([1, 1], [40, 20], 4, 1, 64, 16, seed=7)
+    pool = dev(ref.random_pool(np.random.default_rng(1), batch.num_pages, 1, 16, 64))
+    plan, q = make_plan(batch, dev(batch.page_table)), dev_bf16(batch.q)
+    out, f = torch.full_like(q, 3.0), torch.zeros(16, device="cuda")
+    at = lambda t, off=0: ctypes.c_void_p(t.data_ptr() + off)
+    call = binding().load_library().attn_decode_kv4
+    stream = torch.cuda.current_stream().cuda_stream
+    for sinks, lse in ((at(f, 2), None), (None, at(f, 1)), (at(f, 3), at(f, 2))):
+        assert call(plan.handle, at(q), at(pool), 1.0, 1.0, sinks, at(out), lse, stream) == 1
+    torch.cuda.synchronize()
+    assert torch.all(out == 3.0)
+    assert call(plan.handle, at(q), at(pool), 1.0, 1.0, at(f, 4), at(out), at(f, 32), stream) == 0
+    assert plan.device_error() == 0 and not torch.any(out == 3.0)
