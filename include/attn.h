@@ -429,11 +429,14 @@ ATTN_API attn_status attn_decode_kv4(attn_plan_t plan, const void* q, const void
  *                  slots of the plan's tokens are written; requests without
  *                  query rows are left out.  A weight belongs to a page's slot:
  *                  on a page that two requests of the plan share, which of
- *                  the two requests' weights a slot holds is not defined.
+ *                  the two requests' weights a slot holds is not defined, and
+ *                  with prev = weights one may have been added to the other's.
+ *                  Requests that share pages need buffers (and plans) of their
+ *                  own for weights that can be told apart.
  *   lse            fp32 [total_qo_rows][Hq];   decay finite, >= 0
  *   kv_cache       as in attn_decode;  kv4_cache, k_scale as in attn_decode_kv4
  * Decode and prefill rows alike.  The sum's order is fixed: equal calls give
- * equal bits.  Pages out of range set ATTN_DEVICE_ERR_PAGE_ID and their tokens
+ * equal bits (but in shared slots, see above).  Pages out of range set ATTN_DEVICE_ERR_PAGE_ID and their tokens
  * are skipped.  Host-planned paged plans only.  Async on `stream`.
  */
 ATTN_API attn_status attn_key_weights(attn_plan_t plan, const void* q, const void* kv_cache, const float* lse,

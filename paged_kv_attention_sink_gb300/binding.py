@@ -378,7 +378,8 @@ class Plan:
         appends) plus the attention weight the last `window` query rows (0: all)
         give it, summed over g's query heads.  lse is the rows' log-sum-exp as
         decode / prefill returned it.  weights, prev: fp32 [num_pages, Hkv,
-        page_size].  See attn_key_weights."""
+        page_size]; not defined on pages that two requests of the plan share.
+        See attn_key_weights."""
         return self._key_weights(False, q, kv_cache, lse, weights, prev, decay, window, 1.0, stream)
 
     def key_weights_kv4(self, q, kv4_cache, lse, weights, prev=None, decay: float = 1.0, window: int = 0,

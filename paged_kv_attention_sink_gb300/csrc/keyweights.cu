@@ -30,11 +30,15 @@
 //    the MUFU's 512: the barriers and TMEM loads alone measure 600, and overlap
 //    with the exponentials in part.  Steps of 128 rows of one head measured 200
 //    us where this form then took 193, but lost less with head counts that leave
-//    columns of these steps empty (two prompts, 12 heads per KV head 302 us
-//    instead of 313, 5 heads 135 instead of 138); so built, two warpgroups 223 and four 252 (fewer registers each), steps
-//    of two heads (N = 256) with four warpgroups on 64 columns each 228, the next
-//    step's first columns loaded ahead 209, and a query row per thread with a sum
-//    of 128 keys in registers 297.
+//    columns of these steps empty (prompts with 12 heads per KV head 302 us
+//    instead of 313, with 5 heads 135 instead of 138); so built, two warpgroups
+//    223 and four 252 (fewer registers each), steps of two heads (N = 256) with
+//    four warpgroups on 64 columns each 228, the next step's first columns loaded
+//    ahead 209, and a query row per thread with a sum of 128 keys in registers 297.
+//
+// More than 16 query heads per KV head on decode rows take Q from memory again
+// for every 16 tokens: 64 requests of 4096 tokens, 2 KV heads with 32 query heads
+// of 64 dims, 56 us in bf16 (67 MB) and 70 in 4 bits, bound by that, not by K.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
