@@ -436,8 +436,10 @@ ATTN_API attn_status attn_decode_kv4(attn_plan_t plan, const void* q, const void
  *   lse            fp32 [total_qo_rows][Hq];   decay finite, >= 0
  *   kv_cache       as in attn_decode;  kv4_cache, k_scale as in attn_decode_kv4
  * Decode and prefill rows alike.  The sum's order is fixed: equal calls give
- * equal bits (but in shared slots, see above).  Pages out of range set ATTN_DEVICE_ERR_PAGE_ID and their tokens
- * are skipped.  Host-planned paged plans only.  Async on `stream`.
+ * equal bits (but in shared slots, see above).  Pages out of range set
+ * ATTN_DEVICE_ERR_PAGE_ID and their tokens are skipped.  Host-planned paged
+ * plans only; ATTN_ERR_UNSUPPORTED where the prefill requests have more than
+ * 2^31 - 1 tiles of 128 keys times Hkv.  Async on `stream`.
  */
 ATTN_API attn_status attn_key_weights(attn_plan_t plan, const void* q, const void* kv_cache, const float* lse,
                                       const float* prev, float decay, int32_t window, float* weights, void* stream);
@@ -468,7 +470,7 @@ ATTN_API attn_status attn_key_weights_kv4(attn_plan_t plan, const void* q, const
  *                   NULL: in place, in each request's own first pages; kv_out,
  *                   weights_out and num_pages_out are then the inputs' own, and
  *                   no page may belong to two requests.
- *   1 <= budget, 0 <= recent <= budget
+ *   1 <= budget, 0 <= recent <= budget;  batch * Hkv < 2^30 (else ATTN_ERR_UNSUPPORTED)
  * Slots of the receiving pages past the kept tokens are left as they were.
  * Page ids out of range set ATTN_DEVICE_ERR_PAGE_ID: such a source page's
  * tokens count as NaN weights, and what would be read from or written to such a

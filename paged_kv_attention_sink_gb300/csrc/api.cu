@@ -330,6 +330,7 @@ attn_status key_weights(attn_plan_t plan, bool four, const void* q, const void* 
     if (!q || !pool || !lse || !weights || (decay != 0.f && !prev)) return ATTN_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(pool) || !aligned4(lse) || !aligned4(prev) || !aligned4(weights))
         return ATTN_ERR_INVALID_ARG;
+    if ((int64_t)plan->weight_tiles * plan->Hkv > INT32_MAX) return ATTN_ERR_UNSUPPORTED;   // the grid's CTAs
     if (plan->weight_tiles > 0) {
         if (!four && plan->kv_map_prefill_ptr != pool) {
             if (!make_kv_map(plan->kv_map_prefill, pool, plan, plan->P)) return ATTN_ERR_CUDA;
@@ -358,6 +359,7 @@ attn_status evict(attn_plan_t plan, bool four, const float* weights, const void*
     if (!page_table_out && (pool_out != pool || weights_out != weights || num_pages_out != plan->num_pages))
         return ATTN_ERR_INVALID_ARG;
     if (page_table_out && (num_pages_out <= 0 || !aligned4(page_table_out))) return ATTN_ERR_INVALID_ARG;
+    if ((int64_t)plan->batch * plan->Hkv * 2 > INT32_MAX) return ATTN_ERR_UNSUPPORTED;   // the grid's CTAs
     return attn::launch_evict(plan, four, weights, pool, budget, recent, kept, page_table_out, num_pages_out, pool_out,
                               weights_out, static_cast<cudaStream_t>(stream));
 }
