@@ -75,7 +75,11 @@ typedef enum {
 #define ATTN_DEVICE_ERR_PAGE_ID 1      /* page id outside [0, num_pages_in_pool) */
 #define ATTN_DEVICE_ERR_TIMEOUT 2      /* a bounded wait inside a kernel ran out */
 #define ATTN_DEVICE_ERR_PLAN 4         /* attn_decode_graph: malformed request metadata or
-                                          work beyond the graph plan's capacity */
+                                          work beyond the graph plan's capacity;
+                                          attn_pages_fork: malformed parents, or more
+                                          entries than fit */
+#define ATTN_DEVICE_ERR_PAGES 8        /* attn_pages_*: no free page was left, or a page was
+                                          given up that nothing held */
 
 /* Opaque plan; owned by the library, freed with attn_plan_destroy. */
 typedef struct attn_plan_s* attn_plan_t;
@@ -362,6 +366,153 @@ ATTN_API attn_status attn_unpack_kv_heads(const void* buf, int64_t num_pages, in
                                           int32_t page_size, int32_t head_dim, const int32_t* page_ids,
                                           int64_t n_pages, int32_t head_begin, int32_t n_heads, void* kv_cache,
                                           int32_t* device_error, void* stream);
+
+/*
+ * Rotary positions -- the turn by position that q and k take before attention,
+ * with one axis (text) or several (time, height and width of images and video).
+ * No source describes it: attn_rope and attn_append_kv_rope are interface
+ * additions.  Pair p of a row's first rot_dim dims turns by
+ *
+ *   theta = positions[axis[p]][row] * inv_freq[p]
+ *   (x, y) -> scale * (x cos theta - y sin theta,  x sin theta + y cos theta)
+ *
+ * and the other dims are copied.  The angle is exact to 2^-33 of a turn for every
+ * int32 position; the products are fp32, rounded to bf16 once.
+ *
+ *   rot_dim      a multiple of 16, 16 .. head_dim (else ATTN_ERR_UNSUPPORTED)
+ *   interleaved  0: pair p is dims (p, p + rot_dim / 2);  1: dims (2p, 2p + 1)
+ *   n_axes       1 .. 8
+ *   inv_freq     host fp32 [rot_dim / 2], finite, |inv_freq| < 2^20 (radians per
+ *                position)
+ *   axis         host int32 [rot_dim / 2] in [0, n_axes), or NULL (all 0)
+ *   scale        finite
+ */
+typedef struct {
+    int32_t rot_dim;
+    int32_t interleaved;
+    int32_t n_axes;
+    float scale;
+    const float* inv_freq;
+    const int32_t* axis;
+} attn_rope_spec;
+
+/*
+ * attn_rope -- turns the rows of q and of k (either may be absent: NULL with 0
+ * heads), for attention without a cache, before attn_append_kv4, or, with
+ * inverse = 1 (theta negated: the transposed turn), for their gradients.
+ *
+ *   positions   device int32 [n_axes][rows]
+ *   q, k        bf16 rows of heads, device: element (row, h, d) at
+ *               row * stride + h * head_dim + d; strides in elements, multiples of
+ *               8, at least heads * head_dim; 16-byte aligned.  So slices of a
+ *               fused projection are taken as they are.
+ *   q_out, k_out  likewise; may be the input itself with the input's stride (in
+ *               place), else must not overlap it
+ *   head_dim 64 or 128 (else ATTN_ERR_UNSUPPORTED)
+ * Async on `stream`.
+ *
+ * attn_append_kv_rope -- attn_rope of a step's q and k and attn_append_kv of the
+ * turned k and of v in one pass: q_out gets the turned q, and the plan's cache
+ * positions the turned k (bit-identical to attn_rope followed by attn_append_kv).
+ * Row i is the plan's query row i; its positions are the caller's, not the cache's.
+ *
+ *   q, k_new, v_new  as q and k above, with the plan's heads and head_dim
+ *   q_out            bf16 [total_qo_rows][Hq][head_dim]; may be q where that is
+ *                    contiguous
+ *   kv_cache         as in attn_append_kv, as are bad page ids and plans
+ */
+ATTN_API attn_status attn_rope(const attn_rope_spec* rope, const int32_t* positions, int64_t rows, int32_t head_dim,
+                               const void* q, int64_t q_stride, int32_t num_q_heads, void* q_out,
+                               int64_t q_out_stride, const void* k, int64_t k_stride, int32_t num_k_heads,
+                               void* k_out, int64_t k_out_stride, int32_t inverse, void* stream);
+ATTN_API attn_status attn_append_kv_rope(attn_plan_t plan, const attn_rope_spec* rope, const int32_t* positions,
+                                         const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+                                         const void* v_new, int64_t v_stride, void* q_out, void* kv_cache,
+                                         void* stream);
+
+/*
+ * Page management -- the cache's pages handed about on the device, in stream
+ * order and without the host waiting (no source describes it: attn_pages_* are
+ * interface additions).  The state is one count per page:
+ *
+ *   refs   device int32 [num_pages], 16-byte aligned: how many page-table entries
+ *          hold page p; 0: free.  All zero at first.
+ *
+ * and the pools are whatever is stored by page (each layer's kv_cache or
+ * kv4_cache, weights):
+ *
+ *   pools       host array of n_pools device pointers, 16-byte aligned; page p of
+ *               pool k is the page_bytes[k] bytes (a multiple of 16) at
+ *               pools[k] + p * page_bytes[k]
+ *   device_error  device int32 or NULL (bits are OR-ed in; then dropped silently)
+ *
+ * Calls that change refs read what earlier ones left, so they are issued on one
+ * stream.  Equal calls give equal tables and counts.
+ *
+ * attn_pages_alloc -- the n lowest free pages, in order, into page_ids (int32 [n],
+ * device), held once.  Where fewer are free, the rest of page_ids is -1 and
+ * ATTN_DEVICE_ERR_PAGES is set.
+ *
+ * attn_pages_free -- every listed page is held once less (a page listed twice,
+ * twice).  Ids outside the pool (-1 among them) are skipped and set
+ * ATTN_DEVICE_ERR_PAGE_ID; a page that nothing held stays at 0 and sets
+ * ATTN_DEVICE_ERR_PAGES.
+ *
+ * attn_pages_copy -- page src[i] of every pool into page dst[i], bit for bit; the
+ * dst are distinct and no dst is a src.  Pairs with an id outside the pool are
+ * skipped and set ATTN_DEVICE_ERR_PAGE_ID.  refs are not looked at.
+ *
+ * attn_pages_fork -- children of requests: child c starts as the first kv_lens[p]
+ * tokens of request p = parents[c] (several children may have one parent, which
+ * goes on as it was).  Full pages are shared: the child's entry is the parent's,
+ * held once more.  A last page that is not full, and will be written into, is
+ * copied in every pool into a new page (the lowest free ones, in the children's
+ * order), held once.
+ *   page_table [table_len], kv_indptr [batch + 1], kv_lens [batch], parents [n]   device int32;
+ *                 request p's pages are page_table[kv_indptr[p] ..] as in attn_plan
+ *   page_table_out, indptr_out   device int32 [out_len], [n + 1], outputs: child c's
+ *                 ceil(kv_lens / page_size) entries from indptr_out[c] on; must
+ *                 not overlap the inputs.  Entries past the last are left as they were.
+ *   scratch       device int32 [attn_pages_scratch(n)], for this call alone
+ * A child whose parent is not in [0, batch), or whose kv_lens its entries (within
+ * table_len) do not hold, gets no pages (ATTN_DEVICE_ERR_PLAN).  Where no free page is left its entry
+ * is -1 (ATTN_DEVICE_ERR_PAGES); where the parent's entry is outside the pool it is
+ * -1, or for a last page that is not full a new page that nothing is copied into
+ * (ATTN_DEVICE_ERR_PAGE_ID).  Children of more than out_len entries in all are
+ * refused as a whole: indptr_out is zero, ATTN_DEVICE_ERR_PLAN, nothing else changes.
+ *
+ * attn_pages_compact -- with U pages held, moves those from U on into the free ones
+ * below U, the highest into the lowest, in every pool; refs move with them and
+ * then are positive exactly below U.
+ *   remap         device int32 [num_pages], output: the new id of every page, -1 for
+ *                 pages that were free
+ *   page_table    device int32 [n_entries], changed to the new ids (other tables: look
+ *                 ids up in remap).  Ids outside the pool stay and set
+ *                 ATTN_DEVICE_ERR_PAGE_ID; a free page's becomes -1 and sets
+ *                 ATTN_DEVICE_ERR_PAGES.
+ *   scratch       device int32 [attn_pages_scratch(num_pages / 2)], for this call alone
+ * Plans hold no copy of page ids, so a plan over that page_table stays valid.
+ *
+ * num_pages > 0; n, n_entries, table_len, out_len >= 0, below 2^31.  All are asynchronous on
+ * `stream` and capturable.
+ */
+ATTN_API int64_t attn_pages_scratch(int64_t n);
+ATTN_API attn_status attn_pages_alloc(int32_t* refs, int32_t num_pages, int32_t n, int32_t* page_ids,
+                                      int32_t* device_error, void* stream);
+ATTN_API attn_status attn_pages_free(int32_t* refs, int32_t num_pages, const int32_t* page_ids, int64_t n,
+                                     int32_t* device_error, void* stream);
+ATTN_API attn_status attn_pages_copy(void* const* pools, const int64_t* page_bytes, int32_t n_pools, int32_t num_pages,
+                                     const int32_t* src, const int32_t* dst, int64_t n, int32_t* device_error,
+                                     void* stream);
+ATTN_API attn_status attn_pages_fork(int32_t* refs, int32_t num_pages, const int32_t* page_table,
+                                     int64_t table_len, const int32_t* kv_indptr, const int32_t* kv_lens, int32_t batch,
+                                     int32_t page_size, const int32_t* parents, int32_t n, int32_t* page_table_out,
+                                     int32_t* indptr_out, int64_t out_len, void* const* pools,
+                                     const int64_t* page_bytes, int32_t n_pools, int32_t* scratch,
+                                     int32_t* device_error, void* stream);
+ATTN_API attn_status attn_pages_compact(int32_t* refs, int32_t num_pages, int32_t* page_table, int64_t n_entries,
+                                        int32_t* remap, void* const* pools, const int64_t* page_bytes,
+                                        int32_t n_pools, int32_t* scratch, int32_t* device_error, void* stream);
 
 /*
  * The 4-bit KV cache -- the same pages, heads and tokens as kv_cache in 4 bits

@@ -65,6 +65,14 @@ def _declare(lib):
         "attn_key_weights_kv4": (st, [p, p, p, f32, p, p, f32, i32, p, p]),
         "attn_evict_kv": (st, [p, p, p, i32, i32, p, p, i32, p, p, p]),
         "attn_evict_kv4": (st, [p, p, p, i32, i32, p, p, i32, p, p, p]),
+        "attn_rope": (st, [p, p, i64, i32, p, i64, i32, p, i64, p, i64, i32, p, i64, i32, p]),
+        "attn_append_kv_rope": (st, [p, p, p, p, i64, p, i64, p, i64, p, p, p]),
+        "attn_pages_scratch": (i64, [i64]),
+        "attn_pages_alloc": (st, [p, i32, i32, p, p, p]),
+        "attn_pages_free": (st, [p, i32, p, i64, p, p]),
+        "attn_pages_copy": (st, [p, p, i32, i32, p, p, i64, p, p]),
+        "attn_pages_fork": (st, [p, i32, p, i64, p, p, i32, i32, p, i32, p, p, i64, p, p, i32, p, p, p]),
+        "attn_pages_compact": (st, [p, i32, p, i64, p, p, p, i32, p, p, p]),
         "attn_plan_ragged": (st, [p, p, i32, i32, i32, i32, i32, f32, i32, p, p]),
         "attn_graph_plan": (st, [i32, i32, i32, i32, i32, f32, i32, i64, p, i32, p, p]),
         "attn_decode_graph": (st, [p, p, p, p, p, p, p, p, p, p]),
@@ -171,6 +179,182 @@ def kv4_cache_shape(num_pages: int, num_kv_heads: int, page_size: int, head_dim:
     if page_size % KV4_TOKENS or head_dim % KV4_GROUP:
         raise ValueError("a 4-bit cache needs page_size and head_dim in multiples of 16")
     return (num_pages, 2, num_kv_heads, page_size // KV4_TOKENS, KV4_TOKENS * (head_dim // 2 + head_dim // KV4_GROUP))
+
+
+def _row_stride(device, name, t, rows, heads, head_dim):
+    """Row stride (elements) of t, bf16 [rows, heads, head_dim] on `device`: rows may lie apart
+    (slices of a fused projection), the heads of a row are contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16):
+        raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
+    if t.shape != (rows, heads, head_dim):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {head_dim}]")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != head_dim):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    if rows < 2:
+        return heads * head_dim
+    if s[0] % 8 or s[0] < heads * head_dim:
+        raise ValueError(f"the rows of {name} must lie a multiple of 8 elements apart and not overlap")
+    return s[0]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("inv_freq", ctypes.c_void_p), ("axis", ctypes.c_void_p)]
+
+
+class Rope:
+    """Rotary positions with one axis or several (see attn_rope).
+
+    inv_freq: host floats, one per pair of dims (radians per position); the first
+    2 * len(inv_freq) dims of a head turn.  axis: per pair, the row of `positions`
+    it goes by (default: all 0).  interleaved: pairs are dims (2p, 2p + 1), else
+    (p, p + len(inv_freq)).  scale: multiplies cosines and sines."""
+
+    def __init__(self, inv_freq, axis=None, interleaved: bool = False, scale: float = 1.0):
+        def host(x, dtype):
+            x = x.detach().cpu().numpy() if isinstance(x, torch.Tensor) else x
+            return np.ascontiguousarray(np.asarray(x, dtype=dtype))
+        self._inv_freq = host(inv_freq, np.float32)
+        self._axis = np.zeros(len(self._inv_freq), np.int32) if axis is None else host(axis, np.int32)
+        if self._inv_freq.ndim != 1 or self._axis.shape != self._inv_freq.shape or not len(self._inv_freq):
+            raise ValueError("inv_freq and axis must have one entry per pair of dims")
+        if self._axis.min() < 0:
+            raise ValueError("axis must not be negative")
+        self.n_axes = int(self._axis.max()) + 1
+        self.rot_dim, self.interleaved, self.scale = 2 * len(self._inv_freq), bool(interleaved), float(scale)
+        self._spec = RopeSpec(self.rot_dim, int(self.interleaved), self.n_axes, self.scale, self._inv_freq.ctypes.data,
+                              self._axis.ctypes.data)
+        self._ref = ctypes.addressof(self._spec)
+
+    def _check_positions(self, device, positions, rows):
+        """int32 [n_axes, rows]; [rows] where there is one axis."""
+        one = self.n_axes == 1 and isinstance(positions, torch.Tensor) and positions.dim() == 1
+        _check_cuda(device, "positions", positions, torch.int32, (rows,) if one else (self.n_axes, rows))
+
+    def apply(self, positions, q, k=None, q_out=None, k_out=None, inverse: bool = False, stream=None):
+        """q and k (bf16 [rows, heads, head_dim], rows possibly apart) turned by
+        positions (int32 [n_axes, rows] or, with one axis, [rows]); by the negated
+        angles where `inverse` (what their gradients need).  q_out / k_out may be
+        the inputs (in place).  Returns (q_out, k_out), or q_out alone without k."""
+        if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3):
+            raise TypeError("q must be a CUDA tensor [rows, heads, head_dim]")
+        dev, (rows, H, D) = q.get_device(), q.shape
+        self._check_positions(dev, positions, rows)
+        q_out = _empty_on(stream, q.shape, torch.bfloat16, q.device) if q_out is None else q_out
+        args = [_ptr(q), _row_stride(dev, "q", q, rows, H, D), H, _ptr(q_out), _row_stride(dev, "q_out", q_out, rows, H, D)]
+        if k is None:
+            if k_out is not None:
+                raise ValueError("k_out without k")
+            args += [None, 0, 0, None, 0]
+        else:
+            if not (isinstance(k, torch.Tensor) and k.is_cuda and k.dim() == 3):
+                raise TypeError("k must be a CUDA tensor [rows, heads, head_dim]")
+            Hk = k.shape[1]
+            k_out = _empty_on(stream, k.shape, torch.bfloat16, k.device) if k_out is None else k_out
+            args += [_ptr(k), _row_stride(dev, "k", k, rows, Hk, D), Hk, _ptr(k_out),
+                     _row_stride(dev, "k_out", k_out, rows, Hk, D)]
+        _launch_on(dev, stream, "attn_rope", self._ref, _ptr(positions), rows, D, *args, int(inverse))
+        return q_out if k is None else (q_out, k_out)
+
+
+class PagePool:
+    """The pages of a cache, handed about on the device (see attn_pages_alloc).
+
+    pools: what is stored by page, CUDA tensors [num_pages, ...] (each layer's
+    cache; weights): copies, forks and compaction move a page in all of them.
+    refs: int32 [num_pages], how many page-table entries hold each page (new, all
+    zero, by default).  Calls read what earlier ones left: issue them on one stream."""
+
+    def __init__(self, pools, page_size: int, refs: Optional[torch.Tensor] = None):
+        self.pools = list(pools)
+        if not self.pools or not isinstance(self.pools[0], torch.Tensor) or self.pools[0].dim() < 1:
+            raise TypeError("pools must be CUDA tensors [num_pages, ...]")
+        if page_size < 1:
+            raise ValueError("page_size must be positive")
+        first = self.pools[0]
+        self.num_pages, self.page_size, self._dev, self._device = first.shape[0], int(page_size), first.get_device(), first.device
+        n = len(self.pools)
+        self._ptrs, self._bytes = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)()
+        for i, t in enumerate(self.pools):
+            _check_cuda(self._dev, f"pools[{i}]", t, getattr(t, "dtype", None))
+            if t.dim() < 1 or t.shape[0] != self.num_pages or not t.numel():
+                raise ValueError("every pool must be [num_pages, ...] and not empty")
+            self._ptrs[i], self._bytes[i] = t.data_ptr(), t.numel() // self.num_pages * t.element_size()
+            if self._bytes[i] % 16 or t.data_ptr() % 16:
+                raise ValueError("a page of every pool must be a multiple of 16 bytes, and 16-byte aligned")
+        self.refs = torch.zeros(self.num_pages, dtype=torch.int32, device=self._device) if refs is None else refs
+        _check_cuda(self._dev, "refs", self.refs, torch.int32, (self.num_pages,))
+        if self.refs.data_ptr() % 16:
+            raise ValueError("refs must be 16-byte aligned")
+        self._err = torch.zeros(1, dtype=torch.int32, device=self._device)
+        self._pools = (ctypes.addressof(self._ptrs), ctypes.addressof(self._bytes), n)
+
+    def _ids(self, name, t):
+        _check_cuda(self._dev, name, t, torch.int32)
+        if t.dim() != 1:
+            raise ValueError(f"{name} must have one dimension")
+        return t.numel()
+
+    def alloc(self, n: int, out=None, stream=None):
+        """The n lowest free pages, held once: int32 [n] (-1 where none was left)."""
+        out = _empty_on(stream, (n,), torch.int32, self._device) if out is None else out
+        _check_cuda(self._dev, "out", out, torch.int32, (n,))
+        _launch_on(self._dev, stream, "attn_pages_alloc", _ptr(self.refs), self.num_pages, n, _ptr(out), _ptr(self._err))
+        return out
+
+    def free(self, page_ids, stream=None):
+        """Every listed page is held once less; at 0 it is free."""
+        n = self._ids("page_ids", page_ids)
+        _launch_on(self._dev, stream, "attn_pages_free", _ptr(self.refs), self.num_pages, _ptr(page_ids), n, _ptr(self._err))
+
+    def copy(self, src, dst, stream=None):
+        """Page src[i] of every pool into page dst[i]; the dst are distinct and none is a src."""
+        n = self._ids("src", src)
+        _check_cuda(self._dev, "dst", dst, torch.int32, (n,))
+        _launch_on(self._dev, stream, "attn_pages_copy", *self._pools, self.num_pages, _ptr(src), _ptr(dst), n,
+                   _ptr(self._err))
+
+    def fork(self, page_table, kv_indptr, kv_lens, parents, out_len: int, out=None, indptr_out=None, stream=None):
+        """Children that start as their parents' first kv_lens tokens: full pages
+        shared, a last page that is not full copied.  page_table, kv_indptr
+        [batch + 1], kv_lens [batch], parents [n]: int32 CUDA tensors.  Returns the
+        children's page table (int32 [out_len], out_len at least their pages in
+        all) and its offsets (int32 [n + 1])."""
+        entries = self._ids("page_table", page_table)
+        batch, n = self._ids("kv_lens", kv_lens), self._ids("parents", parents)
+        _check_cuda(self._dev, "kv_indptr", kv_indptr, torch.int32, (batch + 1,))
+        out = _empty_on(stream, (out_len,), torch.int32, self._device) if out is None else out
+        indptr_out = _empty_on(stream, (n + 1,), torch.int32, self._device) if indptr_out is None else indptr_out
+        _check_cuda(self._dev, "out", out, torch.int32, (out_len,))
+        _check_cuda(self._dev, "indptr_out", indptr_out, torch.int32, (n + 1,))
+        scratch = _empty_on(stream, (_lib.attn_pages_scratch(n),), torch.int32, self._device)
+        _launch_on(self._dev, stream, "attn_pages_fork", _ptr(self.refs), self.num_pages, _ptr(page_table), entries,
+                   _ptr(kv_indptr), _ptr(kv_lens), batch, self.page_size, _ptr(parents), n, _ptr(out), _ptr(indptr_out),
+                   out_len, *self._pools, _ptr(scratch), _ptr(self._err))
+        return out, indptr_out
+
+    def compact(self, page_table, remap=None, stream=None):
+        """The pages in use move to the front of the pools; page_table (int32) is
+        changed to their new ids.  Returns every page's new id (int32 [num_pages],
+        -1 for those that were free), by which other tables are mapped."""
+        n = self._ids("page_table", page_table)
+        remap = _empty_on(stream, (self.num_pages,), torch.int32, self._device) if remap is None else remap
+        _check_cuda(self._dev, "remap", remap, torch.int32, (self.num_pages,))
+        scratch = _empty_on(stream, (_lib.attn_pages_scratch(self.num_pages // 2),), torch.int32, self._device)
+        _launch_on(self._dev, stream, "attn_pages_compact", _ptr(self.refs), self.num_pages, _ptr(page_table), n,
+                   _ptr(remap), *self._pools, _ptr(scratch), _ptr(self._err))
+        return remap
+
+    def device_error(self, stream=None) -> int:
+        """Waits for `stream` and returns the ATTN_DEVICE_ERR_* bits that calls left; clears them."""
+        with torch.cuda.device(self._dev), torch.cuda.stream(stream):
+            code = int(self._err.item())
+            if code:
+                self._err.zero_()
+        return code
 
 
 class Plan:
@@ -316,6 +500,21 @@ class Plan:
         _check("attn_append_kv", load_library().attn_append_kv(
             self._handle, _ptr(k_new), _ptr(v_new), _ptr(kv_cache), _stream_ptr(stream)))
         return kv_cache
+
+    def append_kv_rope(self, rope: Rope, positions, q, k_new, v_new, kv_cache, q_out=None, stream=None):
+        """q and k_new turned by their rows' positions (see Rope.apply), the turned
+        k and v_new written into their cache positions; returns the turned q.  q,
+        k_new, v_new: rows possibly apart (slices of a fused projection)."""
+        dev, rows, D, Hkv = self.workspace.get_device(), self.total_rows, self.head_dim, self.num_kv_heads
+        shape = (rows, self.num_qo_heads, D)
+        rope._check_positions(dev, positions, rows)
+        q_out = _empty_on(stream, shape, torch.bfloat16, self.workspace.device) if q_out is None else q_out
+        _check_cuda(dev, "q_out", q_out, torch.bfloat16, shape)
+        _check_cuda(dev, "kv_cache", kv_cache, *self._cache_spec(False))
+        _launch_on(dev, stream, "attn_append_kv_rope", self._handle, rope._ref, _ptr(positions), _ptr(q),
+                   _row_stride(dev, "q", q, *shape), _ptr(k_new), _row_stride(dev, "k_new", k_new, rows, Hkv, D),
+                   _ptr(v_new), _row_stride(dev, "v_new", v_new, rows, Hkv, D), _ptr(q_out), _ptr(kv_cache))
+        return q_out
 
     # -- 4-bit cache ------------------------------------------------------
     def kv4_shape(self, num_pages: Optional[int] = None):
@@ -485,7 +684,7 @@ class RaggedPlan(Plan):
     def append_kv(self, *args, **kwargs):
         raise TypeError("a ragged plan has no KV cache")
 
-    append_kv4 = decode_kv4 = key_weights = key_weights_kv4 = evict_kv = evict_kv4 = kv4_shape = append_kv
+    append_kv_rope = append_kv4 = decode_kv4 = key_weights = key_weights_kv4 = evict_kv = evict_kv4 = kv4_shape = append_kv
     kv_lens = property(append_kv)
 
 
@@ -543,7 +742,7 @@ class GraphPlan(Plan):
     def append_kv(self, *args, **kwargs):
         raise TypeError("a graph plan only decodes")
 
-    append_kv4 = decode_kv4 = key_weights = key_weights_kv4 = evict_kv = evict_kv4 = append_kv
+    append_kv_rope = append_kv4 = decode_kv4 = key_weights = key_weights_kv4 = evict_kv = evict_kv4 = append_kv
     kv_lens = property(append_kv)   # (they are on the device, and change between replays)
 
 

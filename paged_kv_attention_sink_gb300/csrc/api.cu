@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -427,6 +428,196 @@ extern "C" attn_status attn_evict_kv4(attn_plan_t plan, const float* weights, co
                                       int32_t num_pages_out, void* kv4_out, float* weights_out, void* stream) {
     return evict(plan, true, weights, kv4_cache, budget, recent, kept, page_table_out, num_pages_out, kv4_out,
                  weights_out, stream);
+}
+
+// ---------------------------------------------------------- rotary positions
+
+namespace {
+
+// f / 2 pi modulo 1 as a 64-bit fixed-point fraction, to its last bit or two: the
+// product with 1 / 2 pi in two doubles, whole turns dropped.
+uint64_t turns_of(float f) {
+    constexpr double kInv2PiHi = 0x1.45f306dc9c883p-3, kInv2PiLo = -0x1.6b01ec5417056p-57;
+    const double x = std::fabs((double)f), hi = x * kInv2PiHi;
+    const double lo = std::fma(x, kInv2PiHi, -hi) + x * kInv2PiLo;
+    const double scaled = std::ldexp(hi - std::floor(hi), 64), whole = std::floor(scaled);   // exact, below 2^64
+    const uint64_t turns = (uint64_t)whole + (uint64_t)(int64_t)std::nearbyint(scaled - whole + std::ldexp(lo, 64));
+    return f < 0.f ? 0 - turns : turns;
+}
+
+attn_status rope_table(const attn_rope_spec* r, int32_t head_dim, attn::RopeTable& t) {
+    if (!r || !r->inv_freq || r->rot_dim <= 0 || r->rot_dim > head_dim || r->n_axes < 1 || r->n_axes > 8 ||
+        (r->interleaved != 0 && r->interleaved != 1) || !std::isfinite(r->scale))
+        return ATTN_ERR_INVALID_ARG;
+    if ((head_dim != 64 && head_dim != 128) || r->rot_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    t.pairs = r->rot_dim / 2;
+    t.scale = r->scale;
+    for (int p = 0; p < t.pairs; ++p) {
+        const int32_t axis = r->axis ? r->axis[p] : 0;
+        if (axis < 0 || axis >= r->n_axes || !(std::fabs(r->inv_freq[p]) < 0x1p20f)) return ATTN_ERR_INVALID_ARG;
+        t.axis[p] = (uint8_t)axis;
+        t.freq[p] = turns_of(r->inv_freq[p]);
+    }
+    return ATTN_OK;
+}
+
+// Rows of `heads` heads: 16-byte chunks throughout.
+bool valid_rows(const void* x, int64_t stride, int32_t heads, int32_t head_dim) {
+    return x && aligned16(x) && stride % 8 == 0 && stride >= (int64_t)heads * head_dim;
+}
+
+}  // namespace
+
+extern "C" attn_status attn_rope(const attn_rope_spec* rope, const int32_t* positions, int64_t rows, int32_t head_dim,
+                                 const void* q, int64_t q_stride, int32_t num_q_heads, void* q_out,
+                                 int64_t q_out_stride, const void* k, int64_t k_stride, int32_t num_k_heads,
+                                 void* k_out, int64_t k_out_stride, int32_t inverse, void* stream) {
+    if (rows < 0 || num_q_heads < 0 || num_k_heads < 0 || (int64_t)num_q_heads + num_k_heads == 0 ||
+        (inverse != 0 && inverse != 1))
+        return ATTN_ERR_INVALID_ARG;
+    attn::RopeTable t = {};
+    if (attn_status st = rope_table(rope, head_dim, t); st != ATTN_OK) return st;
+    // CTAs of a grid, and items of a CTA's rows, in 31 bits.
+    if (rows > INT32_MAX || (int64_t)num_q_heads + num_k_heads > 65536) return ATTN_ERR_UNSUPPORTED;
+    if (rows == 0) return ATTN_OK;
+    if (!positions || !aligned4(positions)) return ATTN_ERR_INVALID_ARG;
+    if (num_q_heads > 0 && !(valid_rows(q, q_stride, num_q_heads, head_dim) &&
+                             valid_rows(q_out, q_out_stride, num_q_heads, head_dim)))
+        return ATTN_ERR_INVALID_ARG;
+    if (num_k_heads > 0 && !(valid_rows(k, k_stride, num_k_heads, head_dim) &&
+                             valid_rows(k_out, k_out_stride, num_k_heads, head_dim)))
+        return ATTN_ERR_INVALID_ARG;
+    if ((num_q_heads > 0 && q == q_out && q_stride != q_out_stride) ||
+        (num_k_heads > 0 && k == k_out && k_stride != k_out_stride))
+        return ATTN_ERR_INVALID_ARG;
+    return attn::launch_rope(t, rope->interleaved != 0, inverse != 0, positions, rows, head_dim,
+                             {q, q_stride, q_out, q_out_stride, num_q_heads},
+                             {k, k_stride, k_out, k_out_stride, num_k_heads}, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" attn_status attn_append_kv_rope(attn_plan_t plan, const attn_rope_spec* rope, const int32_t* positions,
+                                           const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+                                           const void* v_new, int64_t v_stride, void* q_out, void* kv_cache,
+                                           void* stream) {
+    if (attn_status st = check_paged(plan); st != ATTN_OK) return st;
+    attn::RopeTable t = {};
+    if (attn_status st = rope_table(rope, plan->D, t); st != ATTN_OK) return st;
+    if ((int64_t)plan->Hq + 2 * (int64_t)plan->Hkv > 65536) return ATTN_ERR_UNSUPPORTED;
+    if (plan->info.total_qo_rows == 0) return ATTN_OK;
+    if (!positions || !aligned4(positions) || !valid_rows(q, q_stride, plan->Hq, plan->D) ||
+        !valid_rows(k_new, k_stride, plan->Hkv, plan->D) || !valid_rows(v_new, v_stride, plan->Hkv, plan->D) ||
+        !q_out || !aligned16(q_out) || !kv_cache || !aligned16(kv_cache))
+        return ATTN_ERR_INVALID_ARG;
+    if (q == q_out && q_stride != (int64_t)plan->Hq * plan->D) return ATTN_ERR_INVALID_ARG;
+    return attn::launch_append_kv_rope(plan, t, rope->interleaved != 0, positions, {q, q_stride, q_out, 0, plan->Hq},
+                                       {k_new, k_stride, kv_cache, 0, plan->Hkv},
+                                       {v_new, v_stride, nullptr, 0, plan->Hkv}, static_cast<cudaStream_t>(stream));
+}
+
+// ----------------------------------------------------------- page management
+
+namespace {
+
+attn_status check_pools(void* const* pools, const int64_t* page_bytes, int32_t n_pools) {
+    if (n_pools < 0 || (n_pools > 0 && (!pools || !page_bytes))) return ATTN_ERR_INVALID_ARG;
+    for (int32_t k = 0; k < n_pools; ++k)
+        if (!pools[k] || !aligned16(pools[k]) || page_bytes[k] <= 0 || page_bytes[k] % 16 != 0)
+            return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+attn_status check_refs(const int32_t* refs, int32_t num_pages, const int32_t* device_error) {
+    return num_pages > 0 && refs && aligned16(refs) && aligned4(device_error) ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
+// In launches of as many pools as a launch's arguments hold.
+attn_status copy_pages(void* const* pools, const int64_t* page_bytes, int32_t n_pools, int32_t num_pages,
+                       const int32_t* src, const int32_t* dst, const int32_t* n, int64_t n_max, int32_t* device_error,
+                       cudaStream_t stream) {
+    if (n_max == 0) return ATTN_OK;
+    for (int32_t k0 = 0; k0 < n_pools; k0 += attn::kPagePoolsPerLaunch) {
+        attn::PagePools p = {};
+        p.n = std::min(n_pools - k0, attn::kPagePoolsPerLaunch);
+        for (int32_t k = 0; k < p.n; ++k) {
+            p.pool[k] = static_cast<unsigned char*>(pools[k0 + k]);
+            p.bytes[k] = page_bytes[k0 + k];
+        }
+        if (attn_status st = attn::launch_pages_copy(p, num_pages, src, dst, n, n_max, device_error, stream); st != ATTN_OK)
+            return st;
+    }
+    return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" int64_t attn_pages_scratch(int64_t n) { return attn::page_move_words(n > 0 ? n : 0); }
+
+extern "C" attn_status attn_pages_alloc(int32_t* refs, int32_t num_pages, int32_t n, int32_t* page_ids,
+                                        int32_t* device_error, void* stream) {
+    if (attn_status st = check_refs(refs, num_pages, device_error); st != ATTN_OK) return st;
+    if (n < 0) return ATTN_ERR_INVALID_ARG;
+    if (n == 0) return ATTN_OK;
+    if (!page_ids || !aligned4(page_ids)) return ATTN_ERR_INVALID_ARG;
+    return attn::launch_pages_alloc(refs, num_pages, n, page_ids, device_error, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" attn_status attn_pages_free(int32_t* refs, int32_t num_pages, const int32_t* page_ids, int64_t n,
+                                       int32_t* device_error, void* stream) {
+    if (attn_status st = check_refs(refs, num_pages, device_error); st != ATTN_OK) return st;
+    if (n < 0 || n > INT32_MAX) return ATTN_ERR_INVALID_ARG;
+    if (n == 0) return ATTN_OK;
+    if (!page_ids || !aligned4(page_ids)) return ATTN_ERR_INVALID_ARG;
+    return attn::launch_pages_free(refs, num_pages, page_ids, n, device_error, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" attn_status attn_pages_copy(void* const* pools, const int64_t* page_bytes, int32_t n_pools, int32_t num_pages,
+                                       const int32_t* src, const int32_t* dst, int64_t n, int32_t* device_error,
+                                       void* stream) {
+    if (attn_status st = check_pools(pools, page_bytes, n_pools); st != ATTN_OK) return st;
+    if (num_pages <= 0 || n < 0 || n > INT32_MAX || !aligned4(device_error)) return ATTN_ERR_INVALID_ARG;
+    if (n == 0) return ATTN_OK;
+    if (!src || !dst || !aligned4(src) || !aligned4(dst)) return ATTN_ERR_INVALID_ARG;
+    return copy_pages(pools, page_bytes, n_pools, num_pages, src, dst, nullptr, n, device_error,
+                      static_cast<cudaStream_t>(stream));
+}
+
+extern "C" attn_status attn_pages_fork(int32_t* refs, int32_t num_pages, const int32_t* page_table,
+                                       int64_t table_len, const int32_t* kv_indptr, const int32_t* kv_lens, int32_t batch,
+                                       int32_t page_size, const int32_t* parents, int32_t n, int32_t* page_table_out,
+                                       int32_t* indptr_out, int64_t out_len, void* const* pools,
+                                       const int64_t* page_bytes, int32_t n_pools, int32_t* scratch,
+                                       int32_t* device_error, void* stream) {
+    if (attn_status st = check_refs(refs, num_pages, device_error); st != ATTN_OK) return st;
+    if (attn_status st = check_pools(pools, page_bytes, n_pools); st != ATTN_OK) return st;
+    if (batch < 0 || page_size <= 0 || n < 0 || out_len < 0 || out_len > INT32_MAX) return ATTN_ERR_INVALID_ARG;
+    if (!indptr_out || !scratch || !aligned4(indptr_out) || !aligned4(scratch)) return ATTN_ERR_INVALID_ARG;
+    if (table_len < 0 || table_len > INT32_MAX || (table_len > 0 && !page_table)) return ATTN_ERR_INVALID_ARG;
+    if (n > 0 && (!kv_indptr || !kv_lens || !parents || !aligned4(page_table) || !aligned4(kv_indptr) ||
+                  !aligned4(kv_lens) || !aligned4(parents)))
+        return ATTN_ERR_INVALID_ARG;
+    if (out_len > 0 && (!page_table_out || !aligned4(page_table_out))) return ATTN_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const attn::PageFork f = {page_table, kv_indptr, kv_lens, parents, table_len, batch, n, page_size, page_table_out,
+                              indptr_out, out_len};
+    if (attn_status st = attn::launch_pages_fork(refs, num_pages, f, scratch, device_error, s); st != ATTN_OK) return st;
+    const int32_t *dst = scratch + attn::kMoveHead, *src = dst + n;
+    return copy_pages(pools, page_bytes, n_pools, num_pages, src, dst, scratch, n, device_error, s);
+}
+
+extern "C" attn_status attn_pages_compact(int32_t* refs, int32_t num_pages, int32_t* page_table, int64_t n_entries,
+                                          int32_t* remap, void* const* pools, const int64_t* page_bytes,
+                                          int32_t n_pools, int32_t* scratch, int32_t* device_error, void* stream) {
+    if (attn_status st = check_refs(refs, num_pages, device_error); st != ATTN_OK) return st;
+    if (attn_status st = check_pools(pools, page_bytes, n_pools); st != ATTN_OK) return st;
+    if (n_entries < 0 || n_entries > INT32_MAX || !remap || !scratch || !aligned4(remap) || !aligned4(scratch) ||
+        (n_entries > 0 && (!page_table || !aligned4(page_table))))
+        return ATTN_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (attn_status st = attn::launch_pages_compact(refs, num_pages, page_table, n_entries, remap, scratch, device_error, s);
+        st != ATTN_OK)
+        return st;
+    const int32_t *dst = scratch + attn::kMoveHead, *src = dst + num_pages / 2;
+    return copy_pages(pools, page_bytes, n_pools, num_pages, src, dst, scratch, num_pages / 2, device_error, s);
 }
 
 extern "C" attn_status attn_plan_device_error(attn_plan_t plan, int32_t* code, void* stream) {

@@ -76,6 +76,59 @@ attn_status launch_evict(attn_plan_s* plan, bool four, const float* weights, con
                          int32_t recent, int32_t* kept, const int32_t* page_table_out, int32_t num_pages_out,
                          void* pool_out, float* weights_out, cudaStream_t stream);
 
+// Rotary positions (rope.cu).  freq: each pair's frequency in turns, a 64-bit
+// fixed-point fraction; axis: which row of positions it takes.
+constexpr int kRopeMaxPairs = 64;
+struct RopeTable {
+    uint64_t freq[kRopeMaxPairs];
+    uint8_t axis[kRopeMaxPairs];
+    int32_t pairs;   // a multiple of 8
+    float scale;
+};
+// Rows [rows][heads][head_dim] of bf16 whose last two dimensions are contiguous; strides in elements.
+struct RopeRows {
+    const void* in = nullptr;
+    int64_t stride = 0;
+    void* out = nullptr;
+    int64_t out_stride = 0;
+    int32_t heads = 0;
+};
+attn_status launch_rope(const RopeTable& t, bool inter, bool inverse, const int32_t* positions, int64_t rows,
+                        int32_t head_dim, const RopeRows& q, const RopeRows& k, cudaStream_t stream);
+// q.out: contiguous rows; k.out: the page pool.
+attn_status launch_append_kv_rope(attn_plan_s* plan, const RopeTable& t, bool inter, const int32_t* positions,
+                                  const RopeRows& q, const RopeRows& k, const RopeRows& v, cudaStream_t stream);
+
+// Page management (pages.cu).
+constexpr int kPagePoolsPerLaunch = 64;
+struct PagePools {
+    unsigned char* pool[kPagePoolsPerLaunch];
+    int64_t bytes[kPagePoolsPerLaunch];   // of a page, a multiple of 16
+    int32_t n;
+};
+attn_status launch_pages_alloc(int32_t* refs, int32_t num_pages, int32_t n, int32_t* page_ids, int32_t* err,
+                               cudaStream_t stream);
+attn_status launch_pages_free(int32_t* refs, int32_t num_pages, const int32_t* page_ids, int64_t n, int32_t* err,
+                              cudaStream_t stream);
+struct PageFork {
+    const int32_t *page_table, *kv_indptr, *kv_lens, *parents;
+    int64_t table_len;
+    int32_t batch, n, page_size;
+    int32_t *table_out, *indptr_out;
+    int64_t out_len;
+};
+// scratch: page_move_words(n) int32: the copies that the pools need, written on the device.
+attn_status launch_pages_fork(int32_t* refs, int32_t num_pages, const PageFork& f, int32_t* scratch, int32_t* err,
+                              cudaStream_t stream);
+attn_status launch_pages_compact(int32_t* refs, int32_t num_pages, int32_t* page_table, int64_t entries, int32_t* remap,
+                                 int32_t* scratch, int32_t* err, cudaStream_t stream);
+// Copies pages src[i] -> dst[i], i < *n (device) or n_host where n is NULL, at most n_max, in every pool.
+attn_status launch_pages_copy(const PagePools& pools, int32_t num_pages, const int32_t* src, const int32_t* dst,
+                              const int32_t* n, int64_t n_max, int32_t* err, cudaStream_t stream);
+// Layout of the scratch of `moves` copies: the count, then the pages written, then the pages read.
+constexpr int kMoveHead = 4;
+inline int64_t page_move_words(int64_t moves) { return kMoveHead + 2 * moves; }
+
 }  // namespace attn
 
 namespace attn {

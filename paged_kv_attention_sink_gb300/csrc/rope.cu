@@ -1,0 +1,223 @@
+// Rotary positions with one or more axes: q and k rows turned by pairs of
+// dims, alone or with the turned k and the v written into their HND pages.
+//
+// Pair p of a row turns by theta = positions[axis[p]][row] * inv_freq[p]:
+// (x, y) -> scale (x cos - y sin, x sin + y cos).  Only theta modulo a full
+// turn counts, and a far position times a frequency has more bits than fp32 (or
+// fp32 pairs) keep, so the frequency is held in turns as a 64-bit fixed-point
+// fraction F = round(inv_freq / 2 pi * 2^64): position * F modulo 2^64 is then
+// the angle's fraction of a turn, exact but for the rounding of F (2^31 * 2^-65
+// of a turn at the farthest position), by one integer product.  Its upper 32
+// bits, as a signed number of half turns, go to sincospif.
+//
+// Memory-bound: each row is read and written once, in 16-byte chunks.  A row's
+// angles are the same for all heads, so a CTA takes a few whole rows, computes
+// their cosines and sines into shared memory (one or two per thread) while the
+// first rows' loads are on their way, and each thread then turns 8 pairs at a
+// time: two 16-byte chunks, which hold the pairs' halves (chunk i and the one
+// half the turned width on) or, with neighbouring dims paired, 4 pairs each.
+#include <cstdint>
+
+#include "attn_internal.h"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeUnroll = 4;    // items of a thread whose loads are in flight together
+constexpr int kRopeMaxRows = 8;   // rows of a CTA
+
+struct RopeArgs {
+    RopeTable t;
+    const int32_t* positions;   // [n_axes][rows]
+    int64_t rows;
+    int32_t rows_per_cta, Hq, Hkv, inverse;
+    const uint4 *q, *k, *v;
+    uint4 *q_out, *k_out;       // k_out: the page pool where kCache
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;   // 16-byte chunks
+    // kCache
+    const int2* slots;          // per row: page-table slot, row in the page
+    const int32_t* page_table;
+    int32_t P, num_pages;
+    int32_t* err;
+};
+
+// Turns 8 pairs; t: their (cos, sin), two pairs per float4, `stride` float4 apart.
+template <bool kInter>
+__device__ __forceinline__ void turn(uint4& lo, uint4& hi, const float4* t, int stride) {
+    uint32_t* a = reinterpret_cast<uint32_t*>(&lo);
+    uint32_t* b = reinterpret_cast<uint32_t*>(&hi);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float4 cs = t[j * stride];   // pairs 2j and 2j + 1
+        if constexpr (kInter) {
+            uint32_t* w = j < 2 ? a : b;
+            const int e = (j & 1) * 2;
+            const float2 u = ptx::unpack_bf16x2(w[e]), v = ptx::unpack_bf16x2(w[e + 1]);
+            w[e] = ptx::pack_bf16x2(fmaf(u.x, cs.x, -u.y * cs.y), fmaf(u.x, cs.y, u.y * cs.x));
+            w[e + 1] = ptx::pack_bf16x2(fmaf(v.x, cs.z, -v.y * cs.w), fmaf(v.x, cs.w, v.y * cs.z));
+        } else {
+            const float2 x = ptx::unpack_bf16x2(a[j]), y = ptx::unpack_bf16x2(b[j]);
+            a[j] = ptx::pack_bf16x2(fmaf(x.x, cs.x, -y.x * cs.y), fmaf(x.y, cs.z, -y.y * cs.w));
+            b[j] = ptx::pack_bf16x2(fmaf(x.x, cs.y, y.x * cs.x), fmaf(x.y, cs.w, y.y * cs.z));
+        }
+    }
+}
+
+template <int D, bool kInter, bool kCache>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr int kItems = D / 16;                       // items of a head: 16 dims each
+    __shared__ float4 cs_s[kRopeMaxRows * D / 4];        // [row][pair pair][item]: (cos, sin) of two pairs
+    __shared__ int64_t page_s[kRopeMaxRows];             // kCache: first chunk of the row in its page's K, or -1
+    const int tid = threadIdx.x;
+    const int64_t row0 = (int64_t)blockIdx.x * a.rows_per_cta;
+    const int rows = (int)min((int64_t)a.rows_per_cta, a.rows - row0);
+    const int turned = a.t.pairs / 8;                    // items of a head that turn
+    const int heads = a.Hq + a.Hkv * (kCache ? 2 : 1), per_row = heads * kItems, n = rows * per_row;
+
+    // Where item x lies: the head's first chunk, and the two chunks of the item.
+    auto locate = [&](int x, int& r, int& h, int& i, int& c0, int& c1) {
+        r = x / per_row;
+        const int y = x - r * per_row;
+        h = y / kItems;
+        i = y % kItems;
+        const bool apart = !kInter && i < turned && h < a.Hq + a.Hkv;
+        c0 = apart ? i : 2 * i;
+        c1 = apart ? i + turned : 2 * i + 1;
+    };
+    auto load = [&](int x, uint4& lo, uint4& hi) {
+        int r, h, i, c0, c1;
+        locate(x, r, h, i, c0, c1);
+        const int64_t row = row0 + r;
+        const uint4* src = h < a.Hq ? a.q + row * a.q_stride + h * (D / 8)
+                           : h < a.Hq + a.Hkv ? a.k + row * a.k_stride + (h - a.Hq) * (D / 8)
+                                              : a.v + row * a.v_stride + (h - a.Hq - a.Hkv) * (D / 8);
+        lo = src[c0];
+        hi = src[c1];
+    };
+    auto store = [&](int x, uint4 lo, uint4 hi) {
+        int r, h, i, c0, c1;
+        locate(x, r, h, i, c0, c1);
+        if (h < a.Hq + a.Hkv && i < turned) turn<kInter>(lo, hi, cs_s + r * (D / 4) + i, turned);
+        const int64_t row = row0 + r;
+        uint4* dst;
+        if (h < a.Hq) {
+            dst = a.q_out + row * a.q_out_stride + h * (D / 8);
+        } else if constexpr (kCache) {
+            if (page_s[r] < 0) return;
+            dst = a.k_out + page_s[r] + (int64_t)(h - a.Hq) * a.P * (D / 8);   // V's heads follow K's
+        } else {
+            dst = a.k_out + row * a.k_out_stride + (h - a.Hq) * (D / 8);
+        }
+        dst[c0] = lo;
+        dst[c1] = hi;
+    };
+
+    ptx::grid_dependency_wait();
+    ptx::grid_dependents_go();
+    uint4 lo[kRopeUnroll], hi[kRopeUnroll];
+#pragma unroll
+    for (int u = 0; u < kRopeUnroll; ++u)
+        if (tid + u * kRopeThreads < n) load(tid + u * kRopeThreads, lo[u], hi[u]);
+
+    for (int x = tid; x < rows * a.t.pairs; x += kRopeThreads) {
+        const int r = x / a.t.pairs, p = x - r * a.t.pairs;
+        int64_t pos = a.positions[a.t.axis[p] * a.rows + row0 + r];
+        if (a.inverse) pos = -pos;
+        const uint64_t turns = (uint64_t)pos * a.t.freq[p];
+        float s, c;
+        sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
+        const int item = p >> 3, j = p & 7;
+        reinterpret_cast<float2*>(cs_s)[(r * (D / 4) + (j >> 1) * turned + item) * 2 + (j & 1)] =
+            make_float2(c * a.t.scale, s * a.t.scale);
+    }
+    if constexpr (kCache) {
+        if (tid < rows) {
+            const int2 slot = a.slots[row0 + tid];
+            const int32_t page = a.page_table[slot.x];
+            const bool in = page >= 0 && page < a.num_pages;
+            if (!in) atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
+            page_s[tid] = in ? ((int64_t)page * 2 * a.Hkv * a.P + slot.y) * (D / 8) : -1;
+        }
+    }
+    __syncthreads();
+
+    for (int x = tid; x < n; x += kRopeUnroll * kRopeThreads) {
+        if (x != tid) {
+#pragma unroll
+            for (int u = 0; u < kRopeUnroll; ++u)
+                if (x + u * kRopeThreads < n) load(x + u * kRopeThreads, lo[u], hi[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u)
+            if (x + u * kRopeThreads < n) store(x + u * kRopeThreads, lo[u], hi[u]);
+    }
+}
+
+template <int D, bool kInter, bool kCache>
+attn_status launch(RopeArgs& a, cudaStream_t stream) {
+    int32_t sms = 0;
+    if (!current_sm_count(&sms)) return ATTN_ERR_CUDA;
+    a.rows_per_cta = a.rows <= 8 * (int64_t)sms ? 1 : 4;
+    const int64_t ctas = (a.rows + a.rows_per_cta - 1) / a.rows_per_cta;
+    return launch_dependent(rope_kernel<D, kInter, kCache>, dim3((unsigned)ctas), kRopeThreads, 0, stream, a) == cudaSuccess
+               ? ATTN_OK
+               : ATTN_ERR_CUDA;
+}
+
+template <bool kCache>
+attn_status launch(RopeArgs& a, int32_t head_dim, bool inter, cudaStream_t stream) {
+    if (head_dim == 64) return inter ? launch<64, true, kCache>(a, stream) : launch<64, false, kCache>(a, stream);
+    return inter ? launch<128, true, kCache>(a, stream) : launch<128, false, kCache>(a, stream);
+}
+
+}  // namespace
+
+attn_status launch_rope(const RopeTable& t, bool inter, bool inverse, const int32_t* positions, int64_t rows,
+                        int32_t head_dim, const RopeRows& q, const RopeRows& k, cudaStream_t stream) {
+    RopeArgs a = {};
+    a.t = t;
+    a.positions = positions;
+    a.rows = rows;
+    a.Hq = q.heads;
+    a.Hkv = k.heads;
+    a.inverse = inverse;
+    a.q = static_cast<const uint4*>(q.in);
+    a.k = static_cast<const uint4*>(k.in);
+    a.q_out = static_cast<uint4*>(q.out);
+    a.k_out = static_cast<uint4*>(k.out);
+    a.q_stride = q.stride / 8;
+    a.k_stride = k.stride / 8;
+    a.q_out_stride = q.out_stride / 8;
+    a.k_out_stride = k.out_stride / 8;
+    return launch<false>(a, head_dim, inter, stream);
+}
+
+attn_status launch_append_kv_rope(attn_plan_s* plan, const RopeTable& t, bool inter, const int32_t* positions,
+                                  const RopeRows& q, const RopeRows& k, const RopeRows& v, cudaStream_t stream) {
+    RopeArgs a = {};
+    a.t = t;
+    a.positions = positions;
+    a.rows = plan->info.total_qo_rows;
+    a.Hq = plan->Hq;
+    a.Hkv = plan->Hkv;
+    a.q = static_cast<const uint4*>(q.in);
+    a.k = static_cast<const uint4*>(k.in);
+    a.v = static_cast<const uint4*>(v.in);
+    a.q_out = static_cast<uint4*>(q.out);
+    a.k_out = static_cast<uint4*>(k.out);
+    a.q_stride = q.stride / 8;
+    a.k_stride = k.stride / 8;
+    a.v_stride = v.stride / 8;
+    a.q_out_stride = (int64_t)plan->Hq * plan->D / 8;
+    a.slots = reinterpret_cast<const int2*>(plan->ws + plan->layout.append);
+    a.page_table = plan->page_table;
+    a.P = plan->P;
+    a.num_pages = plan->num_pages;
+    a.err = reinterpret_cast<int32_t*>(plan->ws + plan->layout.err);
+    return launch<true>(a, plan->D, inter, stream);
+}
+
+}  // namespace attn
