@@ -194,6 +194,40 @@ ATTN_API attn_status attn_prefill_ragged(attn_plan_t plan, const void* q, const 
                                          const float* sinks, void* out, float* lse, void* stream);
 
 /*
+ * attn_plan_cross / attn_cross -- cross attention: the query rows of each sequence
+ * (its decoder's) over all of an encoder's states, which have a length of their
+ * own, longer or shorter than the rows; nothing is causal.  No source describes it:
+ * an interface addition.  Rows that look at the same states belong to one
+ * sequence: a prompt's tokens, the beams, samples or draft tokens of a step.  They
+ * then share every read of K and V.
+ *
+ *   qo_indptr  host int32 [batch + 1]: sequence b's query rows, any number
+ *   kv_start, kv_len  host int32 [batch]: sequence b's states are rows
+ *              [kv_start, kv_start + kv_len) of k and v, 0 <= kv_start,
+ *              kv_start + kv_len <= kv_rows.  So k and v may be packed, padded to
+ *              one length, or a store from which sequences come and go; sequences
+ *              may share rows.  Rows that no sequence has are not used (they may
+ *              hold NaN).  kv_len = 0: out = 0, lse = the sink's (-inf without).
+ *   q, out     bf16 [qo_indptr[batch]][Hq][head_dim];  sinks, lse as in attn_prefill
+ *   k, v       bf16 [kv_rows][Hkv][head_dim], rows k_stride / v_stride elements apart
+ *              (multiples of 8, at least Hkv * head_dim), 16-byte aligned: the two
+ *              halves of a fused projection are taken as they are.  Not read, and
+ *              may be NULL, where kv_rows = 0.
+ *   head_dim in {64, 128}; num_qo_heads % num_kv_heads == 0; rows * Hq and kv_rows
+ *   below 2^30 (else ATTN_ERR_UNSUPPORTED)
+ * Workspace, binding and error word as for attn_plan; every other launch refuses
+ * such a plan (ATTN_ERR_INVALID_ARG).  attn_cross writes all rows of out and lse.
+ * The order of every sum is fixed.  Async on `stream`; capturable (after one
+ * uncaptured call with these pointers has built the TMA descriptors).
+ */
+ATTN_API attn_status attn_plan_cross(const int32_t* qo_indptr, const int32_t* kv_start, const int32_t* kv_len,
+                                     int32_t batch, int32_t kv_rows, int32_t num_qo_heads, int32_t num_kv_heads,
+                                     int32_t head_dim, float sm_scale, int32_t num_sms, attn_plan_t* plan_out,
+                                     size_t* workspace_bytes_out);
+ATTN_API attn_status attn_cross(attn_plan_t plan, const void* q, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, const float* sinks, void* out, float* lse, void* stream);
+
+/*
  * attn_merge_states -- combine two attention states over disjoint key sets
  * into the state over their union, by the log-sum-exp rule implied by the
  * split along the KV length in "GPT-OSS on day 0", section "Sink Attention"

@@ -65,6 +65,8 @@ def _declare(lib):
         "attn_key_weights_kv4": (st, [p, p, p, f32, p, p, f32, i32, p, p]),
         "attn_evict_kv": (st, [p, p, p, i32, i32, p, p, i32, p, p, p]),
         "attn_evict_kv4": (st, [p, p, p, i32, i32, p, p, i32, p, p, p]),
+        "attn_plan_cross": (st, [p, p, p, i32, i32, i32, i32, i32, f32, i32, p, p]),
+        "attn_cross": (st, [p, p, p, i64, p, i64, p, p, p, p]),
         "attn_rope": (st, [p, p, i64, i32, p, i64, i32, p, i64, p, i64, i32, p, i64, i32, p]),
         "attn_append_kv_rope": (st, [p, p, p, p, i64, p, i64, p, i64, p, p, p]),
         "attn_pages_scratch": (i64, [i64]),
@@ -686,6 +688,63 @@ class RaggedPlan(Plan):
 
     append_kv_rope = append_kv4 = decode_kv4 = key_weights = key_weights_kv4 = evict_kv = evict_kv4 = kv4_shape = append_kv
     kv_lens = property(append_kv)
+
+
+class CrossPlan(Plan):
+    """A planned batch of cross attention (see attn_plan_cross): sequence b's query
+    rows, [qo_indptr[b], qo_indptr[b + 1]), over all of its encoder states, rows
+    [kv_start[b], kv_start[b] + kv_len[b]) of k and v.  qo_indptr, kv_start, kv_len:
+    host int arrays; kv_rows: rows of k and v."""
+
+    def __init__(self, qo_indptr, kv_start, kv_len, kv_rows: int, num_qo_heads: int, num_kv_heads: int, head_dim: int,
+                 sm_scale: Optional[float] = None, num_sms: int = 0, device="cuda", stream=None,
+                 workspace: Optional[torch.Tensor] = None):
+        lib = load_library()
+        self._handle = None
+        qo, start, lens = _i32_host(qo_indptr), _i32_host(kv_start), _i32_host(kv_len)
+        self.batch = max(0, len(qo) - 1)
+        if len(start) != self.batch or len(lens) != self.batch:
+            raise ValueError("kv_start and kv_len must have one entry per sequence")
+        self.num_qo_heads, self.num_kv_heads, self.head_dim = num_qo_heads, num_kv_heads, head_dim
+        self.sm_scale = float(sm_scale) if sm_scale is not None else head_dim ** -0.5
+        self.total_rows, self.kv_rows = (int(qo[-1]) if len(qo) else 0), int(kv_rows)
+        handle, ws_bytes = ctypes.c_void_p(), ctypes.c_size_t()
+        _check("attn_plan_cross", lib.attn_plan_cross(
+            qo.ctypes.data, start.ctypes.data, lens.ctypes.data, self.batch, self.kv_rows, num_qo_heads, num_kv_heads,
+            head_dim, self.sm_scale, int(num_sms), ctypes.byref(handle), ctypes.byref(ws_bytes)))
+        self._handle = handle
+        need = max(int(ws_bytes.value), 256)
+        if (workspace is not None and workspace.is_cuda and workspace.dtype == torch.uint8
+                and workspace.numel() >= need and workspace.data_ptr() % 256 == 0):
+            self.workspace = workspace
+        else:
+            self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        with torch.cuda.device(self.workspace.device):
+            _check("attn_plan_bind_workspace", lib.attn_plan_bind_workspace(
+                self._handle, _ptr(self.workspace), self.workspace.numel(), _stream_ptr(stream)))
+
+    def attend(self, q, k, v, sinks=None, out=None, lse=None, stream=None):
+        """q bf16 [rows, Hq, D]; k, v bf16 [kv_rows, Hkv, D], rows possibly apart (the
+        halves of a fused projection).  Returns (out, lse); lse is written where given."""
+        dev, H, D = self.workspace.get_device(), self.num_qo_heads, self.head_dim
+        shape, kv = (self.total_rows, H, D), (self.kv_rows, self.num_kv_heads, D)
+        out = _empty_on(stream, shape, torch.bfloat16, self.workspace.device) if out is None else out
+        _check_cuda(dev, "q", q, torch.bfloat16, shape)
+        _check_cuda(dev, "out", out, torch.bfloat16, shape)
+        if sinks is not None:
+            _check_cuda(dev, "sinks", sinks, torch.float32, (H,))
+        if lse is not None:
+            _check_cuda(dev, "lse", lse, torch.float32, (self.total_rows, H))
+        _launch_on(dev, stream, "attn_cross", self._handle, _ptr(q), _ptr(k), _row_stride(dev, "k", k, *kv), _ptr(v),
+                   _row_stride(dev, "v", v, *kv), _ptr(sinks), _ptr(out), _ptr(lse))
+        return out, lse
+
+    def _refuse(self, *args, **kwargs):
+        raise TypeError("a cross-attention plan has no KV cache; use attend(q, k, v, ...)")
+
+    decode = prefill = append_kv = append_kv_rope = append_kv4 = decode_kv4 = key_weights = key_weights_kv4 = evict_kv = \
+        evict_kv4 = kv4_shape = _refuse
+    kv_lens = property(_refuse)
 
 
 class GraphPlan(Plan):

@@ -137,7 +137,7 @@ extern "C" attn_status attn_plan_bind_workspace(attn_plan_t plan, void* workspac
 
 extern "C" attn_status attn_decode(attn_plan_t plan, const void* q, const void* kv_cache,
                                    const float* sinks, void* out, float* lse, void* stream) {
-    if (plan && plan->graph) return ATTN_ERR_INVALID_ARG;   // attn_decode_graph
+    if (plan && (plan->graph || plan->cross)) return ATTN_ERR_INVALID_ARG;   // attn_decode_graph, attn_cross
     if (plan && plan->bound && plan->units.empty()) return ATTN_OK;
     attn_status st = check_launch(plan, q, kv_cache, out);
     if (st != ATTN_OK) return st;
@@ -206,7 +206,7 @@ extern "C" attn_status attn_prefill(attn_plan_t plan, const void* q, const void*
 extern "C" attn_status attn_prefill_ragged(attn_plan_t plan, const void* q, const void* k, const void* v,
                                            const float* sinks, void* out, float* lse, void* stream) {
     if (!plan) return ATTN_ERR_INVALID_ARG;
-    if (!plan->ragged) return ATTN_ERR_INVALID_ARG;   // paged plans go through attn_prefill
+    if (!plan->ragged || plan->cross) return ATTN_ERR_INVALID_ARG;   // paged plans go through attn_prefill
     if (plan->bound && plan->items.empty()) return ATTN_OK;
     attn_status st = check_launch(plan, q, k, out);
     if (st != ATTN_OK) return st;
@@ -229,6 +229,68 @@ extern "C" attn_status attn_prefill_ragged(attn_plan_t plan, const void* q, cons
     }
     return attn::launch_prefill(plan, plan->q_map_prefill, plan->kv_map_prefill, plan->v_map_prefill,
                                 plan->o_map_prefill, sinks, out, lse, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+// Rows of K or V [kv_rows][Hkv][D], `stride` elements apart, in boxes of box_rows
+// tokens x 64 dims of one KV head, as make_ragged_map.
+bool make_cross_map(void* map, const void* x, int64_t stride, const attn_plan_s* p, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)p->D, (cuuint64_t)p->Hkv, (cuuint64_t)p->kv_tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)p->D * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+    cuuint32_t elem[3] = {1, 1, 1};
+    return fn(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+              const_cast<void*>(x), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" attn_status attn_cross(attn_plan_t plan, const void* q, const void* k, int64_t k_stride, const void* v,
+                                  int64_t v_stride, const float* sinks, void* out, float* lse, void* stream) {
+    if (!plan || !plan->cross) return ATTN_ERR_INVALID_ARG;
+    if (!plan->bound) return ATTN_ERR_NOT_BOUND;
+    if (plan->info.total_qo_rows == 0) return ATTN_OK;
+    auto aligned = [](const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
+    if (!q || !out || !aligned16(q) || !aligned16(out) || !aligned(sinks, 4) || !aligned(lse, 4)) return ATTN_ERR_INVALID_ARG;
+    const void* x[2] = {k, v};
+    const int64_t stride[2] = {k_stride, v_stride};
+    for (int i = 0; i < 2 && plan->kv_tokens > 0; ++i) {
+        if (!x[i] || !aligned16(x[i]) || stride[i] % 8 != 0 || stride[i] < (int64_t)plan->Hkv * plan->D)
+            return ATTN_ERR_INVALID_ARG;
+        if (stride[i] >= int64_t{1} << 39) return ATTN_ERR_UNSUPPORTED;   // a tensor map's strides
+    }
+    for (int i = 0; i < 2 && plan->kv_tokens > 0; ++i) {
+        if (plan->cross_ptrs[i] == x[i] && plan->cross_strides[i] == stride[i]) continue;
+        plan->cross_ptrs[i] = nullptr;
+        if (!make_cross_map(plan->cross_maps[i], x[i], stride[i], plan, attn::kCrossKeys) ||
+            !make_cross_map(plan->cross_maps[2 + i], x[i], stride[i], plan, 16) ||
+            !make_cross_map(i ? plan->v_map_prefill : plan->kv_map_prefill, x[i], stride[i], plan, attn::kPrefillKeys))
+            return ATTN_ERR_CUDA;
+        plan->cross_ptrs[i] = x[i];
+        plan->cross_strides[i] = stride[i];
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!plan->items.empty()) {
+        const int G = plan->Hq / plan->Hkv, box = attn::cross_out_box(G), heads = box > 0 ? box : 1;
+        if (plan->q_map_prefill_ptr != q) {
+            if (!make_q_map(plan->q_map_prefill, q, plan, attn::kPrefillRows / G, G)) return ATTN_ERR_CUDA;
+            plan->q_map_prefill_ptr = q;
+        }
+        if (plan->o_map_prefill_ptr != out) {
+            if (!make_q_map(plan->o_map_prefill, out, plan, attn::kPrefillOutRows / heads, heads)) return ATTN_ERR_CUDA;
+            plan->o_map_prefill_ptr = out;
+        }
+        if (attn_status st = attn::launch_prefill(plan, plan->q_map_prefill, plan->kv_map_prefill, plan->v_map_prefill,
+                                                  plan->o_map_prefill, sinks, out, lse, s);
+            st != ATTN_OK)
+            return st;
+    }
+    return attn::launch_cross_few(plan, q, sinks, out, lse, s);
 }
 
 extern "C" attn_status attn_merge_states(const void* va, const float* lsea, const void* vb,

@@ -59,6 +59,17 @@ struct PrefillItem {
 };
 static_assert(sizeof(PrefillItem) == 48, "prefill item is 12 int32");
 
+// Cross attention.  A unit of the kernel for few rows is a DecodeUnit too: up to
+// 16, 32 or 64 (row, query head) pairs of a sequence and KV head (pair p is row
+// q_row + p / G, head kv_head * G + p % G; pairs head0 .. head0 + n_heads - 1) and a
+// chunk of its keys, which are rows page_base + [tok_begin, tok_end) of k and v.
+// Units of 16 pairs come first in the list, then those of 32 and of 64.
+constexpr int kCrossKeys = 64;            // keys of a stage; chunks are whole stages
+constexpr int kCrossMinChunk = 4;         // stages: never split a sequence finer than 256 keys
+// A unit of many rows is a PrefillItem whose head slots hold pairs (prefill.cu).
+// Heads of an output box of 32 pairs, 0 where such a stripe is no box.
+constexpr int cross_out_box(int G) { return 32 % G == 0 ? G : G % 32 == 0 ? 32 : 0; }
+
 // One request of a paged plan, for the kernels that work on whole requests
 // (key weights, eviction).
 struct RequestInfo {
@@ -139,6 +150,7 @@ struct ListLayout {
 // CTAs of the decode kernel resident per SM for a head dim (matches its
 // shared-memory footprint); defined next to the kernel.
 int decode_ctas_per_sm(int head_dim);
+int cross_ctas_per_sm(int head_dim);   // likewise, of the cross-attention kernel for few rows
 
 // SM count of the current device, queried once per device (thread-safe).
 bool current_sm_count(int32_t* out);
@@ -173,6 +185,8 @@ struct attn_plan_s {
     int32_t num_sms = 0;
     const int32_t* page_table = nullptr;  // device, borrowed
     bool ragged = false;                  // contiguous K / V (attn_plan_ragged), no page table
+    bool cross = false;                   // attn_plan_cross (then `ragged` is set too)
+    int32_t cross_units[3] = {0, 0, 0};   // cross: units of 16, 32 and 64 pairs in `units`
     bool graph = false;                   // attn_graph_plan: decode work list built on the device
                                           // (batch = max batch; n_partials / n_groups = capacities)
     int64_t kv_tokens = 0;                // ragged: rows of K and V (kv_indptr[batch])
@@ -213,4 +227,13 @@ struct attn_plan_s {
     const void* v_map_prefill_ptr = nullptr;
     alignas(64) unsigned char o_map_prefill[128];   // out, laid out like q, 32-row boxes
     const void* o_map_prefill_ptr = nullptr;
+    // Cross: K and V in boxes of a stage and of 16 keys, for the addresses and strides they were made for.
+    alignas(64) unsigned char cross_maps[4][128];
+    const void* cross_ptrs[2] = {nullptr, nullptr};
+    int64_t cross_strides[2] = {0, 0};
 };
+
+namespace attn {
+// Orders plan->items longest first and deals them out to the persistent prefill CTAs.
+void deal_prefill_items(attn_plan_s* plan);
+}  // namespace attn

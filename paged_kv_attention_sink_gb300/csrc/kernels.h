@@ -99,6 +99,10 @@ attn_status launch_rope(const RopeTable& t, bool inter, bool inverse, const int3
 attn_status launch_append_kv_rope(attn_plan_s* plan, const RopeTable& t, bool inter, const int32_t* positions,
                                   const RopeRows& q, const RopeRows& k, const RopeRows& v, cudaStream_t stream);
 
+// Cross attention of few rows (cross.cu), from plan->cross_maps; many rows: launch_prefill.
+attn_status launch_cross_few(attn_plan_s* plan, const void* q, const float* sinks, void* out, float* lse,
+                             cudaStream_t stream);
+
 // Page management (pages.cu).
 constexpr int kPagePoolsPerLaunch = 64;
 struct PagePools {

@@ -59,7 +59,7 @@ extern "C" attn_status attn_decode_noalloc(attn_plan_t plan, const void* q, cons
     if (!plan) return ATTN_ERR_INVALID_ARG;
     // A graph plan's work list is built on the device (attn_decode_graph);
     // its host list is empty, so it must not pass for an empty batch.
-    if (plan->graph) return ATTN_ERR_INVALID_ARG;
+    if (plan->graph || plan->cross) return ATTN_ERR_INVALID_ARG;   // (and a cross plan's units are attn_cross's)
     if (plan->units.empty()) return ATTN_OK;
     if (!q || !kv_cache || !out) return ATTN_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(kv_cache) |
@@ -86,7 +86,7 @@ extern "C" attn_status attn_decode_noalloc(attn_plan_t plan, const void* q, cons
 }
 
 extern "C" attn_status attn_decode_noalloc_device_error(attn_plan_t plan, int32_t* code, void* stream) {
-    if (!plan || !code || plan->graph) return ATTN_ERR_INVALID_ARG;
+    if (!plan || !code || plan->graph || plan->cross) return ATTN_ERR_INVALID_ARG;
     const attn::WorkspaceLayout& L = plan->layout;
     if (L.total > kNoAllocScratchBytes) return ATTN_ERR_WORKSPACE_TOO_SMALL;
     unsigned char* scratch = scratch_on_current_device();

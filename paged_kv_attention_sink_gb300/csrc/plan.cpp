@@ -50,6 +50,38 @@ bool current_sm_count(int32_t* out) {
     return true;
 }
 
+// Persistent prefill CTAs: greedy longest-processing-time assignment of the items
+// (longest first, each to the least-loaded CTA); each CTA's items are stored
+// contiguously, longest first.
+void deal_prefill_items(attn_plan_s* plan) {
+    std::stable_sort(plan->items.begin(), plan->items.end(),
+                     [](const PrefillItem& a, const PrefillItem& b) {
+                         return a.n_kv_tiles * a.n_heads > b.n_kv_tiles * b.n_heads;
+                     });
+    if (!plan->items.empty()) {
+        const int ctas = (int)std::min<int64_t>(plan->num_sms, (int64_t)plan->items.size());
+        std::vector<std::vector<PrefillItem>> per(ctas);
+        std::vector<std::pair<int64_t, int>> heap;   // (load, cta), min-heap
+        for (int c = 0; c < ctas; ++c) heap.push_back({0, c});
+        auto cmp = [](const std::pair<int64_t, int>& x, const std::pair<int64_t, int>& y) { return x > y; };
+        std::make_heap(heap.begin(), heap.end(), cmp);
+        for (const PrefillItem& it : plan->items) {
+            std::pop_heap(heap.begin(), heap.end(), cmp);
+            auto& least = heap.back();
+            per[least.second].push_back(it);
+            least.first += (int64_t)it.n_kv_tiles * it.n_heads + 1;   // +1: per-item overhead
+            std::push_heap(heap.begin(), heap.end(), cmp);
+        }
+        plan->items.clear();
+        plan->item_off.assign(1, 0);
+        for (int c = 0; c < ctas; ++c) {
+            plan->items.insert(plan->items.end(), per[c].begin(), per[c].end());
+            plan->item_off.push_back((int32_t)plan->items.size());
+        }
+        plan->prefill_ctas = ctas;
+    }
+}
+
 }  // namespace attn
 
 namespace {
@@ -222,35 +254,7 @@ attn_status build_plan(bool ragged, const int32_t* qo_indptr, const int32_t* kv_
             }
         }
     }
-    // Persistent prefill CTAs: greedy longest-processing-time assignment of
-    // the items (longest first, each to the least-loaded CTA); each CTA's items
-    // are stored contiguously, longest first.
-    std::stable_sort(plan->items.begin(), plan->items.end(),
-                     [](const PrefillItem& a, const PrefillItem& b) {
-                         return a.n_kv_tiles * a.n_heads > b.n_kv_tiles * b.n_heads;
-                     });
-    if (!plan->items.empty()) {
-        const int ctas = (int)std::min<int64_t>(num_sms, (int64_t)plan->items.size());
-        std::vector<std::vector<PrefillItem>> per(ctas);
-        std::vector<std::pair<int64_t, int>> heap;   // (load, cta), min-heap
-        for (int c = 0; c < ctas; ++c) heap.push_back({0, c});
-        auto cmp = [](const std::pair<int64_t, int>& x, const std::pair<int64_t, int>& y) { return x > y; };
-        std::make_heap(heap.begin(), heap.end(), cmp);
-        for (const PrefillItem& it : plan->items) {
-            std::pop_heap(heap.begin(), heap.end(), cmp);
-            auto& least = heap.back();
-            per[least.second].push_back(it);
-            least.first += (int64_t)it.n_kv_tiles * it.n_heads + 1;   // +1: per-item overhead
-            std::push_heap(heap.begin(), heap.end(), cmp);
-        }
-        plan->items.clear();
-        plan->item_off.assign(1, 0);
-        for (int c = 0; c < ctas; ++c) {
-            plan->items.insert(plan->items.end(), per[c].begin(), per[c].end());
-            plan->item_off.push_back((int32_t)plan->items.size());
-        }
-        plan->prefill_ctas = ctas;
-    }
+    deal_prefill_items(plan.get());
 
     // ---- KV append: cache position of every query row (the row's token is
     // appended at t = kv_len - qo_len + i): page-table slot and row in page.

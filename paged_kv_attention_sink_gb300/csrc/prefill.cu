@@ -41,6 +41,13 @@
 // TMEM (512 columns): S0 S1 (128 each), O0 O1 (D each, plus at D = 64 the
 // 16 row-sum columns), and at D = 64 P0 P1 (keys 0..95, 48 columns each); at
 // D = 128 P aliases the first half of S.
+//
+// Cross attention of many rows (kCross) is the same kernel over contiguous K and
+// V without a causal mask.  There is no order among its rows, so a head slot's 128
+// TMEM lanes hold (row, head) pairs: 128 / G rows with all G query heads of the KV
+// head (a box of G heads x 128 / G rows), whatever G is, and an item's two slots
+// are two such row blocks.  With slots of one head each, as above, G = 1 would
+// leave the second slot idle.
 // Every wait is bounded; a timeout sets the device error word.
 #include <cuda.h>
 
@@ -121,6 +128,9 @@ struct PrefillArgs {
     int32_t* err;
     int32_t Hq, Hkv, P, num_pages, causal;
     float scale_log2;
+    int32_t G;           // kCross: query heads of a KV head,
+    int32_t slot_rows;   // rows of a head slot,
+    int32_t boxes;       // whether a softmax warp's 32 pairs are a box of o_map
 };
 
 struct Bars {
@@ -136,7 +146,10 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
 // kRagged: K and V are contiguous [tokens][Hkv][D] arrays (kv_map over K,
 // v_map over V) instead of the paged HND pool (kv_map; v_map unused), and an
 // item's page_base is its first token.
-template <int D, bool kRagged>
+// kCross: such arrays, and head slots of (row, head) pairs: slot i of an item holds
+// rows q_row0 + i * slot_rows on, its first n_rows (i = 0) or reserved0 (i = 1)
+// pairs; n_heads is then the number of slots.
+template <int D, bool kRagged, bool kCross = false>
 __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
 prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                          const __grid_constant__ CUtensorMap kv_map,
@@ -202,6 +215,15 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
     if (warp == 1) {
         ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::kTmemCols);
         ptx::tmem_relinquish();
+    }
+    if (kCross && warp == 3) {
+        // Lanes past the slot's pairs (128 is no multiple of G): no box writes them.
+        const int used = a.slot_rows * a.G;
+        for (int idx = lane; idx < C::kQBufs * 2 * (D / 64) * (128 - used) * 8; idx += 32) {
+            const int atom = idx / ((128 - used) * 8), x = idx - atom * (128 - used) * 8;
+            *reinterpret_cast<uint4*>(smem + C::kOffQ + atom * C::kAtom + used * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+        }
+        ptx::fence_proxy_async_smem();
     }
     if (C::kSplitP && warp == 2) {
         // The ones block of the PV B operand: 16 key rows x 64 N values, N
@@ -274,11 +296,13 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                     break;
                 }
                 if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(B.q_full + 8 * qb, it.n_heads * C::kTile);
+                    const int slot_bytes = kCross ? a.slot_rows * a.G * D * 2 : C::kTile;
+                    ptx::mbar_arrive_expect_tx(B.q_full + 8 * qb, it.n_heads * slot_bytes);
                     for (int i = 0; i < it.n_heads; ++i)
                         for (int c = 0; c < D / 64; ++c)
                             ptx::tma_load_3d(sbase + C::kOffQ + (qb * 2 + i) * C::kTile + c * C::kAtom, &q_map,
-                                             B.q_full + 8 * qb, c * 64, it.head0 + i, it.q_row0);
+                                             B.q_full + 8 * qb, c * 64, kCross ? it.head0 : it.head0 + i,
+                                             kCross ? it.q_row0 + i * a.slot_rows : it.q_row0);
                 }
             }
             const int valid = min(kPrefillKeys, it.kv_len - j * kPrefillKeys);
@@ -505,6 +529,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
         // first 64 bytes of a 128-byte row, 16-byte chunks swizzled by the
         // row (K-major SW128 A operand).
         const uint32_t pb_row = sbase + C::kOffPb + i * C::kAtom + (r >> 3) * 1024 + (r & 7) * 128;
+        const int cross_row = kCross ? r / a.G : 0, cross_head = kCross ? r - cross_row * a.G : 0;
         const float sl2 = a.scale_log2;
         const float poly_a = sl2 * exp2poly::kInvRange;   // scale of the FMA-pipe pairs' argument
         int hj = 0;
@@ -536,7 +561,10 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
         auto epilogue = [&]() -> bool {
             if (!wait_all(B.o_done + 8 * i, (hj - 1) & 1)) return false;   // its last PV
             const PrefillItem ei = a.items[e_item];
-            const int e_row0 = ei.q_row0, e_head = ei.head0 + i, e_rows = ei.n_rows;
+            // This thread's row and head, and the slot's valid rows (kCross: pairs).
+            const int e_rows = kCross && i ? ei.reserved0 : ei.n_rows;
+            const int e_row = kCross ? ei.q_row0 + i * a.slot_rows + cross_row : ei.q_row0 + r;
+            const int e_head = kCross ? ei.head0 + cross_head : ei.head0 + i;
             ptx::tc_fence_after();
             float lt = e_l;
             if constexpr (C::kSplitP) {   // the keys' part of the row sum, next to O
@@ -546,7 +574,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                 lt += __uint_as_float(v[0]);
             }
             const float inv = lt > 0.f ? 1.f / lt : 0.f;
-            if (C::kSplitP && quad * 32 + 32 <= e_rows) {
+            if (C::kSplitP && quad * 32 + 32 <= e_rows && (!kCross || a.boxes)) {
                 if (lane == 0) ptx::bulk_wait_read_all();   // the stripe's previous store has read it
                 __syncwarp();
 #pragma unroll
@@ -568,14 +596,14 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    ptx::tma_store_3d(&o_map, st_stripe, 0, e_head, e_row0 + quad * 32);
+                    ptx::tma_store_3d(&o_map, st_stripe, 0, e_head, e_row);   // lane 0: the stripe's first
                     ptx::bulk_commit_group();
                 }
             } else {
                 // Rows of a ragged last tile (a box would overwrite the next
                 // request's rows) and D = 128: per-thread stores.
                 const bool store = r < e_rows;
-                __nv_bfloat16* orow = a.out + ((size_t)(e_row0 + r) * a.Hq + e_head) * D;
+                __nv_bfloat16* orow = a.out + ((size_t)e_row * a.Hq + e_head) * D;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t v[32];
@@ -594,7 +622,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                     }
                 }
             }
-            if (r < e_rows && a.lse) a.lse[(size_t)(e_row0 + r) * a.Hq + e_head] = e_lse;
+            if (r < e_rows && a.lse) a.lse[(size_t)e_row * a.Hq + e_head] = e_lse;
             return true;
         };
         if (i == 1 && lane == 0) ptx::mbar_arrive(other_turn);
@@ -605,7 +633,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
         for (int item = item_begin; ok && item < item_end; ++item) {
             const PrefillItem it = a.items[item];
             if (i >= it.n_heads) continue;
-            const int head = it.head0 + i;
+            const int head = it.head0 + (kCross ? cross_head : i);
             const int n = it.n_kv_tiles;
             // l: row sum of the bf16-rounded P that the PV MMA consumes (it
             // normalises O); le: the same sum of the unrounded P (it gives lse).
@@ -811,11 +839,11 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
     }
 }
 
-template <int D, bool kRagged>
+template <int D, bool kRagged, bool kCross = false>
 cudaError_t launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& om,
                    const PrefillArgs& args, int grid, cudaStream_t stream) {
     using C = PrefillCfg<D>;
-    auto kernel = prefill_sink_attn_kernel<D, kRagged>;
+    auto kernel = prefill_sink_attn_kernel<D, kRagged, kCross>;
     static std::atomic<bool> configured[kMaxDevices];
     cudaError_t e = once_per_device(configured, [&] {
         cudaFuncAttributes fa;
@@ -849,6 +877,9 @@ attn_status launch_prefill(attn_plan_s* plan, const void* q_map, const void* kv_
     a.num_pages = plan->num_pages;
     a.causal = plan->causal;
     a.scale_log2 = plan->sm_scale * kLog2e;
+    a.G = plan->Hq / plan->Hkv;
+    a.slot_rows = kPrefillRows / a.G;
+    a.boxes = cross_out_box(a.G) > 0;
     const CUtensorMap& qm = *static_cast<const CUtensorMap*>(q_map);
     const CUtensorMap& km = *static_cast<const CUtensorMap*>(kv_map);
     const CUtensorMap& vm = *static_cast<const CUtensorMap*>(v_map ? v_map : kv_map);
@@ -857,7 +888,10 @@ attn_status launch_prefill(attn_plan_s* plan, const void* q_map, const void* kv_
     // kernel holds all of an SM's TMEM).
     const int grid = plan->prefill_ctas;
     cudaError_t e;
-    if (plan->ragged)
+    if (plan->cross)
+        e = plan->D == 64 ? launch<64, true, true>(qm, km, vm, om, a, grid, stream)
+                          : launch<128, true, true>(qm, km, vm, om, a, grid, stream);
+    else if (plan->ragged)
         e = plan->D == 64 ? launch<64, true>(qm, km, vm, om, a, grid, stream)
                           : launch<128, true>(qm, km, vm, om, a, grid, stream);
     else
