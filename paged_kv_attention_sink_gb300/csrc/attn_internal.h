@@ -60,13 +60,26 @@ struct PrefillItem {
 static_assert(sizeof(PrefillItem) == 48, "prefill item is 12 int32");
 
 // Cross attention.  A unit of the kernel for few rows is a DecodeUnit too: up to
-// 16, 32 or 64 (row, query head) pairs of a sequence and KV head (pair p is row
+// 16 or 32 (row, query head) pairs of a sequence and KV head (pair p is row
 // q_row + p / G, head kv_head * G + p % G; pairs head0 .. head0 + n_heads - 1) and a
 // chunk of its keys, which are rows page_base + [tok_begin, tok_end) of k and v.
-// Units of 16 pairs come first in the list, then those of 32 and of 64.
+// Units of 16 pairs come first in the list, then those of 32.
+constexpr int kCrossBlock = 32;           // pairs of a unit at most
 constexpr int kCrossKeys = 64;            // keys of a stage; chunks are whole stages
 constexpr int kCrossMinChunk = 4;         // stages: never split a sequence finer than 256 keys
-// A unit of many rows is a PrefillItem whose head slots hold pairs (prefill.cu).
+// A unit of many rows is a PrefillItem whose head slots hold pairs (prefill.cu): its
+// keys are rows [page_base, page_base + kv_len), a chunk of the sequence's where
+// pos0 >= 0 (the first of its partial states, 16 pairs each); reserved1: which chunk.
+// The partial states of the chunks of up to 32 pairs are joined by a CTA of
+// cross_merge_kernel.
+struct CrossMerge {
+    int32_t q_row0, head0;   // row and first head of pair 0
+    int32_t pair0, pairs;    // the record's pairs, pair0 on
+    int32_t partial0;        // chunk c's states: partial0 + c * stride
+    int32_t n_chunks, stride;
+    int32_t reserved;
+};
+static_assert(sizeof(CrossMerge) == 32, "cross merge is one sector");
 // Heads of an output box of 32 pairs, 0 where such a stripe is no box.
 constexpr int cross_out_box(int G) { return 32 % G == 0 ? G : G % 32 == 0 ? 32 : 0; }
 
@@ -186,7 +199,9 @@ struct attn_plan_s {
     const int32_t* page_table = nullptr;  // device, borrowed
     bool ragged = false;                  // contiguous K / V (attn_plan_ragged), no page table
     bool cross = false;                   // attn_plan_cross (then `ragged` is set too)
-    int32_t cross_units[3] = {0, 0, 0};   // cross: units of 16, 32 and 64 pairs in `units`
+    int32_t cross_units[2] = {0, 0};      // cross: units of 16 and of 32 pairs in `units`
+    bool cross_chunks = false;            // cross: some items have a chunk of the keys
+    int32_t cross_merges = 0;             // cross: CrossMerge records, held in append_slots
     bool graph = false;                   // attn_graph_plan: decode work list built on the device
                                           // (batch = max batch; n_partials / n_groups = capacities)
     int64_t kv_tokens = 0;                // ragged: rows of K and V (kv_indptr[batch])

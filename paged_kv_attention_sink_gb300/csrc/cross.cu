@@ -1,4 +1,4 @@
-// Cross attention of few rows: up to 64 (row, query head) pairs of a sequence and
+// Cross attention of few rows: up to 32 (row, query head) pairs of a sequence and
 // KV head over a chunk of the sequence's keys, which are rows of contiguous
 // K and V [rows][Hkv][D] (the prefill kernel takes sequences of many pairs).
 //
@@ -12,19 +12,17 @@
 //    swizzled; the last stage in boxes of 16, so that no more than 15 keys past the
 //    end are read), full and empty barriers between it and the others.
 //  * The four warps are kTiles m16 tiles of pairs times 4 / kTiles parts of a
-//    stage's keys: with 16 pairs each warp takes 16 of the 64 keys, with 64 pairs
-//    each warp has its own pairs and takes all keys.  A warp's state (max, sums, O)
-//    stays in registers over the chunk.
-//  * S = Q K^T and O += P V are mma.sync m16n8k16.  With 16 to 64 pairs there are 16
-//    to 64 flop per byte of K and V, 100 to 400 TFLOP/s at full HBM speed, which
-//    this path gives; tcgen05's tiles are 64 or 128 pairs high, and its S and P would
-//    go through tensor memory for every 64 keys.
+//    stage's keys: with 16 pairs each warp takes 16 of the 64 keys, with 32 pairs
+//    32.  A warp's state (max, sums, O) stays in registers over the chunk.
+//  * S = Q K^T and O += P V are mma.sync m16n8k16: 16 to 32 flop per byte of K and V,
+//    100 to 200 TFLOP/s at full HBM speed.
 //  * P is rounded to bf16 and O normalised by the sum of that rounded P, lse taken
 //    from the unrounded sum, as in the other attention kernels.
 //  * Keys past the end: scores -inf, and V's fragments zeroed in registers, for
 //    what lies there may be NaN.
-//  * A chunk's state goes to the workspace, and the last CTA of a group (atomic
-//    ticket, no waiting) merges the chunks.
+//  * A chunk's state goes to the workspace; a small kernel joins the chunks.  (With
+//    the last CTA of a sequence joining them, 50 chunks of 32 pairs took some 15 us,
+//    one CTA reading after the other; joined by many CTAs, 4.)
 #include <cuda.h>
 
 #include "attn_internal.h"
@@ -62,7 +60,6 @@ struct CrossArgs {
     const float* sinks;
     float* part_o;
     float* part_lse;
-    int32_t* counters;
     int32_t* err;
     int32_t Hq, G;
     float scale_log2;
@@ -75,6 +72,50 @@ __device__ __forceinline__ void store_bf16x4(__nv_bfloat16* dst, float4 v) {
     w.x = ptx::pack_bf16x2(v.x, v.y);
     w.y = ptx::pack_bf16x2(v.z, v.w);
     *reinterpret_cast<uint2*>(dst) = w;
+}
+
+// The chunks' states of one pair (`state`: the first chunk's, `stride` apart), 4 dims.
+template <int D>
+__device__ __forceinline__ void join_chunks(const CrossArgs& a, size_t state, size_t stride, int n_chunks, int row, int head,
+                                            int d) {
+    constexpr int kBatch = 8;   // chunks whose loads are in flight together
+    float M = -INFINITY, W = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = 0; c0 < n_chunks; c0 += kBatch) {
+        float lc[kBatch];
+        float4 oc[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const size_t at = state + (size_t)(c0 + k) * stride;
+            const bool in = c0 + k < n_chunks;
+            lc[k] = in ? __ldcg(a.part_lse + at) : -INFINITY;
+            oc[k] = in ? __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float mb = M;
+        bool nan = false;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            mb = fmaxf(mb, lc[k]);
+            nan |= lc[k] != lc[k];
+        }
+        if (mb == -INFINITY && !nan) continue;
+        const float sc = M == -INFINITY ? 0.f : ptx::ex2(M - mb);
+        W *= sc;
+        acc = make_float4(acc.x * sc, acc.y * sc, acc.z * sc, acc.w * sc);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const float w = lc[k] == -INFINITY ? 0.f : ptx::ex2(lc[k] - mb);
+            W += w;
+            acc.x += w * oc[k].x;
+            acc.y += w * oc[k].y;
+            acc.z += w * oc[k].z;
+            acc.w += w * oc[k].w;
+        }
+        M = mb;
+    }
+    const float inv = W > 0.f ? 1.f / W : W;
+    store_bf16x4(a.out + ((size_t)row * a.Hq + head) * D + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if (d == 0 && a.lse) a.lse[(size_t)row * a.Hq + head] = (W == 0.f ? -INFINITY : M + log2f(W)) * kLn2;
 }
 
 // k_map, v_map: boxes of 64 keys; k_tail, v_tail: of 16.
@@ -90,7 +131,7 @@ cross_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = ptx::smem_u32(smem), full = sbase + C::kOffBar, empty = full + 8 * C::kStages;
     float* state = reinterpret_cast<float*>(smem + C::kOffState);   // [warp][m | l | e][16]
-    volatile int* flags = reinterpret_cast<volatile int*>(state + 3 * kCrossWarps * 16);   // last, abort
+    volatile int* flags = reinterpret_cast<volatile int*>(state + 3 * kCrossWarps * 16);   // [1]: gave up
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const DecodeUnit u = a.units[blockIdx.x];         // the plan's own list
@@ -361,60 +402,6 @@ cross_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             if (d == 0) a.part_lse[slot] = lse2;
         }
     }
-    if (u.n_chunks == 1) return;
-
-    // Split keys: the last chunk to get here merges them all, in order.
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) flags[0] = atomicAdd(&a.counters[u.group], 1) == u.n_chunks - 1;
-    __syncthreads();
-    if (!flags[0]) return;
-    __threadfence();
-    constexpr int kBatch = 8;   // chunks whose loads are in flight together
-    for (int idx = tid; idx < items; idx += kCrossThreads) {
-        const int p = idx / (D / 4), d = (idx % (D / 4)) * 4;
-        float M = -INFINITY, W = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c0 = 0; c0 < u.n_chunks; c0 += kBatch) {
-            float lc[kBatch];
-            float4 oc[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const size_t slot = ((size_t)u.partial0 + (size_t)(c0 + k) * kTiles) * kMaxSliceHeads + p;
-                const bool in = c0 + k < u.n_chunks;
-                lc[k] = in ? __ldcg(a.part_lse + slot) : -INFINITY;
-                oc[k] = in ? __ldcg(reinterpret_cast<const float4*>(a.part_o + slot * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            float mb = M;
-            bool nan = false;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                mb = fmaxf(mb, lc[k]);
-                nan |= lc[k] != lc[k];
-            }
-            if (mb == -INFINITY && !nan) continue;
-            const float sc = M == -INFINITY ? 0.f : ptx::ex2(M - mb);
-            W *= sc;
-            acc = make_float4(acc.x * sc, acc.y * sc, acc.z * sc, acc.w * sc);
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const float w = lc[k] == -INFINITY ? 0.f : ptx::ex2(lc[k] - mb);
-                W += w;
-                acc.x += w * oc[k].x;
-                acc.y += w * oc[k].y;
-                acc.z += w * oc[k].z;
-                acc.w += w * oc[k].w;
-            }
-            M = mb;
-        }
-        const float inv = W > 0.f ? 1.f / W : W;
-        int row, head;
-        row_head(p, row, head);
-        store_bf16x4(a.out + ((size_t)row * a.Hq + head) * D + d,
-                     make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-        if (d == 0 && a.lse) a.lse[(size_t)row * a.Hq + head] = (W == 0.f ? -INFINITY : M + log2f(W)) * kLn2;
-    }
-    if (tid == 0) a.counters[u.group] = 0;   // ready for the next launch
 }
 
 template <int D, int kTiles>
@@ -429,18 +416,36 @@ cudaError_t launch(const CUtensorMap* maps, const CrossArgs& args, int units, cu
                             maps[3], args);
 }
 
+// Joins the chunks' states of split keys, this kernel's and the prefill kernel's.  A
+// CTA has 32 pairs of a record, a thread 4 dims of one of them at a time.
+constexpr int kMergeThreads = 256, kMergePairs = 32;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads)
+cross_merge_kernel(const CrossMerge* merges, const CrossArgs a) {
+    const CrossMerge m = merges[blockIdx.x];   // the plan's own list
+    ptx::grid_dependency_wait();
+    ptx::grid_dependents_go();
+    for (int idx = threadIdx.x; idx < m.pairs * (D / 4); idx += kMergeThreads) {
+        const int p = m.pair0 + idx / (D / 4), d = (idx % (D / 4)) * 4;
+        join_chunks<D>(a, (size_t)m.partial0 * kMaxSliceHeads + idx / (D / 4), (size_t)m.stride * kMaxSliceHeads, m.n_chunks,
+                       m.q_row0 + p / a.G, m.head0 + p % a.G, d);
+    }
+}
+
 template <int D>
 cudaError_t launch_sizes(attn_plan_s* plan, const CUtensorMap* maps, CrossArgs args, cudaStream_t stream) {
-    for (int size = 0; size < 3; ++size) {
-        const int n = plan->cross_units[size];
-        if (n == 0) continue;
-        const cudaError_t e = size == 0   ? launch<D, 1>(maps, args, n, stream)
-                              : size == 1 ? launch<D, 2>(maps, args, n, stream)
-                                          : launch<D, 4>(maps, args, n, stream);
+    if (plan->cross_units[0] > 0) {
+        const cudaError_t e = launch<D, 1>(maps, args, plan->cross_units[0], stream);
         if (e != cudaSuccess) return e;
-        args.units += n;
+        args.units += plan->cross_units[0];
     }
-    return cudaSuccess;
+    if (plan->cross_units[1] > 0) {
+        const cudaError_t e = launch<D, 2>(maps, args, plan->cross_units[1], stream);
+        if (e != cudaSuccess) return e;
+    }
+    if (plan->cross_merges == 0) return cudaSuccess;
+    return launch_dependent(cross_merge_kernel<D>, dim3(plan->cross_merges), kMergeThreads, 0, stream,
+                            reinterpret_cast<const CrossMerge*>(plan->ws + plan->layout.append), args);
 }
 
 }  // namespace
@@ -457,7 +462,6 @@ attn_status launch_cross_few(attn_plan_s* plan, const void* q, const float* sink
     a.sinks = sinks;
     a.part_o = reinterpret_cast<float*>(plan->ws + plan->layout.part_o);
     a.part_lse = reinterpret_cast<float*>(plan->ws + plan->layout.part_lse);
-    a.counters = reinterpret_cast<int32_t*>(plan->ws + plan->layout.counters);
     a.err = reinterpret_cast<int32_t*>(plan->ws + plan->layout.err);
     a.Hq = plan->Hq;
     a.G = plan->Hq / plan->Hkv;

@@ -3,9 +3,10 @@
 //
 // All rows of a sequence see the same keys, so a KV head's work is a dense
 // product of its (row, query head) pairs with the keys.  Few pairs are bound by
-// reading K and V: units of up to 64 pairs and a chunk of keys, on the kernel of
-// cross.cu.  Many pairs are bound by the tensor cores: items of up to 256 pairs and
-// all keys, on the prefill kernel.
+// reading K and V: units of up to 32 pairs and a chunk of keys, on the kernel of
+// cross.cu.  Many pairs go to the prefill kernel's tensor-core products: items of
+// up to 256 pairs and all keys or, where that would leave SMs without work, a
+// chunk of them, whose states a small kernel joins.
 #include <algorithm>
 #include <cmath>
 #include <exception>
@@ -21,7 +22,16 @@ namespace {
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Pairs of a sequence and KV head from which it goes to the prefill kernel.
-constexpr int64_t kCrossManyPairs = 65;
+constexpr int64_t kCrossManyPairs = 33;
+constexpr int64_t kCrossUnitCost = 4;    // a unit's start and end, in stages
+constexpr int64_t kCrossItemTiles = 4;   // tiles of 128 keys: never split a sequence finer
+constexpr int64_t kCrossItemCost = 2;    // an item's start and end, in tiles
+
+void add_merge(attn_plan_s& plan, const CrossMerge& m) {
+    const int32_t* words = reinterpret_cast<const int32_t*>(&m);
+    plan.append_slots.insert(plan.append_slots.end(), words, words + sizeof m / sizeof(int32_t));
+    ++plan.cross_merges;
+}
 
 attn_status build(const int32_t* qo_indptr, const int32_t* kv_start, const int32_t* kv_len, int32_t batch,
                   int32_t kv_rows, int32_t Hq, int32_t Hkv, int32_t D, float sm_scale, int32_t num_sms,
@@ -61,14 +71,40 @@ attn_status build(const int32_t* qo_indptr, const int32_t* kv_start, const int32
         const int64_t rows = qo_indptr[b + 1] - qo_indptr[b], pairs = rows * G;
         if (rows == 0) continue;
         if (few(pairs, kv_len[b])) {
-            work += (pairs + 63) / 64 * stages_of(kv_len[b]) * Hkv;
+            work += (pairs + kCrossBlock - 1) / kCrossBlock * stages_of(kv_len[b]) * Hkv;
             decode_tokens += kv_len[b];
         } else {
             prefill_pairs += rows * kv_len[b];
         }
     }
-    const int64_t target = 2 * (int64_t)num_sms * cross_ctas_per_sm(D);
-    const int64_t chunk = std::max<int64_t>((work + target - 1) / target, kCrossMinChunk);
+    // The chunk length that gives each CTA slot one unit, two, .. up to four: the one
+    // whose units end first.  The rounds are full ones and a last one, which goes up to
+    // three times as fast, for its CTAs have the memory to themselves; a unit costs
+    // kCrossUnitCost stages more than it has.  (One unit a slot against two: 64 x 1,500
+    // keys of 8 heads 38 us against 42, 1 x 16,000 of 16 heads 13 against 18, but 8 x
+    // 16,000 of 16 heads 99 against 82.)
+    auto chunks_of = [](int64_t n, int64_t size) { return std::max<int64_t>(1, (n + size / 2) / size); };
+    const int64_t slots = (int64_t)num_sms * cross_ctas_per_sm(D);
+    int64_t chunk = INT32_MAX;
+    double least = 0;
+    for (int64_t per_slot = 1; work > 0 && per_slot <= 4; ++per_slot) {
+        const int64_t s = std::max<int64_t>((work - 1) / (slots * per_slot) + 1, kCrossMinChunk);
+        int64_t units = 0, longest = 0;
+        for (int32_t b = 0; b < batch; ++b) {
+            const int64_t pairs = (int64_t)(qo_indptr[b + 1] - qo_indptr[b]) * G;
+            if (pairs == 0 || !few(pairs, kv_len[b])) continue;
+            const int64_t n = stages_of(kv_len[b]), c = chunks_of(n, s);
+            units += (pairs + kCrossBlock - 1) / kCrossBlock * Hkv * c;
+            longest = std::max(longest, (n + c - 1) / c);
+        }
+        const double last = (double)(units % slots) / (double)slots;
+        const double rounds = (double)(units / slots) + (last > 0 ? std::max(last, 1.0 / 3) : 0.0);
+        const double cost = std::max(rounds * ((double)work / (double)units + kCrossUnitCost), (double)longest / 3 + kCrossUnitCost);
+        if (per_slot == 1 || cost < least) {
+            least = cost;
+            chunk = s;
+        }
+    }
     struct Piece {
         int32_t size;   // log2 of the block's 16-pair tiles
         DecodeUnit u;
@@ -78,10 +114,10 @@ attn_status build(const int32_t* qo_indptr, const int32_t* kv_start, const int32
     for (int32_t b = 0; b < batch; ++b) {
         const int64_t rows = qo_indptr[b + 1] - qo_indptr[b], pairs = rows * G;
         if (rows == 0 || !few(pairs, kv_len[b])) continue;
-        const int64_t stages = stages_of(kv_len[b]), n_chunks = std::max<int64_t>(1, (stages + chunk / 2) / chunk);
-        for (int64_t p0 = 0; p0 < pairs; p0 += 64) {
-            const int32_t n_pairs = (int32_t)std::min<int64_t>(64, pairs - p0);
-            const int32_t size = n_pairs <= 16 ? 0 : n_pairs <= 32 ? 1 : 2;
+        const int64_t stages = stages_of(kv_len[b]), n_chunks = chunks_of(stages, chunk);
+        for (int64_t p0 = 0; p0 < pairs; p0 += kCrossBlock) {
+            const int32_t n_pairs = (int32_t)std::min<int64_t>(kCrossBlock, pairs - p0);
+            const int32_t size = n_pairs > 16;
             for (int32_t g = 0; g < Hkv; ++g) {
                 DecodeUnit u{};
                 u.q_row = qo_indptr[b];
@@ -90,13 +126,13 @@ attn_status build(const int32_t* qo_indptr, const int32_t* kv_start, const int32
                 u.head0 = (int32_t)p0;
                 u.n_heads = n_pairs;
                 u.n_chunks = (int32_t)n_chunks;
-                u.group = -1;
-                u.reserved = pairs > 64;   // other blocks read the same keys
+                u.group = -1;   // no merge counter
+                u.reserved = pairs > kCrossBlock;   // other blocks read the same keys
                 if (n_chunks > 1) {
-                    u.group = plan->n_groups++;
                     u.partial0 = (int32_t)partials;
                     partials += n_chunks << size;
                     if (partials > INT32_MAX / kMaxSliceHeads) return ATTN_ERR_UNSUPPORTED;
+                    add_merge(*plan, {u.q_row, g * G, u.head0, n_pairs, u.partial0, (int32_t)n_chunks, 1 << size, 0});
                 }
                 for (int64_t c = 0; c < n_chunks; ++c) {
                     u.chunk = (int32_t)c;
@@ -117,44 +153,93 @@ attn_status build(const int32_t* qo_indptr, const int32_t* kv_start, const int32
         plan->units.push_back(p.u);
         ++plan->cross_units[p.size];
     }
-    plan->n_partials = (int32_t)partials;
 
-    // ---- many pairs: items of one or two head slots of slot_rows rows x G heads.
+    // ---- many pairs: items of up to two head slots of slot_rows rows x G heads.
     const int64_t slot_rows = G <= kPrefillRows ? kPrefillRows / G : 1;
-    int64_t slots = 0;
-    for (int32_t b = 0; b < batch; ++b) {
-        const int64_t rows = qo_indptr[b + 1] - qo_indptr[b];
-        if (rows > 0 && !few(rows * G, kv_len[b])) slots += (rows + slot_rows - 1) / slot_rows * Hkv;
-    }
-    const int64_t per_item = slots <= num_sms ? 1 : 2;   // a slot each while the SMs suffice
-    if (slots > (int64_t)INT32_MAX / (int64_t)sizeof(PrefillItem)) return ATTN_ERR_UNSUPPORTED;
+    auto tiles_of = [](int32_t keys) { return ((int64_t)keys + kPrefillKeys - 1) / kPrefillKeys; };
+    int64_t blocks = 0, tiles = 0;   // of two slots each, and their tiles
     for (int32_t b = 0; b < batch; ++b) {
         const int64_t rows = qo_indptr[b + 1] - qo_indptr[b];
         if (rows == 0 || few(rows * G, kv_len[b])) continue;
-        for (int64_t r0 = 0; r0 < rows; r0 += per_item * slot_rows) {
+        const int64_t n = (rows + 2 * slot_rows - 1) / (2 * slot_rows) * Hkv;
+        blocks += n;
+        tiles += n * tiles_of(kv_len[b]);
+    }
+    if (blocks > (int64_t)INT32_MAX / (int64_t)sizeof(PrefillItem)) return ATTN_ERR_UNSUPPORTED;
+    // Blocks that would fill the SMs a few times over stay whole.  Others are cut
+    // so that the SMs' shares come out even: of chunk lengths that give each SM
+    // one item, two, .., the one whose fullest SM has the least to do, if all items
+    // were alike.
+    int64_t size = INT32_MAX;
+    if (blocks > 0 && blocks < 4 * (int64_t)num_sms) {
+        int64_t best = INT64_MAX;
+        for (int64_t per_sm = 0; per_sm <= 4; ++per_sm) {
+            const int64_t s = per_sm == 0 ? INT32_MAX : std::max((tiles - 1) / (num_sms * per_sm) + 1, kCrossItemTiles);
+            int64_t items = 0, longest = 0;
+            for (int32_t b = 0; b < batch; ++b) {
+                const int64_t rows = qo_indptr[b + 1] - qo_indptr[b], n = tiles_of(kv_len[b]);
+                if (rows == 0 || few(rows * G, kv_len[b])) continue;
+                const int64_t c = chunks_of(n, s);
+                items += (rows + 2 * slot_rows - 1) / (2 * slot_rows) * Hkv * c;
+                longest = std::max(longest, (n - 1) / c + 1);
+            }
+            const int64_t rounds = (items - 1) / num_sms + 1;
+            const int64_t cost = std::max(rounds * ((tiles - 1) / items + 1 + kCrossItemCost), longest + kCrossItemCost);
+            if (cost < best) {
+                best = cost;
+                size = s;
+            }
+        }
+    }
+    for (int32_t b = 0; b < batch; ++b) {
+        const int64_t rows = qo_indptr[b + 1] - qo_indptr[b];
+        if (rows == 0 || few(rows * G, kv_len[b])) continue;
+        const int64_t n = tiles_of(kv_len[b]), n_chunks = chunks_of(n, size);
+        for (int64_t r0 = 0; r0 < rows; r0 += 2 * slot_rows) {
             const int64_t left = rows - r0;
             for (int32_t g = 0; g < Hkv; ++g) {
                 PrefillItem it{};
                 it.q_row0 = (int32_t)(qo_indptr[b] + r0);
                 it.n_rows = (int32_t)(std::min(left, slot_rows) * G);
-                it.reserved0 = per_item == 2 && left > slot_rows ? (int32_t)(std::min(left - slot_rows, slot_rows) * G) : 0;
+                it.reserved0 = left > slot_rows ? (int32_t)(std::min(left - slot_rows, slot_rows) * G) : 0;
                 it.n_heads = it.reserved0 > 0 ? 2 : 1;
-                it.page_base = kv_start[b];
-                it.kv_len = it.key_end = kv_len[b];
                 it.kv_head = g;
                 it.head0 = g * G;
-                it.n_kv_tiles = (kv_len[b] - 1) / kPrefillKeys + 1;
-                plan->items.push_back(it);
+                it.pos0 = -1;
+                const int64_t partial0 = partials;
+                for (int64_t c = 0; c < n_chunks; ++c) {
+                    const int64_t t0 = c * n / n_chunks, t1 = (c + 1) * n / n_chunks;
+                    it.page_base = (int32_t)(kv_start[b] + t0 * kPrefillKeys);
+                    it.kv_len = (int32_t)(std::min<int64_t>(kv_len[b], t1 * kPrefillKeys) - t0 * kPrefillKeys);
+                    it.key_end = it.kv_len;
+                    it.n_kv_tiles = (int32_t)(t1 - t0);
+                    it.reserved1 = (int32_t)c;
+                    if (n_chunks > 1) {
+                        plan->cross_chunks = true;
+                        it.pos0 = (int32_t)partials;
+                        partials += it.n_heads * (kPrefillRows / kMaxSliceHeads);
+                        if (partials > INT32_MAX / kMaxSliceHeads) return ATTN_ERR_UNSUPPORTED;
+                    }
+                    plan->items.push_back(it);
+                }
+                for (int i = 0; n_chunks > 1 && i < it.n_heads; ++i) {
+                    const int32_t pairs = i ? it.reserved0 : it.n_rows;
+                    for (int32_t p = 0; p < pairs; p += kCrossBlock)
+                        add_merge(*plan, {(int32_t)(it.q_row0 + i * slot_rows), it.head0, p, std::min(kCrossBlock, pairs - p),
+                                          (int32_t)(partial0 + (i * kPrefillRows + p) / kMaxSliceHeads), (int32_t)n_chunks,
+                                          it.n_heads * (kPrefillRows / kMaxSliceHeads), 0});
+                }
             }
         }
     }
+    plan->n_partials = (int32_t)partials;
     deal_prefill_items(plan.get());
 
     WorkspaceLayout& L = plan->layout;
     size_t off = 0;
     L.units = off;    off = align_up(off + plan->units.size() * sizeof(DecodeUnit), 256);
     L.items = off;    off = align_up(off + plan->items.size() * sizeof(PrefillItem), 256);
-    L.append = off;
+    L.append = off;   off = align_up(off + plan->append_slots.size() * sizeof(int32_t), 256);
     L.item_off = off; off = align_up(off + plan->item_off.size() * sizeof(int32_t), 256);
     L.counters = off; off = align_up(off + (size_t)plan->n_groups * sizeof(int32_t), 256);
     L.err = off;      off = align_up(off + sizeof(int32_t), 256);
@@ -167,7 +252,7 @@ attn_status build(const int32_t* qo_indptr, const int32_t* kv_start, const int32
     I.batch = batch;
     I.total_qo_rows = (int32_t)total_rows;
     I.num_decode_units = (int32_t)plan->units.size();
-    I.num_decode_groups_split = plan->n_groups;
+    I.num_decode_groups_split = plan->cross_merges;
     I.num_decode_partials = plan->n_partials;
     I.decode_chunk_blocks = (int32_t)std::min<int64_t>(chunk * (kCrossKeys / kBlockTokens), INT32_MAX);
     I.num_prefill_items = (int32_t)plan->items.size();

@@ -131,6 +131,8 @@ struct PrefillArgs {
     int32_t G;           // kCross: query heads of a KV head,
     int32_t slot_rows;   // rows of a head slot,
     int32_t boxes;       // whether a softmax warp's 32 pairs are a box of o_map
+    float* part_o;       // partial states of split keys
+    float* part_lse;
 };
 
 struct Bars {
@@ -149,7 +151,11 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
 // kCross: such arrays, and head slots of (row, head) pairs: slot i of an item holds
 // rows q_row0 + i * slot_rows on, its first n_rows (i = 0) or reserved0 (i = 1)
 // pairs; n_heads is then the number of slots.
-template <int D, bool kRagged, bool kCross = false>
+// kChunks: items may have a chunk of the keys (pos0 >= 0), whose normalised O and
+// lse go to the workspace.  A kernel of its own: with that second way out, the one
+// for whole keys took 15% longer at D = 128 (1,013 -> 1,163 us for 64 x 512 pairs
+// over 16,000 keys of 4 heads).
+template <int D, bool kRagged, bool kCross = false, bool kChunks = false>
 __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
 prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                          const __grid_constant__ CUtensorMap kv_map,
@@ -574,6 +580,24 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                 lt += __uint_as_float(v[0]);
             }
             const float inv = lt > 0.f ? 1.f / lt : 0.f;
+            if (kChunks && ei.pos0 >= 0) {   // a chunk of the keys: its state in fp32
+                const size_t part = (size_t)(ei.pos0 + i * (kPrefillRows / kMaxSliceHeads)) * kMaxSliceHeads + r;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    ptx::tmem_ld32(t_o + c * 32, v);
+                    ptx::tc_wait_ld();
+                    if (r < e_rows) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(a.part_o + part * D + c * 32 + e) =
+                                make_float4(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv,
+                                            __uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
+                    }
+                }
+                if (r < e_rows) a.part_lse[part] = e_lse;
+                return true;
+            }
             if (C::kSplitP && quad * 32 + 32 <= e_rows && (!kCross || a.boxes)) {
                 if (lane == 0) ptx::bulk_wait_read_all();   // the stripe's previous store has read it
                 __syncwarp();
@@ -622,7 +646,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                     }
                 }
             }
-            if (r < e_rows && a.lse) a.lse[(size_t)e_row * a.Hq + e_head] = e_lse;
+            if (r < e_rows && a.lse) a.lse[(size_t)e_row * a.Hq + e_head] = kChunks ? e_lse * kLn2 : e_lse;
             return true;
         };
         if (i == 1 && lane == 0) ptx::mbar_arrive(other_turn);
@@ -640,7 +664,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
             // At D = 64 the keys' part of l accumulates in TMEM next to O (the
             // ones column), and l here holds only the sink's term.
             float m_use = -INFINITY, l = 0.f, le = 0.f;
-            if (a.sinks != nullptr) {
+            if (a.sinks != nullptr && (!kChunks || it.reserved1 == 0)) {
                 m_use = a.sinks[head] * kLog2e;
                 l = le = 1.f;
             }
@@ -819,7 +843,10 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
             e_l = l;
             // le >= 1 here (the term that set the running max contributes 1), so
             // the MUFU's approximate lg2 is within 2^-22 of log2(le).
-            e_lse = le > 0.f ? (m_use + __log2f(le)) * kLn2 : -INFINITY;
+            // (kChunks: in log2 until it is stored.  kCross: NaN passes, or a chunk of NaN
+            // would count for nothing.)
+            const bool any = kCross ? !(le <= 0.f) : le > 0.f;
+            e_lse = any ? (m_use + __log2f(le)) * (kChunks ? 1.f : kLn2) : -INFINITY;
             hj += n;
         }
         if (ok && epi) ok = epilogue();
@@ -839,11 +866,11 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
     }
 }
 
-template <int D, bool kRagged, bool kCross = false>
+template <int D, bool kRagged, bool kCross = false, bool kChunks = false>
 cudaError_t launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& om,
                    const PrefillArgs& args, int grid, cudaStream_t stream) {
     using C = PrefillCfg<D>;
-    auto kernel = prefill_sink_attn_kernel<D, kRagged, kCross>;
+    auto kernel = prefill_sink_attn_kernel<D, kRagged, kCross, kChunks>;
     static std::atomic<bool> configured[kMaxDevices];
     cudaError_t e = once_per_device(configured, [&] {
         cudaFuncAttributes fa;
@@ -880,6 +907,8 @@ attn_status launch_prefill(attn_plan_s* plan, const void* q_map, const void* kv_
     a.G = plan->Hq / plan->Hkv;
     a.slot_rows = kPrefillRows / a.G;
     a.boxes = cross_out_box(a.G) > 0;
+    a.part_o = reinterpret_cast<float*>(plan->ws + plan->layout.part_o);
+    a.part_lse = reinterpret_cast<float*>(plan->ws + plan->layout.part_lse);
     const CUtensorMap& qm = *static_cast<const CUtensorMap*>(q_map);
     const CUtensorMap& km = *static_cast<const CUtensorMap*>(kv_map);
     const CUtensorMap& vm = *static_cast<const CUtensorMap*>(v_map ? v_map : kv_map);
@@ -888,7 +917,10 @@ attn_status launch_prefill(attn_plan_s* plan, const void* q_map, const void* kv_
     // kernel holds all of an SM's TMEM).
     const int grid = plan->prefill_ctas;
     cudaError_t e;
-    if (plan->cross)
+    if (plan->cross && plan->cross_chunks)
+        e = plan->D == 64 ? launch<64, true, true, true>(qm, km, vm, om, a, grid, stream)
+                          : launch<128, true, true, true>(qm, km, vm, om, a, grid, stream);
+    else if (plan->cross)
         e = plan->D == 64 ? launch<64, true, true>(qm, km, vm, om, a, grid, stream)
                           : launch<128, true, true>(qm, km, vm, om, a, grid, stream);
     else if (plan->ragged)

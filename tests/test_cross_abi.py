@@ -77,15 +77,16 @@ def test_the_binding_refuses_the_other_calls():
         binding.CrossPlan([0, 1], [0, 0], [1, 1], 4, 8, 2, 64)
 
 
+@pytest.mark.parametrize("sms", [152, 4])
 @pytest.mark.parametrize("Hq,Hkv,D,seed", [(8, 2, 64, 0), (16, 16, 64, 1), (64, 4, 128, 2), (20, 4, 64, 3), (9, 3, 128, 4),
                                            (160, 1, 64, 5), (128, 1, 128, 6), (64, 8, 64, 7), (7, 1, 64, 8)])
-def test_every_pair_and_key_once(lib, Hq, Hkv, D, seed):
+def test_every_pair_and_key_once(lib, Hq, Hkv, D, seed, sms):
     rng = np.random.default_rng(seed)
     G = Hq // Hkv
     qo = [0, 1, 1, 3, 16 // min(G, 16), 64 // min(G, 64) + 1, 200, 700, int(rng.integers(1, 40)), 5, 64]
     kv = [9, 0, 1, 64, 65, 5000, 129, 1500, 40000, 0, 640]
     start = [int(rng.integers(0, 100)) for _ in kv]
-    st, h, _ = plan(lib, qo, start, kv, 45000, Hq, Hkv, D)
+    st, h, _ = plan(lib, qo, start, kv, 45000, Hq, Hkv, D, sms=sms)
     assert st == OK
     info, units, items = units_of(lib, h)
     ind = np.concatenate([[0], np.cumsum(qo)])
@@ -95,28 +96,37 @@ def test_every_pair_and_key_once(lib, Hq, Hkv, D, seed):
         for p in pairs:
             seen.setdefault((b, g, p), []).append((t0, t1, chunk))
 
-    slots = set()
+    slots, merges = set(), 0
     for q_row, first, g, p0, n, t0, t1, chunk, n_chunks, group, partial0, shared in units.tolist():
         b = int(np.searchsorted(ind, q_row, "right")) - 1
-        assert q_row == ind[b] and first == start[b] and 1 <= n <= 64 and 0 <= t0 <= t1 <= kv[b]
-        assert t0 % 64 == 0 and (t1 % 64 == 0 or t1 == kv[b]) and shared == (qo[b] * G > 64)
+        assert q_row == ind[b] and first == start[b] and 1 <= n <= 32 and 0 <= t0 <= t1 <= kv[b]
+        assert t0 % 64 == 0 and (t1 % 64 == 0 or t1 == kv[b]) and shared == (qo[b] * G > 32)
         add(b, g, range(p0, p0 + n), t0, t1, (chunk, n_chunks))
-        tiles = 1 if n <= 16 else 2 if n <= 32 else 4
+        tiles = 1 if n <= 16 else 2
         for s in range(tiles if n_chunks > 1 else 0):
             slot = partial0 + chunk * tiles + s
             assert 0 <= slot < info.num_decode_partials and slot not in slots
             slots.add(slot)
-        assert (group >= 0) == (n_chunks > 1) and group < info.num_decode_groups_split
-    assert len(slots) == info.num_decode_partials
-    sizes = [1 if n <= 16 else 2 if n <= 32 else 4 for n in units[:, 4]]
+        merges += (n_chunks > 1 and chunk == 0)
+    sizes = [1 if n <= 16 else 2 for n in units[:, 4]]
     assert sizes == sorted(sizes)
     rows = 128 // min(G, 128)
-    for q_row0, n0, first, kv_len, _, g, head0, n_slots, tiles, key_end, n1, _ in items.tolist():
+    chunks = {}
+    for q_row0, n0, first, kv_len, partial, g, head0, n_slots, tiles, key_end, n1, c in items.tolist():
+        chunks[q_row0, g] = max(chunks.get((q_row0, g), 0), c + 1)
+    for q_row0, n0, first, kv_len, partial, g, head0, n_slots, tiles, key_end, n1, c in items.tolist():
         b = int(np.searchsorted(ind, q_row0, "right")) - 1
-        assert first == start[b] and kv_len == kv[b] == key_end > 0 and tiles == -(-kv_len // 128) and head0 == g * G
+        t0 = first - start[b]
+        assert t0 % 128 == 0 and kv_len == key_end > 0 and tiles == -(-kv_len // 128) and head0 == g * G
+        assert (partial >= 0) == (chunks[q_row0, g] > 1)
+        for s in range(8 * n_slots if partial >= 0 else 0):
+            assert 0 <= partial + s < info.num_decode_partials and partial + s not in slots
+            slots.add(partial + s)
+        merges += (-(-n0 // 32) - (-n1 // 32)) * (partial >= 0 and c == 0)
         assert n_slots == (2 if n1 else 1) and 0 < n0 <= 128 and n1 <= 128 and (not n1 or n0 == rows * G)
         p0 = (q_row0 - int(ind[b])) * G
-        add(b, g, range(p0, p0 + n0 + n1), 0, kv_len, (0, 1))
+        add(b, g, range(p0, p0 + n0 + n1), t0, t0 + kv_len, (c, chunks[q_row0, g]))
+    assert len(slots) == info.num_decode_partials and merges == info.num_decode_groups_split
     for b in range(len(qo)):
         for g in range(Hkv):
             for p in range(qo[b] * G):

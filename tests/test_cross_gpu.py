@@ -96,7 +96,7 @@ def test_single_rows(Hq, Hkv, D, sinks):
 @pytest.mark.parametrize("Hq,Hkv,D", HEADS)
 @pytest.mark.parametrize("padded,fused", [(True, True), (False, False)])
 def test_rows_of_every_number(Hq, Hkv, D, padded, fused):
-    """Blocks of one to four tiles, the border to the prefill kernel, several blocks and slots; no rows, no keys."""
+    """Blocks of one and two tiles, the border to the prefill kernel, several blocks and slots; no rows, no keys."""
     qo = [2, 3, 0, 5, 8, 11, 16, 17, 33, 63, 64, 65, 127, 129, 260, 4, 30]
     kv = [70, 16, 9, 33, 64, 65, 129, 1, 128, 200, 257, 64, 300, 127, 500, 0, 0]
     plan, *_ = check(qo, kv, Hq, Hkv, D, True, padded=padded, fused=fused, seed=D)
@@ -110,6 +110,14 @@ def test_long_keys_are_split(Hq, Hkv, D, qo):
     assert plan.info()["num_decode_partials"] > 0
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,qo", [(8, 2, 64, 20), (4, 4, 128, 300), (64, 8, 64, 5), (10, 2, 64, 97), (6, 1, 128, 22),
+                                          (48, 1, 64, 3), (130, 1, 128, 2)])
+def test_many_rows_over_split_keys(Hq, Hkv, D, qo):
+    plan, *_ = check([qo, qo, 1, qo], [5000, 700, 9000, 1153], Hq, Hkv, D, qo % 2 == 0, seed=qo)
+    info = plan.info()
+    assert info["num_decode_partials"] > 0 and (Hq // Hkv > 128 or info["num_prefill_items"] > 2 * Hkv)
+
+
 @pytest.mark.parametrize("G,D", [(1, 64), (3, 64), (5, 128), (32, 64), (48, 64), (64, 64), (96, 128), (127, 64), (128, 64), (160, 64)])
 def test_many_rows_of_every_group(G, D):
     """Slots of 128 / G rows: full ones, ragged ones, output boxes and single rows."""
@@ -119,12 +127,12 @@ def test_many_rows_of_every_group(G, D):
 
 def test_large_scores_raise_the_maximum():
     """Scores that pass the first tile's maximum by far; tolerances grow with them (2^-24 (D + 4) of |s| <= 2000: 2^-7)."""
-    for qo in ([1, 70], [5, 200]):
+    for qo, sms in (([1, 70], 0), ([5, 200], 0), ([30, 150], 2)):
         q, k, v, s, start, rows = inputs(qo, [900, 1000], 8, 2, 64, True, seed=3)
         k[start[0] + 700] *= 40
         k[start[1] + 999] *= 40
         q = q * 8
-        plan = binding().CrossPlan([0, qo[0], sum(qo)], start, [900, 1000], rows, 8, 2, 64)
+        plan = binding().CrossPlan([0, qo[0], sum(qo)], start, [900, 1000], rows, 8, 2, 64, num_sms=sms)
         out, lse = plan.attend(q, k, v, s, lse=torch.empty(sum(qo), 8, device="cuda"))
         want, mag, want_lse = plain(q, k, v, s, qo, start, [900, 1000], 0.125)
         assert bool(((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -7 + 2.0 ** -6) * mag).all())
@@ -133,9 +141,9 @@ def test_large_scores_raise_the_maximum():
 
 def test_infinite_and_nan_states():
     """A NaN in one KV head's keys or values reaches that head's rows of that sequence, and no others."""
-    qo, kv = [3, 70, 2], [100, 300, 40]
+    qo, kv = [3, 70, 2], [100, 3000, 40]                     # (the second's keys are split)
     plan, (q, k, v, s), clean, _ = check(qo, kv, 8, 4, 64, False, padded=False, fused=False, seed=5)
-    k[100 + 250, 1, 7], v[5, 2, 3], v[399, 0, :] = float("nan"), float("nan"), float("inf")
+    k[100 + 250, 1, 7], v[5, 2, 3], v[3099, 0, :] = float("nan"), float("nan"), float("inf")
     out, _ = plan.attend(q, k, v, s)
     bad = torch.zeros_like(out, dtype=torch.bool)
     bad[3:73, 2:4] = True
