@@ -502,8 +502,8 @@ uint64_t turns_of(float f) {
     constexpr double kInv2PiHi = 0x1.45f306dc9c883p-3, kInv2PiLo = -0x1.6b01ec5417056p-57;
     const double x = std::fabs((double)f), hi = x * kInv2PiHi;
     const double lo = std::fma(x, kInv2PiHi, -hi) + x * kInv2PiLo;
-    const double scaled = std::ldexp(hi - std::floor(hi), 64), whole = std::floor(scaled);   // exact, below 2^64
-    const uint64_t turns = (uint64_t)whole + (uint64_t)(int64_t)std::nearbyint(scaled - whole + std::ldexp(lo, 64));
+    const double scaled = (hi - std::floor(hi)) * 0x1p64, whole = std::floor(scaled);   // exact, below 2^64
+    const uint64_t turns = (uint64_t)whole + (uint64_t)(int64_t)std::nearbyint(scaled - whole + lo * 0x1p64);
     return f < 0.f ? 0 - turns : turns;
 }
 
@@ -592,21 +592,25 @@ attn_status check_refs(const int32_t* refs, int32_t num_pages, const int32_t* de
     return num_pages > 0 && refs && aligned16(refs) && aligned4(device_error) ? ATTN_OK : ATTN_ERR_INVALID_ARG;
 }
 
-// In launches of as many pools as a launch's arguments hold.
-attn_status copy_pages(void* const* pools, const int64_t* page_bytes, int32_t n_pools, int32_t num_pages,
+// Pools k0 on, as many as a launch's arguments hold.
+attn::PagePools some_pools(void* const* pools, const int64_t* page_bytes, int32_t n_pools, int32_t k0) {
+    attn::PagePools p = {};
+    p.n = std::min(n_pools - k0, attn::kPagePoolsPerLaunch);
+    for (int32_t k = 0; k < p.n; ++k) {
+        p.pool[k] = static_cast<unsigned char*>(pools[k0 + k]);
+        p.bytes[k] = page_bytes[k0 + k];
+    }
+    return p;
+}
+
+attn_status copy_pages(void* const* pools, const int64_t* page_bytes, int32_t n_pools, int32_t k0, int32_t num_pages,
                        const int32_t* src, const int32_t* dst, const int32_t* n, int64_t n_max, int32_t* device_error,
                        cudaStream_t stream) {
-    if (n_max == 0) return ATTN_OK;
-    for (int32_t k0 = 0; k0 < n_pools; k0 += attn::kPagePoolsPerLaunch) {
-        attn::PagePools p = {};
-        p.n = std::min(n_pools - k0, attn::kPagePoolsPerLaunch);
-        for (int32_t k = 0; k < p.n; ++k) {
-            p.pool[k] = static_cast<unsigned char*>(pools[k0 + k]);
-            p.bytes[k] = page_bytes[k0 + k];
-        }
-        if (attn_status st = attn::launch_pages_copy(p, num_pages, src, dst, n, n_max, device_error, stream); st != ATTN_OK)
+    for (; k0 < n_pools; k0 += attn::kPagePoolsPerLaunch)
+        if (attn_status st = attn::launch_pages_copy(some_pools(pools, page_bytes, n_pools, k0), num_pages, src, dst, n,
+                                                     n_max, device_error, stream);
+            st != ATTN_OK)
             return st;
-    }
     return ATTN_OK;
 }
 
@@ -639,7 +643,7 @@ extern "C" attn_status attn_pages_copy(void* const* pools, const int64_t* page_b
     if (num_pages <= 0 || n < 0 || n > INT32_MAX || !aligned4(device_error)) return ATTN_ERR_INVALID_ARG;
     if (n == 0) return ATTN_OK;
     if (!src || !dst || !aligned4(src) || !aligned4(dst)) return ATTN_ERR_INVALID_ARG;
-    return copy_pages(pools, page_bytes, n_pools, num_pages, src, dst, nullptr, n, device_error,
+    return copy_pages(pools, page_bytes, n_pools, 0, num_pages, src, dst, nullptr, n, device_error,
                       static_cast<cudaStream_t>(stream));
 }
 
@@ -661,9 +665,12 @@ extern "C" attn_status attn_pages_fork(int32_t* refs, int32_t num_pages, const i
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const attn::PageFork f = {page_table, kv_indptr, kv_lens, parents, table_len, batch, n, page_size, page_table_out,
                               indptr_out, out_len};
-    if (attn_status st = attn::launch_pages_fork(refs, num_pages, f, scratch, device_error, s); st != ATTN_OK) return st;
+    if (attn_status st = attn::launch_pages_fork(refs, num_pages, f, some_pools(pools, page_bytes, n_pools, 0), scratch,
+                                                 device_error, s);
+        st != ATTN_OK)
+        return st;
     const int32_t *dst = scratch + attn::kMoveHead, *src = dst + n;
-    return copy_pages(pools, page_bytes, n_pools, num_pages, src, dst, scratch, n, device_error, s);
+    return copy_pages(pools, page_bytes, n_pools, attn::kPagePoolsPerLaunch, num_pages, src, dst, scratch, n, device_error, s);
 }
 
 extern "C" attn_status attn_pages_compact(int32_t* refs, int32_t num_pages, int32_t* page_table, int64_t n_entries,
@@ -675,11 +682,13 @@ extern "C" attn_status attn_pages_compact(int32_t* refs, int32_t num_pages, int3
         (n_entries > 0 && (!page_table || !aligned4(page_table))))
         return ATTN_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (attn_status st = attn::launch_pages_compact(refs, num_pages, page_table, n_entries, remap, scratch, device_error, s);
+    if (attn_status st = attn::launch_pages_compact(refs, num_pages, page_table, n_entries, remap,
+                                                    some_pools(pools, page_bytes, n_pools, 0), scratch, device_error, s);
         st != ATTN_OK)
         return st;
     const int32_t *dst = scratch + attn::kMoveHead, *src = dst + num_pages / 2;
-    return copy_pages(pools, page_bytes, n_pools, num_pages, src, dst, scratch, num_pages / 2, device_error, s);
+    return copy_pages(pools, page_bytes, n_pools, attn::kPagePoolsPerLaunch, num_pages, src, dst, scratch, num_pages / 2,
+                      device_error, s);
 }
 
 extern "C" attn_status attn_plan_device_error(attn_plan_t plan, int32_t* code, void* stream) {

@@ -417,8 +417,8 @@ cudaError_t launch(const CUtensorMap* maps, const CrossArgs& args, int units, cu
 }
 
 // Joins the chunks' states of split keys, this kernel's and the prefill kernel's.  A
-// CTA has 32 pairs of a record, a thread 4 dims of one of them at a time.
-constexpr int kMergeThreads = 256, kMergePairs = 32;
+// CTA has a record's up to 32 pairs, a thread 4 dims of one of them at a time.
+constexpr int kMergeThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
 cross_merge_kernel(const CrossMerge* merges, const CrossArgs a) {

@@ -121,12 +121,13 @@ struct PageFork {
     int32_t *table_out, *indptr_out;
     int64_t out_len;
 };
-// scratch: page_move_words(n) int32: the copies that the pools need, written on the device.
-attn_status launch_pages_fork(int32_t* refs, int32_t num_pages, const PageFork& f, int32_t* scratch, int32_t* err,
-                              cudaStream_t stream);
+// Forks and compactions copy in `pools`, the first ones of the call; the copies that
+// other pools need are then in scratch (page_move_words(n) int32, on the device).
+attn_status launch_pages_fork(int32_t* refs, int32_t num_pages, const PageFork& f, const PagePools& pools,
+                              int32_t* scratch, int32_t* err, cudaStream_t stream);
 attn_status launch_pages_compact(int32_t* refs, int32_t num_pages, int32_t* page_table, int64_t entries, int32_t* remap,
-                                 int32_t* scratch, int32_t* err, cudaStream_t stream);
-// Copies pages src[i] -> dst[i], i < *n (device) or n_host where n is NULL, at most n_max, in every pool.
+                                 const PagePools& pools, int32_t* scratch, int32_t* err, cudaStream_t stream);
+// Copies pages src[i] -> dst[i], i < *n (device; NULL: n_max) <= n_max, in every pool.
 attn_status launch_pages_copy(const PagePools& pools, int32_t num_pages, const int32_t* src, const int32_t* dst,
                               const int32_t* n, int64_t n_max, int32_t* err, cudaStream_t stream);
 // Layout of the scratch of `moves` copies: the count, then the pages written, then the pages read.

@@ -10,9 +10,9 @@
 // that in a microsecond or two, and a wider grid would need a second launch to
 // join its parts.  The first reading's lines are in L1 or L2 for the second.
 //
-// Copies are memory-bound: a persistent grid takes (page, pool, 16 KB) pieces,
-// 64 bytes per thread in flight.  How many pages move is only known on the
-// device, so the grid reads the count there; nothing waits on the host.
+// Copies are memory-bound: CTAs take (page, pool, 16 KB) pieces, 64 bytes per
+// thread in flight.  How many pages move is only known on the device, so the
+// grid reads the count there; nothing waits on the host.
 //
 // All counts and tables are integers changed by atomics or by one owner: equal
 // calls give equal results whatever the order.
@@ -31,45 +31,60 @@ constexpr int kScanWarps = kScanCtas * kScanThreads / 32;
 constexpr int kPagesPerStep = 128;      // per warp: four counts per lane
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBytes = 16384;       // a piece: four 16-byte chunks per thread
-constexpr int kMoveCtasPerSm = 8;
+// CTAs per SM of a copy's grid, eight times what is resident: the hardware hands them
+// out as SMs come free (half a pool of 36K 32 KB pages in two layers: 195 us with 8,
+// 185 with 16, 179 with 64; a grid without a cap would be mostly empty where few of
+// the pages that could move do).
+constexpr int kMoveCtasPerSm = 64;
 
 // ------------------------------------------------------- sums over the cluster
 
+template <int N>
 struct ClusterSums {
-    int64_t warp[32];
-    int64_t total[2];   // of this CTA; two, used in turn
+    int64_t warp[N][32];
+    int64_t total[N];   // of this CTA
 };
 
-// Exclusive prefix of v over all threads of the cluster in order, and the sum.
-// Every thread calls it; `turn` alternates between calls.
-__device__ __forceinline__ int64_t cluster_prefix(int64_t v, ClusterSums& s, int turn, int64_t& sum) {
+// Exclusive prefixes of v over all threads of the cluster in order, and the sums,
+// of N values at once (a barrier of the cluster costs about a microsecond).  Every
+// thread calls it, once per `s`; what threads wrote before is visible after it.
+template <int N>
+__device__ __forceinline__ void cluster_prefix(int64_t (&v)[N], int64_t (&sum)[N], ClusterSums<N>& s) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t inc = v;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-    }
-    __syncthreads();   // the warps' sums of the call before have been read
-    if (lane == 31) s.warp[warp] = inc;
-    __syncthreads();
-    int64_t before = 0, all = 0;
-#pragma unroll 8
-    for (int w = 0; w < 32; ++w) {
-        const int64_t x = s.warp[w];
-        before += w < warp ? x : 0;
-        all += x;
-    }
-    if (threadIdx.x == 0) s.total[turn] = all;
-    ptx::cluster_sync();
-    const uint32_t rank = ptx::cluster_rank(), addr = ptx::smem_u32(&s.total[turn]);
-    sum = 0;
+    int64_t inc[N];
 #pragma unroll
-    for (uint32_t c = 0; c < kScanCtas; ++c) {
-        const int64_t x = ptx::ld_cluster_s64(addr, c);
-        before += c < rank ? x : 0;
-        sum += x;
+    for (int k = 0; k < N; ++k) {
+        inc[k] = v[k];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, inc[k], o);
+            if (lane >= o) inc[k] += x;
+        }
+        if (lane == 31) s.warp[k][warp] = inc[k];
     }
-    return before + inc - v;
+    __syncthreads();
+    if (warp < N) {   // warp k: the warps' sums of value k, up to each
+        int64_t x = s.warp[warp][lane];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        s.warp[warp][lane] = x;
+        if (lane == 31) s.total[warp] = x;
+    }
+    ptx::cluster_sync();
+    const uint32_t rank = ptx::cluster_rank();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        int64_t before = warp > 0 ? s.warp[k][warp - 1] : 0;
+        sum[k] = 0;
+#pragma unroll
+        for (uint32_t c = 0; c < kScanCtas; ++c) {
+            const int64_t x = ptx::ld_cluster_s64(ptx::smem_u32(&s.total[k]), c);
+            before += c < rank ? x : 0;
+            sum[k] += x;
+        }
+        v[k] = before + inc[k] - v[k];
+    }
 }
 
 // ------------------------------------------------------------------ free pages
@@ -152,13 +167,14 @@ __device__ __forceinline__ void flag(int32_t* err, int bit) {
 
 __global__ void __cluster_dims__(kScanCtas) __launch_bounds__(kScanThreads)
 alloc_kernel(int32_t* refs, int32_t num_pages, int32_t n, int32_t* page_ids, int32_t* err) {
-    __shared__ ClusterSums sums;
+    __shared__ ClusterSums<1> sums;
     ptx::grid_dependency_wait();
     ptx::grid_dependents_go();
     const WarpPages part(num_pages);
-    int64_t free_pages;
-    const int64_t before = cluster_prefix(count_free(refs, num_pages, part), sums, 0, free_pages);
-    take_free(refs, num_pages, part, warp_base(before), n, [&](int64_t rank, int32_t page) {
+    int64_t before[1] = {count_free(refs, num_pages, part)}, all[1];
+    cluster_prefix(before, all, sums);
+    const int64_t free_pages = all[0];
+    take_free(refs, num_pages, part, warp_base(before[0]), n, [&](int64_t rank, int32_t page) {
         page_ids[rank] = page;
         refs[page] = 1;
     });
@@ -205,28 +221,28 @@ struct Child {
 
 __global__ void __cluster_dims__(kScanCtas) __launch_bounds__(kScanThreads)
 fork_kernel(int32_t* refs, int32_t num_pages, const PageFork f, int32_t* scratch, int32_t* err) {
-    __shared__ ClusterSums sums;
+    __shared__ ClusterSums<3> sums;
     ptx::grid_dependency_wait();
     ptx::grid_dependents_go();
     const WarpPages part(num_pages);
     const int32_t thread = blockIdx.x * kScanThreads + threadIdx.x, threads = kScanCtas * kScanThreads;
     const int32_t c0 = (int32_t)((int64_t)thread * f.n / threads), c1 = (int32_t)((int64_t)(thread + 1) * f.n / threads);
-    int64_t entries = 0, fresh = 0;
+    int64_t v[3] = {0, 0, 0}, all[3];   // table entries, pages to copy, free pages
     bool bad = false;
     for (int32_t c = c0; c < c1; ++c) {
         const Child child(f, c);
-        entries += child.pages;
-        fresh += child.part;
+        v[0] += child.pages;
+        v[1] += child.part;
         bad |= child.bad;
     }
-    int64_t all_entries, all_fresh, free_pages;
-    int64_t at = cluster_prefix(entries, sums, 0, all_entries);
-    int64_t rank = cluster_prefix(fresh, sums, 1, all_fresh);
-    const bool refused = all_entries > f.out_len;
-    const int64_t before = cluster_prefix(refused ? 0 : count_free(refs, num_pages, part), sums, 0, free_pages);
+    v[2] = count_free(refs, num_pages, part);
+    cluster_prefix(v, all, sums);
+    const bool refused = all[0] > f.out_len;
+    const int64_t all_entries = all[0], all_fresh = all[1], free_pages = all[2];
+    int64_t at = v[0], rank = v[1];
     int32_t *dst = scratch + kMoveHead, *src = dst + f.n;
     if (!refused)
-        take_free(refs, num_pages, part, warp_base(before), all_fresh, [&](int64_t r, int32_t page) {
+        take_free(refs, num_pages, part, warp_base(v[2]), all_fresh, [&](int64_t r, int32_t page) {
             dst[r] = page;
             refs[page] = 1;
         });
@@ -249,18 +265,37 @@ fork_kernel(int32_t* refs, int32_t num_pages, const PageFork f, int32_t* scratch
     }
 }
 
-// The first n entries of a child are its parent's own pages, held once more.
+// Entries of a child but for a copied last page are its parent's own pages, held
+// once more.  The search for an entry's child begins in shared memory, in up to
+// kShareOffsets of the children's offsets.
+constexpr int kShareOffsets = 1024;
 __device__ void share_pages(int32_t* refs, int32_t num_pages, const PageFork& f, int32_t* err, int32_t block, int32_t blocks) {
+    __shared__ int32_t offsets[kShareOffsets];
+    const int32_t step = (f.n - 1) / kShareOffsets + 1, known = (f.n - 1) / step + 1;   // (n >= 1)
+    for (int32_t k = threadIdx.x; k < known; k += kMoveThreads) offsets[k] = f.indptr_out[k * step];
     const int64_t total = f.indptr_out[f.n];
+    __syncthreads();
     for (int64_t e = (int64_t)block * kMoveThreads + threadIdx.x; e < total; e += (int64_t)blocks * kMoveThreads) {
-        int32_t lo = 0, hi = f.n - 1;   // the last child that begins at or before e
+        int32_t lo = 0, hi = known - 1;   // the last child that begins at or before e
         while (lo < hi) {
             const int32_t mid = lo + (hi - lo + 1) / 2;
-            if (f.indptr_out[mid] <= e) lo = mid;
+            if (offsets[mid] <= e) lo = mid;
             else hi = mid - 1;
         }
+        int32_t first = offsets[lo];
+        lo *= step;
+        hi = min(lo + step, f.n) - 1;
+        while (lo < hi) {
+            const int32_t mid = lo + (hi - lo + 1) / 2, x = f.indptr_out[mid];
+            if (x <= e) {
+                lo = mid;
+                first = x;
+            } else {
+                hi = mid - 1;
+            }
+        }
         const Child child(f, lo);
-        const int32_t j = (int32_t)(e - f.indptr_out[lo]);
+        const int32_t j = (int32_t)(e - first);
         if (j >= child.pages - child.part) continue;   // the copied page: fork_kernel's
         const int32_t page = f.page_table[child.base + j];
         const bool in = page >= 0 && page < num_pages;
@@ -276,14 +311,15 @@ __device__ void share_pages(int32_t* refs, int32_t num_pages, const PageFork& f,
 // used ones from U on, highest first.
 __global__ void __cluster_dims__(kScanCtas) __launch_bounds__(kScanThreads)
 compact_kernel(int32_t* refs, int32_t num_pages, int32_t* remap, int32_t* scratch) {
-    __shared__ ClusterSums sums;
+    __shared__ ClusterSums<1> sums, hole_sums;
     ptx::grid_dependency_wait();
     ptx::grid_dependents_go();
     const WarpPages part(num_pages);
     int32_t *dst = scratch + kMoveHead, *src = dst + num_pages / 2;
-    int64_t free_pages, holes = 0, all_holes;
-    int64_t base = warp_base(cluster_prefix(count_free(refs, num_pages, part), sums, 0, free_pages));
-    const int64_t used = num_pages - free_pages;
+    int64_t before[1] = {count_free(refs, num_pages, part)}, all_free[1], holes[1] = {0}, all_holes[1];
+    cluster_prefix(before, all_free, sums);
+    int64_t base = warp_base(before[0]);
+    const int64_t used = num_pages - all_free[0];
     for (int32_t s = part.begin; s < part.end; ++s) {
         int32_t page;
         const uint32_t bits = free_bits(load_counts(refs, num_pages, s, page));
@@ -296,7 +332,7 @@ compact_kernel(int32_t* refs, int32_t num_pages, int32_t* remap, int32_t* scratc
             if (bits >> k & 1) {
                 if (page < used) {
                     dst[rank] = page;
-                    ++holes;
+                    ++holes[0];
                 }
                 ++rank;
                 remap[page] = -1;
@@ -307,10 +343,10 @@ compact_kernel(int32_t* refs, int32_t num_pages, int32_t* remap, int32_t* scratc
             }
         }
     }
-    cluster_prefix(holes, sums, 1, all_holes);   // also: dst and src are complete
+    cluster_prefix(holes, all_holes, hole_sums);   // also: dst and src are complete
     const int32_t thread = blockIdx.x * kScanThreads + threadIdx.x;
-    if (thread == 0) scratch[0] = (int32_t)all_holes;
-    for (int64_t i = thread; i < all_holes; i += kScanCtas * kScanThreads) {
+    if (thread == 0) scratch[0] = (int32_t)all_holes[0];
+    for (int64_t i = thread; i < all_holes[0]; i += kScanCtas * kScanThreads) {
         const int32_t to = dst[i], from = src[i];
         remap[from] = to;
         refs[to] = refs[from];
@@ -335,14 +371,37 @@ __device__ void remap_table(int32_t num_pages, int32_t* table, int64_t entries, 
 
 // ------------------------------------------------------------------------ copy
 
+// What the first CTAs of a copy do: the table that goes with it (kNone: nothing).
+enum class Table { kNone, kShare, kRemap };
+struct TableWork {
+    int32_t blocks;      // CTAs
+    int32_t* refs;       // kShare
+    PageFork fork;
+    int32_t* table;      // kRemap
+    int64_t entries;
+    const int32_t* remap;
+};
+
+template <Table kTable>
 __global__ void __launch_bounds__(kMoveThreads)
 copy_kernel(const __grid_constant__ PagePools pools, int32_t num_pages, const int32_t* src, const int32_t* dst,
-            const int32_t* n_dev, int64_t n, int32_t pieces, int32_t* err) {
+            const int32_t* n_dev, int64_t n, int32_t pieces, int32_t* err, const __grid_constant__ TableWork t) {
     ptx::grid_dependency_wait();
     ptx::grid_dependents_go();
+    if constexpr (kTable != Table::kNone) {
+        if ((int32_t)blockIdx.x < t.blocks) {
+            if constexpr (kTable == Table::kShare)
+                share_pages(t.refs, num_pages, t.fork, err, blockIdx.x, t.blocks);
+            else
+                remap_table(num_pages, t.table, t.entries, t.remap, err, blockIdx.x, t.blocks);
+            return;
+        }
+    }
+    const int32_t block = kTable == Table::kNone ? blockIdx.x : blockIdx.x - t.blocks;
+    const int32_t blocks = kTable == Table::kNone ? gridDim.x : gridDim.x - t.blocks;
     if (n_dev) n = min(n, (int64_t)*n_dev);
     const int64_t per_page = (int64_t)pools.n * pieces, units = n * per_page;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    for (int64_t u = block; u < units; u += blocks) {
         const int64_t i = u / per_page;
         const int32_t x = (int32_t)(u - i * per_page), k = x / pieces, piece = x - k * pieces;
         const int64_t bytes = pools.bytes[k], off = (int64_t)piece * kMoveBytes;
@@ -366,29 +425,30 @@ copy_kernel(const __grid_constant__ PagePools pools, int32_t num_pages, const in
     }
 }
 
-__global__ void __launch_bounds__(kMoveThreads)
-share_kernel(int32_t* refs, int32_t num_pages, const PageFork f, int32_t* err) {
-    ptx::grid_dependency_wait();
-    ptx::grid_dependents_go();
-    share_pages(refs, num_pages, f, err, blockIdx.x, gridDim.x);
-}
-
-__global__ void __launch_bounds__(kMoveThreads)
-remap_kernel(int32_t num_pages, int32_t* table, int64_t entries, const int32_t* remap, int32_t* err) {
-    ptx::grid_dependency_wait();
-    ptx::grid_dependents_go();
-    remap_table(num_pages, table, entries, remap, err, blockIdx.x, gridDim.x);
-}
-
-// CTAs for `work` items of a CTA each, at most `per_sm` per SM; 0: no device.
-int grid_for(int64_t work, int per_sm) {
+// CTAs for `work` items of a CTA each; 0: no device.
+int grid_for(int64_t work) {
     int32_t sms = 0;
     if (!current_sm_count(&sms)) return 0;
-    const int64_t cap = (int64_t)sms * per_sm;
+    const int64_t cap = (int64_t)sms * kMoveCtasPerSm;
     return (int)(work < cap ? work : cap);
 }
 
 attn_status done(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+
+template <Table kTable>
+attn_status copy(const PagePools& pools, int32_t num_pages, const int32_t* src, const int32_t* dst, const int32_t* n,
+                 int64_t n_max, int32_t* err, TableWork t, int64_t entries, cudaStream_t stream) {
+    int64_t largest = 0;
+    for (int32_t k = 0; k < pools.n; ++k) largest = pools.bytes[k] > largest ? pools.bytes[k] : largest;
+    const int64_t pieces = (largest + kMoveBytes - 1) / kMoveBytes, work = n_max * pools.n * pieces;
+    const int64_t table_work = kTable == Table::kNone ? 0 : (entries + kMoveThreads - 1) / kMoveThreads;
+    if (work + table_work == 0) return ATTN_OK;
+    const int grid = grid_for(work);
+    t.blocks = grid_for(table_work);
+    if (grid + t.blocks == 0) return ATTN_ERR_CUDA;
+    return done(launch_dependent(copy_kernel<kTable>, dim3(grid + t.blocks), kMoveThreads, 0, stream, pools, num_pages, src,
+                                 dst, n, n_max, (int32_t)pieces, err, t));
+}
 
 }  // namespace
 
@@ -399,44 +459,38 @@ attn_status launch_pages_alloc(int32_t* refs, int32_t num_pages, int32_t n, int3
 
 attn_status launch_pages_free(int32_t* refs, int32_t num_pages, const int32_t* page_ids, int64_t n, int32_t* err,
                               cudaStream_t stream) {
-    const int grid = grid_for((n + kMoveThreads - 1) / kMoveThreads, kMoveCtasPerSm);
+    const int grid = grid_for((n + kMoveThreads - 1) / kMoveThreads);
     if (grid == 0) return ATTN_ERR_CUDA;
     return done(launch_dependent(free_kernel, dim3(grid), kMoveThreads, 0, stream, refs, num_pages, page_ids, n, err));
 }
 
-attn_status launch_pages_fork(int32_t* refs, int32_t num_pages, const PageFork& f, int32_t* scratch, int32_t* err,
-                              cudaStream_t stream) {
-    if (cudaError_t e = launch_dependent(fork_kernel, dim3(kScanCtas), kScanThreads, 0, stream, refs, num_pages, f, scratch, err);
-        e != cudaSuccess)
+attn_status launch_pages_copy(const PagePools& pools, int32_t num_pages, const int32_t* src, const int32_t* dst,
+                              const int32_t* n, int64_t n_max, int32_t* err, cudaStream_t stream) {
+    return copy<Table::kNone>(pools, num_pages, src, dst, n, n_max, err, {}, 0, stream);
+}
+
+attn_status launch_pages_fork(int32_t* refs, int32_t num_pages, const PageFork& f, const PagePools& pools,
+                              int32_t* scratch, int32_t* err, cudaStream_t stream) {
+    if (launch_dependent(fork_kernel, dim3(kScanCtas), kScanThreads, 0, stream, refs, num_pages, f, scratch, err) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    if (f.out_len == 0) return ATTN_OK;
-    const int grid = grid_for((f.out_len + kMoveThreads - 1) / kMoveThreads, kMoveCtasPerSm);
-    if (grid == 0) return ATTN_ERR_CUDA;
-    return done(launch_dependent(share_kernel, dim3(grid), kMoveThreads, 0, stream, refs, num_pages, f, err));
+    if (f.n == 0) return ATTN_OK;
+    TableWork t = {};
+    t.refs = refs;
+    t.fork = f;
+    const int32_t* dst = scratch + kMoveHead;
+    return copy<Table::kShare>(pools, num_pages, dst + f.n, dst, scratch, f.n, err, t, f.out_len, stream);
 }
 
 attn_status launch_pages_compact(int32_t* refs, int32_t num_pages, int32_t* page_table, int64_t entries, int32_t* remap,
-                                 int32_t* scratch, int32_t* err, cudaStream_t stream) {
-    if (cudaError_t e = launch_dependent(compact_kernel, dim3(kScanCtas), kScanThreads, 0, stream, refs, num_pages,
-                                         remap, scratch);
-        e != cudaSuccess)
+                                 const PagePools& pools, int32_t* scratch, int32_t* err, cudaStream_t stream) {
+    if (launch_dependent(compact_kernel, dim3(kScanCtas), kScanThreads, 0, stream, refs, num_pages, remap, scratch) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    if (entries == 0) return ATTN_OK;
-    const int grid = grid_for((entries + kMoveThreads - 1) / kMoveThreads, kMoveCtasPerSm);
-    if (grid == 0) return ATTN_ERR_CUDA;
-    return done(launch_dependent(remap_kernel, dim3(grid), kMoveThreads, 0, stream, num_pages, page_table, entries,
-                                 static_cast<const int32_t*>(remap), err));
-}
-
-attn_status launch_pages_copy(const PagePools& pools, int32_t num_pages, const int32_t* src, const int32_t* dst,
-                              const int32_t* n, int64_t n_max, int32_t* err, cudaStream_t stream) {
-    int64_t largest = 0;
-    for (int32_t k = 0; k < pools.n; ++k) largest = pools.bytes[k] > largest ? pools.bytes[k] : largest;
-    const int64_t pieces = (largest + kMoveBytes - 1) / kMoveBytes;
-    const int grid = grid_for(n_max * pools.n * pieces, kMoveCtasPerSm);
-    if (grid == 0) return ATTN_ERR_CUDA;
-    return done(launch_dependent(copy_kernel, dim3(grid), kMoveThreads, 0, stream, pools, num_pages, src, dst, n, n_max,
-                                 (int32_t)pieces, err));
+    TableWork t = {};
+    t.table = page_table;
+    t.entries = entries;
+    t.remap = remap;
+    const int32_t* dst = scratch + kMoveHead;
+    return copy<Table::kRemap>(pools, num_pages, dst + num_pages / 2, dst, scratch, num_pages / 2, err, t, entries, stream);
 }
 
 }  // namespace attn

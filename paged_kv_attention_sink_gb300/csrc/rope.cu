@@ -10,12 +10,16 @@
 // of a turn at the farthest position), by one integer product.  Its upper 32
 // bits, as a signed number of half turns, go to sincospif.
 //
-// Memory-bound: each row is read and written once, in 16-byte chunks.  A row's
-// angles are the same for all heads, so a CTA takes a few whole rows, computes
-// their cosines and sines into shared memory (one or two per thread) while the
-// first rows' loads are on their way, and each thread then turns 8 pairs at a
-// time: two 16-byte chunks, which hold the pairs' halves (chunk i and the one
-// half the turned width on) or, with neighbouring dims paired, 4 pairs each.
+// Memory-bound: each row is read and written once, in 16-byte chunks.  A thread
+// turns 8 pairs at a time, an item: two chunks, which hold the pairs' halves (chunk
+// i and the one half the turned width on) or, with neighbouring dims paired, 4
+// pairs each.  All rows' items, head by head, are one long list, of which a CTA has
+// 1,024, four per thread, loaded at once: every thread of every CTA has the same
+// work, wherever the rows begin.  (CTAs of whole rows left the last of their items
+// to a quarter of their loads.)  A row's angles are the same for all heads: a CTA
+// computes its one to fourteen rows' cosines and sines into shared memory while its
+// loads are on their way.
+#include <algorithm>
 #include <cstdint>
 
 #include "attn_internal.h"
@@ -27,13 +31,14 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeUnroll = 4;    // items of a thread whose loads are in flight together
-constexpr int kRopeMaxRows = 8;   // rows of a CTA
+constexpr int kRopeItems = kRopeThreads * kRopeUnroll;   // of a CTA
+constexpr int kRopeMaxRows = 16;  // rows that a CTA's items may lie in
 
 struct RopeArgs {
     RopeTable t;
     const int32_t* positions;   // [n_axes][rows]
     int64_t rows;
-    int32_t rows_per_cta, Hq, Hkv, inverse;
+    int32_t items, Hq, Hkv, inverse;   // items: of a CTA
     const uint4 *q, *k, *v;
     uint4 *q_out, *k_out;       // k_out: the page pool where kCache
     int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;   // 16-byte chunks
@@ -72,17 +77,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     __shared__ float4 cs_s[kRopeMaxRows * D / 4];        // [row][pair pair][item]: (cos, sin) of two pairs
     __shared__ int64_t page_s[kRopeMaxRows];             // kCache: first chunk of the row in its page's K, or -1
     const int tid = threadIdx.x;
-    const int64_t row0 = (int64_t)blockIdx.x * a.rows_per_cta;
-    const int rows = (int)min((int64_t)a.rows_per_cta, a.rows - row0);
     const int turned = a.t.pairs / 8;                    // items of a head that turn
-    const int heads = a.Hq + a.Hkv * (kCache ? 2 : 1), per_row = heads * kItems, n = rows * per_row;
+    const int heads = a.Hq + a.Hkv * (kCache ? 2 : 1), per_row = heads * kItems;
+    const int64_t first = (int64_t)blockIdx.x * a.items, row0 = first / per_row;
+    const int skip = (int)(first - row0 * per_row);      // items of row 0 before the CTA's
+    const int n = (int)min((int64_t)a.items, a.rows * per_row - first), rows = (skip + n - 1) / per_row + 1;
 
     // Where item x lies: the head's first chunk, and the two chunks of the item.
     auto locate = [&](int x, int& r, int& h, int& i, int& c0, int& c1) {
-        r = x / per_row;
-        const int y = x - r * per_row;
-        h = y / kItems;
-        i = y % kItems;
+        const int y = skip + x;
+        r = y / per_row;
+        const int z = y - r * per_row;
+        h = z / kItems;
+        i = z % kItems;
         const bool apart = !kInter && i < turned && h < a.Hq + a.Hkv;
         c0 = apart ? i : 2 * i;
         c1 = apart ? i + turned : 2 * i + 1;
@@ -144,24 +151,22 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     }
     __syncthreads();
 
-    for (int x = tid; x < n; x += kRopeUnroll * kRopeThreads) {
-        if (x != tid) {
 #pragma unroll
-            for (int u = 0; u < kRopeUnroll; ++u)
-                if (x + u * kRopeThreads < n) load(x + u * kRopeThreads, lo[u], hi[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u)
-            if (x + u * kRopeThreads < n) store(x + u * kRopeThreads, lo[u], hi[u]);
-    }
+    for (int u = 0; u < kRopeUnroll; ++u)
+        if (tid + u * kRopeThreads < n) store(tid + u * kRopeThreads, lo[u], hi[u]);
 }
 
 template <int D, bool kInter, bool kCache>
 attn_status launch(RopeArgs& a, cudaStream_t stream) {
     int32_t sms = 0;
     if (!current_sm_count(&sms)) return ATTN_ERR_CUDA;
-    a.rows_per_cta = a.rows <= 8 * (int64_t)sms ? 1 : 4;
-    const int64_t ctas = (a.rows + a.rows_per_cta - 1) / a.rows_per_cta;
+    // One item per thread where that leaves no SM with more than a few CTAs: the
+    // smallest calls are over sooner.
+    const int64_t per_row = (int64_t)(a.Hq + a.Hkv * (kCache ? 2 : 1)) * (D / 16), total = a.rows * per_row;
+    const int64_t most = total <= 4 * (int64_t)sms * kRopeThreads ? kRopeThreads : kRopeItems;
+    a.items = (int32_t)std::min<int64_t>(most, (kRopeMaxRows - 2) * per_row);
+    const int64_t ctas = (total + a.items - 1) / a.items;
+    if (ctas > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
     return launch_dependent(rope_kernel<D, kInter, kCache>, dim3((unsigned)ctas), kRopeThreads, 0, stream, a) == cudaSuccess
                ? ATTN_OK
                : ATTN_ERR_CUDA;

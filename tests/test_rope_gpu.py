@@ -45,7 +45,7 @@ CASES = [  # rows, Hq, Hkv, D, rot, axes, interleaved, inverse, scale, slack
     (7, 12, 3, 128, 112, 3, False, False, 1.25, 24),
     (65, 16, 16, 64, 48, 4, True, False, 0.5, 0),
     (130, 64, 8, 64, 64, 1, True, True, 1.0, 136),
-    (1217, 4, 4, 128, 96, 8, False, True, 1.0, 8),         # four rows per CTA from 1,217 rows on
+    (1217, 4, 4, 128, 96, 8, False, True, 1.0, 8),
     (1221, 3, 1, 128, 16, 3, True, False, 2.0, 0),
     (1500, 64, 4, 128, 128, 3, False, False, 1.0, 0),
 ]
