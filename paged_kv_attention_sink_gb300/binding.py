@@ -134,6 +134,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # (the tensors' CUDA is initialised)
 
 
 def _stream_ptr(stream=None):
@@ -146,6 +147,9 @@ def _stream_ptr(stream=None):
 
 def _check_cuda(device, name, t, dtype, shape=None):
     """t must be a contiguous CUDA tensor of dtype (and shape) on `device`, an ordinal."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.get_device() == device
+            and t.is_contiguous() and (shape is None or t.shape == shape)):
+        return
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous {dtype} CUDA tensor")
     if shape is not None and t.shape != shape:
@@ -159,10 +163,12 @@ def _launch_on(device, stream, fn_name, *args):
     runs, and the current stream is looked up, on the device that holds the
     tensors."""
     fn = getattr(_lib, fn_name)
-    if device != torch.cuda.current_device():
+    if device != _current_device():
         with torch.cuda.device(device):
             return _check(fn_name, fn(*args, _stream_ptr(stream)))
-    _check(fn_name, fn(*args, _stream_ptr(stream)))
+    status = fn(*args, _raw_stream(device) if stream is None and _raw_stream is not None else _stream_ptr(stream))
+    if status != 0:
+        _check(fn_name, status)
 
 
 def _empty_on(stream, shape, dtype, device):
@@ -186,6 +192,11 @@ def kv4_cache_shape(num_pages: int, num_kv_heads: int, page_size: int, head_dim:
 def _row_stride(device, name, t, rows, heads, head_dim):
     """Row stride (elements) of t, bf16 [rows, heads, head_dim] on `device`: rows may lie apart
     (slices of a fused projection), the heads of a row are contiguous."""
+    if (rows > 1 and isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.bfloat16
+            and t.get_device() == device and t.shape == (rows, heads, head_dim)):
+        row, head, dim = t.stride()
+        if dim == 1 and head == head_dim and row % 8 == 0 and row >= heads * head_dim:
+            return row
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16):
         raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
     if t.shape != (rows, heads, head_dim):

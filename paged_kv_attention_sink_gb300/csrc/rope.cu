@@ -31,14 +31,13 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeUnroll = 4;    // items of a thread whose loads are in flight together
-constexpr int kRopeItems = kRopeThreads * kRopeUnroll;   // of a CTA
 constexpr int kRopeMaxRows = 16;  // rows that a CTA's items may lie in
 
 struct RopeArgs {
     RopeTable t;
     const int32_t* positions;   // [n_axes][rows]
     int64_t rows;
-    int32_t items, Hq, Hkv, inverse;   // items: of a CTA
+    int32_t heads, Hq, Hkv, inverse;   // heads: of a CTA
     const uint4 *q, *k, *v;
     uint4 *q_out, *k_out;       // k_out: the page pool where kCache
     int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;   // 16-byte chunks
@@ -76,66 +75,56 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     constexpr int kItems = D / 16;                       // items of a head: 16 dims each
     __shared__ float4 cs_s[kRopeMaxRows * D / 4];        // [row][pair pair][item]: (cos, sin) of two pairs
     __shared__ int64_t page_s[kRopeMaxRows];             // kCache: first chunk of the row in its page's K, or -1
-    const int tid = threadIdx.x;
+    // A thread's items lie at the same place in their heads, kStep heads apart.
+    constexpr int kStep = kRopeThreads / kItems;
+    const int tid = threadIdx.x, i = tid % kItems;
     const int turned = a.t.pairs / 8;                    // items of a head that turn
-    const int heads = a.Hq + a.Hkv * (kCache ? 2 : 1), per_row = heads * kItems;
-    const int64_t first = (int64_t)blockIdx.x * a.items, row0 = first / per_row;
-    const int skip = (int)(first - row0 * per_row);      // items of row 0 before the CTA's
-    const int n = (int)min((int64_t)a.items, a.rows * per_row - first), rows = (skip + n - 1) / per_row + 1;
-
-    // Where item x lies: the head's first chunk, and the two chunks of the item.
-    auto locate = [&](int x, int& r, int& h, int& i, int& c0, int& c1) {
-        const int y = skip + x;
-        r = y / per_row;
-        const int z = y - r * per_row;
-        h = z / kItems;
-        i = z % kItems;
-        const bool apart = !kInter && i < turned && h < a.Hq + a.Hkv;
-        c0 = apart ? i : 2 * i;
-        c1 = apart ? i + turned : 2 * i + 1;
-    };
-    auto load = [&](int x, uint4& lo, uint4& hi) {
-        int r, h, i, c0, c1;
-        locate(x, r, h, i, c0, c1);
-        const int64_t row = row0 + r;
-        const uint4* src = h < a.Hq ? a.q + row * a.q_stride + h * (D / 8)
-                           : h < a.Hq + a.Hkv ? a.k + row * a.k_stride + (h - a.Hq) * (D / 8)
-                                              : a.v + row * a.v_stride + (h - a.Hq - a.Hkv) * (D / 8);
-        lo = src[c0];
-        hi = src[c1];
-    };
-    auto store = [&](int x, uint4 lo, uint4 hi) {
-        int r, h, i, c0, c1;
-        locate(x, r, h, i, c0, c1);
-        if (h < a.Hq + a.Hkv && i < turned) turn<kInter>(lo, hi, cs_s + r * (D / 4) + i, turned);
-        const int64_t row = row0 + r;
-        uint4* dst;
-        if (h < a.Hq) {
-            dst = a.q_out + row * a.q_out_stride + h * (D / 8);
-        } else if constexpr (kCache) {
-            if (page_s[r] < 0) return;
-            dst = a.k_out + page_s[r] + (int64_t)(h - a.Hq) * a.P * (D / 8);   // V's heads follow K's
-        } else {
-            dst = a.k_out + row * a.k_out_stride + (h - a.Hq) * (D / 8);
-        }
-        dst[c0] = lo;
-        dst[c1] = hi;
-    };
+    const int heads = a.Hq + a.Hkv * (kCache ? 2 : 1);
+    const uint64_t first = (uint64_t)blockIdx.x * a.heads;   // the CTA's heads, counted through the rows
+    const int64_t row0 = first >> 32 ? (int64_t)(first / (uint32_t)heads) : (int64_t)((uint32_t)first / (uint32_t)heads);
+    const int skip = (int)(first - (uint64_t)row0 * heads);  // heads of row 0 before them
+    const int n = (int)min((int64_t)a.heads, a.rows * heads - (int64_t)first), rows = (skip + n - 1) / heads + 1;
+    const int step_rows = kStep / heads, step_heads = kStep - step_rows * heads;
+    const int y = skip + tid / kItems, r0 = y / heads, h0 = y - r0 * heads;
+    const bool turns = i < turned;
+    const int c0 = !kInter && turns ? i : 2 * i, c1 = !kInter && turns ? i + turned : 2 * i + 1;   // chunks of the item
 
     ptx::grid_dependency_wait();
     ptx::grid_dependents_go();
     uint4 lo[kRopeUnroll], hi[kRopeUnroll];
+    {
+        int r = r0, h = h0;
 #pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u)
-        if (tid + u * kRopeThreads < n) load(tid + u * kRopeThreads, lo[u], hi[u]);
+        for (int u = 0; u < kRopeUnroll; ++u) {
+            if (tid / kItems + u * kStep < n) {
+                const int64_t row = row0 + r;
+                if (kCache && h >= a.Hq + a.Hkv) {
+                    const uint4* src = a.v + row * a.v_stride + (h - a.Hq - a.Hkv) * (D / 8);
+                    lo[u] = src[2 * i];
+                    hi[u] = src[2 * i + 1];
+                } else {
+                    const uint4* src = h < a.Hq ? a.q + row * a.q_stride + h * (D / 8)
+                                                : a.k + row * a.k_stride + (h - a.Hq) * (D / 8);
+                    lo[u] = src[c0];
+                    hi[u] = src[c1];
+                }
+            }
+            r += step_rows;
+            h += step_heads;
+            if (h >= heads) {
+                h -= heads;
+                ++r;
+            }
+        }
+    }
 
     for (int x = tid; x < rows * a.t.pairs; x += kRopeThreads) {
         const int r = x / a.t.pairs, p = x - r * a.t.pairs;
         int64_t pos = a.positions[a.t.axis[p] * a.rows + row0 + r];
         if (a.inverse) pos = -pos;
-        const uint64_t turns = (uint64_t)pos * a.t.freq[p];
+        const uint64_t angle = (uint64_t)pos * a.t.freq[p];
         float s, c;
-        sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
+        sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &s, &c);
         const int item = p >> 3, j = p & 7;
         reinterpret_cast<float2*>(cs_s)[(r * (D / 4) + (j >> 1) * turned + item) * 2 + (j & 1)] =
             make_float2(c * a.t.scale, s * a.t.scale);
@@ -151,9 +140,31 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     }
     __syncthreads();
 
+    int r = r0, h = h0;
 #pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u)
-        if (tid + u * kRopeThreads < n) store(tid + u * kRopeThreads, lo[u], hi[u]);
+    for (int u = 0; u < kRopeUnroll; ++u) {
+        if (tid / kItems + u * kStep < n) {
+            const bool is_v = kCache && h >= a.Hq + a.Hkv;
+            if (turns && !is_v) turn<kInter>(lo[u], hi[u], cs_s + r * (D / 4) + i, turned);
+            uint4* dst;
+            if (h < a.Hq)
+                dst = a.q_out + (row0 + r) * a.q_out_stride + h * (D / 8);
+            else if constexpr (kCache)
+                dst = page_s[r] < 0 ? nullptr : a.k_out + page_s[r] + (int64_t)(h - a.Hq) * a.P * (D / 8);   // V's heads follow K's
+            else
+                dst = a.k_out + (row0 + r) * a.k_out_stride + (h - a.Hq) * (D / 8);
+            if (!kCache || dst != nullptr) {
+                dst[is_v ? 2 * i : c0] = lo[u];
+                dst[is_v ? 2 * i + 1 : c1] = hi[u];
+            }
+        }
+        r += step_rows;
+        h += step_heads;
+        if (h >= heads) {
+            h -= heads;
+            ++r;
+        }
+    }
 }
 
 template <int D, bool kInter, bool kCache>
@@ -162,10 +173,10 @@ attn_status launch(RopeArgs& a, cudaStream_t stream) {
     if (!current_sm_count(&sms)) return ATTN_ERR_CUDA;
     // One item per thread where that leaves no SM with more than a few CTAs: the
     // smallest calls are over sooner.
-    const int64_t per_row = (int64_t)(a.Hq + a.Hkv * (kCache ? 2 : 1)) * (D / 16), total = a.rows * per_row;
-    const int64_t most = total <= 4 * (int64_t)sms * kRopeThreads ? kRopeThreads : kRopeItems;
-    a.items = (int32_t)std::min<int64_t>(most, (kRopeMaxRows - 2) * per_row);
-    const int64_t ctas = (total + a.items - 1) / a.items;
+    const int64_t heads = (int64_t)a.Hq + a.Hkv * (kCache ? 2 : 1), total = a.rows * heads;
+    const int64_t step = kRopeThreads / (D / 16), most = total <= 4 * sms * step ? step : kRopeUnroll * step;
+    a.heads = (int32_t)std::min<int64_t>(most, (kRopeMaxRows - 2) * heads);
+    const int64_t ctas = (total + a.heads - 1) / a.heads;
     if (ctas > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
     return launch_dependent(rope_kernel<D, kInter, kCache>, dim3((unsigned)ctas), kRopeThreads, 0, stream, a) == cudaSuccess
                ? ATTN_OK
