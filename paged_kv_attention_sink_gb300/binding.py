@@ -288,6 +288,8 @@ class PagePool:
         if page_size < 1:
             raise ValueError("page_size must be positive")
         first = self.pools[0]
+        if not 0 < first.shape[0] < 1 << 31:
+            raise ValueError("a pool must have 1 to 2^31 - 1 pages")
         self.num_pages, self.page_size, self._dev, self._device = first.shape[0], int(page_size), first.get_device(), first.device
         n = len(self.pools)
         self._ptrs, self._bytes = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)()
@@ -712,6 +714,8 @@ class CrossPlan(Plan):
                  workspace: Optional[torch.Tensor] = None):
         lib = load_library()
         self._handle = None
+        if not 0 <= kv_rows < 1 << 31 or any(np.any(np.asarray(x) > 0x7fffffff) for x in (qo_indptr, kv_start, kv_len)):
+            raise ValueError("rows and lengths must be below 2^31")
         qo, start, lens = _i32_host(qo_indptr), _i32_host(kv_start), _i32_host(kv_len)
         self.batch = max(0, len(qo) - 1)
         if len(start) != self.batch or len(lens) != self.batch:

@@ -284,7 +284,7 @@ __device__ void share_pages(int32_t* refs, int32_t num_pages, const PageFork& f,
         }
         int32_t first = offsets[lo];
         lo *= step;
-        hi = min(lo + step, f.n) - 1;
+        hi = (int32_t)min((int64_t)lo + step, (int64_t)f.n) - 1;
         while (lo < hi) {
             const int32_t mid = lo + (hi - lo + 1) / 2, x = f.indptr_out[mid];
             if (x <= e) {

@@ -75,6 +75,10 @@ def test_the_binding_refuses_the_other_calls():
         empty.kv_lens
     with pytest.raises(ValueError):
         binding.CrossPlan([0, 1], [0, 0], [1, 1], 4, 8, 2, 64)
+    for bad in (dict(kv_rows=2 ** 31), dict(kv_rows=-1), dict(kv_start=[2 ** 32]), dict(kv_len=[2 ** 31])):
+        with pytest.raises(ValueError):
+            binding.CrossPlan(**{**dict(qo_indptr=[0, 1], kv_start=[0], kv_len=[1], kv_rows=4, num_qo_heads=8, num_kv_heads=2,
+                                        head_dim=64), **bad})
 
 
 @pytest.mark.parametrize("sms", [152, 4])

@@ -201,6 +201,16 @@ def test_other_tensors_strides_and_streams_through_one_plan():
     assert torch.equal(other, out)
 
 
+def test_outputs_that_start_in_the_middle_of_a_sector():
+    qo, kv = [3, 90, 40], [50, 333, 5000]
+    plan, (q, k, v, s), out, lse = check(qo, kv, 16, 4, 64, True, seed=10)
+    buf = torch.zeros(out.numel() + 16, dtype=torch.bfloat16, device="cuda")
+    mine = buf[8:8 + out.numel()].view(out.shape)
+    assert mine.data_ptr() % 32 == 16
+    plan.attend(q, k, v, s, mine)
+    assert torch.equal(mine, out) and not buf[:8].any() and not buf[-8:].any()
+
+
 def test_captured_and_replayed():
     qo, kv = [1, 5, 200, 2], [70, 9000, 300, 0]
     plan, (q, k, v, s), out, lse = check(qo, kv, 16, 4, 64, True, seed=9)

@@ -137,6 +137,21 @@ def test_fork(num_pages, used, batch, children, page_size):
     same(mine, plain)
 
 
+def test_fork_and_compact_in_more_pools_than_a_launch_holds():
+    rng = np.random.default_rng(20)
+    table, indptr, lens, refs = ref.random_state(rng, 60, 30, 6, 16)
+    mine, plain = pair(rng, 60, 16, refs, (4, 12, 8, 4100) * 34)
+    out, _ = fork_both(mine, plain, table, indptr, lens, [0, 1, 2, 3, 4, 5, 5, 5])
+    same(mine, plain)
+    mine.free(dev(table))
+    plain.free(table.tolist())
+    got = dev(out)
+    remap = mine.compact(got)
+    want, want_remap = plain.compact(out)
+    assert got.tolist() == want and remap.tolist() == want_remap
+    same(mine, plain)
+
+
 def test_fork_takes_a_prefix_and_ignores_spare_pages():
     rng = np.random.default_rng(3)
     table, refs = np.array([7, 3, 9, 1]), np.zeros(12, int)
