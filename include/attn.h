@@ -215,8 +215,9 @@ ATTN_API attn_status attn_prefill_ragged(attn_plan_t plan, const void* q, const 
  *              may be NULL, where kv_rows = 0.
  *   head_dim in {64, 128}; num_qo_heads % num_kv_heads == 0; rows * Hq and kv_rows
  *   below 2^30 (else ATTN_ERR_UNSUPPORTED)
- * Workspace, binding and error word as for attn_plan; every other launch refuses
- * such a plan (ATTN_ERR_INVALID_ARG).  attn_cross writes all rows of out and lse.
+ * Workspace, binding and error word as for attn_plan (attn_plan_info: num_decode_units
+ * counts the work of few rows, num_prefill_items that of many); every other launch
+ * refuses such a plan (ATTN_ERR_INVALID_ARG).  attn_cross writes all rows of out and lse.
  * The order of every sum is fixed.  Async on `stream`; capturable (after one
  * uncaptured call with these pointers has built the TMA descriptors).
  */

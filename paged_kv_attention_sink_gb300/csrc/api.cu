@@ -517,7 +517,7 @@ attn_status rope_table(const attn_rope_spec* r, int32_t head_dim, attn::RopeTabl
     for (int p = 0; p < t.pairs; ++p) {
         const int32_t axis = r->axis ? r->axis[p] : 0;
         if (axis < 0 || axis >= r->n_axes || !(std::fabs(r->inv_freq[p]) < 0x1p20f)) return ATTN_ERR_INVALID_ARG;
-        t.axis[p] = (uint8_t)axis;
+        t.axes[p / 16] |= (uint64_t)axis << p % 16 * 4;
         t.freq[p] = turns_of(r->inv_freq[p]);
     }
     return ATTN_OK;

@@ -23,6 +23,13 @@
 //  * A chunk's state goes to the workspace; a small kernel joins the chunks.  (With
 //    the last CTA of a sequence joining them, 50 chunks of 32 pairs took some 15 us,
 //    one CTA reading after the other; joined by many CTAs, 4.)
+//
+// Measured: 48 x 5 beams over 1,500 keys of 16 heads x 64 dims (295 MB) 45 us, 6.6 TB/s;
+// 16 rows over 2K-32K keys, 16 query heads on each of 4 KV heads x 128 dims (644 MB) 98,
+// 6.6 TB/s (0.97 of the copy rate; issue 21%, tensor pipe 19%).  Small calls are the
+// latency of one kernel, 2.6 us in a graph.  With 32 pairs it takes a tenth to a
+// fifth longer than with 16: both read the same, and a warp's products and softmax
+// double.
 #include <cuda.h>
 
 #include "attn_internal.h"

@@ -77,11 +77,11 @@ attn_status launch_evict(attn_plan_s* plan, bool four, const float* weights, con
                          void* pool_out, float* weights_out, cudaStream_t stream);
 
 // Rotary positions (rope.cu).  freq: each pair's frequency in turns, a 64-bit
-// fixed-point fraction; axis: which row of positions it takes.
+// fixed-point fraction; axes: which row of positions it takes, 4 bits each.
 constexpr int kRopeMaxPairs = 64;
 struct RopeTable {
     uint64_t freq[kRopeMaxPairs];
-    uint8_t axis[kRopeMaxPairs];
+    uint64_t axes[kRopeMaxPairs / 16];
     int32_t pairs;   // a multiple of 8
     float scale;
 };

@@ -17,8 +17,16 @@
 // 1,024, four per thread, loaded at once: every thread of every CTA has the same
 // work, wherever the rows begin.  (CTAs of whole rows left the last of their items
 // to a quarter of their loads.)  A row's angles are the same for all heads: a CTA
-// computes its one to fourteen rows' cosines and sines into shared memory while its
-// loads are on their way.
+// computes its rows' cosines and sines (up to 63 rows', where they have few heads)
+// into shared memory while its loads are on their way.
+//
+// Measured: 18K rows of 72 heads of 128 dims with their pages (733 MB) 107 us, 6.9
+// TB/s, the copy rate (issue 68% of the slots); 123 with CTAs of whole rows; 118 with
+// the pages looked up after the angles and a pair's frequency and axis read from
+// the parameters by each lane (its own: 32 reads one after the other), 123 and 135
+// with 2 and 6 items per thread then.  Rows of 2 heads of 64 dims are bound by
+// their angles, one of 400K rows in 68 us (195 with those reads).  64 rows: 2.6 us in a
+// graph, a launch and three dependent loads.
 #include <algorithm>
 #include <cstdint>
 
@@ -30,8 +38,9 @@ namespace attn {
 namespace {
 
 constexpr int kRopeThreads = 256;
+static_assert(kRopeThreads / 32 * 8 >= kRopeMaxPairs, "the warps load the table");
 constexpr int kRopeUnroll = 4;    // items of a thread whose loads are in flight together
-constexpr int kRopeMaxRows = 16;  // rows that a CTA's items may lie in
+constexpr int kRopeMaxRows = 64;  // rows that a CTA's items may lie in
 
 struct RopeArgs {
     RopeTable t;
@@ -74,6 +83,7 @@ template <int D, bool kInter, bool kCache>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int kItems = D / 16;                       // items of a head: 16 dims each
     __shared__ float4 cs_s[kRopeMaxRows * D / 4];        // [row][pair pair][item]: (cos, sin) of two pairs
+    __shared__ uint64_t freq_s[kRopeMaxPairs];
     __shared__ int64_t page_s[kRopeMaxRows];             // kCache: first chunk of the row in its page's K, or -1
     // A thread's items lie at the same place in their heads, kStep heads apart.
     constexpr int kStep = kRopeThreads / kItems;
@@ -91,6 +101,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 
     ptx::grid_dependency_wait();
     ptx::grid_dependents_go();
+    int2 slot = make_int2(0, 0);   // the longest chain of loads begins first
+    if (kCache && tid < rows) slot = a.slots[row0 + tid];
     uint4 lo[kRopeUnroll], hi[kRopeUnroll];
     {
         int r = r0, h = h0;
@@ -118,25 +130,34 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         }
     }
 
-    for (int x = tid; x < rows * a.t.pairs; x += kRopeThreads) {
-        const int r = x / a.t.pairs, p = x - r * a.t.pairs;
-        int64_t pos = a.positions[a.t.axis[p] * a.rows + row0 + r];
+    // A thread has one pair, of every few rows.
+    const int pair_rows = kRopeThreads / a.t.pairs, first_row = tid / a.t.pairs, p = tid - first_row * a.t.pairs;
+    const uint64_t axes = p < 32 ? (p < 16 ? a.t.axes[0] : a.t.axes[1]) : (p < 48 ? a.t.axes[2] : a.t.axes[3]);
+    const int32_t* positions = a.positions + (int64_t)(axes >> (p & 15) * 4 & 15) * a.rows + row0;
+    const bool mine = first_row < pair_rows && first_row < rows;
+    const int32_t first_pos = mine ? positions[first_row] : 0;
+    // The frequencies, from the parameters one at a time, a warp 8 of them: lanes that
+    // read different parameters wait for one another (so the axes are packed).
+    for (int k = 0; k < 8; ++k) {
+        const int x = (tid >> 5) * 8 + k;
+        if ((tid & 31) == 0 && x < a.t.pairs) freq_s[x] = a.t.freq[x];
+    }
+    if (kCache && tid < rows) {
+        const int32_t page = a.page_table[slot.x];
+        const bool in = page >= 0 && page < a.num_pages;
+        if (!in) atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
+        page_s[tid] = in ? ((int64_t)page * 2 * a.Hkv * a.P + slot.y) * (D / 8) : -1;
+    }
+    __syncthreads();
+    for (int r = first_row; mine && r < rows; r += pair_rows) {
+        int64_t pos = r == first_row ? first_pos : positions[r];
         if (a.inverse) pos = -pos;
-        const uint64_t angle = (uint64_t)pos * a.t.freq[p];
+        const uint64_t angle = (uint64_t)pos * freq_s[p];
         float s, c;
         sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &s, &c);
         const int item = p >> 3, j = p & 7;
         reinterpret_cast<float2*>(cs_s)[(r * (D / 4) + (j >> 1) * turned + item) * 2 + (j & 1)] =
             make_float2(c * a.t.scale, s * a.t.scale);
-    }
-    if constexpr (kCache) {
-        if (tid < rows) {
-            const int2 slot = a.slots[row0 + tid];
-            const int32_t page = a.page_table[slot.x];
-            const bool in = page >= 0 && page < a.num_pages;
-            if (!in) atomicOr(a.err, ATTN_DEVICE_ERR_PAGE_ID);
-            page_s[tid] = in ? ((int64_t)page * 2 * a.Hkv * a.P + slot.y) * (D / 8) : -1;
-        }
     }
     __syncthreads();
 

@@ -47,6 +47,8 @@ CASES = [  # rows, Hq, Hkv, D, rot, axes, interleaved, inverse, scale, slack
     (130, 64, 8, 64, 64, 1, True, True, 1.0, 136),
     (1217, 4, 4, 128, 96, 8, False, True, 1.0, 8),
     (1221, 3, 1, 128, 16, 3, True, False, 2.0, 0),
+    (6001, 1, 1, 64, 64, 2, False, False, 1.0, 0),          # few heads: many rows to a CTA
+    (5000, 2, 1, 128, 128, 2, True, True, 1.0, 8),
     (1500, 64, 4, 128, 128, 3, False, False, 1.0, 0),
 ]
 
