@@ -444,7 +444,8 @@ typedef struct {
  *               fused projection are taken as they are.
  *   q_out, k_out  likewise; may be the input itself with the input's stride (in
  *               place), else must not overlap it
- *   head_dim 64 or 128 (else ATTN_ERR_UNSUPPORTED)
+ *   head_dim 64 or 128, rows below 2^31, at most 65,536 heads in all (else
+ *   ATTN_ERR_UNSUPPORTED)
  * Async on `stream`.
  *
  * attn_append_kv_rope -- attn_rope of a step's q and k and attn_append_kv of the
@@ -507,8 +508,9 @@ ATTN_API attn_status attn_append_kv_rope(attn_plan_t plan, const attn_rope_spec*
  *   page_table [table_len], kv_indptr [batch + 1], kv_lens [batch], parents [n]   device int32;
  *                 request p's pages are page_table[kv_indptr[p] ..] as in attn_plan
  *   page_table_out, indptr_out   device int32 [out_len], [n + 1], outputs: child c's
- *                 ceil(kv_lens / page_size) entries from indptr_out[c] on; must
- *                 not overlap the inputs.  Entries past the last are left as they were.
+ *                 ceil(kv_lens / page_size) entries from indptr_out[c] on; must not
+ *                 overlap the inputs (page_table and kv_indptr are compared).  Entries
+ *                 past the last are left as they were.
  *   scratch       device int32 [attn_pages_scratch(n)], for this call alone
  * A child whose parent is not in [0, batch), or whose kv_lens its entries (within
  * table_len) do not hold, gets no pages (ATTN_DEVICE_ERR_PLAN).  Where no free page is left its entry

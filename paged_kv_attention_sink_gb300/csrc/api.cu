@@ -662,6 +662,13 @@ extern "C" attn_status attn_pages_fork(int32_t* refs, int32_t num_pages, const i
                   !aligned4(kv_lens) || !aligned4(parents)))
         return ATTN_ERR_INVALID_ARG;
     if (out_len > 0 && (!page_table_out || !aligned4(page_table_out))) return ATTN_ERR_INVALID_ARG;
+    auto overlap = [](const int32_t* x, int64_t nx, const int32_t* y, int64_t ny) {
+        return nx > 0 && ny > 0 && reinterpret_cast<uintptr_t>(x) < reinterpret_cast<uintptr_t>(y) + ny * sizeof(int32_t) &&
+               reinterpret_cast<uintptr_t>(y) < reinterpret_cast<uintptr_t>(x) + nx * sizeof(int32_t);
+    };
+    if (n > 0 && (overlap(page_table_out, out_len, page_table, table_len) ||
+                  overlap(indptr_out, (int64_t)n + 1, kv_indptr, (int64_t)batch + 1)))
+        return ATTN_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const attn::PageFork f = {page_table, kv_indptr, kv_lens, parents, table_len, batch, n, page_size, page_table_out,
                               indptr_out, out_len};

@@ -118,6 +118,41 @@ def test_many_rows_over_split_keys(Hq, Hkv, D, qo):
     assert info["num_decode_partials"] > 0 and (Hq // Hkv > 128 or info["num_prefill_items"] > 2 * Hkv)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,qo,kv", [(8, 1, 64, 1, 1000003), (2, 1, 128, 150, 200003), (2, 2, 64, 12, 300001)])
+def test_very_long_keys(Hq, Hkv, D, qo, kv):
+    check([qo], [kv], Hq, Hkv, D, True, seed=1, padded=False)
+
+
+def test_states_past_4_gb():
+    """Rows whose offsets pass 32 bits, in bytes and in elements."""
+    rows, Hkv, D = 300000, 64, 128
+    both = torch.empty(rows, 2 * Hkv, D, dtype=torch.bfloat16, device="cuda")       # 9.8 GB
+    g = torch.Generator(device="cuda").manual_seed(3)
+    start, kv = [0, rows - 1000, rows - 77], [100, 900, 77]
+    for s, n in zip(start, kv):
+        both[s:s + n] = torch.randn(n, 2 * Hkv, D, device="cuda", generator=g).to(torch.bfloat16)
+    k, v = both[:, :Hkv], both[:, Hkv:]
+    qo = [2, 70, 1]
+    q = torch.randn(sum(qo), Hkv, D, device="cuda", generator=g).to(torch.bfloat16)
+    plan = binding().CrossPlan(np.concatenate([[0], np.cumsum(qo)]), start, kv, rows, Hkv, Hkv, D)
+    out, _ = plan.attend(q, k, v)
+    want, mag, _ = plain(q, k, v, None, qo, start, kv, D ** -0.5)
+    assert bool(((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -7 + 2.0 ** -10) * mag).all())
+
+
+def test_two_plans_at_once():
+    """Each with its own workspace, on its own stream."""
+    cases = [([3, 200, 1], [9000, 700, 4000]), ([5, 64, 2, 90], [1500, 3000, 64, 5000])]
+    made = [check(qo, kv, 16, 4, 64, True, seed=20 + i) for i, (qo, kv) in enumerate(cases)]
+    streams, outs = [torch.cuda.Stream() for _ in made], []
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = [plan.attend(*x, stream=s)[0] for (plan, x, _, _), s in zip(made, streams)]
+    torch.cuda.synchronize()
+    for out, (plan, _, want, _) in zip(outs, made):
+        assert torch.equal(out, want) and plan.device_error() == 0
+
+
 @pytest.mark.parametrize("G,D", [(1, 64), (3, 64), (5, 128), (32, 64), (48, 64), (64, 64), (96, 128), (127, 64), (128, 64), (160, 64)])
 def test_many_rows_of_every_group(G, D):
     """Slots of 128 / G rows: full ones, ragged ones, output boxes and single rows."""

@@ -28,7 +28,10 @@ def copy(lib, pl=pools(), num_pages=9, src=P, dst=P, n=0, err=P):
     return lib.attn_pages_copy(*pl, num_pages, src, dst, n, err, None)
 
 
-def fork(lib, refs=P, num_pages=9, table=P, table_len=2, indptr=P, lens=P, batch=2, size=16, parents=P, n=1, out=P, out_indptr=P,
+A, B = ctypes.c_void_p(0x30000), ctypes.c_void_p(0x40000)
+
+
+def fork(lib, refs=P, num_pages=9, table=P, table_len=2, indptr=P, lens=P, batch=2, size=16, parents=P, n=1, out=A, out_indptr=B,
          out_len=1, pl=pools(), scratch=P, err=P):
     return lib.attn_pages_fork(refs, num_pages, table, table_len, indptr, lens, batch, size, parents, n, out, out_indptr, out_len, *pl,
                                scratch, err, None)
@@ -56,7 +59,8 @@ def test_bad_state(lib, bad):
     (copy, dict(n=1, src=None)), (copy, dict(n=1, dst=ODD2)), (copy, dict(err=ODD2)), (fork, dict(batch=-1)), (fork, dict(size=0)),
     (fork, dict(n=-1)), (fork, dict(out_len=-1)), (fork, dict(out_len=1 << 31)), (fork, dict(table=None)), (fork, dict(table_len=-1)), (fork, dict(table_len=1 << 31)), (fork, dict(indptr=ODD2)),
     (fork, dict(lens=None)), (fork, dict(parents=None)), (fork, dict(out=None)), (fork, dict(out_indptr=None)),
-    (fork, dict(scratch=None)), (fork, dict(scratch=ODD2)), (compact, dict(n=-1)), (compact, dict(n=1 << 31)),
+    (fork, dict(out=P)), (fork, dict(out=ctypes.c_void_p(0x10004))), (fork, dict(out=ctypes.c_void_p(0xfffc), out_len=2)),
+    (fork, dict(out_indptr=P)), (fork, dict(out_indptr=ctypes.c_void_p(0x10008))), (fork, dict(scratch=None)), (fork, dict(scratch=ODD2)), (compact, dict(n=-1)), (compact, dict(n=1 << 31)),
     (compact, dict(table=None)), (compact, dict(table=ODD2)), (compact, dict(remap=None)), (compact, dict(scratch=None))])
 def test_bad_arguments(lib, call, bad):
     assert call(lib, **bad) == INVALID

@@ -88,6 +88,18 @@ def test_far_and_negative_positions():
     check(out, q, cos, sin, False)
 
 
+def test_rows_further_apart_than_32_bits():
+    buf = torch.zeros((3 << 30) + 4096, dtype=torch.bfloat16, device="cuda")        # 6.4 GB
+    q = torch.as_strided(buf, (4, 3, 64), (1 << 30, 64, 1))
+    q.copy_(rows_of(4, 3, 64, 0, 8))
+    rope = binding().Rope((0.9 ** np.arange(32)).astype(np.float32))
+    pos = torch.tensor([3, 1, 4, 100], dtype=torch.int32, device="cuda")
+    want = rope.apply(pos, q.contiguous())
+    assert torch.equal(rope.apply(pos, q), want)
+    rope.apply(pos, q, q_out=q)
+    assert torch.equal(q, want)
+
+
 def test_it_is_its_gradient_transposed():
     """out = R q, so the gradient of sum(w out) by q is R^T w: against autograd and differences of the 64-bit form."""
     freq = (100.0 ** (-np.arange(24) / 24)).astype(np.float32)
