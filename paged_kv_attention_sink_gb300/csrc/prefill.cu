@@ -50,8 +50,9 @@
 // leave the second slot idle.  Measured: nine prompts of 0.2K-2K rows over up to 6.4K
 // keys, 64 heads on 8 of 64 dims, 645 us, 1,050 TFLOP/s, the chain of a tile (scores'
 // load, exponentials, P, PV) as in prefill.  Slower: the scores released right after
-// their load, the row maximum taken by that load (tcgen05.ld.red), 7%; a row's
-// softmax shared by two warps, four on a scheduler, 20% and 33%.
+// their load, the row maximum taken by that load (tcgen05.ld.red), 7%; halves of a
+// tile at a time 13-15%; a row's softmax shared by two warps, four on a scheduler,
+// 20% and 33%.
 // Every wait is bounded; a timeout sets the device error word.
 #include <cuda.h>
 
