@@ -110,9 +110,9 @@ attn_status build(const int32_t* qo_indptr, const int32_t* kv_start, const int32
             chunk = s;
         }
     }
+    // A block's chunk, for every KV head in turn (its heads' rows lie side by side).
     struct Piece {
-        int32_t size;   // log2 of the block's 16-pair tiles
-        DecodeUnit u;
+        int32_t b, p0, n_pairs, size, chunk, n_chunks, t0, t1, partial0;   // size: log2 of the 16-pair tiles
     };
     std::vector<Piece> pieces;
     int64_t partials = 0;
@@ -121,42 +121,46 @@ attn_status build(const int32_t* qo_indptr, const int32_t* kv_start, const int32
         if (rows == 0 || !few(pairs, kv_len[b])) continue;
         const int64_t stages = stages_of(kv_len[b]), n_chunks = chunks_of(stages, chunk);
         for (int64_t p0 = 0; p0 < pairs; p0 += kCrossBlock) {
-            const int32_t n_pairs = (int32_t)std::min<int64_t>(kCrossBlock, pairs - p0);
-            const int32_t size = n_pairs > 16;
-            for (int32_t g = 0; g < Hkv; ++g) {
-                DecodeUnit u{};
-                u.q_row = qo_indptr[b];
-                u.page_base = kv_start[b];
-                u.kv_head = g;
-                u.head0 = (int32_t)p0;
-                u.n_heads = n_pairs;
-                u.n_chunks = (int32_t)n_chunks;
-                u.group = -1;   // no merge counter
-                u.reserved = pairs > kCrossBlock;   // other blocks read the same keys
-                if (n_chunks > 1) {
-                    u.partial0 = (int32_t)partials;
-                    partials += n_chunks << size;
-                    if (partials > INT32_MAX / kMaxSliceHeads) return ATTN_ERR_UNSUPPORTED;
-                    add_merge(*plan, {u.q_row, g * G, u.head0, n_pairs, u.partial0, (int32_t)n_chunks, 1 << size, 0});
-                }
-                for (int64_t c = 0; c < n_chunks; ++c) {
-                    u.chunk = (int32_t)c;
-                    u.tok_begin = (int32_t)(c * stages / n_chunks * kCrossKeys);
-                    u.tok_end = (int32_t)std::min<int64_t>(kv_len[b], (c + 1) * stages / n_chunks * kCrossKeys);
-                    pieces.push_back({size, u});
-                }
+            Piece p{b, (int32_t)p0, (int32_t)std::min<int64_t>(kCrossBlock, pairs - p0), 0, 0, (int32_t)n_chunks, 0, 0, (int32_t)partials};
+            p.size = p.n_pairs > 16;
+            if (n_chunks > 1) {
+                const int64_t per_head = n_chunks << p.size;
+                partials += per_head * Hkv;
+                if (partials > INT32_MAX / kMaxSliceHeads) return ATTN_ERR_UNSUPPORTED;
+                for (int32_t g = 0; g < Hkv; ++g)
+                    add_merge(*plan, {qo_indptr[b], g * G, p.p0, p.n_pairs, (int32_t)(p.partial0 + g * per_head), p.n_chunks,
+                                      1 << p.size, 0});
+            }
+            for (int64_t c = 0; c < n_chunks; ++c) {
+                p.chunk = (int32_t)c;
+                p.t0 = (int32_t)(c * stages / n_chunks * kCrossKeys);
+                p.t1 = (int32_t)std::min<int64_t>(kv_len[b], (c + 1) * stages / n_chunks * kCrossKeys);
+                pieces.push_back(p);
             }
         }
     }
-    if (pieces.size() > (size_t)INT32_MAX / sizeof(DecodeUnit)) return ATTN_ERR_UNSUPPORTED;
+    if (pieces.size() > (size_t)INT32_MAX / sizeof(DecodeUnit) / Hkv) return ATTN_ERR_UNSUPPORTED;
     std::stable_sort(pieces.begin(), pieces.end(), [](const Piece& x, const Piece& y) {
-        const int32_t a = x.u.tok_end - x.u.tok_begin, b = y.u.tok_end - y.u.tok_begin;
-        return x.size != y.size ? x.size < y.size : a > b;   // longest first
+        return x.size != y.size ? x.size < y.size : x.t1 - x.t0 > y.t1 - y.t0;   // longest first
     });
-    plan->units.reserve(pieces.size());
+    plan->units.reserve(pieces.size() * Hkv);
     for (const Piece& p : pieces) {
-        plan->units.push_back(p.u);
-        ++plan->cross_units[p.size];
+        DecodeUnit u{};
+        u.q_row = qo_indptr[p.b];
+        u.page_base = kv_start[p.b];
+        u.head0 = p.p0;
+        u.n_heads = p.n_pairs;
+        u.tok_begin = p.t0;
+        u.tok_end = p.t1;
+        u.chunk = p.chunk;
+        u.n_chunks = p.n_chunks;
+        u.group = -1;   // no merge counter
+        u.reserved = (int64_t)(qo_indptr[p.b + 1] - qo_indptr[p.b]) * G > kCrossBlock;   // other blocks read the same keys
+        for (u.kv_head = 0; u.kv_head < Hkv; ++u.kv_head) {
+            u.partial0 = p.n_chunks > 1 ? p.partial0 + u.kv_head * (p.n_chunks << p.size) : 0;
+            plan->units.push_back(u);
+        }
+        plan->cross_units[p.size] += Hkv;
     }
 
     // ---- many pairs: items of up to two head slots of slot_rows rows x G heads.
@@ -171,11 +175,11 @@ attn_status build(const int32_t* qo_indptr, const int32_t* kv_start, const int32
         tiles += n * tiles_of(kv_len[b]);
     }
     if (blocks > (int64_t)INT32_MAX / (int64_t)sizeof(PrefillItem)) return ATTN_ERR_UNSUPPORTED;
-    // Blocks that would fill the SMs a few times over stay whole.  Others are cut
-    // so that the SMs' shares come out even: of chunk lengths that give each SM
-    // one item, two, .., the one whose fullest SM has the least to do, if all items
-    // were alike.
-    int64_t size = INT32_MAX;
+    // Blocks that would fill the SMs a few times over stay whole, but for those that
+    // are longer than an SM's share.  Others are cut so that the SMs' shares come
+    // out even: of chunk lengths that give each SM one item, two, .., the one whose
+    // fullest SM has the least to do, if all items were alike.
+    int64_t size = std::max((tiles + num_sms - 1) / num_sms, kCrossItemTiles);
     if (blocks > 0 && blocks < 4 * (int64_t)num_sms) {
         int64_t best = INT64_MAX;
         for (int64_t per_sm = 0; per_sm <= 4; ++per_sm) {

@@ -140,3 +140,20 @@ def test_every_pair_and_key_once(lib, Hq, Hkv, D, seed, sms):
                 assert [x[2] for x in parts] == [(c, len(parts)) for c in range(len(parts))]
     assert not seen
     lib.attn_plan_destroy(h)
+
+
+def test_one_long_sequence_among_many_short_ones_is_split(lib):
+    """No item or unit is much longer than an even share of the work."""
+    for rows in (40, 3):                                           # the prefill kernel's, and few rows
+        qo, kv = [rows] * 800, [200] * 799 + [600000]
+        start = [0] * 800
+        st, h, _ = plan(lib, qo, start, kv, 600000)
+        assert st == OK
+        _, units, items = units_of(lib, h)
+        if rows == 40:
+            share = items[:, 8].sum() / 152
+            assert len(units) == 0 and items[:, 8].max() <= 1.5 * share + 1
+        else:
+            lens = (units[:, 6] - units[:, 5] + 63) // 64
+            assert len(items) == 0 and lens.max() <= 1.5 * lens.sum() / (3 * 152) + 4
+        lib.attn_plan_destroy(h)
