@@ -80,7 +80,8 @@ struct CrossMerge {
     int32_t reserved;
 };
 static_assert(sizeof(CrossMerge) == 32, "cross merge is one sector");
-// Heads of an output box of 32 pairs, 0 where such a stripe is no box.
+// Heads of an output box of 32 pairs, 0 where such a stripe is no box.  (64 x 128 rows
+// over 300 keys, 64 heads on 8 of 64 dims: 72 us through boxes, 82 by threads' own stores.)
 constexpr int cross_out_box(int G) { return 32 % G == 0 ? G : G % 32 == 0 ? 32 : 0; }
 
 // One request of a paged plan, for the kernels that work on whole requests
