@@ -146,3 +146,44 @@ def test_prompts_beams_and_compaction(Hq, Hkv, D, P):
     loop.drop(range(7 - 1))
     loop.pages.free(loop.table)
     assert not loop.pages.refs.any() and loop.pages.device_error() == 0
+
+
+def test_compressed_pages_and_weights_are_forked_and_compacted_alike():
+    """A child's 4-bit pages and key weights are its parent's, wherever they lie: equal queries give equal bits."""
+    from paged_kv_attention_sink_gb300 import binding
+    Hq, Hkv, D, P, n = 16, 4, 64, 32, 40
+    g = torch.Generator(device="cuda").manual_seed(5)
+    lens = [70, 5 * P, 9]
+    counts = [-(-m // P) for m in lens]
+    pool = torch.zeros(binding.kv4_cache_shape(n, Hkv, P, D), dtype=torch.uint8, device="cuda")
+    weights = torch.zeros(n, Hkv, P, device="cuda")
+    pages = binding.PagePool([pool, weights], P)
+    pages.alloc(3)                                              # others' pages
+    table = pages.alloc(sum(counts))
+
+    def plan_of(table, lens, qo):
+        c = [-(-m // P) for m in lens]
+        return binding.Plan(np.concatenate([[0], np.cumsum(qo)]), np.concatenate([[0], np.cumsum(c)]), table,
+                            [m - (k - 1) * P for m, k in zip(lens, c)], Hq, Hkv, D, P, num_pages=n)
+
+    rows = lambda m, h: torch.randn(m, h, D, device="cuda", generator=g).to(torch.bfloat16)
+    plan_of(table, lens, lens).append_kv4(rows(sum(lens), Hkv), rows(sum(lens), Hkv), pool)
+    q = rows(3, Hq)
+    plan = plan_of(table, lens, [1, 1, 1])
+    out, lse = plan.decode_kv4(q, pool, lse=torch.empty(3, Hq, device="cuda"))
+    plan.key_weights_kv4(q, pool, lse, weights, decay=0.0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    parents = [2, 0, 0, 1]
+    child, indptr = pages.fork(table, torch.tensor(np.concatenate([[0], np.cumsum(counts)]), **i32), torch.tensor(lens, **i32),
+                               torch.tensor(parents, **i32), sum(counts[b] for b in parents))
+    pages.free(table)
+    want = weights[table.long()]
+    pages.compact(child)
+    assert int((pages.refs > 0).sum()) == int(child.max()) + 1
+    forked = plan_of(child, [lens[b] for b in parents], [1] * 4)
+    got, got_lse = forked.decode_kv4(q[parents], pool, lse=torch.empty(4, Hq, device="cuda"))
+    assert torch.equal(got, out[parents]) and torch.equal(got_lse, lse[parents])
+    first = np.concatenate([[0], np.cumsum(counts)])
+    order = torch.tensor(np.concatenate([np.arange(first[b], first[b + 1]) for b in parents]), device="cuda")
+    assert torch.equal(weights[child.long()], want[order])
+    assert pages.device_error() == 0 and forked.device_error() == 0
