@@ -274,7 +274,6 @@ extern "C" attn_status attn_cross(attn_plan_t plan, const void* q, const void* k
         plan->cross_ptrs[i] = x[i];
         plan->cross_strides[i] = stride[i];
     }
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!plan->items.empty()) {
         const int G = plan->Hq / plan->Hkv, box = attn::cross_out_box(G), heads = box > 0 ? box : 1;
         if (plan->q_map_prefill_ptr != q) {
@@ -285,12 +284,9 @@ extern "C" attn_status attn_cross(attn_plan_t plan, const void* q, const void* k
             if (!make_q_map(plan->o_map_prefill, out, plan, attn::kPrefillOutRows / heads, heads)) return ATTN_ERR_CUDA;
             plan->o_map_prefill_ptr = out;
         }
-        if (attn_status st = attn::launch_prefill(plan, plan->q_map_prefill, plan->kv_map_prefill, plan->v_map_prefill,
-                                                  plan->o_map_prefill, sinks, out, lse, s);
-            st != ATTN_OK)
-            return st;
     }
-    return attn::launch_cross_few(plan, q, sinks, out, lse, s);
+    return attn::launch_cross(plan, q, plan->q_map_prefill, plan->o_map_prefill, sinks, out, lse,
+                              static_cast<cudaStream_t>(stream));
 }
 
 extern "C" attn_status attn_merge_states(const void* va, const float* lsea, const void* vb,

@@ -70,6 +70,8 @@ struct CrossArgs {
     int32_t* err;
     int32_t Hq, G;
     float scale_log2;
+    int32_t late;   // runs beside the launch before it,
+    int32_t open;   // lets the one after it run beside it (launch_cross)
 };
 
 __device__ __forceinline__ uint32_t ld_b32(const __nv_bfloat16* p) { return *reinterpret_cast<const uint32_t*>(p); }
@@ -152,7 +154,8 @@ cross_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         ptx::fence_mbar_init();
     }
     __syncthreads();
-    ptx::grid_dependency_wait();
+    if (!a.late) ptx::grid_dependency_wait();
+    if (a.open) ptx::grid_dependents_go();
 
     const int wm = warp % kTiles, part = warp / kTiles;   // (products)
     const int gq = lane >> 2, tq = lane & 3;
@@ -351,6 +354,7 @@ cross_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
     }
     __syncthreads();                 // the stages are free
     ptx::grid_dependents_go();
+    if (a.late) ptx::grid_dependency_wait();   // (ends after the launch before it)
     if (flags[1]) return;            // a wait ran out: nothing is written
 
     if (warp < kCrossWarps) {
@@ -424,34 +428,25 @@ cudaError_t launch(const CUtensorMap* maps, const CrossArgs& args, int units, cu
 }
 
 // Joins the chunks' states of split keys, this kernel's and the prefill kernel's.  A
-// CTA has a record's up to 32 pairs, a thread 4 dims of one of them at a time.
+// thread has 4 dims of a pair, a CTA as many pairs of a record as that makes.
 constexpr int kMergeThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
 cross_merge_kernel(const CrossMerge* merges, const CrossArgs a) {
-    const CrossMerge m = merges[blockIdx.x];   // the plan's own list
+    constexpr int kPairs = kMergeThreads / (D / 4), kCtas = kCrossBlock / kPairs;   // CTAs of a record
+    const CrossMerge m = merges[blockIdx.x / kCtas];   // the plan's own list
     ptx::grid_dependency_wait();
     ptx::grid_dependents_go();
-    for (int idx = threadIdx.x; idx < m.pairs * (D / 4); idx += kMergeThreads) {
-        const int p = m.pair0 + idx / (D / 4), d = (idx % (D / 4)) * 4;
-        join_chunks<D>(a, (size_t)m.partial0 * kMaxSliceHeads + idx / (D / 4), (size_t)m.stride * kMaxSliceHeads, m.n_chunks,
-                       m.q_row0 + p / a.G, m.head0 + p % a.G, d);
-    }
+    const int p = blockIdx.x % kCtas * kPairs + threadIdx.x / (D / 4), x = m.pair0 + p;
+    if (p < m.pairs)
+        join_chunks<D>(a, (size_t)m.partial0 * kMaxSliceHeads + p, (size_t)m.stride * kMaxSliceHeads, m.n_chunks,
+                       m.q_row0 + x / a.G, m.head0 + x % a.G, threadIdx.x % (D / 4) * 4);
 }
 
 template <int D>
-cudaError_t launch_sizes(attn_plan_s* plan, const CUtensorMap* maps, CrossArgs args, cudaStream_t stream) {
-    if (plan->cross_units[0] > 0) {
-        const cudaError_t e = launch<D, 1>(maps, args, plan->cross_units[0], stream);
-        if (e != cudaSuccess) return e;
-        args.units += plan->cross_units[0];
-    }
-    if (plan->cross_units[1] > 0) {
-        const cudaError_t e = launch<D, 2>(maps, args, plan->cross_units[1], stream);
-        if (e != cudaSuccess) return e;
-    }
-    if (plan->cross_merges == 0) return cudaSuccess;
-    return launch_dependent(cross_merge_kernel<D>, dim3(plan->cross_merges), kMergeThreads, 0, stream,
+cudaError_t launch_merge(const attn_plan_s* plan, const CrossArgs& args, cudaStream_t stream) {
+    constexpr int kCtas = kCrossBlock / (kMergeThreads / (D / 4));
+    return launch_dependent(cross_merge_kernel<D>, dim3(plan->cross_merges * kCtas), kMergeThreads, 0, stream,
                             reinterpret_cast<const CrossMerge*>(plan->ws + plan->layout.append), args);
 }
 
@@ -459,8 +454,14 @@ cudaError_t launch_sizes(attn_plan_s* plan, const CUtensorMap* maps, CrossArgs a
 
 int cross_ctas_per_sm(int head_dim) { return head_dim == 64 ? CrossCfg<64>::kCtas : CrossCfg<128>::kCtas; }
 
-attn_status launch_cross_few(attn_plan_s* plan, const void* q, const float* sinks, void* out, float* lse,
-                             cudaStream_t stream) {
+// The kernels for 16 pairs, for 32 and for many write different rows and read nothing of
+// one another, so that each may run beside the one before it: the first waits for
+// what is on the stream and then lets the next one start; those (`late`) wait only
+// before they end, so that whatever follows them follows all.  In turn, each would
+// leave SMs idle while its last CTAs run (23 sequences of up to 38 rows over 0.7K-1.4K
+// keys, 8 heads on 4 of 128 dims: 39 us in turn, 27 beside one another).
+attn_status launch_cross(attn_plan_s* plan, const void* q, const void* q_map, const void* o_map, const float* sinks,
+                         void* out, float* lse, cudaStream_t stream) {
     CrossArgs a;
     a.units = reinterpret_cast<const DecodeUnit*>(plan->ws + plan->layout.units);
     a.q = static_cast<const __nv_bfloat16*>(q);
@@ -473,8 +474,25 @@ attn_status launch_cross_few(attn_plan_s* plan, const void* q, const float* sink
     a.Hq = plan->Hq;
     a.G = plan->Hq / plan->Hkv;
     a.scale_log2 = plan->sm_scale * kLog2e;
+    a.late = a.open = 0;
     const CUtensorMap* maps = reinterpret_cast<const CUtensorMap*>(plan->cross_maps);
-    const cudaError_t e = plan->D == 64 ? launch_sizes<64>(plan, maps, a, stream) : launch_sizes<128>(plan, maps, a, stream);
+    for (int size = 0; size < 2; ++size) {
+        const int n = plan->cross_units[size];
+        if (n == 0) continue;
+        a.open = (size == 0 && plan->cross_units[1] > 0) || !plan->items.empty();
+        const cudaError_t e = plan->D == 64 ? (size ? launch<64, 2>(maps, a, n, stream) : launch<64, 1>(maps, a, n, stream))
+                                            : (size ? launch<128, 2>(maps, a, n, stream) : launch<128, 1>(maps, a, n, stream));
+        if (e != cudaSuccess) return ATTN_ERR_CUDA;
+        a.units += n;
+        a.late = 1;
+    }
+    if (!plan->items.empty()) {
+        const attn_status st = launch_prefill(plan, q_map, plan->kv_map_prefill, plan->v_map_prefill, o_map, sinks, out,
+                                              lse, stream, a.late != 0);
+        if (st != ATTN_OK) return st;
+    }
+    if (plan->cross_merges == 0) return ATTN_OK;
+    const cudaError_t e = plan->D == 64 ? launch_merge<64>(plan, a, stream) : launch_merge<128>(plan, a, stream);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

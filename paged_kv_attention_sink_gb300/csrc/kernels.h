@@ -39,9 +39,10 @@ attn_status launch_decode(attn_plan_s* plan, const void* q, const void* kv_map, 
                           void* out, float* lse, cudaStream_t stream);
 // v_map: the V tensor map of a ragged plan (NULL for a paged plan); o_map:
 // `out` with the same layout and box as q_map (full 128-row tiles are stored
-// through it).
+// through it).  late: a cross plan's launch beside the one before it (launch_cross).
 attn_status launch_prefill(attn_plan_s* plan, const void* q_map, const void* kv_map, const void* v_map,
-                           const void* o_map, const float* sinks, void* out, float* lse, cudaStream_t stream);
+                           const void* o_map, const float* sinks, void* out, float* lse, cudaStream_t stream,
+                           bool late = false);
 // in_f32 / out_f32: value states / merged values are fp32 (else bf16).
 attn_status launch_merge_states(const void* va, const float* lsea, const void* vb, const float* lseb, void* vout,
                                 float* lseout, int64_t rows, int head_dim, bool in_f32, bool out_f32,
@@ -99,9 +100,10 @@ attn_status launch_rope(const RopeTable& t, bool inter, bool inverse, const int3
 attn_status launch_append_kv_rope(attn_plan_s* plan, const RopeTable& t, bool inter, const int32_t* positions,
                                   const RopeRows& q, const RopeRows& k, const RopeRows& v, cudaStream_t stream);
 
-// Cross attention of few rows (cross.cu), from plan->cross_maps; many rows: launch_prefill.
-attn_status launch_cross_few(attn_plan_s* plan, const void* q, const float* sinks, void* out, float* lse,
-                             cudaStream_t stream);
+// Cross attention (cross.cu): few rows from plan->cross_maps, many through launch_prefill
+// (q_map, o_map: of these alone).
+attn_status launch_cross(attn_plan_s* plan, const void* q, const void* q_map, const void* o_map, const float* sinks,
+                         void* out, float* lse, cudaStream_t stream);
 
 // Page management (pages.cu).
 constexpr int kPagePoolsPerLaunch = 64;

@@ -54,10 +54,13 @@ bool current_sm_count(int32_t* out) {
 // (longest first, each to the least-loaded CTA); each CTA's items are stored
 // contiguously, longest first.
 void deal_prefill_items(attn_plan_s* plan) {
+    // What an item costs next to others; a cross item's slot shares less with the other.
+    const bool cross = plan->cross;
+    auto load = [cross](const PrefillItem& it) {
+        return cross ? (int64_t)it.n_kv_tiles * (2 + it.n_heads) : (int64_t)(it.n_kv_tiles * it.n_heads);
+    };
     std::stable_sort(plan->items.begin(), plan->items.end(),
-                     [](const PrefillItem& a, const PrefillItem& b) {
-                         return a.n_kv_tiles * a.n_heads > b.n_kv_tiles * b.n_heads;
-                     });
+                     [&](const PrefillItem& a, const PrefillItem& b) { return load(a) > load(b); });
     if (!plan->items.empty()) {
         const int ctas = (int)std::min<int64_t>(plan->num_sms, (int64_t)plan->items.size());
         std::vector<std::vector<PrefillItem>> per(ctas);
@@ -69,7 +72,7 @@ void deal_prefill_items(attn_plan_s* plan) {
             std::pop_heap(heap.begin(), heap.end(), cmp);
             auto& least = heap.back();
             per[least.second].push_back(it);
-            least.first += (int64_t)it.n_kv_tiles * it.n_heads + 1;   // +1: per-item overhead
+            least.first += load(it) + (cross ? 8 : 1);   // per-item overhead
             std::push_heap(heap.begin(), heap.end(), cmp);
         }
         plan->items.clear();

@@ -29,8 +29,10 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // rows' heads, so more than 128 heads per KV head stay with the kernel for few.
 constexpr int64_t kCrossManyPairs = 33;
 constexpr int64_t kCrossUnitCost = 4;    // a unit's start and end, in stages
+constexpr double kCrossFewStages = 6;    // stages a CTA slot that sequences of many pairs may have and be treated as few
 constexpr int64_t kCrossItemTiles = 4;   // tiles of 128 keys: never split a sequence finer
-constexpr int64_t kCrossItemCost = 2;    // an item's start and end, in tiles
+constexpr double kCrossItemCost = 2;     // an item's start and end, in tiles of two slots
+constexpr double kCrossSplitCost = 4;    // the chunks' states and their joining, likewise
 
 void add_merge(attn_plan_s& plan, const CrossMerge& m) {
     const int32_t* words = reinterpret_cast<const int32_t*>(&m);
@@ -68,9 +70,27 @@ attn_status build(const int32_t* qo_indptr, const int32_t* kv_start, const int32
     plan->kv_tokens = kv_rows;
     const int G = Hq / Hkv;
 
+    const int64_t slots = (int64_t)num_sms * cross_ctas_per_sm(D);
     // ---- few pairs (and none but the sinks to see): blocks of pairs x chunks of keys.
-    auto few = [&](int64_t pairs, int32_t keys) { return keys == 0 || pairs < kCrossManyPairs || G > kPrefillRows; };
     auto stages_of = [](int32_t keys) { return ((int64_t)keys + kCrossKeys - 1) / kCrossKeys; };
+    // The sequences of many pairs go to the kernel for few all the same where they are
+    // little work: up to kCrossFewStages stages a CTA slot, a block's start and end counted.
+    // Kernel for few against the one for many: 5 sequences of 61 rows over up to 35 keys, 5
+    // heads on 1 of 64 dims 4.5 us against 8.5; 4 of up to 160 rows over 680 keys, 4 heads on
+    // 2 of 128 dims 11.9 against 20.0; beyond the limit 6 of up to 976 rows over 17 keys, 10
+    // heads on 5 of 64 dims 11.0 against 7.6.  Over 124 mixes that the choice changes by 2 %
+    // or more, a limit of 2, 4, 5, 6, 8 or 16 takes 6.1, 2.1, 1.1, 1.0, 2.1 or 2.9 % longer
+    // than the better kernel for each would (geometric mean); one that 6 gets wrong is 1
+    // sequence of up to 1,922 rows over 19 keys, 6 heads on 2 of 128 dims: 13.4 us where
+    // 10.3 was to be had.
+    double short_work = 0;
+    for (int32_t b = 0; b < batch; ++b) {
+        const int64_t pairs = (int64_t)(qo_indptr[b + 1] - qo_indptr[b]) * G;
+        if (pairs >= kCrossManyPairs && kv_len[b] > 0)
+            short_work += (double)((pairs + kCrossBlock - 1) / kCrossBlock * Hkv * (stages_of(kv_len[b]) + kCrossUnitCost));
+    }
+    const bool all_few = G > kPrefillRows || short_work <= kCrossFewStages * (double)slots;
+    auto few = [&](int64_t pairs, int32_t keys) { return keys == 0 || pairs < kCrossManyPairs || all_few; };
     int64_t work = 0, decode_tokens = 0, prefill_pairs = 0;
     for (int32_t b = 0; b < batch; ++b) {
         const int64_t rows = qo_indptr[b + 1] - qo_indptr[b], pairs = rows * G;
@@ -89,7 +109,6 @@ attn_status build(const int32_t* qo_indptr, const int32_t* kv_start, const int32
     // keys of 8 heads 38 us against 42, 1 x 16,000 of 16 heads 13 against 18, but 8 x
     // 16,000 of 16 heads 99 against 82.)
     auto chunks_of = [](int64_t n, int64_t size) { return std::max<int64_t>(1, (n + size / 2) / size); };
-    const int64_t slots = (int64_t)num_sms * cross_ctas_per_sm(D);
     int64_t chunk = INT32_MAX;
     double least = 0;
     for (int64_t per_slot = 1; work > 0 && per_slot <= 4; ++per_slot) {
@@ -177,24 +196,34 @@ attn_status build(const int32_t* qo_indptr, const int32_t* kv_start, const int32
     if (blocks > (int64_t)INT32_MAX / (int64_t)sizeof(PrefillItem)) return ATTN_ERR_UNSUPPORTED;
     // Blocks that would fill the SMs a few times over stay whole, but for those that
     // are longer than an SM's share.  Others are cut so that the SMs' shares come
-    // out even: of chunk lengths that give each SM one item, two, .., the one whose
-    // fullest SM has the least to do, if all items were alike.
+    // out even: of the chunk lengths that give each SM one item, two, .., the one that
+    // ends first, in tiles of two slots: items that are alike take rounds, others
+    // are dealt out to about even shares; a tile of one slot costs 3/4, an item
+    // kCrossItemCost, the chunks' states and their joining kCrossSplitCost.
     int64_t size = std::max((tiles + num_sms - 1) / num_sms, kCrossItemTiles);
     if (blocks > 0 && blocks < 4 * (int64_t)num_sms) {
-        int64_t best = INT64_MAX;
-        for (int64_t per_sm = 0; per_sm <= 4; ++per_sm) {
+        double best = 0;
+        for (int64_t per_sm = 0; per_sm <= 6; ++per_sm) {
             const int64_t s = per_sm == 0 ? INT32_MAX : std::max((tiles - 1) / (num_sms * per_sm) + 1, kCrossItemTiles);
-            int64_t items = 0, longest = 0;
+            int64_t items = 0;
+            double all = 0, longest = 0;
+            bool split = false;
             for (int32_t b = 0; b < batch; ++b) {
                 const int64_t rows = qo_indptr[b + 1] - qo_indptr[b], n = tiles_of(kv_len[b]);
                 if (rows == 0 || few(rows * G, kv_len[b])) continue;
-                const int64_t c = chunks_of(n, s);
-                items += (rows + 2 * slot_rows - 1) / (2 * slot_rows) * Hkv * c;
-                longest = std::max(longest, (n - 1) / c + 1);
+                const int64_t c = chunks_of(n, s), twos = (rows + slot_rows - 1) / (2 * slot_rows);
+                const int64_t ones = (rows + slot_rows - 1) / slot_rows % 2;
+                const double len = (double)((n - 1) / c + 1);
+                items += (twos + ones) * Hkv * c;
+                all += (double)(Hkv * c) * ((double)twos * (len + kCrossItemCost) + (double)ones * (0.75 * len + kCrossItemCost));
+                longest = std::max(longest, (twos > 0 ? len : 0.75 * len) + kCrossItemCost);
+                split = split || c > 1;
             }
-            const int64_t rounds = (items - 1) / num_sms + 1;
-            const int64_t cost = std::max(rounds * ((tiles - 1) / items + 1 + kCrossItemCost), longest + kCrossItemCost);
-            if (cost < best) {
+            const double mean = all / (double)items;
+            const bool alike = longest <= 1.25 * mean;
+            const double cost = (alike ? (double)((items - 1) / num_sms + 1) * mean
+                                       : std::max(longest, all / num_sms + 0.5 * mean)) + (split ? kCrossSplitCost : 0);
+            if (per_sm == 0 || cost < best) {
                 best = cost;
                 size = s;
             }

@@ -136,6 +136,7 @@ struct PrefillArgs {
     int32_t G;           // kCross: query heads of a KV head,
     int32_t slot_rows;   // rows of a head slot,
     int32_t boxes;       // whether a softmax warp's 32 pairs are a box of o_map
+    int32_t late;        // runs beside the launch before it (launch_cross)
     float* part_o;       // partial states of split keys
     float* part_lse;
 };
@@ -251,6 +252,8 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // (A cross launch is a programmatic dependent; the items above are the plan's own.)
+    if (kCross && !a.late) ptx::grid_dependency_wait();
 
 
     auto fail = [&](int code) {
@@ -859,6 +862,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
         if (lane == 0) ptx::bulk_wait_all();   // output stores complete before the CTA exits
     }
 
+    if (kCross && a.late) ptx::grid_dependency_wait();   // ends after the launch before it
     // Tear-down: each MMA thread's last commit arrives on `drain` once every
     // MMA it issued is complete; then the TMEM columns are released.
     ptx::tc_fence_before();
@@ -886,6 +890,7 @@ cudaError_t launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorM
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (e != cudaSuccess) return e;
+    if constexpr (kCross) return launch_dependent(kernel, dim3(grid), C::kThreads, C::kSmem, stream, qm, km, vm, om, args);
     kernel<<<grid, C::kThreads, C::kSmem, stream>>>(qm, km, vm, om, args);
     return cudaGetLastError();
 }
@@ -893,7 +898,7 @@ cudaError_t launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorM
 }  // namespace
 
 attn_status launch_prefill(attn_plan_s* plan, const void* q_map, const void* kv_map, const void* v_map,
-                           const void* o_map, const float* sinks, void* out, float* lse, cudaStream_t stream) {
+                           const void* o_map, const float* sinks, void* out, float* lse, cudaStream_t stream, bool late) {
     if (plan->items.empty()) return ATTN_OK;
     PrefillArgs a;
     a.items = reinterpret_cast<const PrefillItem*>(plan->ws + plan->layout.items);
@@ -912,6 +917,7 @@ attn_status launch_prefill(attn_plan_s* plan, const void* q_map, const void* kv_
     a.G = plan->Hq / plan->Hkv;
     a.slot_rows = kPrefillRows / a.G;
     a.boxes = cross_out_box(a.G) > 0;
+    a.late = late;
     a.part_o = reinterpret_cast<float*>(plan->ws + plan->layout.part_o);
     a.part_lse = reinterpret_cast<float*>(plan->ws + plan->layout.part_lse);
     const CUtensorMap& qm = *static_cast<const CUtensorMap*>(q_map);

@@ -94,14 +94,14 @@ def test_single_rows(Hq, Hkv, D, sinks):
 
 
 @pytest.mark.parametrize("Hq,Hkv,D", HEADS)
-@pytest.mark.parametrize("padded,fused", [(True, True), (False, False)])
-def test_rows_of_every_number(Hq, Hkv, D, padded, fused):
+@pytest.mark.parametrize("padded,fused,sms", [(True, True, 3), (False, False, 20), (True, False, 0)])
+def test_rows_of_every_number(Hq, Hkv, D, padded, fused, sms):
     """Blocks of one and two tiles, the border to the prefill kernel, several blocks and slots; no rows, no keys."""
     qo = [2, 3, 0, 5, 8, 11, 16, 17, 33, 63, 64, 65, 127, 129, 260, 4, 30]
     kv = [70, 16, 9, 33, 64, 65, 129, 1, 128, 200, 257, 64, 300, 127, 500, 0, 0]
-    plan, *_ = check(qo, kv, Hq, Hkv, D, True, padded=padded, fused=fused, seed=D)
+    plan, *_ = check(qo, kv, Hq, Hkv, D, True, padded=padded, fused=fused, seed=D, num_sms=sms)
     info = plan.info()
-    assert info["num_prefill_items"] > 0 and info["num_decode_units"] > 0
+    assert info["num_decode_units"] > 0 and (sms != 3 or info["num_prefill_items"] > 0)
 
 
 @pytest.mark.parametrize("Hq,Hkv,D,qo", [(8, 2, 64, 3), (64, 4, 128, 1), (16, 16, 64, 5), (4, 1, 64, 16), (6, 2, 128, 11)])
@@ -113,9 +113,10 @@ def test_long_keys_are_split(Hq, Hkv, D, qo):
 @pytest.mark.parametrize("Hq,Hkv,D,qo", [(8, 2, 64, 20), (4, 4, 128, 300), (64, 8, 64, 5), (10, 2, 64, 97), (6, 1, 128, 22),
                                           (48, 1, 64, 3), (130, 1, 128, 2)])
 def test_many_rows_over_split_keys(Hq, Hkv, D, qo):
-    plan, *_ = check([qo, qo, 1, qo], [5000, 700, 9000, 1153], Hq, Hkv, D, qo % 2 == 0, seed=qo)
+    plan, *_ = check([qo, qo, 1, qo], [5000, 700, 9000, 1153], Hq, Hkv, D, qo % 2 == 0, seed=qo, num_sms=12)
     info = plan.info()
     assert info["num_decode_partials"] > 0 and (Hq // Hkv > 128 or info["num_prefill_items"] > 2 * Hkv)
+    check([qo, qo, 1, qo], [5000, 700, 9000, 1153], Hq, Hkv, D, qo % 2 == 1, seed=qo)
 
 
 @pytest.mark.parametrize("Hq,Hkv,D,qo,kv", [(8, 1, 64, 1, 1000003), (2, 1, 128, 150, 200003), (2, 2, 64, 12, 300001)])
@@ -140,6 +141,33 @@ def test_states_past_4_gb():
     assert bool(((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -7 + 2.0 ** -10) * mag).all())
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_kernels_beside_one_another_follow_what_came_before_and_are_followed(D):
+    """Calls that feed one another: each reads the last one's output as queries, on one stream, many times over, and
+    the same with every kernel of the first waiting for a late one."""
+    qo, kv = [1, 9, 40, 3, 100, 7], [3000, 700, 2000, 65, 900, 5000]
+    plan, (q, k, v, s), *_ = check(qo, kv, 8, 2, D, False, seed=30, num_sms=10)
+    info = plan.info()
+    assert info["num_prefill_items"] and info["num_decode_units"] and info["num_decode_partials"]
+    x = q.clone()
+    want = []
+    for _ in range(4):
+        x = plan.attend(x, k, v)[0]
+        torch.cuda.synchronize()
+        want.append(x.clone())
+    buf = [torch.empty_like(q), torch.empty_like(q)]
+    for _ in range(20):
+        buf[0].copy_(q)
+        for i in range(4):
+            plan.attend(buf[i % 2], k, v, out=buf[(i + 1) % 2])
+        assert torch.equal(buf[0], want[-1])
+        torch.cuda._sleep(20000)
+        buf[0].zero_().add_(q)
+        for i in range(3):
+            plan.attend(buf[i % 2], k, v, out=buf[(i + 1) % 2])
+        assert torch.equal(buf[1], want[2])
+
+
 def test_two_plans_at_once():
     """Each with its own workspace, on its own stream."""
     cases = [([3, 200, 1], [9000, 700, 4000]), ([5, 64, 2, 90], [1500, 3000, 64, 5000])]
@@ -157,12 +185,12 @@ def test_two_plans_at_once():
 def test_many_rows_of_every_group(G, D):
     """Slots of 128 / G rows: full ones, ragged ones, output boxes and single rows."""
     check([300, 65, 128], [200, 385, 64], 2 * G, 2, D, True, seed=G, num_sms=4)      # two slots an item
-    check([130 // G + 70 // min(G, 70), 1], [130, 7], 2 * G, 2, D, False, seed=G)     # one
+    check([130 // G + 70 // min(G, 70), 1], [130, 7], 2 * G, 2, D, False, seed=G, num_sms=1)     # one
 
 
 def test_large_scores_raise_the_maximum():
     """Scores that pass the first tile's maximum by far; tolerances grow with them (2^-24 (D + 4) of |s| <= 2000: 2^-7)."""
-    for qo, sms in (([1, 70], 0), ([5, 200], 0), ([30, 150], 2)):
+    for qo, sms in (([1, 70], 0), ([5, 200], 3), ([30, 150], 2)):
         q, k, v, s, start, rows = inputs(qo, [900, 1000], 8, 2, 64, True, seed=3)
         k[start[0] + 700] *= 40
         k[start[1] + 999] *= 40
@@ -177,7 +205,8 @@ def test_large_scores_raise_the_maximum():
 def test_infinite_and_nan_states():
     """A NaN in one KV head's keys or values reaches that head's rows of that sequence, and no others."""
     qo, kv = [3, 70, 2], [100, 3000, 40]                     # (the second's keys are split)
-    plan, (q, k, v, s), clean, _ = check(qo, kv, 8, 4, 64, False, padded=False, fused=False, seed=5)
+    plan, (q, k, v, s), clean, _ = check(qo, kv, 8, 4, 64, False, padded=False, fused=False, seed=5, num_sms=40)
+    assert plan.info()["num_prefill_items"] > 4
     k[100 + 250, 1, 7], v[5, 2, 3], v[3099, 0, :] = float("nan"), float("nan"), float("inf")
     out, _ = plan.attend(q, k, v, s)
     bad = torch.zeros_like(out, dtype=torch.bool)
@@ -189,11 +218,12 @@ def test_infinite_and_nan_states():
 
 def test_all_scores_at_minus_infinity():
     """Keys of -inf against positive queries leave nothing to see: as without keys."""
-    for rows in (2, 80):
+    for rows, sms in ((2, 0), (80, 0), (80, 1)):
         q = torch.ones(rows, 4, 64, dtype=torch.bfloat16, device="cuda")
         k = torch.full((50, 2, 64), -float("inf"), dtype=torch.bfloat16, device="cuda")
         v = torch.ones_like(k)
-        plan = binding().CrossPlan([0, rows], [0], [50], 50, 4, 2, 64)
+        plan = binding().CrossPlan([0, rows], [0], [50], 50, 4, 2, 64, num_sms=sms)
+        assert (plan.info()["num_prefill_items"] > 0) == (sms == 1)
         out, lse = plan.attend(q, k, v, lse=torch.empty(rows, 4, device="cuda"))
         assert not out.any() and bool((lse == -float("inf")).all())
         sinks = torch.tensor([1.0, -2.0, 0.0, 30.0], device="cuda")
@@ -224,7 +254,8 @@ def test_no_states_at_all():
 
 def test_other_tensors_strides_and_streams_through_one_plan():
     qo, kv = [1, 90, 3], [50, 333, 1000]
-    plan, (q, k, v, s), out, lse = check(qo, kv, 16, 4, 64, True, seed=8)
+    plan, (q, k, v, s), out, lse = check(qo, kv, 16, 4, 64, True, seed=8, num_sms=8)
+    assert plan.info()["num_prefill_items"]
     k2, v2 = torch.zeros(len(k), 7, 64, dtype=torch.bfloat16, device="cuda"), v.contiguous()
     k2[:, 2:6] = k
     assert torch.equal(plan.attend(q, k2[:, 2:6], v2, s)[0], out)
@@ -238,7 +269,8 @@ def test_other_tensors_strides_and_streams_through_one_plan():
 
 def test_outputs_that_start_in_the_middle_of_a_sector():
     qo, kv = [3, 90, 40], [50, 333, 5000]
-    plan, (q, k, v, s), out, lse = check(qo, kv, 16, 4, 64, True, seed=10)
+    plan, (q, k, v, s), out, lse = check(qo, kv, 16, 4, 64, True, seed=10, num_sms=8)
+    assert plan.info()["num_prefill_items"]
     buf = torch.zeros(out.numel() + 16, dtype=torch.bfloat16, device="cuda")
     mine = buf[8:8 + out.numel()].view(out.shape)
     assert mine.data_ptr() % 32 == 16
@@ -248,7 +280,9 @@ def test_outputs_that_start_in_the_middle_of_a_sector():
 
 def test_captured_and_replayed():
     qo, kv = [1, 5, 200, 2], [70, 9000, 300, 0]
-    plan, (q, k, v, s), out, lse = check(qo, kv, 16, 4, 64, True, seed=9)
+    plan, (q, k, v, s), out, lse = check(qo, kv, 16, 4, 64, True, seed=9, num_sms=8)   # all kernels
+    info = plan.info()
+    assert info["num_prefill_items"] and info["num_decode_partials"]
     graph = torch.cuda.CUDAGraph()
     plan.attend(q, k, v, s, out, lse)
     torch.cuda.synchronize()

@@ -34,9 +34,10 @@ def close(out, want, mag):
 class Loop:
     """A batch of requests on one layer: page tables on the device, lengths on the host, and what they should hold."""
 
-    def __init__(self, Hq, Hkv, D, P, num_pages, enc_lens, seed):
+    def __init__(self, Hq, Hkv, D, P, num_pages, enc_lens, seed, sms):
         from paged_kv_attention_sink_gb300 import binding
         self.B, self.Hq, self.Hkv, self.D, self.P = binding, Hq, Hkv, D, P
+        self.sms = sms                                     # what cross attention is planned for: 1 takes every kernel
         self.g = torch.Generator(device="cuda").manual_seed(seed)
         self.pool = torch.full((num_pages, 2, Hkv, P, D), float("nan"), dtype=torch.bfloat16, device="cuda")
         self.pages = binding.PagePool([self.pool], P)
@@ -82,7 +83,8 @@ class Loop:
         # Requests of one encoder are neighbours: their rows are one sequence's.
         first = [b for b in range(len(new)) if b == 0 or self.enc_of[b] != self.enc_of[b - 1]]
         cross = self.B.CrossPlan([qo[b] for b in first] + [qo[-1]], [self.enc_start[self.enc_of[b]] for b in first],
-                                 [self.enc_lens[self.enc_of[b]] for b in first], len(self.enc), self.Hq, self.Hkv, self.D)
+                                 [self.enc_lens[self.enc_of[b]] for b in first], len(self.enc), self.Hq, self.Hkv, self.D,
+                                 num_sms=self.sms)
         got, _ = cross.attend(out, self.enc[:, :self.Hkv], self.enc[:, self.Hkv:])
         for b in range(len(new)):
             e, r = self.enc_of[b], slice(qo[b], qo[b + 1])
@@ -124,9 +126,9 @@ class Loop:
         self.lens, self.kv, self.enc_of = ([x[b] for b in keep] for x in (self.lens, self.kv, self.enc_of))
 
 
-@pytest.mark.parametrize("Hq,Hkv,D,P", [(8, 2, 64, 16), (16, 4, 128, 32)])
-def test_prompts_beams_and_compaction(Hq, Hkv, D, P):
-    loop = Loop(Hq, Hkv, D, P, 90, [70, 1500, 0], seed=D)
+@pytest.mark.parametrize("Hq,Hkv,D,P,sms", [(8, 2, 64, 16, 0), (16, 4, 128, 32, 1), (16, 2, 64, 16, 1)])
+def test_prompts_beams_and_compaction(Hq, Hkv, D, P, sms):
+    loop = Loop(Hq, Hkv, D, P, 90, [70, 1500, 0], seed=D, sms=sms)
     for e in (0, 1, 2):
         loop.add(1, e)
     loop.step([5 * P, 37, 2 * P - 1])           # prompts: a full last page, a ragged one, one to be filled
