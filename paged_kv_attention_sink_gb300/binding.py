@@ -309,12 +309,14 @@ class PagePool:
 
     def _ids(self, name, t):
         _check_cuda(self._dev, name, t, torch.int32)
-        if t.dim() != 1:
-            raise ValueError(f"{name} must have one dimension")
+        if t.dim() != 1 or t.numel() >= 1 << 31:
+            raise ValueError(f"{name} must have one dimension and fewer than 2^31 entries")
         return t.numel()
 
     def alloc(self, n: int, out=None, stream=None):
         """The n lowest free pages, held once: int32 [n] (-1 where none was left)."""
+        if not 0 <= n < 1 << 31:
+            raise ValueError("n must be 0 to 2^31 - 1")
         out = _empty_on(stream, (n,), torch.int32, self._device) if out is None else out
         _check_cuda(self._dev, "out", out, torch.int32, (n,))
         _launch_on(self._dev, stream, "attn_pages_alloc", _ptr(self.refs), self.num_pages, n, _ptr(out), _ptr(self._err))

@@ -299,3 +299,17 @@ def test_the_binding_refuses():
                  lambda: pages.fork(ids, dev([0, 1, 2]), ids, ids, 2, out=ids[:1])):
         with pytest.raises((TypeError, ValueError)):
             call()
+
+
+def test_counts_past_31_bits_are_refused():
+    """None is cut to the 32 bits that the C entry points take."""
+    B = binding()
+    pages = B.PagePool([torch.zeros(8, 4, device="cuda")], 16)
+    for n in (-1, 1 << 31, (1 << 32) + 5):
+        with pytest.raises(ValueError):
+            pages.alloc(n)
+    ids, many = dev([1, 2]), torch.empty(1 << 31, dtype=torch.int32, device="cuda")
+    for call in (lambda: pages.free(many), lambda: pages.fork(ids, dev([0, 1, 2]), ids, many, 2)):
+        with pytest.raises(ValueError):
+            call()
+    assert not pages.refs.any() and pages.device_error() == 0
