@@ -689,8 +689,11 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
             // max raised and O rescaled.  Any max is a valid softmax shift, so
             // the result does not depend on when it moves.  The redo re-enters
             // the loop body for the same tile (the S wait returns at once), so
-            // the scores need not stay live past the exponentials.
-            bool redo = false;
+            // the scores need not stay live past the exponentials.  A max of -inf is
+            // none, though: while some row of the warp has seen only scores of -inf,
+            // `raise` keeps the max of such rows (whose sums and O are 0, so that
+            // nothing is to be rescaled) following the tiles.
+            bool redo = false, raise = true;
             for (int j = 0; j < n; ++j) {
                 const int t = hj + j;
                 if (!wait_all(B.s_full + 8 * i, t & 1)) { ok = false; break; }
@@ -713,7 +716,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                 // At D = 64 the previous PV must be done before O is touched or
                 // P is overwritten (at D = 128 it is: S of tile j waited for it).
                 bool prev_done = !C::kSeparateP || t == 0;
-                if (j == 0 || redo) {
+                if (raise || redo) {
                     // Raise the running max to cover this tile (row max: 16
                     // independent chains of 3-input max, then a tree).
                     float mq[16];
@@ -725,11 +728,12 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
                     for (int k = 0; k < 5; ++k) mq[k] = ptx::max3(mq[k], mq[5 + k], mq[10 + k]);
                     const float tmax = ptx::max3(ptx::max3(mq[0], mq[1], mq[2]), ptx::max3(mq[3], mq[4], mq[15]), mq[15]);
-                    const float m_new = fmaxf(m_use, tmax * sl2);
+                    const float m_new = j == 0 || redo || m_use == -INFINITY ? fmaxf(m_use, tmax * sl2) : m_use;
                     const float alpha = m_new > m_use ? ptx::ex2(m_use - m_new) : 1.f;
                     l *= alpha;
                     le *= alpha;
                     m_use = m_new;
+                    raise = __any_sync(0xffffffffu, m_new == -INFINITY);
                     if (redo) {   // rescale what the earlier tiles put in O
                         if (!prev_done) {
                             if (!wait_all(B.o_done + 8 * i, (t - 1) & 1)) { ok = false; break; }
