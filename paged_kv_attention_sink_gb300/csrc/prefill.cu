@@ -587,7 +587,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                 ptx::tc_wait_ld();
                 lt += __uint_as_float(v[0]);
             }
-            const float inv = lt > 0.f ? 1.f / lt : 0.f;
+            const float inv = lt > 0.f ? 1.f / lt : lt;   // (no keys: 0; NaN stays)
             if (kChunks && ei.pos0 >= 0) {   // a chunk of the keys: its state in fp32
                 const size_t part = (size_t)(ei.pos0 + i * (kPrefillRows / kMaxSliceHeads)) * kMaxSliceHeads + r;
 #pragma unroll
@@ -729,7 +729,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                     for (int k = 0; k < 5; ++k) mq[k] = ptx::max3(mq[k], mq[5 + k], mq[10 + k]);
                     const float tmax = ptx::max3(ptx::max3(mq[0], mq[1], mq[2]), ptx::max3(mq[3], mq[4], mq[15]), mq[15]);
                     const float m_new = j == 0 || redo || m_use == -INFINITY ? fmaxf(m_use, tmax * sl2) : m_use;
-                    const float alpha = m_new > m_use ? ptx::ex2(m_use - m_new) : 1.f;
+                    const float alpha = m_new == m_use ? 1.f : ptx::ex2(m_use - m_new);   // (a sink of NaN stays one)
                     l *= alpha;
                     le *= alpha;
                     m_use = m_new;
