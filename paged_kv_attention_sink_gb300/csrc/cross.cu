@@ -199,14 +199,11 @@ cross_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 }
             }
         }
-        if (!ok) {
-            if (lane == 0) {
-                atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
-                flags[1] = 1;
-            }
-            for (int t = max(0, it - C::kStages); t < it; ++t)   // what is in flight lands before the CTA ends
-                ptx::mbar_wait(full + 8 * (t % C::kStages), (t / C::kStages) & 1);
+        if (!ok && lane == 0) {
+            atomicOr(a.err, ATTN_DEVICE_ERR_TIMEOUT);
+            flags[1] = 1;
         }
+        ptx::await_copies(full, C::kStages, it);
     } else {
         // --------------------------------------------------------- products
         uint32_t qa[D / 16][4];

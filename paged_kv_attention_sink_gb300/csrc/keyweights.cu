@@ -398,7 +398,7 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
                                      page * 2 * a.Hkv + g);
         }
         if (lane == 0) {
-            int s = 0;
+            int s = 0;   // steps whose q is on its way
             for (int h0 = 0, row = r.q_row0 + i0; s < n_steps; ++s) {
                 const int st = s % C::kStages;
                 if (s >= C::kStages && !ptx::mbar_wait(s_full + 8 * st, (s / C::kStages - 1) & 1)) {
@@ -415,10 +415,8 @@ key_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __gri
                     row += rows;
                 }
             }
-            // Copies still in flight when a wait ran out land before the CTA exits.
-            if (s < n_steps)
-                for (int k = max(0, s - C::kStages); k < s; ++k)
-                    ptx::mbar_wait(q_full + 8 * (k % C::kStages), (k / C::kStages) & 1);
+            ptx::await_copies(q_full, C::kStages, s);
+            if (!kFour) ptx::await_copies(k_full, 1, 1);
         }
         __syncwarp();
     } else if (warp == C::kEpilogueWarps + 2) {

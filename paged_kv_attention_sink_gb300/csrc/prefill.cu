@@ -276,8 +276,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
         const uint32_t empty0 = is_k ? B.k_empty : B.v_empty;
         const uint32_t dst0 = sbase + (is_k ? C::kOffK : C::kOffV);
         const uint64_t policy = ptx::policy_evict_last();
-        int jg = 0, n_item = 0, n_aux = 0, issued = 0;
-        bool ok = true;
+        int jg = 0, n_item = 0, n_aux = 0, issued = 0, q_issued = 0;
         // The page ids of the next tile are loaded (one per lane) while the
         // current tile is issued, so the dependent global load never sits
         // between two tiles.
@@ -292,7 +291,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
         PrefillItem it = a.items[item];
         int page = load_pages(it, 0);
         while (item < item_end) {
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
             int item_n = item, j_n = j + 1;
             PrefillItem it_n = it;
             if (j_n == it.n_kv_tiles) {
@@ -306,7 +305,6 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                 const int qb = n_item % C::kQBufs;
                 if (n_item >= C::kQBufs && !wait_all(B.q_empty + 8 * qb, ((n_item / C::kQBufs) - 1) & 1)) {
                     fail(ATTN_DEVICE_ERR_TIMEOUT);
-                    ok = false;
                     break;
                 }
                 if (lane == 0) {
@@ -318,6 +316,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                                              B.q_full + 8 * qb, c * 64, kCross ? it.head0 : it.head0 + i,
                                              kCross ? it.q_row0 + i * a.slot_rows : it.q_row0);
                 }
+                q_issued = n_item + 1;
             }
             const int valid = min(kPrefillKeys, it.kv_len - j * kPrefillKeys);
             const int n_load = (valid + P - 1) / P;
@@ -331,7 +330,6 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
             const int st = jg % n_stages;
             if (jg >= n_stages && !wait_all(empty0 + 8 * st, ((jg / n_stages) - 1) & 1)) {
                 fail(ATTN_DEVICE_ERR_TIMEOUT);
-                ok = false;
                 break;
             }
             // V rows past the end of the sequence must be zeroed before the MMA
@@ -356,7 +354,6 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                 // zero V rows [valid, 128) (they may hold anything), publish.
                 if (!wait_all(B.v_aux, n_aux & 1)) {
                     fail(ATTN_DEVICE_ERR_TIMEOUT);
-                    ok = false;
                     break;
                 }
                 ++n_aux;
@@ -379,11 +376,8 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
             it = it_n;
             page = page_n;
         }
-        if (!ok) {
-            // Let the copies still in flight land before the CTA exits.
-            for (int t = max(0, issued - n_stages); t < issued; ++t)
-                ptx::mbar_wait(full0 + 8 * (t % n_stages), (t / n_stages) & 1);
-        }
+        ptx::await_copies(full0, n_stages, issued);
+        ptx::await_copies(B.q_full, C::kQBufs, q_issued);
     } else if (warp == 1 || warp == 2) {
         // ================================================================ MMA issuers
         // One warp per head slot, so neither head's MMAs wait behind the other

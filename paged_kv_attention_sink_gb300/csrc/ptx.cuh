@@ -71,6 +71,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     }
 }
 
+// For the warp that fills a ring of `stages`, at its end: waits until the copies of
+// the `issued` stages so far have landed.  Where another warp gave up a wait, nobody
+// else does, and copies must not reach shared memory that the next CTA has.
+__device__ __forceinline__ void await_copies(uint32_t full, int stages, int issued) {
+    for (int t = max(0, issued - stages); t < issued; ++t) mbar_wait(full + 8 * (t % stages), (t / stages) & 1);
+}
+
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
