@@ -217,7 +217,9 @@ ATTN_API attn_status attn_prefill_ragged(attn_plan_t plan, const void* q, const 
  *   below 2^30 (else ATTN_ERR_UNSUPPORTED)
  * Workspace, binding and error word as for attn_plan (attn_plan_info: num_decode_units
  * counts the work of few rows, num_prefill_items that of many); every other launch
- * refuses such a plan (ATTN_ERR_INVALID_ARG).  attn_cross writes all rows of out and lse.
+ * refuses such a plan (ATTN_ERR_INVALID_ARG).  attn_cross writes all rows of out and lse,
+ * but for those of work that recorded ATTN_DEVICE_ERR_TIMEOUT and, until
+ * attn_plan_device_error has read that, of all sequences whose keys are split.
  * The order of every sum is fixed.  Async on `stream`; capturable (after one
  * uncaptured call with these pointers has built the TMA descriptors).
  */
