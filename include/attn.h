@@ -506,7 +506,11 @@ ATTN_API attn_status attn_append_kv_rope(attn_plan_t plan, const attn_rope_spec*
  * goes on as it was).  Full pages are shared: the child's entry is the parent's,
  * held once more.  A last page that is not full, and will be written into, is
  * copied in every pool into a new page (the lowest free ones, in the children's
- * order), held once.
+ * order), held once.  Parent and children may append from there on, but nothing may
+ * write into a shared page.  attn_evict_kv does so in place (evict into new pages,
+ * page_table_out, and free the old ones), and so does an append to a request that was
+ * shortened below its fork.  attn_key_weights writes the weights of every cached key:
+ * requests that share pages each need a weights buffer and a plan of their own.
  *   page_table [table_len], kv_indptr [batch + 1], kv_lens [batch], parents [n]   device int32;
  *                 request p's pages are page_table[kv_indptr[p] ..] as in attn_plan
  *   page_table_out, indptr_out   device int32 [out_len], [n + 1], outputs: child c's

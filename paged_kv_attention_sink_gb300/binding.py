@@ -339,7 +339,9 @@ class PagePool:
         shared, a last page that is not full copied.  page_table, kv_indptr
         [batch + 1], kv_lens [batch], parents [n]: int32 CUDA tensors.  Returns the
         children's page table (int32 [out_len], out_len at least their pages in
-        all) and its offsets (int32 [n + 1])."""
+        all) and its offsets (int32 [n + 1]).  Nothing may write into shared pages:
+        evict such requests into new ones (page_table_out), not in place, and give
+        each a weights buffer of its own for key_weights."""
         entries = self._ids("page_table", page_table)
         batch, n = self._ids("kv_lens", kv_lens), self._ids("parents", parents)
         _check_cuda(self._dev, "kv_indptr", kv_indptr, torch.int32, (batch + 1,))
