@@ -413,9 +413,10 @@ ATTN_API attn_status attn_unpack_kv_heads(const void* buf, int64_t num_pages, in
  *   theta = positions[axis[p]][row] * inv_freq[p]
  *   (x, y) -> scale * (x cos theta - y sin theta,  x sin theta + y cos theta)
  *
- * and the other dims are copied.  The angle is held modulo a turn, within 2^-31 of
- * one at every int32 position; its cosine and sine and the products are fp32,
- * rounded to bf16 once.
+ * and the other dims are copied.  The angle is taken modulo a turn in 64-bit
+ * integers, within 2^-31 of a turn at every int32 position, and then rounded to fp32
+ * half turns, by up to 2^-26 of a turn; its cosine and sine and the products are
+ * fp32, rounded to bf16 once.
  *
  *   rot_dim      a multiple of 16, 16 .. head_dim (else ATTN_ERR_UNSUPPORTED)
  *   interleaved  0: pair p is dims (p, p + rot_dim / 2);  1: dims (2p, 2p + 1)

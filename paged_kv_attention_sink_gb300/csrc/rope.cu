@@ -8,7 +8,9 @@
 // fraction F = round(inv_freq / 2 pi * 2^64): position * F modulo 2^64 is then
 // the angle's fraction of a turn, exact but for the rounding of F (2^31 * 2^-65
 // of a turn at the farthest position), by one integer product.  Its upper 32
-// bits, as a signed number of half turns, go to sincospif.
+// bits, as a signed number of half turns, go to sincospif: in fp32, which rounds them
+// by up to 2^-25 of a half turn, less than 2^-23 radians (bf16 then rounds the row by
+// 2^-8 of its values).
 //
 // Memory-bound: each row is read and written once, in 16-byte chunks.  A thread
 // turns 8 pairs at a time, an item: two chunks, which hold the pairs' halves (chunk
