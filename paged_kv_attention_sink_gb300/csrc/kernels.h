@@ -18,6 +18,18 @@ namespace attn {
 // loads (or asynchronous copies) alone: neither __ldg nor a const __restrict__
 // parameter, whose loads may take the read-only path and be moved before the
 // wait, for they promise that the data does not change while the kernel runs.
+// What a plan's own lists hold is uploaded ahead of every launch and may be read
+// before the wait.
+//
+// The `late` kernels of a cross-attention call (launch_cross) are the exception: they
+// read q, k and v and write their rows before they wait.  That is sound only behind a
+// kernel of the same call that waits before it calls grid_dependents_go(), or behind
+// another late one that follows such a kernel: whatever came before the call is then
+// complete when a late one starts.  A late kernel writes nothing that the kernels
+// which it overlaps read or write, reads nothing that they write, and itself waits
+// before it ends, on every path, so that what follows it follows all of them.  No
+// kernel that opens before its wait (append and expand of 4-bit pages, eviction, key
+// weights of prompts) may stand in front of a late one.
 template <class... Params, class... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                              Args&&... args) {
