@@ -124,7 +124,10 @@ def _check(fn: str, status: int, extra: str = ""):
 def _i32_host(a) -> np.ndarray:
     if isinstance(a, torch.Tensor):
         a = a.detach().cpu().numpy()
-    return np.ascontiguousarray(np.asarray(a), dtype=np.int32)
+    a = np.asarray(a)
+    if a.dtype != np.int32 and a.size and not (a.min() >= -1 << 31 and a.max() < 1 << 31):
+        raise ValueError("indices and lengths must fit in 32 bits")
+    return np.ascontiguousarray(a, dtype=np.int32)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -227,11 +230,9 @@ class Rope:
     (p, p + len(inv_freq)).  scale: multiplies cosines and sines."""
 
     def __init__(self, inv_freq, axis=None, interleaved: bool = False, scale: float = 1.0):
-        def host(x, dtype):
-            x = x.detach().cpu().numpy() if isinstance(x, torch.Tensor) else x
-            return np.ascontiguousarray(np.asarray(x, dtype=dtype))
-        self._inv_freq = host(inv_freq, np.float32)
-        self._axis = np.zeros(len(self._inv_freq), np.int32) if axis is None else host(axis, np.int32)
+        inv_freq = inv_freq.detach().cpu().numpy() if isinstance(inv_freq, torch.Tensor) else inv_freq
+        self._inv_freq = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float32))
+        self._axis = np.zeros(len(self._inv_freq), np.int32) if axis is None else _i32_host(axis)
         if self._inv_freq.ndim != 1 or self._axis.shape != self._inv_freq.shape or not len(self._inv_freq):
             raise ValueError("inv_freq and axis must have one entry per pair of dims")
         if self._axis.min() < 0:
@@ -285,8 +286,8 @@ class PagePool:
         self.pools = list(pools)
         if not self.pools or not isinstance(self.pools[0], torch.Tensor) or self.pools[0].dim() < 1:
             raise TypeError("pools must be CUDA tensors [num_pages, ...]")
-        if page_size < 1:
-            raise ValueError("page_size must be positive")
+        if not 0 < page_size < 1 << 31:
+            raise ValueError("page_size must be 1 to 2^31 - 1")
         first = self.pools[0]
         if not 0 < first.shape[0] < 1 << 31:
             raise ValueError("a pool must have 1 to 2^31 - 1 pages")
@@ -718,8 +719,8 @@ class CrossPlan(Plan):
                  workspace: Optional[torch.Tensor] = None):
         lib = load_library()
         self._handle = None
-        if not 0 <= kv_rows < 1 << 31 or any(np.any(np.asarray(x) > 0x7fffffff) for x in (qo_indptr, kv_start, kv_len)):
-            raise ValueError("rows and lengths must be below 2^31")
+        if not 0 <= kv_rows < 1 << 31:
+            raise ValueError("kv_rows must be 0 to 2^31 - 1")
         qo, start, lens = _i32_host(qo_indptr), _i32_host(kv_start), _i32_host(kv_len)
         self.batch = max(0, len(qo) - 1)
         if len(start) != self.batch or len(lens) != self.batch:
