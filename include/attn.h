@@ -515,8 +515,7 @@ ATTN_API attn_status attn_append_kv_rope(attn_plan_t plan, const attn_rope_spec*
  *   page_table [table_len], kv_indptr [batch + 1], kv_lens [batch], parents [n]   device int32;
  *                 request p's pages are page_table[kv_indptr[p] ..] as in attn_plan
  *   page_table_out, indptr_out   device int32 [out_len], [n + 1], outputs: child c's
- *                 ceil(kv_lens / page_size) entries from indptr_out[c] on; must not
- *                 overlap the inputs (page_table and kv_indptr are compared).  Entries
+ *                 ceil(kv_lens / page_size) entries from indptr_out[c] on.  Entries
  *                 past the last are left as they were.
  *   scratch       device int32 [attn_pages_scratch(n)], for this call alone
  * A child whose parent is not in [0, batch), or whose kv_lens its entries (within
@@ -538,8 +537,10 @@ ATTN_API attn_status attn_append_kv_rope(attn_plan_t plan, const attn_rope_spec*
  *   scratch       device int32 [attn_pages_scratch(num_pages / 2)], for this call alone
  * Plans hold no copy of page ids, so a plan over that page_table stays valid.
  *
- * num_pages > 0; n, n_entries, table_len, out_len >= 0, below 2^31.  All are asynchronous on
- * `stream` and capturable.
+ * num_pages > 0; n, n_entries, table_len, out_len >= 0, below 2^31.  What a call writes (refs,
+ * outputs, scratch, the page_table of attn_pages_compact) must overlap neither what it
+ * reads nor anything else it writes (compared, but for the pools' contents:
+ * ATTN_ERR_INVALID_ARG).  All are asynchronous on `stream` and capturable.
  */
 ATTN_API int64_t attn_pages_scratch(int64_t n);
 ATTN_API attn_status attn_pages_alloc(int32_t* refs, int32_t num_pages, int32_t n, int32_t* page_ids,

@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cstring>
 #include <exception>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -588,6 +589,26 @@ attn_status check_refs(const int32_t* refs, int32_t num_pages, const int32_t* de
     return num_pages > 0 && refs && aligned16(refs) && aligned4(device_error) ? ATTN_OK : ATTN_ERR_INVALID_ARG;
 }
 
+// n int32 at p.  The scans read their inputs twice and count on the same values, so
+// that what a call writes may overlap neither what it reads nor anything else it writes.
+struct Words {
+    const int32_t* p;
+    int64_t n;
+};
+bool overlap(Words x, Words y) {
+    return x.n > 0 && y.n > 0 && reinterpret_cast<uintptr_t>(x.p) < reinterpret_cast<uintptr_t>(y.p) + y.n * sizeof(int32_t) &&
+           reinterpret_cast<uintptr_t>(y.p) < reinterpret_cast<uintptr_t>(x.p) + x.n * sizeof(int32_t);
+}
+bool apart(std::initializer_list<Words> written, std::initializer_list<Words> read) {
+    for (const Words* w = written.begin(); w != written.end(); ++w) {
+        for (const Words* x = w + 1; x != written.end(); ++x)
+            if (overlap(*w, *x)) return false;
+        for (const Words& r : read)
+            if (overlap(*w, r)) return false;
+    }
+    return true;
+}
+
 // Pools k0 on, as many as a launch's arguments hold.
 attn::PagePools some_pools(void* const* pools, const int64_t* page_bytes, int32_t n_pools, int32_t k0) {
     attn::PagePools p = {};
@@ -619,7 +640,7 @@ extern "C" attn_status attn_pages_alloc(int32_t* refs, int32_t num_pages, int32_
     if (attn_status st = check_refs(refs, num_pages, device_error); st != ATTN_OK) return st;
     if (n < 0) return ATTN_ERR_INVALID_ARG;
     if (n == 0) return ATTN_OK;
-    if (!page_ids || !aligned4(page_ids)) return ATTN_ERR_INVALID_ARG;
+    if (!page_ids || !aligned4(page_ids) || !apart({{refs, num_pages}, {page_ids, n}}, {})) return ATTN_ERR_INVALID_ARG;
     return attn::launch_pages_alloc(refs, num_pages, n, page_ids, device_error, static_cast<cudaStream_t>(stream));
 }
 
@@ -628,7 +649,7 @@ extern "C" attn_status attn_pages_free(int32_t* refs, int32_t num_pages, const i
     if (attn_status st = check_refs(refs, num_pages, device_error); st != ATTN_OK) return st;
     if (n < 0 || n > INT32_MAX) return ATTN_ERR_INVALID_ARG;
     if (n == 0) return ATTN_OK;
-    if (!page_ids || !aligned4(page_ids)) return ATTN_ERR_INVALID_ARG;
+    if (!page_ids || !aligned4(page_ids) || !apart({{refs, num_pages}}, {{page_ids, n}})) return ATTN_ERR_INVALID_ARG;
     return attn::launch_pages_free(refs, num_pages, page_ids, n, device_error, static_cast<cudaStream_t>(stream));
 }
 
@@ -658,12 +679,9 @@ extern "C" attn_status attn_pages_fork(int32_t* refs, int32_t num_pages, const i
                   !aligned4(kv_lens) || !aligned4(parents)))
         return ATTN_ERR_INVALID_ARG;
     if (out_len > 0 && (!page_table_out || !aligned4(page_table_out))) return ATTN_ERR_INVALID_ARG;
-    auto overlap = [](const int32_t* x, int64_t nx, const int32_t* y, int64_t ny) {
-        return nx > 0 && ny > 0 && reinterpret_cast<uintptr_t>(x) < reinterpret_cast<uintptr_t>(y) + ny * sizeof(int32_t) &&
-               reinterpret_cast<uintptr_t>(y) < reinterpret_cast<uintptr_t>(x) + nx * sizeof(int32_t);
-    };
-    if (n > 0 && (overlap(page_table_out, out_len, page_table, table_len) ||
-                  overlap(indptr_out, (int64_t)n + 1, kv_indptr, (int64_t)batch + 1)))
+    if (!apart({{refs, num_pages}, {page_table_out, out_len}, {indptr_out, (int64_t)n + 1}, {scratch, attn_pages_scratch(n)}},
+               {{page_table, n > 0 ? table_len : 0}, {kv_indptr, n > 0 ? (int64_t)batch + 1 : 0}, {kv_lens, n > 0 ? batch : 0},
+                {parents, n}}))
         return ATTN_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const attn::PageFork f = {page_table, kv_indptr, kv_lens, parents, table_len, batch, n, page_size, page_table_out,
@@ -683,6 +701,8 @@ extern "C" attn_status attn_pages_compact(int32_t* refs, int32_t num_pages, int3
     if (attn_status st = check_pools(pools, page_bytes, n_pools); st != ATTN_OK) return st;
     if (n_entries < 0 || n_entries > INT32_MAX || !remap || !scratch || !aligned4(remap) || !aligned4(scratch) ||
         (n_entries > 0 && (!page_table || !aligned4(page_table))))
+        return ATTN_ERR_INVALID_ARG;
+    if (!apart({{refs, num_pages}, {page_table, n_entries}, {remap, num_pages}, {scratch, attn_pages_scratch(num_pages / 2)}}, {}))
         return ATTN_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (attn_status st = attn::launch_pages_compact(refs, num_pages, page_table, n_entries, remap,
