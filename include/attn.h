@@ -691,7 +691,13 @@ ATTN_API attn_status attn_plan_get_info(attn_plan_t plan, attn_plan_info* info);
  * head0, n_heads, n_kv_tiles, key_end, reserved, reserved (pos0 = absolute
  * position of the tile's first query; key_end = one past the last key any
  * row of the tile may see).  `capacity` counts units/items; at most that many
- * are copied.
+ * are copied.  In a cross plan a unit's or item's keys are rows page_base +
+ * [tok_begin, tok_end) or [0, kv_len) of k and v, and its rows and heads are pairs: pair p
+ * from (q_row, kv_head * G) on is row p / G, head p % G of the KV head's G.  A unit has
+ * pairs head0 .. head0 + n_heads - 1 of its sequence; an item has n_rows pairs from q_row0
+ * on and, where n_heads = 2, as many as the first reserved word says from row
+ * q_row0 + 128 / G on; pos0 >= 0 marks a chunk of split keys, the second reserved
+ * word being which.
  */
 ATTN_API attn_status attn_plan_get_decode_units(attn_plan_t plan, int32_t* units, int64_t capacity);
 ATTN_API attn_status attn_plan_get_prefill_items(attn_plan_t plan, int32_t* items, int64_t capacity);

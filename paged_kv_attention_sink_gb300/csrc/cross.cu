@@ -26,10 +26,11 @@
 //
 // Measured: 48 x 5 beams over 1,500 keys of 16 heads x 64 dims (295 MB) 45 us, 6.6 TB/s;
 // 16 rows over 2K-32K keys, 16 query heads on each of 4 KV heads x 128 dims (644 MB) 98,
-// 6.6 TB/s (0.97 of the copy rate; issue 21%, tensor pipe 19%).  Small calls are the
-// latency of one kernel, 2.6 us in a graph.  With 32 pairs it takes a tenth to a
-// fifth longer than with 16: both read the same, and a warp's products and softmax
-// double.
+// 6.6 TB/s (0.97 of the copy rate; issue 21%, tensor pipe 20%).  Small calls are the
+// latency of one kernel, 2.5 to 2.9 us in a graph.  With 32 pairs it takes a seventh to
+// a quarter longer than with 16 (64 x 1,500 keys of 8 heads of 64 dims 40 and 47 us, 32 x
+// 1,500 of 16 heads of 128 dims 61 and 69, 1 x 16,000 of 16 heads of 64 dims 13.1 and
+// 16.2): both read the same, and a warp's chain of products and softmax doubles.
 #include <cuda.h>
 
 #include "attn_internal.h"

@@ -14,8 +14,8 @@
 // thread in flight.  How many pages move is only known on the device, so the
 // grid reads the count there; nothing waits on the host.
 //
-// Measured (in a graph): a fork of 32 children of 8 heads x 64 dims in two layers 9
-// us with its free, 1,024 children (382 MB copied, 37K entries shared) 94; the scan of
+// Measured (in a graph): a fork of 32 children of 8 heads x 64 dims in two layers 11
+// us with its free, 1,024 children (382 MB copied, 37K entries shared) 96; the scan of
 // 36K pages and its moves 12 (latency: two exchanges of the cluster and three
 // dependent loads), the copy after it 160 (1.12 GB, 7.0 TB/s).
 //

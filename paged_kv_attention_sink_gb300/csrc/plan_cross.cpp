@@ -78,8 +78,9 @@ attn_status build(const int32_t* qo_indptr, const int32_t* kv_start, const int32
     // Kernel for few against the one for many: 5 sequences of 61 rows over up to 35 keys, 5
     // heads on 1 of 64 dims 4.5 us against 8.5; 4 of up to 160 rows over 680 keys, 4 heads on
     // 2 of 128 dims 11.9 against 20.0; beyond the limit 6 of up to 976 rows over 17 keys, 10
-    // heads on 5 of 64 dims 11.0 against 7.6.  Over 124 mixes that the choice changes by 2 %
-    // or more, a limit of 2, 4, 5, 6, 8 or 16 takes 6.1, 2.1, 1.1, 1.0, 2.1 or 2.9 % longer
+    // heads on 5 of 64 dims 11.0 against 7.6.  Of the cross cases that perf/more_operators.py
+    // draws for seeds 0 to 699 the choice changes 124 by 2 % or more.  Over these a limit
+    // of 2, 4, 5, 6, 8 or 16 takes 6.1, 2.1, 1.1, 1.0, 2.1 or 2.9 % longer
     // than the better kernel for each would (geometric mean); one that 6 gets wrong is 1
     // sequence of up to 1,922 rows over 19 keys, 6 heads on 2 of 128 dims: 13.4 us where
     // 10.3 was to be had.

@@ -48,7 +48,7 @@
 // head (a box of G heads x 128 / G rows), whatever G is, and an item's two slots
 // are two such row blocks.  With slots of one head each, as above, G = 1 would
 // leave the second slot idle.  Measured: nine prompts of 0.2K-2K rows over up to 6.4K
-// keys, 64 heads on 8 of 64 dims, 645 us, 1,050 TFLOP/s, the chain of a tile (scores'
+// keys, 64 heads on 8 of 64 dims, 642 us, 1,055 TFLOP/s, the chain of a tile (scores'
 // load, exponentials, P, PV) as in prefill.  Slower: the scores released right after
 // their load, the row maximum taken by that load (tcgen05.ld.red), 7%; halves of a
 // tile at a time 13-15%; a row's softmax shared by two warps, four on a scheduler,

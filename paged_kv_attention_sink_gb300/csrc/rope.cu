@@ -26,9 +26,12 @@
 // TB/s, the copy rate (issue 68% of the slots); 123 with CTAs of whole rows; 118 with
 // the pages looked up after the angles and a pair's frequency and axis read from
 // the parameters by each lane (its own: 32 reads one after the other), 123 and 135
-// with 2 and 6 items per thread then.  Rows of 2 heads of 64 dims are bound by
-// their angles, one of 400K rows in 68 us (195 with those reads).  64 rows: 2.6 us in a
-// graph, a launch and three dependent loads.
+// with 2 and 6 items per thread then.  64 rows: 2.7 us in a graph, a launch and three
+// dependent loads.  Rows of few heads are bound by the angles' chain: a CTA of rows of
+// two heads has 62 of them, so that a thread has up to eight angles one after the
+// other, each after the first behind its position's load, and half of its items are
+// none.  400K rows of two heads of 64 dims, where the bytes take 30 us: 61 us; 50 with
+// positions computed instead of loaded, 54 without sines and cosines, 41 without both.
 #include <algorithm>
 #include <cstdint>
 
