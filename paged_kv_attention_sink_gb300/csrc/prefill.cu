@@ -113,7 +113,7 @@ struct PrefillCfg {
     static constexpr int kOffOnes = kOffStage + (kSplitP ? 2 * kAtom : 0);  // 16 key rows x 128 B
     static constexpr int kOffBar = kOffOnes + (kSplitP ? 2048 : 0);
     static constexpr int kNumBars = 2 * kQBufs + 2 * kStagesK + 2 * kStagesV + 8 + 2 + 8;
-    static constexpr int kSmem = 1024 + kOffBar + kNumBars * 8 + 16;
+    static constexpr int kSmem = 1024 + kOffBar + kNumBars * 8 + 32;
     static constexpr uint32_t kTmemCols = 512;
     // TMEM columns of head slot i (every region starts on a multiple of 32).
     // D = 64:  S 0 | 128, O (+ row sum) 256 | 384, P keys 0..95 at 336 | 464.
@@ -175,6 +175,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
     uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_mem + C::kNumBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* issued_s = abort_flag + 1;   // K tiles, V tiles, Qs whose copies were issued, for the tear-down
 
     Bars B;
     B.q_full = ptx::smem_u32(bar_mem);
@@ -276,7 +277,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
         const uint32_t empty0 = is_k ? B.k_empty : B.v_empty;
         const uint32_t dst0 = sbase + (is_k ? C::kOffK : C::kOffV);
         const uint64_t policy = ptx::policy_evict_last();
-        int jg = 0, n_item = 0, n_aux = 0, issued = 0, q_issued = 0;
+        int jg = 0, n_item = 0, n_aux = 0, issued = 0;
         // The page ids of the next tile are loaded (one per lane) while the
         // current tile is issued, so the dependent global load never sits
         // between two tiles.
@@ -316,7 +317,6 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                                              B.q_full + 8 * qb, c * 64, kCross ? it.head0 : it.head0 + i,
                                              kCross ? it.q_row0 + i * a.slot_rows : it.q_row0);
                 }
-                q_issued = n_item + 1;
             }
             const int valid = min(kPrefillKeys, it.kv_len - j * kPrefillKeys);
             const int n_load = (valid + P - 1) / P;
@@ -330,6 +330,7 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
             const int st = jg % n_stages;
             if (jg >= n_stages && !wait_all(empty0 + 8 * st, ((jg / n_stages) - 1) & 1)) {
                 fail(ATTN_DEVICE_ERR_TIMEOUT);
+                j = 1;   // (this item's Q is on its way)
                 break;
             }
             // V rows past the end of the sequence must be zeroed before the MMA
@@ -376,8 +377,8 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
             it = it_n;
             page = page_n;
         }
-        ptx::await_copies(full0, n_stages, issued);
-        ptx::await_copies(B.q_full, C::kQBufs, q_issued);
+        if (lane == 0) issued_s[is_k ? 0 : 1] = issued;
+        if (is_k && lane == 0) issued_s[2] = n_item + (j > 0);
     } else if (warp == 1 || warp == 2) {
         // ================================================================ MMA issuers
         // One warp per head slot, so neither head's MMAs wait behind the other
@@ -865,6 +866,14 @@ prefill_sink_attn_kernel(const __grid_constant__ CUtensorMap q_map,
     // MMA it issued is complete; then the TMEM columns are released.
     ptx::tc_fence_before();
     __syncthreads();
+    // Where a warp gave up, nobody has waited for the last copies: they land before the CTA
+    // ends.  (At the end of the loading warps' own code, unconditionally, these waits took
+    // 0.6% of a paged prefill of 64 dims.)
+    if (warp == 0 && *abort_flag) {
+        ptx::await_copies(B.k_full, C::kStagesK, issued_s[0]);
+        ptx::await_copies(B.v_full, C::kStagesV, issued_s[1]);
+        ptx::await_copies(B.q_full, C::kQBufs, issued_s[2]);
+    }
     if (warp == 1) {
         if (lane == 0) ptx::mbar_wait(B.drain, 0);
         __syncwarp();
